@@ -11,14 +11,12 @@
 
 #include "../../include/streamkl.h"
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 
 using namespace streamkl;
 
-namespace {
-
-constexpr int kMaxSplits = 64;
-constexpr int64_t kDefaultWaitNs = 2000000000LL;
+namespace streamkl {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -79,6 +77,55 @@ int decode_splits(int64_t units, int k_tiles, int sms) {
     if (s > kMaxSplits) s = kMaxSplits;
     return s < 1 ? 1 : static_cast<int>(s);
 }
+
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+}  // namespace
+
+// 4-D map over [B, H, N, d] bf16 with a (64 x rows x heads) box, 128-byte
+// swizzle; rows outside [0, N) read as zero.  A box of several heads lands
+// in shared memory as heads * rows consecutive 128-byte rows, head-major.
+bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const int64_t N = is_q ? s->Nq : s->Nk;
+    const int64_t sb = is_q ? s->q_stride_b : s->k_stride_b;
+    const int64_t sh = is_q ? s->q_stride_h : s->k_stride_h;
+    const int64_t sn = is_q ? s->q_stride_n : s->k_stride_n;
+    cuuint64_t dims[4] = {cuuint64_t(s->d), cuuint64_t(N), cuuint64_t(is_q ? s->H : kv_heads(s)), cuuint64_t(s->B)};
+    cuuint64_t strides[3] = {cuuint64_t(sn * 2), cuuint64_t(sh * 2), cuuint64_t(sb * 2)};
+    cuuint32_t box[4] = {cuuint32_t(kSwizzleCols), cuuint32_t(box_rows), cuuint32_t(box_heads), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+float resolve_scale(float scale, int d) {
+    if (!(scale > 0.f) || std::isinf(scale)) return 1.0f / std::sqrt(static_cast<float>(d));
+    return scale;
+}
+
+int64_t wait_limit(const streamkl_options* opt) {
+    return (opt && opt->wait_limit_ns > 0) ? opt->wait_limit_ns : kDefaultWaitNs;
+}
+
+}  // namespace streamkl
+
+namespace {
 
 struct FwdPlan {
     bool decode;
@@ -192,50 +239,6 @@ streamkl_status plan_bwd(const streamkl_shape* s, int setting, int causal, const
     // bf16 gradients from a mode that adds dQ up: dQ is accumulated in float32 in the workspace first
     if ((pl->fused || pl->keysplit) && pl->bf16) pl->ws_bytes += size_t(BH) * s->Nq * s->d * sizeof(float);
     return STREAMKL_OK;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// 4-D map over [B, H, N, d] bf16 with a (64 x rows x heads) box, 128-byte
-// swizzle; rows outside [0, N) read as zero.  A box of several heads lands
-// in shared memory as heads * rows consecutive 128-byte rows, head-major.
-bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows,
-              int box_heads = 1) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    const int64_t N = is_q ? s->Nq : s->Nk;
-    const int64_t sb = is_q ? s->q_stride_b : s->k_stride_b;
-    const int64_t sh = is_q ? s->q_stride_h : s->k_stride_h;
-    const int64_t sn = is_q ? s->q_stride_n : s->k_stride_n;
-    cuuint64_t dims[4] = {cuuint64_t(s->d), cuuint64_t(N), cuuint64_t(is_q ? s->H : kv_heads(s)), cuuint64_t(s->B)};
-    cuuint64_t strides[3] = {cuuint64_t(sn * 2), cuuint64_t(sh * 2), cuuint64_t(sb * 2)};
-    cuuint32_t box[4] = {cuuint32_t(kSwizzleCols), cuuint32_t(box_rows), cuuint32_t(box_heads), 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-float resolve_scale(float scale, int d) {
-    if (!(scale > 0.f) || std::isinf(scale)) return 1.0f / std::sqrt(static_cast<float>(d));
-    return scale;
-}
-
-int64_t wait_limit(const streamkl_options* opt) {
-    return (opt && opt->wait_limit_ns > 0) ? opt->wait_limit_ns : kDefaultWaitNs;
 }
 
 }  // namespace

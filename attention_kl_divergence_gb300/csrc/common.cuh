@@ -82,6 +82,34 @@ struct CombineParams {
     float* LSE2;
 };
 
+// Norm and rotation of the query heads (side 0) and the key heads (side 1).
+struct NormRopeSide {
+    int H;
+    const void* x;          // [B, H, N, d] bf16
+    void* y;                // forward: output, bf16; backward: the gradient of y, bf16 or float32
+    void* dx;               // backward only, bf16
+    const void* w;          // [d] bf16 or float32, or null (weights of one)
+    void* dw;               // backward only, as w, or null
+    int64_t x_b, x_h, x_n;  // element strides
+    int64_t y_b, y_h, y_n;
+    int64_t dx_b, dx_h, dx_n;
+};
+
+struct NormRopeParams {
+    NormRopeSide side[2];
+    int B, N, Hq, Hk;
+    int rot;                // rotated values per head, a multiple of 8
+    bool interleaved;       // pairs (2e, 2e + 1) instead of (e, e + rot / 2)
+    bool weight_bf16, grad_bf16, pos_int64;
+    float eps;
+    const float* table;     // [table_rows][rot / 2][2]: cosine, sine
+    int64_t table_rows;
+    const void* positions;  // [B, N] int32 or int64, or null: start + n
+    int64_t start;
+    float* part;            // backward: [ctas][d] parts of dw
+    int ctas_q;             // backward: CTAs of the query heads
+};
+
 // Partial state of one row over a key range, in the units the kernels keep:
 //   m1, m2  running reference maxima of the raw dot products z = <q, k>
 //   l1, l2  sum_j 2^(c (z_t[j] - m_t)),  c = scale * log2(e)

@@ -31,4 +31,12 @@ cudaError_t launch_bwd_joint(int d, const CUtensorMap* qmaps, const CUtensorMap*
 cudaError_t launch_bwd_decode(int d, int setting, const CUtensorMap* maps, const BwdParams& p, int ctas,
                               cudaStream_t stream);
 
+// Norm and rotation of query and key heads.  norm_rope_bwd_ctas plans the
+// gradient pass: its CTAs, and how many of them take the query heads.
+cudaError_t launch_norm_rope_fwd(int d, const NormRopeParams& p, cudaStream_t stream);
+void norm_rope_bwd_ctas(const NormRopeParams& p, int sms, int* ctas_q, int* ctas);
+cudaError_t launch_norm_rope_bwd(int d, const NormRopeParams& p, int ctas, cudaStream_t stream);
+cudaError_t launch_rope_table(const double* inv_freq, int64_t rows, int half, float* table, int sms,
+                              cudaStream_t stream);
+
 }  // namespace streamkl

@@ -9,7 +9,14 @@ Functions mirror the C ABI in ``include/streamkl.h``:
     kl_bwd_joint(g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=False) -> (dQ1, dK1, dQ2, dK2)
 
 plus ``fwd_plan`` / ``bwd_plan`` (what a call launches) and ``AttentionKL``,
-an autograd Function.  There is no fallback: without the compiled library
+an autograd Function.  The step before the divergence, the norm of query and
+key heads with their rotation:
+
+    rope_table(rows, rot, device) -> table
+    qk_norm_rope(q, k, wq, wk, table, positions=None) -> (q', k')
+    qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, table, positions=None) -> (dq, dk, dwq, dwk)
+
+and ``QKNormRope``, its autograd Function.  There is no fallback: without the compiled library
 every call raises.
 """
 from __future__ import annotations
@@ -47,6 +54,17 @@ class Plan(ctypes.Structure):
                 ("launches", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hk", "N", "d", "rot", "interleaved", "weight_bf16",
+                                              "grad_bf16", "pos_int64")] + \
+        [("eps", ctypes.c_float), ("table_rows", ctypes.c_int64), ("start", ctypes.c_int64)] + \
+        [(n, Strides) for n in ("q", "k", "yq", "yk", "dq", "dk")]
+
+
 class StreamKLError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -56,7 +74,8 @@ class StreamKLError(RuntimeError):
 EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd", "streamkl_workspace_status",
             "streamkl_status_string", "streamkl_version", "streamkl_fwd_noalloc", "streamkl_noalloc_status",
             "streamkl_fwd_workspace_bytes", "streamkl_bwd_workspace_bytes", "streamkl_bwd_joint_plan",
-            "streamkl_bwd_joint")
+            "streamkl_bwd_joint", "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd",
+            "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table")
 
 _lock = threading.Lock()
 _lib = None
@@ -92,11 +111,18 @@ def load(build_if_stale: bool = True):
         lib.streamkl_bwd_workspace_bytes.argtypes = [sp, I, I]
         lib.streamkl_fwd_workspace_bytes.restype = Z
         lib.streamkl_bwd_workspace_bytes.restype = Z
+        nr = ctypes.POINTER(NormRope)
+        lib.streamkl_norm_rope_fwd.argtypes = [nr, *[P] * 9]
+        lib.streamkl_norm_rope_bwd.argtypes = [nr, *[P] * 13, Z, P]
+        lib.streamkl_norm_rope_workspace_bytes.argtypes = [nr]
+        lib.streamkl_norm_rope_workspace_bytes.restype = Z
+        lib.streamkl_rope_table.argtypes = [P, ctypes.c_int64, ctypes.c_int32, P, P]
         lib.streamkl_status_string.argtypes = [I]
         lib.streamkl_status_string.restype = ctypes.c_char_p
         for name in ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd",
                      "streamkl_workspace_status", "streamkl_version", "streamkl_fwd_noalloc",
-                     "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint"):
+                     "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint",
+                     "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -373,3 +399,140 @@ class AttentionKL(torch.autograd.Function):
                                 grad_dtype=torch.bfloat16)
                 grads[slot], grads[slot + 1] = dQ, dK
         return tuple(grads)
+
+
+# ---------------------------------------------------------------------------
+# Norm of query and key heads with the position rotation
+# ---------------------------------------------------------------------------
+def rope_table(rows, rot, device, base=10000.0, inv_freq=None) -> torch.Tensor:
+    """Cosines and sines of the positions below ``rows`` as float32 [rows, rot/2, 2],
+    from angles in float64.  inv_freq (rot/2 values) replaces base^(-2e/rot), for
+    scaled frequencies.  Made once and kept; it synchronises nothing."""
+    rot, rows = int(rot), int(rows)
+    if rot < 8 or rot % 8 or rot > 128 or rows < 1:
+        raise ValueError(f"rot must be a multiple of 8 up to 128 and rows at least 1, got {rot} and {rows}")
+    if inv_freq is None:
+        inv_freq = [float(base) ** (-2.0 * e / rot) for e in range(rot // 2)]
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64).to(device).contiguous()
+    if freq.numel() != rot // 2 or not freq.is_cuda:
+        raise ValueError(f"inv_freq must hold rot/2 = {rot // 2} values and device must be a CUDA device")
+    with torch.cuda.device(freq.device):
+        table = torch.empty((rows, rot // 2, 2), dtype=torch.float32, device=freq.device)
+        _raise(load().streamkl_rope_table(_ptr(freq), rows, rot // 2, _ptr(table), _stream(freq.device)),
+               "streamkl_rope_table")
+    return table
+
+
+def _heads(name, t, dtypes, device=None, shape=None):
+    """A [B, H, N, d] tensor that the kernels read or write through its strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor{'' if device is None else f' on {device}'}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be [B, H, N, d]{'' if shape is None else f' = {tuple(shape)}'}, got {tuple(t.shape)}")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have d contiguous")
+    # the stride of an axis with one entry is never used
+    return Strides(*[t.stride(k) if t.shape[k] > 1 else 0 for k in range(3)])
+
+
+def _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved):
+    desc = NormRope()
+    desc.q, desc.k = _heads("q", q, (torch.bfloat16,)), _heads("k", k, (torch.bfloat16,), q.device)
+    B, Hq, N, d = q.shape
+    if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+        raise ValueError("q and k must share B, N and d")
+    if d not in (64, 128):
+        raise ValueError(f"d must be 64 or 128, got {d}")
+    types = {w.dtype for w in (wq, wk) if w is not None}
+    if len(types) > 1 or not types <= {torch.float32, torch.bfloat16}:
+        raise ValueError("wq and wk must both be float32 or both bf16")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _check_tensor(name, w, (d,), w.dtype, q.device)
+    rot = 0
+    if table is not None:
+        if not isinstance(table, torch.Tensor) or table.dim() != 3:
+            raise ValueError("table must be [rows, rot/2, 2] (see rope_table)")
+        rot = 2 * table.shape[1]
+        _check_tensor("table", table, (table.shape[0], rot // 2, 2), torch.float32, q.device)
+        if rot > d or rot % 8 or rot == 0 or table.shape[0] == 0:
+            raise ValueError(f"the table rotates {rot} values by {table.shape[0]} positions: rot must be a multiple of 8 up to d = {d}")
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be an int32 or int64 tensor")
+        _check_tensor("positions", positions, (B, N), positions.dtype, q.device)
+    desc.B, desc.Hq, desc.Hk, desc.N, desc.d, desc.rot = B, Hq, k.shape[1], N, d, rot
+    desc.interleaved, desc.eps = int(bool(interleaved)), float(eps)
+    desc.weight_bf16 = int(torch.bfloat16 in types)
+    desc.pos_int64 = int(positions is not None and positions.dtype == torch.int64)
+    desc.table_rows, desc.start = (table.shape[0] if table is not None else 0), int(start)
+    return desc
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False, out=None):
+    """(q', k'): every head of q [B, Hq, N, d] and k [B, Hk, N, d] (bf16, any strides with d contiguous) divided by
+    its root mean square, times wq / wk ([d], float32 or bf16; None: ones), its first 2 * table.shape[1] values turned
+    by the angles of its position (positions [B, N], else start + n; table from rope_table; None: no rotation).  out: two
+    bf16 tensors of the same shapes, any strides (rows of a cache, or q and k themselves); new contiguous ones otherwise."""
+    desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k))
+    yq, yk = out
+    desc.yq = _heads("out[0]", yq, (torch.bfloat16,), q.device, q.shape)
+    desc.yk = _heads("out[1]", yk, (torch.bfloat16,), q.device, k.shape)
+    with torch.cuda.device(q.device):
+        _raise(load().streamkl_norm_rope_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(table),
+                                             _ptr(positions), _ptr(yq), _ptr(yk), _stream(q.device)),
+               "streamkl_norm_rope_fwd")
+    return yq, yk
+
+
+def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6,
+                     interleaved=False, workspace=None, out=None):
+    """(dq, dk, dwq, dwk) of sum(dyq q') + sum(dyk k') for qk_norm_rope's arguments; dyq, dyk are both bf16 or both
+    float32 (kl_bwd's gradients as they come), any strides with d contiguous.  dq, dk are bf16, dwq, dwk of the weights'
+    type (None without weights).  out: (dq, dk) to write into.  Equal inputs give equal bits."""
+    desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+    types = (torch.bfloat16, torch.float32)
+    desc.yq = _heads("dyq", dyq, types, q.device, q.shape)
+    desc.yk = _heads("dyk", dyk, (dyq.dtype,), q.device, k.shape)
+    desc.grad_bf16 = int(dyq.dtype == torch.bfloat16)
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k))
+    dq, dk = out
+    desc.dq = _heads("out[0]", dq, (torch.bfloat16,), q.device, q.shape)
+    desc.dk = _heads("out[1]", dk, (torch.bfloat16,), q.device, k.shape)
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    lib = load()
+    with torch.cuda.device(q.device):
+        nbytes = int(lib.streamkl_norm_rope_workspace_bytes(ctypes.byref(desc)))
+        # nothing in this workspace is read before it is written: no need to clear a new one
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device) if workspace is None \
+            else _check_workspace(workspace, nbytes, q.device)
+        _raise(lib.streamkl_norm_rope_bwd(ctypes.byref(desc), _ptr(dyq), _ptr(dyk), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
+                                          _ptr(table), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+                                          _ptr(workspace), workspace.numel(), _stream(q.device)),
+               "streamkl_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+class QKNormRope(torch.autograd.Function):
+    """(q', k') of qk_norm_rope with gradients to q, k, wq and wk.  Saves its
+    inputs and recomputes the norms in the backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False):
+        ctx.save_for_backward(q, k, wq, wk, table, positions)
+        ctx.how = dict(start=start, eps=eps, interleaved=interleaved)
+        return qk_norm_rope(q, k, wq, wk, table, positions, **ctx.how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, table, positions = ctx.saved_tensors
+        dyq, dyk = (torch.zeros_like(x, memory_format=torch.contiguous_format) if g is None else g.contiguous()
+                    for g, x in ((dyq, q), (dyk, k)))
+        grads = qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, table, positions, **ctx.how)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None, None, None)

@@ -227,6 +227,75 @@ STREAMKL_API streamkl_status streamkl_fwd_noalloc(const streamkl_shape* shape, c
  * copy).  Allocates nothing. */
 STREAMKL_API streamkl_status streamkl_noalloc_status(streamkl_stream_t stream, uint32_t* device_error);
 
+/* ---------------------------------------------------------------------------
+ * Norm of query and key heads with the position rotation, and its gradient.
+ *
+ * The step before the divergence: for every head x (d values) of q and k
+ *
+ *     r = (mean(x^2) + eps)^(-1/2),   y = R(position) (r x * w)
+ *
+ * where R turns the first `rot` values of the head as pairs, (e, e + rot/2)
+ * or, interleaved, (2e, 2e + 1), by the angle of the position and pair e:
+ * (a, b) -> (a cos - b sin, b cos + a sin).  One launch covers q and k.
+ *
+ *  - q [B, Hq, N, d] and k [B, Hk, N, d] are bf16 with d contiguous, read
+ *    through element strides (multiples of 8; 0 repeats along an axis), so
+ *    that views of one packed projection need no copy; d is 64 or 128, rot a
+ *    multiple of 8 up to d (0: norm only).  y is bf16 with strides of its
+ *    own (e.g. rows of a cache); yq may be q and yk may be k.
+ *  - wq, wk: [d], float32 or bf16 (weight_bf16), or NULL for weights of one.
+ *  - table: float32 [table_rows, rot/2, 2], cosine and sine of each position
+ *    and pair (streamkl_rope_table makes one).  positions: [B, N], int32 or
+ *    int64 (pos_int64), contiguous, or NULL for start + n.  A row whose
+ *    position is outside the table gets NaN in the rotated values (and in
+ *    its gradients, and so in dwq / dwk).
+ *  - N = 0 is allowed: nothing is written but zeros to dwq and dwk.
+ *  - Statistics and sums are float32; every output is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t b, h, n; /* element strides of the B, H and N axes */
+} streamkl_strides;
+
+typedef struct {
+    int32_t B, Hq, Hk, N, d, rot;
+    int32_t interleaved; /* 0: pairs (e, e + rot/2), 1: pairs (2e, 2e + 1) */
+    int32_t weight_bf16; /* wq, wk (and dwq, dwk): 0 = float32, 1 = bf16    */
+    int32_t grad_bf16;   /* dyq, dyk of the backward: 0 = float32, 1 = bf16 */
+    int32_t pos_int64;   /* positions: 0 = int32, 1 = int64                 */
+    float eps;
+    int64_t table_rows;
+    int64_t start;           /* first position when positions is NULL */
+    streamkl_strides q, k;   /* q and k */
+    streamkl_strides yq, yk; /* yq and yk, or in the backward dyq and dyk */
+    streamkl_strides dq, dk; /* backward only: dq and dk */
+} streamkl_norm_rope;
+
+/* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+STREAMKL_API streamkl_status streamkl_norm_rope_fwd(const streamkl_norm_rope* desc, const void* q, const void* k,
+                                                    const void* wq, const void* wk, const float* table,
+                                                    const void* positions, void* yq, void* yk,
+                                                    streamkl_stream_t stream);
+
+/* Gradient of sum(dyq * yq) + sum(dyk * yk): dq, dk (bf16, strided) and
+ * dwq, dwk ([d], the weights' type; NULL to skip one).  dq may be dyq and dk
+ * may be dyk when those are bf16 with the same strides.  The sums run in a
+ * fixed order: equal inputs give equal bits.  workspace as for the other
+ * calls; its size is streamkl_norm_rope_workspace_bytes, which returns 0 for
+ * an invalid description or when no CUDA device is current.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+STREAMKL_API size_t streamkl_norm_rope_workspace_bytes(const streamkl_norm_rope* desc);
+STREAMKL_API streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* desc, const void* dyq, const void* dyk,
+                                                    const void* q, const void* k, const void* wq, const void* wk,
+                                                    const float* table, const void* positions, void* dq, void* dk,
+                                                    void* dwq, void* dwk, void* workspace, size_t workspace_bytes,
+                                                    streamkl_stream_t stream);
+
+/* table[n][e] = (cos, sin) of n * inv_freq[e] for n < rows, e < half, from
+ * angles in float64 (at position 10^6 a float32 angle is off by 0.03).
+ * inv_freq: device float64 [half].  Errors: INVALID_ARG, CUDA. */
+STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t rows, int32_t half, float* table,
+                                                 streamkl_stream_t stream);
+
 /* Synchronises `stream`, reads the workspace's device error word into
  * *device_error (if not NULL), clears it, and returns STREAMKL_ERR_TIMEOUT if
  * it was set, STREAMKL_OK otherwise (or CUDA on a failed copy). */
