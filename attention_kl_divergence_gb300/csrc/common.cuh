@@ -82,6 +82,20 @@ struct CombineParams {
     float* LSE2;
 };
 
+// Masks that key_ranges turns into key ranges (null or 0: not used).
+struct KeyRangeParams {
+    int B, Nq, Nk, causal, window;
+    const int32_t* q_lengths;  // [B]
+    const int32_t* k_lengths;  // [B]
+    const int32_t* prefix;     // [B]
+    const int32_t* docs;       // bounds, [num_docs] or [B, num_docs]
+    int num_docs;
+    int64_t doc_stride;        // 0 or num_docs
+    int32_t* begin;
+    int32_t* end;
+    int32_t* offset;
+};
+
 // Norm and rotation of the query heads (side 0) and the key heads (side 1).
 struct NormRopeSide {
     int H;

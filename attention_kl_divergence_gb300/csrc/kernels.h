@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "score.cuh"
 
 namespace streamkl {
 
@@ -30,6 +31,15 @@ cudaError_t launch_bwd_joint(int d, const CUtensorMap* qmaps, const CUtensorMap*
                              const BwdParams& pkv, int ctas_q, int ctas_kv, cudaStream_t stream);
 cudaError_t launch_bwd_decode(int d, int setting, const CUtensorMap* maps, const BwdParams& p, int ctas,
                               cudaStream_t stream);
+
+// Score-modified divergence; mode: kScore* of score.cuh.  Maps as for fwd_tile /
+// fwd_decode, and as for bwd_kv.
+cudaError_t launch_score_fwd(int d, int mode, bool decode, const CUtensorMap* maps, const FwdParams& p,
+                             const ScoreParams& sp, int ctas, cudaStream_t stream);
+cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
+                             const ScoreParams& sp, int ctas, cudaStream_t stream);
+
+cudaError_t launch_key_ranges(const KeyRangeParams& p, cudaStream_t stream);
 
 // Norm and rotation of query and key heads.  norm_rope_bwd_ctas plans the
 // gradient pass: its CTAs, and how many of them take the query heads.

@@ -1,0 +1,161 @@
+// score.cuh -- how a raw dot product z = <q, k> becomes a score, and which keys
+// a query row sees; shared by the forward and backward kernels of the
+// score-modified divergence.
+//
+//   S = cap tanh(scale z / cap) - slope |i + offset - j|      (cap 0: scale z)
+//
+// The kernels keep x = log2(e) S, so that a probability is one ex2.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace streamkl {
+
+// What the kernels are compiled for.
+//   kScorePlain    no cap, no bias: x = c z, applied inside the exponent's FMA
+//   kScoreBounded  both sides capped, |x| <= kBoundedMax: sums of 2^x of any
+//                  length fit float32, so no running maximum is needed
+//   kScoreGeneral  any cap and bias, running maxima
+constexpr int kScorePlain = 0, kScoreBounded = 1, kScoreGeneral = 2;
+// 2^x with |x| <= 80: a sum of 2^31 of them is at most 2^111, times a score
+// difference (2^8) at most 2^119; the smallest one, 2^-80, is a normal number.
+constexpr float kBoundedMax = 80.f;
+
+// tanh(u) / u as a polynomial in u^2 (interpolated at the Chebyshev nodes of
+// the interval, so close to the best of its degree):
+//   4 terms, |u| <= 0.375: relative error 6e-8
+//   8 terms, |u| <= 1.2:   relative error 5e-8
+// beyond, 1 - 2 / (1 + e^2u) has no cancellation left to lose bits to.
+constexpr float kTanhNear = 0.375f, kTanhMid = 1.2f;
+
+// With r = scale / cap and u = r z.  An uncapped side has lim = 0.
+struct ScoreSide {
+    float near[4];       // coefficients of z, z^3, z^5, z^7 (lim, r and its powers folded in)
+    float mid[8];        // coefficients of u, u^3, ... (lim folded in)
+    float z_near, z_mid; // bounds of the polynomials on |z|
+    float ratio;         // r
+    float lim;           // log2(e) cap
+    float inv_lim;       // 1 / lim (0 when uncapped)
+    float c;             // log2(e) scale
+    const float* slopes; // [H] or null
+};
+
+struct ScoreParams {
+    ScoreSide side[2];
+    const int32_t* begin;   // [B, Nq] or null: 0
+    const int32_t* end;     // [B, Nq] or null: Nk
+    const int32_t* offset;  // [B] or null: Nk - Nq
+    int causal;
+    // backward: bounds of the visible keys of each 64-row query tile, [B][tiles][2]
+    int32_t* tile_range;
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Position of query row i of batch b among the keys.
+__device__ __forceinline__ int64_t row_position(const ScoreParams& s, int Nq, int Nk, int b, int i) {
+    return static_cast<int64_t>(i) + (s.offset ? s.offset[b] : Nk - Nq);
+}
+
+// Keys [x, y) that row i sees, inside [0, Nk); (0, 0) for none or a row past the end.
+__device__ __forceinline__ int2 row_range(const ScoreParams& s, int Nq, int Nk, int b, int i) {
+    if (i >= Nq) return make_int2(0, 0);
+    const size_t r = static_cast<size_t>(b) * Nq + i;
+    const int lo = s.begin ? max(s.begin[r], 0) : 0;
+    int hi = s.end ? min(s.end[r], Nk) : Nk;
+    if (s.causal) {
+        const int64_t next = row_position(s, Nq, Nk, b, i) + 1;
+        hi = static_cast<int>(next < hi ? (next > 0 ? next : 0) : hi);
+    }
+    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// Any finite z.  An infinite one becomes NaN, as it would without the cap: the
+// cap does not hide a broken token.  NaN stays NaN.
+__device__ __forceinline__ float score_far(float z, const ScoreSide& s) {
+    const float u = z * s.ratio, a = fabsf(u), y = u * u;
+    float r = s.mid[7];
+#pragma unroll
+    for (int k = 6; k >= 0; --k) r = fmaf(r, y, s.mid[k]);
+    const float t = fmaf(a, 0.f, s.lim - __fdividef(2.f * s.lim, 1.f + ex2(a * (2.f * kLog2e))));
+    return a <= kTanhMid ? u * r : copysignf(t, z);
+}
+
+template <int W>
+__device__ __forceinline__ float abs_max(const float (&z)[W]) {
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int e = 0; e < W; e += 4) {
+        a = max3f(a, fabsf(z[e]), fabsf(z[e + 1]));
+        b = max3f(b, fabsf(z[e + 2]), fabsf(z[e + 3]));
+    }
+    return fmaxf(a, b);  // NaN is passed over: every form below keeps it NaN
+}
+
+// z -> x in place, without the bias.  A warp takes the shortest form that
+// fits every score of its lanes.
+template <int W>
+__device__ __forceinline__ void cap_scores(float (&z)[W], const ScoreSide& s) {
+    if (s.lim == 0.f) {
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const float2 x = __fmul2_rn(make_float2(z[e], z[e + 1]), splat(s.c));
+            z[e] = x.x;
+            z[e + 1] = x.y;
+        }
+        return;
+    }
+    const float top = abs_max(z);
+    if (__all_sync(0xffffffffu, top <= s.z_near)) {
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const float2 v = make_float2(z[e], z[e + 1]), y = __fmul2_rn(v, v);
+            float2 r = __ffma2_rn(splat(s.near[3]), y, splat(s.near[2]));
+            r = __ffma2_rn(r, y, splat(s.near[1]));
+            r = __ffma2_rn(r, y, splat(s.near[0]));
+            const float2 x = __fmul2_rn(v, r);
+            z[e] = x.x;
+            z[e + 1] = x.y;
+        }
+    } else if (__all_sync(0xffffffffu, top <= s.z_mid)) {
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const float2 u = __fmul2_rn(make_float2(z[e], z[e + 1]), splat(s.ratio)), y = __fmul2_rn(u, u);
+            float2 r = splat(s.mid[7]);
+#pragma unroll
+            for (int k = 6; k >= 0; --k) r = __ffma2_rn(r, y, splat(s.mid[k]));
+            const float2 x = __fmul2_rn(u, r);
+            z[e] = x.x;
+            z[e + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) z[e] = score_far(z[e], s);
+    }
+}
+
+// Finish of a row from its state in x units (c = 1, scale = ln 2) or in raw
+// units (plain: scale = the softmax scale).  The difference of the two
+// log-sum-exps is taken before they are rounded: KL is often far smaller than
+// either.  `empty`: the row sees no key.
+__device__ __forceinline__ void finish_scored(const RowState& s, float scale, bool empty, float& kl, float& lse1,
+                                              float& lse2) {
+    if (empty) {
+        kl = 0.f;
+        lse1 = lse2 = -INFINITY;
+        return;
+    }
+    const float a = logf(s.l1), b = logf(s.l2), r = s.l2 / s.l1;
+    lse1 = fmaf(scale, s.m1, a);
+    lse2 = fmaf(scale, s.m2, b);
+    const float d = r > 1e-30f && r < 1e30f ? logf(r) : b - a;
+    kl = fmaf(scale, s.acc / s.l1 + (s.m2 - s.m1), d);
+    if (!(s.l1 > 0.f && s.l2 > 0.f)) kl = lse1 = lse2 = __int_as_float(0x7fc00000);  // NaN or -inf scores alone
+}
+
+}  // namespace streamkl

@@ -9,7 +9,14 @@ Functions mirror the C ABI in ``include/streamkl.h``:
     kl_bwd_joint(g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=False) -> (dQ1, dK1, dQ2, dK2)
 
 plus ``fwd_plan`` / ``bwd_plan`` (what a call launches) and ``AttentionKL``,
-an autograd Function.  The step before the divergence, the norm of query and
+an autograd Function.  The divergence of attentions with capped or biased
+scores and a key range per row:
+
+    key_ranges(B, Nq, Nk, device, causal=True, ...) -> (begin, end, offset)
+    kl_score_fwd(Scores(cap1=50.0, begin=begin, end=end), Q1, K1, Q2, K2) -> (KL, LSE1, LSE2)
+    kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2) -> (dQ, dK)
+
+and ``ScoredAttentionKL``, its autograd Function.  The step before the divergence, the norm of query and
 key heads with their rotation:
 
     rope_table(rows, rot, device) -> table
@@ -58,6 +65,11 @@ class Strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
 
 
+class Score(ctypes.Structure):
+    _fields_ = [("cap1", ctypes.c_float), ("cap2", ctypes.c_float)] + \
+        [(n, ctypes.c_void_p) for n in ("slopes1", "slopes2", "begin", "end", "offset")]
+
+
 class NormRope(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hk", "N", "d", "rot", "interleaved", "weight_bf16",
                                               "grad_bf16", "pos_int64")] + \
@@ -75,7 +87,8 @@ EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_
             "streamkl_status_string", "streamkl_version", "streamkl_fwd_noalloc", "streamkl_noalloc_status",
             "streamkl_fwd_workspace_bytes", "streamkl_bwd_workspace_bytes", "streamkl_bwd_joint_plan",
             "streamkl_bwd_joint", "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd",
-            "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table")
+            "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table", "streamkl_score_fwd_plan", "streamkl_score_fwd",
+            "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges")
 
 _lock = threading.Lock()
 _lib = None
@@ -111,6 +124,13 @@ def load(build_if_stale: bool = True):
         lib.streamkl_bwd_workspace_bytes.argtypes = [sp, I, I]
         lib.streamkl_fwd_workspace_bytes.restype = Z
         lib.streamkl_bwd_workspace_bytes.restype = Z
+        sc = ctypes.POINTER(Score)
+        i32 = ctypes.c_int32
+        lib.streamkl_score_fwd_plan.argtypes = [sp, op, pp]
+        lib.streamkl_score_fwd.argtypes = [sp, sc, P, P, P, P, F, I, P, P, P, P, Z, op, P]
+        lib.streamkl_score_bwd_plan.argtypes = [sp, I, op, pp]
+        lib.streamkl_score_bwd.argtypes = [sp, sc, I, P, P, P, P, P, P, P, P, F, I, P, P, P, Z, op, P]
+        lib.streamkl_key_ranges.argtypes = [i32, i32, i32, I, i32, P, P, P, P, i32, i32, P, P, P, P]
         nr = ctypes.POINTER(NormRope)
         lib.streamkl_norm_rope_fwd.argtypes = [nr, *[P] * 9]
         lib.streamkl_norm_rope_bwd.argtypes = [nr, *[P] * 13, Z, P]
@@ -122,7 +142,9 @@ def load(build_if_stale: bool = True):
         for name in ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd",
                      "streamkl_workspace_status", "streamkl_version", "streamkl_fwd_noalloc",
                      "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint",
-                     "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table"):
+                     "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table",
+                     "streamkl_score_fwd_plan", "streamkl_score_fwd", "streamkl_score_bwd_plan", "streamkl_score_bwd",
+                     "streamkl_key_ranges"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -398,6 +420,170 @@ class AttentionKL(torch.autograd.Function):
                 dQ, dK = kl_bwd(setting, g, Q1, K1, Q2, K2, KL, L1, L2, causal=ctx.causal, scale=ctx.scale,
                                 grad_dtype=torch.bfloat16)
                 grads[slot], grads[slot + 1] = dQ, dK
+        return tuple(grads)
+
+
+# ---------------------------------------------------------------------------
+# Divergence of attentions with modified scores
+# ---------------------------------------------------------------------------
+class Scores:
+    """How the raw products q.k of the teacher (1) and the student (2) become scores, and which keys each row sees:
+
+        S_t = cap_t tanh(scale q.k / cap_t) - slopes_t[h] |i + offset[b] - j|,   begin[b, i] <= j < end[b, i]
+
+    cap 0: no cap; slopes (float32 [H]), begin / end (int32 [B, Nq]) and offset (int32 [B], the key position of
+    row 0) may be None: no bias, every key, Nk - Nq.  key_ranges makes begin, end and offset from masks."""
+
+    __slots__ = ("cap1", "cap2", "slopes1", "slopes2", "begin", "end", "offset")
+
+    def __init__(self, cap1=0.0, cap2=0.0, slopes1=None, slopes2=None, begin=None, end=None, offset=None):
+        self.cap1, self.cap2 = float(cap1), float(cap2)
+        self.slopes1, self.slopes2, self.begin, self.end, self.offset = slopes1, slopes2, begin, end, offset
+
+    def tensors(self):
+        return self.slopes1, self.slopes2, self.begin, self.end, self.offset
+
+    def _struct(self, Q1):
+        B, H, Nq, _ = Q1.shape
+        for name, shape, dtype in (("slopes1", (H,), torch.float32), ("slopes2", (H,), torch.float32),
+                                   ("begin", (B, Nq), torch.int32), ("end", (B, Nq), torch.int32),
+                                   ("offset", (B,), torch.int32)):
+            t = getattr(self, name)
+            if t is not None:
+                _check_tensor(name, t, shape, dtype, Q1.device)
+        return Score(self.cap1, self.cap2, *(None if t is None else t.data_ptr() for t in self.tensors()))
+
+
+def key_ranges(B, Nq, Nk, device, causal=True, window=0, prefix=None, docs=None, q_lengths=None, k_lengths=None):
+    """(begin, end, offset) of Scores from masks.  Row i of batch b stands at key position p = i + offset[b], with
+    offset = k_lengths - q_lengths (int32 [B]; None: Nk, Nq); rows behind q_lengths see nothing.  It sees the keys below
+    k_lengths with j <= p (causal), p - window < j < p + window (window > 0), any j < prefix[b] (int32 [B], not with
+    window or docs), and of p's document alone (docs: nondecreasing int32 bounds, [M] for every batch or [B, M]; document
+    m is docs[m] <= j < docs[m + 1])."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    with torch.cuda.device(device):
+        device = torch.device("cuda", torch.cuda.current_device())
+        for name, t in (("prefix", prefix), ("q_lengths", q_lengths), ("k_lengths", k_lengths)):
+            if t is not None:
+                _check_tensor(name, t, (B,), torch.int32, device)
+        bounds = per_batch = 0
+        if docs is not None:
+            if not isinstance(docs, torch.Tensor) or docs.dim() not in (1, 2):
+                raise ValueError("docs must be an int32 tensor [M] or [B, M]")
+            bounds, per_batch = docs.shape[-1], int(docs.dim() == 2)
+            _check_tensor("docs", docs, (B, bounds) if per_batch else (bounds,), torch.int32, device)
+        begin, end = (torch.empty((B, Nq), dtype=torch.int32, device=device) for _ in range(2))
+        offset = torch.empty((B,), dtype=torch.int32, device=device)
+        _raise(load().streamkl_key_ranges(B, Nq, Nk, int(bool(causal)), int(window), _ptr(q_lengths), _ptr(k_lengths),
+                                          _ptr(prefix), _ptr(docs), bounds, per_batch, _ptr(begin), _ptr(end),
+                                          _ptr(offset), _stream(device)), "streamkl_key_ranges")
+    return begin, end, offset
+
+
+def _scores(scores):
+    if not isinstance(scores, Scores):
+        raise ValueError("scores must be a Scores")
+    return scores
+
+
+def score_fwd_plan(Q1, K1, num_splits=0) -> Plan:
+    plan = Plan()
+    with torch.cuda.device(Q1.device):
+        _raise(load().streamkl_score_fwd_plan(ctypes.byref(make_shape(Q1, K1)), ctypes.byref(_opts(num_splits)),
+                                              ctypes.byref(plan)), "streamkl_score_fwd_plan")
+    return plan
+
+
+def score_bwd_plan(Q1, K1, setting, grad_dtype=torch.float32) -> Plan:
+    plan = Plan()
+    with torch.cuda.device(Q1.device):
+        _raise(load().streamkl_score_bwd_plan(ctypes.byref(make_shape(Q1, K1)), int(setting),
+                                              ctypes.byref(_opts(grad_bf16=_grad_flag(grad_dtype))),
+                                              ctypes.byref(plan)), "streamkl_score_bwd_plan")
+    return plan
+
+
+def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0, workspace=None, out=None,
+                 wait_limit_ns=0, debug_flags=0):
+    """Per-row KL(P1 || P2), LSE1, LSE2 as float32 [B, H, Nq] for the scores that ``scores`` describes.  A row that
+    sees no key has KL = 0 and LSE = -inf; what a row does not see (NaN included) has no effect on it."""
+    _check_qk(Q1, K1, Q2, K2)
+    lib, shape, opts, plan = load(), make_shape(Q1, K1), _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
+    score = _scores(scores)._struct(Q1)
+    B, H, Nq, _ = Q1.shape
+    with torch.cuda.device(Q1.device):
+        _raise(lib.streamkl_score_fwd_plan(ctypes.byref(shape), ctypes.byref(opts), ctypes.byref(plan)),
+               "streamkl_score_fwd_plan")
+        if out is None:
+            out = tuple(torch.empty((B, H, Nq), dtype=torch.float32, device=Q1.device) for _ in range(3))
+        for name, t in zip(("KL", "LSE1", "LSE2"), out):
+            _check_tensor(name, t, (B, H, Nq), torch.float32, Q1.device)
+        workspace = _check_workspace(workspace, plan.workspace_bytes, Q1.device)
+        KL, L1, L2 = out
+        _raise(lib.streamkl_score_fwd(ctypes.byref(shape), ctypes.byref(score), _ptr(Q1), _ptr(K1), _ptr(Q2), _ptr(K2),
+                                      ctypes.c_float(0.0 if scale is None else float(scale)), int(bool(causal)),
+                                      _ptr(KL), _ptr(L1), _ptr(L2), _ptr(workspace), workspace.numel(),
+                                      ctypes.byref(opts), _stream(Q1.device)), "streamkl_score_fwd")
+    return KL, L1, L2
+
+
+def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=False, scale=None, workspace=None, out=None,
+                 wait_limit_ns=0, debug_flags=0, grad_dtype=torch.float32):
+    """(dQ, dK) of the trainable side of kl_score_fwd: setting 1 -> (Q2, K2), 2 -> (Q1, K1), as kl_bwd.  dQ is added
+    up in float32 in no fixed order (like kl_bwd's fused mode)."""
+    _check_qk(Q1, K1, Q2, K2)
+    lib, shape, plan = load(), make_shape(Q1, K1), Plan()
+    opts = _opts(0, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
+    score = _scores(scores)._struct(Q1)
+    B, H, Nq, d = Q1.shape
+    Hk, Nk = K1.shape[1], K1.shape[2]
+    with torch.cuda.device(Q1.device):
+        _raise(lib.streamkl_score_bwd_plan(ctypes.byref(shape), int(setting), ctypes.byref(opts), ctypes.byref(plan)),
+               "streamkl_score_bwd_plan")
+        for name, t in (("g", g), ("KL", KL), ("LSE1", LSE1), ("LSE2", LSE2)):
+            _check_tensor(name, t, (B, H, Nq), torch.float32, Q1.device)
+        if out is None:
+            out = (torch.empty((B, H, Nq, d), dtype=grad_dtype, device=Q1.device),
+                   torch.empty((B, Hk, Nk, d), dtype=grad_dtype, device=Q1.device))
+        _check_tensor("dQ", out[0], (B, H, Nq, d), grad_dtype, Q1.device)
+        _check_tensor("dK", out[1], (B, Hk, Nk, d), grad_dtype, Q1.device)
+        workspace = _check_workspace(workspace, plan.workspace_bytes, Q1.device)
+        dQ, dK = out
+        _raise(lib.streamkl_score_bwd(ctypes.byref(shape), ctypes.byref(score), int(setting), _ptr(g), _ptr(Q1), _ptr(K1),
+                                      _ptr(Q2), _ptr(K2), _ptr(KL), _ptr(LSE1), _ptr(LSE2),
+                                      ctypes.c_float(0.0 if scale is None else float(scale)), int(bool(causal)),
+                                      _ptr(dQ), _ptr(dK), _ptr(workspace), workspace.numel(), ctypes.byref(opts),
+                                      _stream(Q1.device)), "streamkl_score_bwd")
+    return dQ, dK
+
+
+class ScoredAttentionKL(torch.autograd.Function):
+    """Per-row divergence of kl_score_fwd with gradients to whichever sides' Q and K require them (AttentionKL's
+    settings), in bf16 like the inputs.  ``scores`` describes constants: slopes get no gradient."""
+
+    @staticmethod
+    def forward(ctx, Q1, K1, Q2, K2, scores, causal=False, scale=None):
+        if any(t is not None and t.requires_grad for t in _scores(scores).tensors()):
+            raise ValueError("the tensors of scores are constants: they get no gradient")
+        KL, L1, L2 = kl_score_fwd(scores, Q1, K1, Q2, K2, causal=causal, scale=scale)
+        ctx.save_for_backward(Q1, K1, Q2, K2, KL, L1, L2, *scores.tensors())
+        ctx.caps, ctx.causal, ctx.scale = (scores.cap1, scores.cap2), causal, scale
+        return KL
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gKL):
+        Q1, K1, Q2, K2, KL, L1, L2, *given = ctx.saved_tensors
+        scores = Scores(*ctx.caps, *given)
+        g = gKL.float().contiguous()
+        grads = [None] * 7
+        for setting, slot in ((1, 2), (2, 0)):
+            if ctx.needs_input_grad[slot] or ctx.needs_input_grad[slot + 1]:
+                grads[slot], grads[slot + 1] = kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, L1, L2,
+                                                            causal=ctx.causal, scale=ctx.scale,
+                                                            grad_dtype=torch.bfloat16)
         return tuple(grads)
 
 

@@ -228,6 +228,83 @@ STREAMKL_API streamkl_status streamkl_fwd_noalloc(const streamkl_shape* shape, c
 STREAMKL_API streamkl_status streamkl_noalloc_status(streamkl_stream_t stream, uint32_t* device_error);
 
 /* ---------------------------------------------------------------------------
+ * Divergence of two attentions with modified scores.
+ *
+ * The divergence above with, per side t,
+ *
+ *     S_t = cap_t tanh(scale z_t / cap_t) - slopes_t[h] |i + offset[b] - j|
+ *
+ * for z_t = <q_t, k_t> of query row i and key j (cap_t = 0: scale z_t; slopes_t
+ * NULL: no bias), and with the keys of each row restricted to a range:
+ *
+ *     begin[b, i] <= j < end[b, i],  and when causal  j <= i + offset[b].
+ *
+ * offset[b] is the key position of query row 0 (NULL: Nk - Nq, the bottom-right
+ * alignment).  The ranges express causal, document, sliding-window and prefix
+ * masks, padded batches and caches of unequal lengths, for both sides alike.
+ *
+ *  - begin, end: int32 [B, Nq], contiguous; NULL: 0 and Nk.  Values outside
+ *    [0, Nk] are clamped.  offset: int32 [B].  slopes1, slopes2: float32 [H].
+ *    All on the device.
+ *  - A row that sees no key has KL = 0, LSE1 = LSE2 = -inf and zero gradients;
+ *    a key that no row sees gets zero gradients; causal with Nq > Nk is allowed.
+ *  - What a row does not see has no effect on its outputs and gradients, NaN
+ *    and infinities included.  A visible one (or a product that overflows
+ *    float32) makes the row NaN, capped or not.
+ *  - A capped side needs 1e-5 <= scale / cap <= 1e5 (UNSUPPORTED otherwise).
+ *  - The backward is the fused one (dQ added up in float32 in no fixed order);
+ *    opt->bwd_mode must be 0.  Its gradients include the slope of the cap,
+ *    1 - tanh^2.  begin, end, offset, slopes, caps and scale as in the forward.
+ *  - Layouts, strides, dtypes, shared keys, workspace and streams as above.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    float cap1, cap2;       /* the teacher's and the student's; 0 = none */
+    const float* slopes1;
+    const float* slopes2;
+    const int32_t* begin;
+    const int32_t* end;
+    const int32_t* offset;
+} streamkl_score;
+
+/* score == NULL: plain scores, every key visible (up to causal).  Paths of the
+ * plans: 0 tile forward, 1 decode forward (Nq <= 16), 2 fused backward.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+STREAMKL_API streamkl_status streamkl_score_fwd_plan(const streamkl_shape* shape, const streamkl_options* opt,
+                                                     streamkl_plan* plan);
+STREAMKL_API streamkl_status streamkl_score_fwd(const streamkl_shape* shape, const streamkl_score* score,
+                                                const void* Q1, const void* K1, const void* Q2, const void* K2,
+                                                float scale, int causal, float* KL, float* LSE1, float* LSE2,
+                                                void* workspace, size_t workspace_bytes, const streamkl_options* opt,
+                                                streamkl_stream_t stream);
+STREAMKL_API streamkl_status streamkl_score_bwd_plan(const streamkl_shape* shape, int setting,
+                                                     const streamkl_options* opt, streamkl_plan* plan);
+STREAMKL_API streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_score* score, int setting,
+                                                const float* g, const void* Q1, const void* K1, const void* Q2,
+                                                const void* K2, const float* KL, const float* LSE1, const float* LSE2,
+                                                float scale, int causal, void* dQ, void* dK, void* workspace,
+                                                size_t workspace_bytes, const streamkl_options* opt,
+                                                streamkl_stream_t stream);
+
+/* Key ranges (begin, end, offset of streamkl_score) from the usual masks.  Query
+ * row i < q_lengths[b] stands at key position p = i + offset[b], offset[b] =
+ * k_lengths[b] - q_lengths[b] (lengths NULL: Nq, Nk; clamped to them); later
+ * rows see nothing.  It sees the keys j < k_lengths[b] with
+ *   causal:      j <= p;
+ *   window > 0:  p - window < j < p + window;
+ *   prefix [B]:  j <= p or j < prefix[b] (with causal; not with window or docs:
+ *                UNSUPPORTED, the visible keys would not be one range);
+ *   docs:        j in the document of p; num_bounds nondecreasing bounds, [num_bounds]
+ *                or with docs_per_batch [B, num_bounds], document m being keys
+ *                docs[m] <= j < docs[m + 1] (rows outside every document see nothing).
+ * begin, end: int32 [B, Nq]; offset: int32 [B]; written by one launch.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+STREAMKL_API streamkl_status streamkl_key_ranges(int32_t B, int32_t Nq, int32_t Nk, int causal, int32_t window,
+                                                 const int32_t* q_lengths, const int32_t* k_lengths,
+                                                 const int32_t* prefix, const int32_t* docs, int32_t num_bounds,
+                                                 int32_t docs_per_batch, int32_t* begin, int32_t* end, int32_t* offset,
+                                                 streamkl_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Norm of query and key heads with the position rotation, and its gradient.
  *
  * The step before the divergence: for every head x (d values) of q and k
