@@ -75,6 +75,14 @@ streamkl_status make_score(const streamkl_score* s, float scale, int causal, Sco
     return STREAMKL_OK;
 }
 
+// Heads of a group of the CTAs' order: four waves of CTAs, so that the CTAs with
+// the most work of a group start before the lighter ones end, and no more: a
+// group's tiles are to stay in L2.
+int order_group(int64_t heads, int tiles, int sms) {
+    const int64_t g = (4LL * sms + tiles - 1) / tiles;
+    return static_cast<int>(std::min(heads, g));
+}
+
 bool options_ok(const streamkl_options* opt) {
     return !opt || (opt->num_splits >= 0 && (opt->grad_bf16 == 0 || opt->grad_bf16 == 1) && opt->bwd_mode == 0 &&
                     !(opt->debug_flags & ~STREAMKL_DEBUG_INJECT_STALL));
@@ -82,7 +90,7 @@ bool options_ok(const streamkl_options* opt) {
 
 struct ScoreFwdPlan {
     bool decode;
-    int heads_per_cta, num_splits, ctas, num_q_tiles, num_k_tiles;
+    int heads_per_cta, num_splits, ctas, num_q_tiles, num_k_tiles, group;
     size_t ws_bytes;
 };
 
@@ -113,15 +121,16 @@ streamkl_status plan_score_fwd(const streamkl_shape* s, const streamkl_options* 
     if (units * splits > INT32_MAX || BH * s->Nq > (int64_t(1) << 38)) return STREAMKL_ERR_UNSUPPORTED;
     pl->num_splits = splits;
     pl->ctas = static_cast<int>(units * splits);
+    pl->group = order_group(BH, pl->num_q_tiles, sms);
     pl->ws_bytes = kStatusBytes;
     if (splits > 1) pl->ws_bytes += size_t(5) * splits * size_t(BH) * s->Nq * sizeof(float);
     return STREAMKL_OK;
 }
 
 struct ScoreBwdPlan {
-    int ctas, num_q_tiles, num_k_tiles;
+    int ctas, num_q_tiles, num_k_tiles, group;
     bool bf16;
-    size_t range_bytes, ws_bytes;
+    size_t row_bytes, key_bytes, ws_bytes;
 };
 
 streamkl_status plan_score_bwd(const streamkl_shape* s, int setting, const streamkl_options* opt, ScoreBwdPlan* pl) {
@@ -133,13 +142,15 @@ streamkl_status plan_score_bwd(const streamkl_shape* s, int setting, const strea
     pl->num_q_tiles = (s->Nq + 63) / 64;
     pl->num_k_tiles = (s->Nk + kBlockK - 1) / kBlockK;
     const int64_t ctas = int64_t(s->B) * kv_heads(s) * pl->num_k_tiles;
-    // the iterations of a CTA are counted in 32 bits; the range table has a block per tile and batch
-    if (ctas > INT32_MAX || s->B > 65535 || int64_t(pl->num_q_tiles) * (s->H / kv_heads(s)) > INT32_MAX)
+    // the iterations of a CTA are counted in 32 bits; the prepare kernel has a block per query tile and head
+    if (ctas > INT32_MAX || int64_t(s->B) * s->H * pl->num_q_tiles > INT32_MAX || int64_t(pl->num_q_tiles) * (s->H / kv_heads(s)) > INT32_MAX)
         return STREAMKL_ERR_UNSUPPORTED;
     pl->ctas = static_cast<int>(ctas);
+    pl->group = order_group(int64_t(s->B) * kv_heads(s), pl->num_k_tiles, sms);
     pl->bf16 = opt && opt->grad_bf16 == 1;
-    pl->range_bytes = (size_t(s->B) * pl->num_q_tiles * 8 + 255) / 256 * 256;
-    pl->ws_bytes = kStatusBytes + pl->range_bytes;
+    pl->row_bytes = (score_bwd_row_bytes(int64_t(s->B) * s->H, pl->num_q_tiles) + 255) / 256 * 256;
+    pl->key_bytes = (score_bwd_key_bytes(s->B, pl->num_q_tiles) + 255) / 256 * 256;
+    pl->ws_bytes = kStatusBytes + pl->row_bytes + pl->key_bytes;
     if (pl->bf16) pl->ws_bytes += size_t(s->B) * s->H * s->Nq * s->d * sizeof(float);
     return STREAMKL_OK;
 }
@@ -198,6 +209,7 @@ streamkl_status streamkl_score_fwd(const streamkl_shape* shape, const streamkl_s
     p.num_splits = pl.num_splits;
     p.kv_group = shape->H / kv_heads(shape);
     p.heads_per_cta = pl.heads_per_cta;
+    p.order_group = pl.group;
     p.scale = mode == kScorePlain ? sc : kLn2;  // unit of the running state: raw products, or log2(e) S
     p.scale_log2e = sc * kLog2e;
     p.KL = KL;
@@ -222,7 +234,7 @@ streamkl_status streamkl_score_bwd_plan(const streamkl_shape* shape, int setting
     plan->path = 2;
     plan->num_splits = 1;
     plan->num_ctas = pl.ctas;
-    plan->launches = pl.bf16 ? 4 : 3;  // zero dQ, tile ranges, gradient kernel (+ bf16 conversion)
+    plan->launches = pl.bf16 ? 3 : 2;  // prepare (zeros dQ), gradient kernel (+ bf16 conversion)
     plan->workspace_bytes = pl.ws_bytes;
     return STREAMKL_OK;
 }
@@ -253,7 +265,8 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     if (workspace_bytes < pl.ws_bytes) return STREAMKL_ERR_WORKSPACE;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    sp.tile_range = reinterpret_cast<int32_t*>(ws + kStatusBytes);
+    sp.rows = reinterpret_cast<float*>(ws + kStatusBytes);
+    sp.keys = ws + kStatusBytes + pl.row_bytes;
     // Q boxes of 64 rows, K boxes of 128 rows
     CUtensorMap maps[4];
     if (!make_map(&maps[0], Q1, shape, true, 64) || !make_map(&maps[1], K1, shape, false, kBlockK) ||
@@ -269,6 +282,7 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     p.H_kv = kv_heads(shape);
     p.kv_group = shape->H / p.H_kv;
     p.num_splits = 1;
+    p.order_group = pl.group;
     p.scale = sc;
     p.scale_log2e = sc * kLog2e;
     p.g = g;
@@ -278,13 +292,12 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     p.dQ = dQ;
     p.dK = dK;
     p.grad_bf16 = pl.bf16 ? 1 : 0;
-    p.dQacc = pl.bf16 ? reinterpret_cast<float*>(ws + kStatusBytes + pl.range_bytes) : static_cast<float*>(dQ);
+    p.dQacc = pl.bf16 ? reinterpret_cast<float*>(ws + kStatusBytes + pl.row_bytes + pl.key_bytes) : static_cast<float*>(dQ);
     p.status = static_cast<unsigned int*>(workspace);
     p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
     p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t dq_elems = size_t(shape->B) * shape->H * shape->Nq * shape->d;
-    if (cudaMemsetAsync(p.dQacc, 0, dq_elems * sizeof(float), s) != cudaSuccess) return STREAMKL_ERR_CUDA;
     if (launch_score_bwd(shape->d, setting, mode, maps, p, sp, pl.ctas, s) != cudaSuccess) return STREAMKL_ERR_CUDA;
     if (pl.bf16) {
         int sms = 0;

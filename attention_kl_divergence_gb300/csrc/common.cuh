@@ -32,6 +32,7 @@ struct FwdParams {
     int diag_off;        // Nk - Nq
     int kv_group;        // query heads per key head (1 = no sharing)
     int heads_per_cta;   // decode: query heads of one key head packed into a CTA's query columns
+    int order_group;     // score tile forward: heads whose tiles are interleaved, see grouped_order
     float scale;         // softmax scale
     float scale_log2e;   // scale * log2(e): raw dot product -> base-2 exponent
     float* KL;           // [B*H*Nq]
@@ -53,6 +54,7 @@ struct BwdParams {
     int H_kv;            // key heads
     int kv_group;        // query heads per key head
     int num_splits;      // key-split backward: key-range splits per key head
+    int order_group;     // score backward: key heads whose tiles are interleaved, see grouped_order
     float scale;
     float scale_log2e;
     const float* g;      // [B*H*Nq] upstream gradient dL/dKL

@@ -36,6 +36,8 @@ cudaError_t launch_bwd_decode(int d, int setting, const CUtensorMap* maps, const
 // fwd_decode, and as for bwd_kv.
 cudaError_t launch_score_fwd(int d, int mode, bool decode, const CUtensorMap* maps, const FwdParams& p,
                              const ScoreParams& sp, int ctas, cudaStream_t stream);
+size_t score_bwd_row_bytes(int64_t bh, int q_tiles);     // workspace of sp.rows and
+size_t score_bwd_key_bytes(int64_t batch, int q_tiles);  // of sp.keys
 cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
                              const ScoreParams& sp, int ctas, cudaStream_t stream);
 

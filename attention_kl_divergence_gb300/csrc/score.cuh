@@ -49,8 +49,8 @@ struct ScoreParams {
     const int32_t* end;     // [B, Nq] or null: Nk
     const int32_t* offset;  // [B] or null: Nk - Nq
     int causal;
-    // backward: bounds of the visible keys of each 64-row query tile, [B][tiles][2]
-    int32_t* tile_range;
+    float* rows;            // backward: per-row constants and key ranges of the
+    void* keys;             // query tiles (score_bwd.cu)
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -71,6 +71,13 @@ __device__ __forceinline__ int2 row_range(const ScoreParams& s, int Nq, int Nk, 
         hi = static_cast<int>(next < hi ? (next > 0 ? next : 0) : hi);
     }
     return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Unit u of heads x tiles in groups of `group` heads: (head, tile), tiles slow and heads fast in a group.
+__device__ __forceinline__ int2 grouped_order(int u, int tiles, int heads, int group) {
+    const int g = u / (group * tiles), first = g * group, n = min(group, heads - first);
+    const int r = u - first * tiles, t = r / n;
+    return make_int2(first + r - t * n, t);
 }
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
@@ -97,45 +104,66 @@ __device__ __forceinline__ float abs_max(const float (&z)[W]) {
     return fmaxf(a, b);  // NaN is passed over: every form below keeps it NaN
 }
 
-// z -> x in place, without the bias.  A warp takes the shortest form that
-// fits every score of its lanes.
 template <int W>
-__device__ __forceinline__ void cap_scores(float (&z)[W], const ScoreSide& s) {
-    if (s.lim == 0.f) {
+__device__ __forceinline__ void cap_near(float (&z)[W], const ScoreSide& s) {
 #pragma unroll
-        for (int e = 0; e < W; e += 2) {
-            const float2 x = __fmul2_rn(make_float2(z[e], z[e + 1]), splat(s.c));
-            z[e] = x.x;
-            z[e + 1] = x.y;
-        }
-        return;
+    for (int e = 0; e < W; e += 2) {
+        const float2 v = make_float2(z[e], z[e + 1]), y = __fmul2_rn(v, v);
+        float2 r = __ffma2_rn(splat(s.near[3]), y, splat(s.near[2]));
+        r = __ffma2_rn(r, y, splat(s.near[1]));
+        r = __ffma2_rn(r, y, splat(s.near[0]));
+        const float2 x = __fmul2_rn(v, r);
+        z[e] = x.x;
+        z[e + 1] = x.y;
     }
-    const float top = abs_max(z);
-    if (__all_sync(0xffffffffu, top <= s.z_near)) {
+}
+
+template <int W>
+__device__ __forceinline__ void cap_mid(float (&z)[W], const ScoreSide& s) {
 #pragma unroll
-        for (int e = 0; e < W; e += 2) {
-            const float2 v = make_float2(z[e], z[e + 1]), y = __fmul2_rn(v, v);
-            float2 r = __ffma2_rn(splat(s.near[3]), y, splat(s.near[2]));
-            r = __ffma2_rn(r, y, splat(s.near[1]));
-            r = __ffma2_rn(r, y, splat(s.near[0]));
-            const float2 x = __fmul2_rn(v, r);
-            z[e] = x.x;
-            z[e + 1] = x.y;
+    for (int e = 0; e < W; e += 2) {
+        const float2 u = __fmul2_rn(make_float2(z[e], z[e + 1]), splat(s.ratio)), y = __fmul2_rn(u, u);
+        float2 r = splat(s.mid[7]);
+#pragma unroll
+        for (int k = 6; k >= 0; --k) r = __ffma2_rn(r, y, splat(s.mid[k]));
+        const float2 x = __fmul2_rn(u, r);
+        z[e] = x.x;
+        z[e + 1] = x.y;
+    }
+}
+
+// z -> x in place for both sides, without the bias.  A warp takes the shortest
+// form that fits every score of its lanes.
+template <int MODE, int W>
+__device__ __forceinline__ void cap_scores(float (&z1)[W], float (&z2)[W], const ScoreSide& s1, const ScoreSide& s2) {
+    if (MODE == kScorePlain) return;
+    const float top1 = abs_max(z1), top2 = abs_max(z2);
+    if (MODE == kScoreGeneral) {  // a side may have no cap
+        if (s1.lim == 0.f) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) z1[e] *= s1.c;
         }
-    } else if (__all_sync(0xffffffffu, top <= s.z_mid)) {
+        if (s2.lim == 0.f) {
 #pragma unroll
-        for (int e = 0; e < W; e += 2) {
-            const float2 u = __fmul2_rn(make_float2(z[e], z[e + 1]), splat(s.ratio)), y = __fmul2_rn(u, u);
-            float2 r = splat(s.mid[7]);
-#pragma unroll
-            for (int k = 6; k >= 0; --k) r = __ffma2_rn(r, y, splat(s.mid[k]));
-            const float2 x = __fmul2_rn(u, r);
-            z[e] = x.x;
-            z[e + 1] = x.y;
+            for (int e = 0; e < W; ++e) z2[e] *= s2.c;
         }
+    }
+    const bool c1 = MODE == kScoreBounded || s1.lim != 0.f, c2 = MODE == kScoreBounded || s2.lim != 0.f;
+    if (__all_sync(0xffffffffu, (!c1 || top1 <= s1.z_near) && (!c2 || top2 <= s2.z_near))) {
+        if (c1) cap_near(z1, s1);
+        if (c2) cap_near(z2, s2);
+    } else if (__all_sync(0xffffffffu, (!c1 || top1 <= s1.z_mid) && (!c2 || top2 <= s2.z_mid))) {
+        if (c1) cap_mid(z1, s1);
+        if (c2) cap_mid(z2, s2);
     } else {
+        if (c1) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) z[e] = score_far(z[e], s);
+            for (int e = 0; e < W; ++e) z1[e] = score_far(z1[e], s1);
+        }
+        if (c2) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) z2[e] = score_far(z2[e], s2);
+        }
     }
 }
 

@@ -21,23 +21,16 @@ namespace streamkl {
 
 namespace {
 
-// What the 128 keys are to a half (32 rows) of a query tile.
-constexpr int kHalfPart = 0, kHalfWhole = 1, kHalfNone = 2;
-
-// Per-row constants of the recompute; a row that sees no key contributes nothing.
-// An infinite LSE (from an infinite score) counts as NaN, as in its own softmax.
-template <int SETTING>
-__device__ __forceinline__ void scored_constants(const BwdParams& p, size_t row, bool live, float& la, float& xb,
-                                                 float& g) {
-    la = xb = g = 0.f;
-    if (!live) return;
-    const float l1 = p.LSE1[row], l2 = p.LSE2[row];
-    const float nan = __int_as_float(0x7fc00000);
-    la = fabsf(l1) < INFINITY ? l1 * kLog2e : nan;
-    const float other = fabsf(l2) < INFINITY ? l2 : nan;
-    xb = SETTING == 1 ? other * kLog2e : (l1 - other) + p.KL[row];
-    g = p.g[row];
-}
+// The backward's workspace, written by score_prepare_kernel:
+//   rows   [B*H][q tiles][3][64] floats: -LSE1 (log2), -xb and g * scale of each row
+//   keys   [B][q tiles] KeyBlock: the ranges of the tile's rows and their bounds
+// Both are read by bulk copies of a tile's block.
+struct KeyBlock {
+    int32_t begin[kBwdTile], end[kBwdTile];
+    int4 bounds[2];  // per half: lowest begin, highest end of a row with keys; highest begin, lowest end of all rows
+};
+constexpr int kRowBlockBytes = 3 * kBwdTile * 4;
+static_assert(sizeof(KeyBlock) == 2 * kBwdTile * 4 + 32, "packed");
 
 __device__ __forceinline__ bool has_nonfinite_bf16(uint32_t u) {
     return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
@@ -53,42 +46,74 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
 // the tile at `qt`, and this thread's row of the key tile at `kt`.  Several
 // warps may find the same row: they all write zeros.
 template <int D>
-__device__ __noinline__ void clear_nonfinite(uint32_t qt, int r0, uint32_t kt, int key_row, int lane) {
+__device__ __forceinline__ void clear_nonfinite(uint32_t qt, int r0, uint32_t kt, int key_row, int lane) {
+#pragma unroll 1
     for (int r = r0; r < r0 + 32; ++r) {
         bool bad = false;
+#pragma unroll
         for (int c = 0; c < D / kSwizzleCols; ++c)
             bad |= has_nonfinite_bf16(ld_shared_u32(qt + c * kBwdTile * 128 + r * 128 + lane * 4));
-        if (__any_sync(0xffffffffu, bad))
+        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
             for (int c = 0; c < D / kSwizzleCols; ++c)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(qt + c * kBwdTile * 128 + r * 128 + lane * 4), "r"(0u)
                              : "memory");
+        }
     }
     bool bad = false;
+#pragma unroll 1
     for (int k = 0; k < D / 2; ++k)
         bad |= has_nonfinite_bf16(ld_shared_u32(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4));
-    if (bad)
+    if (bad) {
+#pragma unroll 1
         for (int k = 0; k < D / 2; ++k)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4),
                          "r"(0u)
                          : "memory");
+    }
     __syncwarp();
 }
 
-// Bounds of the keys that the rows of each 64-row query tile see: block (tile, b).
-__global__ void __launch_bounds__(kBwdTile) score_tile_range_kernel(const __grid_constant__ ScoreParams sp, int Nq, int Nk) {
-    __shared__ int2 part[2];
-    const int2 r = row_range(sp, Nq, Nk, blockIdx.y, blockIdx.x * kBwdTile + threadIdx.x);
-    const int lo = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT32_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, r.y);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_int2(lo, hi);
-    __syncthreads();
-    if (threadIdx.x == 0)
-        reinterpret_cast<int2*>(sp.tile_range)[static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x] =
-            make_int2(min(part[0].x, part[1].x), max(part[0].y, part[1].y));
+// One block per (64-row query tile, batch and head): the constants of its rows,
+// the ranges of the tile (the first head's block) and zeros in its rows of dQ.
+// A row that sees no key gets zero constants; an infinite LSE (from an infinite
+// score) counts as NaN, as in its own softmax.
+__global__ void __launch_bounds__(256) score_prepare_kernel(const __grid_constant__ BwdParams p,
+                                                            const __grid_constant__ ScoreParams sp, int setting, int d) {
+    const size_t block = blockIdx.x;
+    const int bh = static_cast<int>(block / p.num_q_tiles), tile = static_cast<int>(block - static_cast<size_t>(bh) * p.num_q_tiles);
+    const int b = bh / p.H, h = bh - b * p.H;
+    const int rows = min(kBwdTile, p.Nq - tile * kBwdTile);
+    float4* dq = reinterpret_cast<float4*>(p.dQacc + (static_cast<size_t>(bh) * p.Nq + tile * kBwdTile) * d);
+    for (int k = threadIdx.x; k < rows * d / 4; k += blockDim.x) dq[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (threadIdx.x >= kBwdTile) return;
+    const int r = threadIdx.x, i = tile * kBwdTile + r;
+    const int2 keys = row_range(sp, p.Nq, p.Nk, b, i);
+    const bool live = keys.x < keys.y;
+    float la = 0.f, xb = 0.f, g = 0.f;
+    if (live) {
+        const size_t row = static_cast<size_t>(bh) * p.Nq + i;
+        const float l1 = p.LSE1[row], l2 = p.LSE2[row], nan = __int_as_float(0x7fc00000);
+        const float other = fabsf(l2) < INFINITY ? l2 : nan;
+        la = fabsf(l1) < INFINITY ? l1 * kLog2e : nan;
+        xb = setting == 1 ? other * kLog2e : (l1 - other) + p.KL[row];
+        g = p.g[row];
+    }
+    float* out = sp.rows + block * (3 * kBwdTile);
+    out[r] = -la;
+    out[kBwdTile + r] = -xb;
+    out[2 * kBwdTile + r] = g * p.scale;  // the softmax scale of both gradients
+    if (h != 0) return;
+    KeyBlock& kb = static_cast<KeyBlock*>(sp.keys)[static_cast<size_t>(b) * p.num_q_tiles + tile];
+    kb.begin[r] = keys.x;
+    kb.end[r] = keys.y;
+    const int lo = __reduce_min_sync(0xffffffffu, live ? keys.x : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, keys.y);
+    const int in_lo = __reduce_max_sync(0xffffffffu, live ? keys.x : INT32_MAX), in_hi = __reduce_min_sync(0xffffffffu, keys.y);
+    if ((r & 31) == 0) kb.bounds[r >> 5] = make_int4(lo, hi, in_lo, in_hi);
 }
 
 // ---------------------------------------------------------------------------
-// CTA = 128 keys; 64-row query tiles.  Warps: 0 TMA + per-row constants, 1 TMEM +
+// CTA = 128 keys; 64-row query tiles.  Warps: 0 copies, 1 TMEM +
 // score MMAs, 2-9 recompute/dS (two warpgroups, one key per thread, each taking
 // 32 of the tile's 64 query rows), 10-13 dQ^T accumulator -> bulk reduce-add into
 // global dQ, 14 gradient MMAs.  TMEM: K1|K2 as the A operand of the score MMAs
@@ -104,7 +129,7 @@ struct ScoreKvSmem {
     // dK MMAs, so freed after dK), the other side's (read by the score MMAs
     // only, so freed right after them: half as deep does), and the per-row
     // constants (freed once the update warps have read them).
-    static constexpr int kQt = NST, kQn = NST / 2, kNv = NST >= 8 ? 4 : 3;
+    static constexpr int kQt = NST, kQn = NST / 2, kNv = NST >= 8 ? 4 : 2;
     static constexpr int k1 = 0;
     static constexpr int k2 = kKBytes;
     static constexpr int qt = 2 * kKBytes;
@@ -114,10 +139,9 @@ struct ScoreKvSmem {
     // d = 64: a zero 64-feature atom pads the dQ^T MMA's A operand (K_t^T) to M = 128
     static constexpr int zero = ds + 2 * kNumDs * kDsBytes;
     static constexpr int kZeroBytes = D < 128 ? kBlockK * 128 : 0;
-    static constexpr int vec = zero + kZeroBytes;  // [kNv][3][64] floats
-    static constexpr int mask = vec + kNv * 3 * kBwdTile * 4;  // [kNv][64] visible keys: begin | end << 8
-    static constexpr int kind = mask + kNv * kBwdTile * 2;     // [kNv][2 halves] kHalf*
-    static constexpr int bars = kind + ((kNv * 8 + 15) / 16) * 16;
+    static constexpr int vec = zero + kZeroBytes;      // [kNv][3][64] floats
+    static constexpr int keys = vec + kNv * kRowBlockBytes;  // [kNv] KeyBlock
+    static constexpr int bars = keys + kNv * static_cast<int>(sizeof(KeyBlock));
     static constexpr int bar_k = bars;
     static constexpr int bar_qtfull = bar_k + 8;
     static constexpr int bar_qtempty = bar_qtfull + 8 * kQt;
@@ -160,17 +184,16 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
     int* tile_span = reinterpret_cast<int*>(gbase + L::misc + 8);
     float* vec = reinterpret_cast<float*>(gbase + L::vec);
-    uint16_t* mask = reinterpret_cast<uint16_t*>(gbase + L::mask);
-    int* kind = reinterpret_cast<int*>(gbase + L::kind);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kGradWarp = kSbThreads / 32 - 1;  // issues the gradient MMAs
 
-    // head-major: resident CTAs share one head's query tiles through L2; key
-    // tile 0 is seen by the most query rows under a causal mask and comes first
-    // (a key head serves kv_group query heads: the CTA visits every query tile of each of them,
-    // so dK sums the group's gradients without a second pass)
-    const int bkv = blockIdx.x / p.num_k_tiles;  // flat (batch, key head)
-    const int nt = blockIdx.x - bkv * p.num_k_tiles;
+    // Groups of key heads, a few waves of CTAs each, so that resident CTAs share query
+    // tiles through L2; in a group the first key tiles of every head, which the most
+    // rows see under a causal mask, come first.  (A key head serves kv_group query
+    // heads: the CTA visits every query tile of each of them, so dK sums the group's
+    // gradients without a second pass.)
+    const int2 at = grouped_order(blockIdx.x, p.num_k_tiles, p.B * p.H_kv, p.order_group);
+    const int bkv = at.x, nt = at.y;  // flat (batch, key head), key tile
     const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
     const int n0 = nt * kBlockK;
     const uint32_t kt_tile = base + (SETTING == 1 ? L::k2 : L::k1);  // trainable keys
@@ -186,7 +209,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             mbar_init(base + L::bar_qnempty + 8 * s, 1);
         }
         for (int s = 0; s < L::kNv; ++s) {
-            mbar_init(base + L::bar_vfull + 8 * s, 32);
+            mbar_init(base + L::bar_vfull + 8 * s, 1);
             mbar_init(base + L::bar_vempty + 8 * s, 256);
         }
         for (int s = 0; s < L::kNumDs; ++s) {
@@ -214,11 +237,12 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     __syncthreads();
     // the query tiles with a row that sees one of these keys: from the first to the last of them
     {
-        const int2* range = reinterpret_cast<const int2*>(sp.tile_range) + static_cast<size_t>(b) * p.num_q_tiles;
+        const KeyBlock* blocks = static_cast<const KeyBlock*>(sp.keys) + static_cast<size_t>(b) * p.num_q_tiles;
         int first = INT32_MAX, last = -1;
         for (int t = threadIdx.x; t < p.num_q_tiles; t += kSbThreads) {
-            const int2 r = range[t];
-            if (r.x - kBlockK < n0 && r.y > n0 && r.x < r.y) {
+            const int4 a = blocks[t].bounds[0], c = blocks[t].bounds[1];
+            const int lo = min(a.x, c.x), hi = max(a.y, c.y);
+            if (lo < hi && lo - kBlockK < n0 && hi > n0) {
                 first = min(first, t);
                 last = max(last, t);
             }
@@ -243,8 +267,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     auto qtile = [&](int m) { return m_start + (p.kv_group == 1 ? m : m % per_head); };
 
     if (warp == 0) {
-        // ------------------------------------------------ TMA + row constants
-        if (lane == 0) {
+        // ------------------------------------------------ copies
+        if (lane == 0 && n_tiles > 0) {
             prefetch_tensormap(&tQ1);
             prefetch_tensormap(&tK1);
             prefetch_tensormap(&tQ2);
@@ -255,60 +279,46 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 tma_load_4d(base + L::k1 + c * kBlockK * 128, &tK1, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
                 tma_load_4d(base + L::k2 + c * kBlockK * 128, &tK2, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
             }
-        }
-        const uint64_t keep = policy_evict_last();
-        const CUtensorMap* tqt = SETTING == 1 ? &tQ2 : &tQ1;  // the trainable side's queries
-        const CUtensorMap* tqn = SETTING == 1 ? &tQ1 : &tQ2;
-        int n_qt = 0, n_qn = 0;  // tiles whose copies were issued, per ring
-        int st = 0, sn = 0, sv = 0;
-        uint32_t pt = 0, pn = 0, pv = 0;
-        for (int m = 0; m < n_tiles; ++m) {
-            const int r0 = qtile(m) * kBwdTile;
-            const int h = qhead(m);
-            if (!wait_all(base + L::bar_qtempty + 8 * st, pt ^ 1, wc, kErrWaitOther)) break;
-            if (lane == 0) {
-                const uint32_t fb = base + L::bar_qtfull + 8 * st, dst = base + L::qt + st * L::kQBytes;
-                mbar_arrive_expect_tx(fb, L::kQBytes);
+            const uint64_t keep = policy_evict_last();
+            const CUtensorMap* tqt = SETTING == 1 ? &tQ2 : &tQ1;  // the trainable side's queries
+            const CUtensorMap* tqn = SETTING == 1 ? &tQ1 : &tQ2;
+            const KeyBlock* blocks = static_cast<const KeyBlock*>(sp.keys) + static_cast<size_t>(b) * p.num_q_tiles;
+            int n_qt = 0, n_qn = 0, n_v = 0;  // tiles whose copies were issued, per ring
+            int st = 0, sn = 0, sv = 0;
+            uint32_t pt = 0, pn = 0, pv = 0;
+            int h = hk * p.kv_group, t = m_start;
+            for (int m = 0; m < n_tiles; ++m) {
+                const int r0 = t * kBwdTile;
+                if (!mbar_wait(base + L::bar_qtempty + 8 * st, pt ^ 1, wc, kErrWaitOther)) break;
+                const uint32_t fq = base + L::bar_qtfull + 8 * st, dq = base + L::qt + st * L::kQBytes;
+                mbar_arrive_expect_tx(fq, L::kQBytes);
 #pragma unroll
                 for (int c = 0; c < D / kSwizzleCols; ++c)
-                    tma_load_4d_hint(dst + c * kBwdTile * 128, tqt, fb, c * kSwizzleCols, r0, h, b, keep);
-            }
-            ++n_qt;
-            if (!wait_all(base + L::bar_qnempty + 8 * sn, pn ^ 1, wc, kErrWaitOther)) break;
-            if (lane == 0) {
-                const uint32_t fb = base + L::bar_qnfull + 8 * sn, dst = base + L::qn + sn * L::kQBytes;
-                mbar_arrive_expect_tx(fb, L::kQBytes);
+                    tma_load_4d_hint(dq + c * kBwdTile * 128, tqt, fq, c * kSwizzleCols, r0, h, b, keep);
+                ++n_qt;
+                if (!mbar_wait(base + L::bar_qnempty + 8 * sn, pn ^ 1, wc, kErrWaitOther)) break;
+                const uint32_t fn = base + L::bar_qnfull + 8 * sn, dn = base + L::qn + sn * L::kQBytes;
+                mbar_arrive_expect_tx(fn, L::kQBytes);
 #pragma unroll
                 for (int c = 0; c < D / kSwizzleCols; ++c)
-                    tma_load_4d_hint(dst + c * kBwdTile * 128, tqn, fb, c * kSwizzleCols, r0, h, b, keep);
+                    tma_load_4d_hint(dn + c * kBwdTile * 128, tqn, fn, c * kSwizzleCols, r0, h, b, keep);
+                ++n_qn;
+                if (!mbar_wait(base + L::bar_vempty + 8 * sv, pv ^ 1, wc, kErrWaitOther)) break;
+                const uint32_t fv = base + L::bar_vfull + 8 * sv;
+                mbar_arrive_expect_tx(fv, kRowBlockBytes + static_cast<uint32_t>(sizeof(KeyBlock)));
+                const size_t row_block = (static_cast<size_t>(b) * p.H + h) * p.num_q_tiles + t;
+                bulk_load(base + L::vec + sv * kRowBlockBytes, sp.rows + row_block * (3 * kBwdTile), kRowBlockBytes, fv);
+                bulk_load(base + L::keys + sv * static_cast<uint32_t>(sizeof(KeyBlock)), blocks + t, sizeof(KeyBlock), fv);
+                ++n_v;
+                if (++st == L::kQt) st = 0, pt ^= 1;
+                if (++sn == L::kQn) sn = 0, pn ^= 1;
+                if (++sv == L::kNv) sv = 0, pv ^= 1;
+                if (++t == m_start + per_head) {
+                    t = m_start;
+                    ++h;
+                }
             }
-            ++n_qn;
-            if (!wait_all(base + L::bar_vempty + 8 * sv, pv ^ 1, wc, kErrWaitOther)) break;
-            // per query row: -la, -xb and g * scale (the softmax scale of both
-            // gradients is folded into dS, so neither epilogue multiplies)
-            float* v = vec + sv * 3 * kBwdTile;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = lane + 32 * k;
-                const int i = r0 + r;
-                const int2 keys = row_range(sp, p.Nq, p.Nk, b, i);
-                float la, xb, g;
-                scored_constants<SETTING>(p, (static_cast<size_t>(b) * p.H + h) * p.Nq + i, keys.x < keys.y, la, xb, g);
-                v[r] = -la;
-                v[kBwdTile + r] = -xb;
-                v[2 * kBwdTile + r] = g * p.scale;
-                const int kb = min(max(keys.x - n0, 0), kBlockK), ke = min(max(keys.y - n0, 0), kBlockK);
-                mask[sv * kBwdTile + r] = static_cast<uint16_t>(kb | (ke << 8));
-                const bool all = __all_sync(0xffffffffu, kb == 0 && ke == kBlockK);
-                const bool none = __all_sync(0xffffffffu, kb >= ke);
-                if (lane == 0) kind[sv * 2 + k] = all ? kHalfWhole : none ? kHalfNone : kHalfPart;
-            }
-            mbar_arrive(base + L::bar_vfull + 8 * sv);
-            if (++st == L::kQt) st = 0, pt ^= 1;
-            if (++sn == L::kQn) sn = 0, pn ^= 1;
-            if (++sv == L::kNv) sv = 0, pv ^= 1;
-        }
-        if (lane == 0) {  // every issued copy has landed (and, unless aborting, been consumed)
+            // every issued copy has landed (and, unless aborting, been consumed)
             drain_wait_b(base + L::bar_k, 0, kDrainNs);
             for (int j = max(0, n_qt - L::kQt); j < n_qt; ++j) {
                 const uint32_t bo = 8 * (j % L::kQt), ph = (j / L::kQt) & 1;
@@ -319,6 +329,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 const uint32_t bo = 8 * (j % L::kQn), ph = (j / L::kQn) & 1;
                 drain_wait_b(base + L::bar_qnfull + bo, ph, kDrainNs);
                 if (!*abort_flag) drain_wait_b(base + L::bar_qnempty + bo, ph, kDrainNs);
+            }
+            for (int j = max(0, n_v - L::kNv); j < n_v; ++j) {
+                const uint32_t bo = 8 * (j % L::kNv), ph = (j / L::kNv) & 1;
+                drain_wait_b(base + L::bar_vfull + bo, ph, kDrainNs);
+                if (!*abort_flag) drain_wait_b(base + L::bar_vempty + bo, ph, kDrainNs);
             }
         }
     } else if (warp == 1) {
@@ -411,7 +426,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             int issued = 0, s2 = 0, dsb = 0;
             uint32_t dsph = 0, qt_lo = qt_lo0;
             // the key tiles (A of dQ^T) have landed before any dS exists; the wait states it
-            if (mbar_wait(base + L::bar_k, 0, wc, kErrWaitK)) {
+            if (n_tiles > 0 && mbar_wait(base + L::bar_k, 0, wc, kErrWaitK)) {
                 for (int m = 0; m < n_tiles; ++m) {
                     if (!mbar_wait(base + L::bar_dsfull + 8 * dsb, dsph, wc, kErrWaitOther)) break;
                     tc_fence_after();
@@ -489,31 +504,33 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             tc_wait_ld();
             tc_fence_before();
             mbar_arrive(base + L::bar_sempty);  // the next score tile may overwrite S now
-            const int part = kind[sv * 2 + wg];
+            const KeyBlock& kb = reinterpret_cast<const KeyBlock*>(gbase + L::keys)[sv];
+            const int4 bounds = kb.bounds[wg];
+            const bool whole = bounds.z <= n0 && bounds.w >= n0 + kBlockK;  // every row sees every key
             // bit e: query row r0 + e sees this thread's key
-            uint32_t vis = part == kHalfWhole ? 0xffffffffu : 0u;
+            uint32_t vis = 0xffffffffu;
             bool bad = false;
-            if (part != kHalfWhole) {
-                const uint4* m4 = reinterpret_cast<const uint4*>(mask + sv * kBwdTile + wg * 32);
+            if (!whole) {
+                vis = 0u;
+                const int4* lo4 = reinterpret_cast<const int4*>(kb.begin + wg * 32);
+                const int4* hi4 = reinterpret_cast<const int4*>(kb.end + wg * 32);
 #pragma unroll
-                for (int e8 = 0; e8 < 4; ++e8) {
-                    const uint4 w = m4[e8];
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const int4 lo = lo4[e4], hi = hi4[e4];
+                    const int los[4] = {lo.x, lo.y, lo.z, lo.w}, his[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t f = u[k >> 1] >> (16 * (k & 1));
-                        const bool v = row >= static_cast<int>(f & 0xffu) && row < static_cast<int>((f >> 8) & 0xffu);
-                        const float zt = SETTING == 1 ? z2[8 * e8 + k] : z1[8 * e8 + k];
-                        vis |= static_cast<uint32_t>(v) << (8 * e8 + k);
-                        bad |= !v && !(fabsf(zt) < INFINITY);
-                        if (!v) z1[8 * e8 + k] = z2[8 * e8 + k] = 0.f;  // no effect on the form of cap_scores
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = 4 * e4 + k;
+                        if (j >= los[k] && j < his[k]) {
+                            vis |= 1u << e;
+                        } else {
+                            bad |= !(fabsf(SETTING == 1 ? z2[e] : z1[e]) < INFINITY);
+                            z1[e] = z2[e] = 0.f;  // no effect on the form of cap_scores
+                        }
                     }
                 }
             }
-            if (MODE != kScorePlain && part != kHalfNone) {
-                cap_scores(z1, sp.side[0]);
-                cap_scores(z2, sp.side[1]);
-            }
+            cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
             float sl1 = 0.f, sl2 = 0.f, d0 = 0.f;
             if (MODE == kScoreGeneral) {
                 const int h = qhead(m);
@@ -555,7 +572,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 }
             }
             mbar_arrive(base + L::bar_vempty + 8 * sv);  // this tile's row constants are read
-            if (part != kHalfWhole) {
+            if (!whole) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     if (!((vis >> e) & 1u)) dsv[e] = 0.f;
@@ -574,7 +591,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             mbar_arrive(base + L::bar_dsfull + 8 * dsb);
         }
         // epilogue: dK row = scale * accumulator; each warpgroup writes half the columns
-        if (ok && wait_all(base + L::bar_done, 0, wc, kErrWaitOther)) {
+        if (ok && (n_tiles == 0 || wait_all(base + L::bar_done, 0, wc, kErrWaitOther))) {
             tc_fence_after();
             void* out = reinterpret_cast<uint8_t*>(p.dK) +
                         (static_cast<size_t>(bkv) * p.Nk + j) * D * (p.grad_bf16 ? 2 : 4);
@@ -696,9 +713,12 @@ cudaError_t launch_mode(int d, int setting, const CUtensorMap* m, const BwdParam
 
 }  // namespace
 
+size_t score_bwd_row_bytes(int64_t bh, int q_tiles) { return static_cast<size_t>(bh) * q_tiles * kRowBlockBytes; }
+size_t score_bwd_key_bytes(int64_t batch, int q_tiles) { return static_cast<size_t>(batch) * q_tiles * sizeof(KeyBlock); }
+
 cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
                              const ScoreParams& sp, int ctas, cudaStream_t stream) {
-    score_tile_range_kernel<<<dim3(p.num_q_tiles, p.B), kBwdTile, 0, stream>>>(sp, p.Nq, p.Nk);
+    score_prepare_kernel<<<static_cast<unsigned>(p.B * p.H) * p.num_q_tiles, 256, 0, stream>>>(p, sp, setting, d);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return mode == kScorePlain     ? launch_mode<kScorePlain>(d, setting, maps, p, sp, ctas, stream)

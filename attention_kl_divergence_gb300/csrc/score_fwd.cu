@@ -18,13 +18,18 @@ namespace streamkl {
 namespace {
 
 constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 stale
-constexpr int kSfGroups = 2;       // update warpgroups: each takes half of a tile's columns
+// Update warpgroups of the tile kernel, each taking its share of a tile's columns.
+#ifndef SFP
+#define SFP 2
+#define SFB 4
+#define SFG 4
+#endif
+constexpr int sf_groups(int mode) { return mode == kScorePlain ? SFP : mode == kScoreBounded ? SFB : SFG; }
 // warp 0 TMA, warp 1 the S1 MMAs, the update warpgroups, and a last warp for the S2 MMAs
-constexpr int kSfThreads = 64 + 128 * kSfGroups + 32;
-constexpr int kSfS2Warp = kSfThreads / 32 - 1;
+constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 32; }
 constexpr uint64_t kSfDrainNs = 200000000ull;  // in-flight copies and MMAs retire before a CTA exits
 
-template <int D, int NST>
+template <int D, int NST, int GROUPS>
 struct ScoreTileSmem {
     static constexpr int kQBytes = kBlockQ * D * 2;
     static constexpr int kKBytes = kBlockK * D * 2;
@@ -40,7 +45,7 @@ struct ScoreTileSmem {
     static constexpr int misc = bar_done + 16;    // tmem base (4 B), abort flag (4 B)
     static constexpr int span = misc + 16;        // [4 warps]{lowest begin, highest end}
     static constexpr int red = span + 32;         // [groups - 1][5][128] floats: the other groups' row states
-    static constexpr int total = red + (kSfGroups - 1) * 5 * 128 * 4;
+    static constexpr int total = red + (GROUPS - 1) * 5 * 128 * 4;
     static constexpr int alloc = total + 1024;    // slack for 1024-byte alignment
 };
 
@@ -162,11 +167,12 @@ __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_s
 // last warp the S2 MMAs, the others the update (one query row per thread).
 // ---------------------------------------------------------------------------
 template <int D, int NST, int MODE>
-__global__ void __launch_bounds__(kSfThreads, 1)
+__global__ void __launch_bounds__(sf_threads(MODE), 1)
     score_fwd_tile_kernel(const __grid_constant__ CUtensorMap tQ1, const __grid_constant__ CUtensorMap tK1,
                           const __grid_constant__ CUtensorMap tQ2, const __grid_constant__ CUtensorMap tK2,
                           const __grid_constant__ FwdParams p, const __grid_constant__ ScoreParams sp) {
-    using L = ScoreTileSmem<D, NST>;
+    constexpr int kGroups = sf_groups(MODE), kS2Warp = sf_threads(MODE) / 32 - 1;
+    using L = ScoreTileSmem<D, NST, sf_groups(MODE)>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -176,14 +182,12 @@ __global__ void __launch_bounds__(kSfThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // head-major: resident CTAs share one head's key tiles through L2; the last
-    // query tiles, which see the most keys under a causal mask, come first
-    const int per_head = p.num_q_tiles * p.num_splits;
-    const int bh = blockIdx.x / per_head;
-    const int rem = blockIdx.x - bh * per_head;
-    const int qi = rem / p.num_splits;
-    const int split = rem - qi * p.num_splits;
-    const int qt = p.num_q_tiles - 1 - qi;
+    // Groups of heads, a few waves of CTAs each, so that resident CTAs share key
+    // tiles through L2; in a group the last query tiles of every head, which see
+    // the most keys under a causal mask, come first.
+    const int unit = blockIdx.x / p.num_splits, split = blockIdx.x - unit * p.num_splits;
+    const int2 at = grouped_order(unit, p.num_q_tiles, p.B * p.H, p.order_group);
+    const int bh = at.x, qt = p.num_q_tiles - 1 - at.y;
     const int b = bh / p.H, h = bh - b * p.H;
     const int hk = h / p.kv_group;
     const int q0 = qt * kBlockQ;
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kSfThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(base + L::bar_sfull + 8 * s, 2);  // S1 and S2 of the buffer are complete
-            mbar_init(base + L::bar_sempty + 8 * s, 128 * kSfGroups);
+            mbar_init(base + L::bar_sempty + 8 * s, 128 * kGroups);
         }
         mbar_init(base + L::bar_done, 1);
         mbar_init(base + L::bar_done + 8, 1);
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kSfThreads, 1)
                 if (!*abort_flag) score_drain(base + L::bar_kempty + 8 * (j % NST), (j / NST) & 1, kSfDrainNs);
             }
         }
-    } else if (warp == 1 || warp == kSfS2Warp) {
+    } else if (warp == 1 || warp == kS2Warp) {
         // ------------------------------------------------------------ MMA
         // Two threads issue the MMAs, S1 = Q1 K1^T (warp 1) and S2 = Q2 K2^T
         // (the last warp), each committing its own arrival on the shared
@@ -315,10 +319,10 @@ __global__ void __launch_bounds__(kSfThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ online update (warps 2 .. 2 + 4 groups)
-        // kSfGroups warpgroups split every tile's 128 columns; each keeps its
+        // kGroups warpgroups split every tile's 128 columns; each keeps its
         // own running state per row, and the states of a row are merged at the
         // end (the same log-sum-exp merge as the Split-K combine).
-        constexpr int kChunks = 4 / kSfGroups;  // 32-column chunks per group and tile
+        constexpr int kChunks = 4 / kGroups;  // 32-column chunks per group and tile
         const int wg = (warp - 2) >> 2;
         const int wq = warp & 3;
         const int row = wq * 32 + lane;
@@ -327,6 +331,11 @@ __global__ void __launch_bounds__(kSfThreads, 1)
         const float c = MODE == kScorePlain ? p.scale_log2e : 1.f;
         const float tau = kScoreTau / c;
         const int2 range = row_range(sp, p.Nq, p.Nk, b, i);
+        // keys [warp_lo, warp_hi) are seen by some row of the warp, [whole_lo, whole_hi) by all of them
+        const int warp_lo = __reduce_min_sync(0xffffffffu, range.x < range.y ? range.x : INT32_MAX);
+        const int warp_hi = __reduce_max_sync(0xffffffffu, range.y);
+        const int whole_lo = __reduce_max_sync(0xffffffffu, range.x);
+        const int whole_hi = __reduce_min_sync(0xffffffffu, range.y);
         const int64_t pos = row_position(sp, p.Nq, p.Nk, b, i);
         float sl1 = 0.f, sl2 = 0.f;
         if (MODE == kScoreGeneral) {
@@ -347,31 +356,32 @@ __global__ void __launch_bounds__(kSfThreads, 1)
 #pragma unroll 1
             for (int cc = 0; cc < kChunks; ++cc) {
                 const int ch = kChunks * wg + cc;
-                // columns of this chunk that the row sees; an empty row's range is past the chunk
-                const int first = range.x < range.y ? range.x - j0 - ch * 32 : 32, last = range.y - 1 - j0 - ch * 32;
-                const bool any = __any_sync(0xffffffffu, first <= 31 && last >= 0);
-                float z1[32], z2[32];
-                if (any) {
-                    tmem_ld32(t1 + ch * 32, z1);
-                    tmem_ld32(t2 + ch * 32, z2);
-                    tc_wait_ld();
+                const int c0 = j0 + ch * 32;  // the chunk's first key
+                const bool any = c0 < warp_hi && c0 + 32 > warp_lo;
+                const bool whole = c0 >= whole_lo && c0 + 32 <= whole_hi;
+                const int first = range.x - c0, last = range.y - 1 - c0;  // columns that the row sees
+                if (!any) {
+                    if (cc == kChunks - 1) {
+                        tc_fence_before();
+                        mbar_arrive(base + L::bar_sempty + 8 * buf);
+                    }
+                    continue;
                 }
+                float z1[32], z2[32];
+                tmem_ld32(t1 + ch * 32, z1);
+                tmem_ld32(t2 + ch * 32, z2);
+                tc_wait_ld();
                 if (cc == kChunks - 1) {
                     tc_fence_before();
                     mbar_arrive(base + L::bar_sempty + 8 * buf);
                 }
-                if (!any) continue;
-                const bool whole = __all_sync(0xffffffffu, first <= 0 && last >= 31);
                 if (!whole) {
                     hide(z1, first, last);
                     hide(z2, first, last);
                 }
-                if (MODE != kScorePlain) {
-                    cap_scores(z1, sp.side[0]);
-                    cap_scores(z2, sp.side[1]);
-                }
+                cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
                 if (MODE == kScoreGeneral) {
-                    const float d0 = static_cast<float>(pos - (j0 + ch * 32));
+                    const float d0 = static_cast<float>(pos - c0);
                     if (sl1 != 0.f) add_bias(z1, sl1, d0);
                     if (sl2 != 0.f) add_bias(z2, sl2, d0);
                 }
@@ -390,9 +400,9 @@ __global__ void __launch_bounds__(kSfThreads, 1)
             r[384 + row] = st.m2;
             r[512 + row] = st.l2;
         }
-        asm volatile("bar.sync 1, %0;" ::"r"(128 * kSfGroups) : "memory");  // the update warps only
+        asm volatile("bar.sync 1, %0;" ::"r"(128 * kGroups) : "memory");  // the update warps only
         if (wg == 0) {
-            for (int k = 0; k < kSfGroups - 1; ++k) {
+            for (int k = 0; k < kGroups - 1; ++k) {
                 const float* r = red + k * 5 * 128;
                 const RowState o{r[row], r[128 + row], r[256 + row], r[384 + row], r[512 + row]};
                 merge_state(st, o, c);
@@ -628,10 +638,7 @@ __global__ void __launch_bounds__(192, 1)
                     }
                 }
             }
-            if (MODE != kScorePlain) {
-                cap_scores(z1, sp.side[0]);
-                cap_scores(z2, sp.side[1]);
-            }
+            cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 if (q < nq) {
@@ -736,12 +743,12 @@ namespace {
 
 template <int D, int NST, int MODE>
 cudaError_t launch_tile(const CUtensorMap* m, const FwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
-    constexpr int bytes = ScoreTileSmem<D, NST>::alloc;
+    constexpr int bytes = ScoreTileSmem<D, NST, sf_groups(MODE)>::alloc;
     static_assert(bytes <= 232448, "shared memory");
     auto k = score_fwd_tile_kernel<D, NST, MODE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k<<<ctas, kSfThreads, bytes, st>>>(m[0], m[1], m[2], m[3], p, sp);
+    k<<<ctas, sf_threads(MODE), bytes, st>>>(m[0], m[1], m[2], m[3], p, sp);
     return cudaGetLastError();
 }
 
