@@ -64,6 +64,32 @@ __device__ __forceinline__ void load4(const void* p, bool bf16, int64_t at, floa
     }
 }
 
+// 4 values as they lie in memory, so that a warp's loads can all be issued
+// before the first of them is used.
+template <bool BF16>
+struct Raw4 {
+    uint2 u;
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    }
+    __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = __uint_as_float(u.x << 16);
+        v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16);
+        v[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+};
+template <>
+struct Raw4<false> {
+    float4 f;
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    }
+    __device__ __forceinline__ void zero() { f = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w; }
+};
+
 __device__ __forceinline__ void store4(void* p, int64_t at, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
         make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -141,7 +167,7 @@ __device__ __forceinline__ void load_weights(const void* w, bool bf16, const Spa
 }  // namespace
 
 // One CTA: kNrTokens neighbouring tokens x kNrHeads heads of q or of k.
-template <int D>
+template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const NormRopeParams p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,27 +179,37 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const NormRop
     const NormRopeSide& s = p.side[chunk >= chunks_q];
     const int h0 = (chunk - (chunk >= chunks_q ? chunks_q : 0)) * kNrHeads;
     const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-    const Span sp = lane_span(t, p.rot, p.interleaved);
+    const Span sp = lane_span(t, p.rot, INTERLEAVED);
+    const int64_t xin = b * s.x_b + n * s.x_n, yout = b * s.y_b + n * s.y_n;
+    constexpr int STEPS = kNrHeads / ROWS;
+    Raw4<true> ra[STEPS], rb[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const int h = h0 + k * ROWS + sub;
+        ra[k].zero();
+        rb[k].zero();
+        if (h < s.H) {
+            ra[k].load(s.x, xin + h * s.x_h + sp.a);
+            rb[k].load(s.x, xin + h * s.x_h + sp.b);
+        }
+    }
     const Turn turn = load_turn(p, sp, b, n);
     float wa[4], wb[4];
     load_weights(s.w, p.weight_bf16, sp, wa, wb);
-    const int64_t xin = b * s.x_b + n * s.x_n, yout = b * s.y_b + n * s.y_n;
 #pragma unroll
-    for (int k = 0; k < kNrHeads / ROWS; ++k) {
+    for (int k = 0; k < STEPS; ++k) {
         const int h = h0 + k * ROWS + sub;
         const bool live = h < s.H;
-        float xa[4] = {0.f, 0.f, 0.f, 0.f}, xb[4] = {0.f, 0.f, 0.f, 0.f};
-        if (live) {
-            load4(s.x, true, xin + h * s.x_h + sp.a, xa);
-            load4(s.x, true, xin + h * s.x_h + sp.b, xb);
-        }
+        float xa[4], xb[4];
+        ra[k].get(xa);
+        rb[k].get(xb);
         float q = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) q = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], q));
         const float r = rsqrtf(row_sum<LANES>(q) * (1.f / D) + p.eps);
 #pragma unroll
         for (int e = 0; e < 4; ++e) xa[e] = xa[e] * r * wa[e], xb[e] = xb[e] * r * wb[e];
-        if (sp.turned) rotate<false>(xa, xb, turn, p.interleaved);
+        if (sp.turned) rotate<false>(xa, xb, turn, INTERLEAVED);
         if (live) {
             store4(s.y, yout + h * s.y_h + sp.a, xa);
             store4(s.y, yout + h * s.y_h + sp.b, xb);
@@ -184,7 +220,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const NormRop
 // Gradient.  CTAs [0, ctas_q) walk the query heads, the others the key heads;
 // each sums its rows' part of dw in registers, then over its warps, and writes
 // it to part[cta][D].  The order of every sum is fixed.
-template <int D>
+template <int D, bool INTERLEAVED, bool GRAD_BF16>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeParams p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES;
     __shared__ float red[kNrThreads / 32][D];
@@ -197,7 +233,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
     const int chunks = (s.H + kNrHeads - 1) / kNrHeads;
     const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
     const int64_t items = (tokens + kNrTokens - 1) / kNrTokens * chunks;
-    const Span sp = lane_span(t, p.rot, p.interleaved);
+    const Span sp = lane_span(t, p.rot, INTERLEAVED);
+    constexpr int STEPS = kNrHeads / ROWS;
     float wa[4], wb[4], da[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
     load_weights(s.w, p.weight_bf16, sp, wa, wb);
     for (int64_t it = first; it < items; it += step) {
@@ -205,21 +242,34 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
         if (token >= tokens) continue;
         const int h0 = static_cast<int>(it % chunks) * kNrHeads;
         const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-        const Turn turn = load_turn(p, sp, b, n);
         const int64_t xin = b * s.x_b + n * s.x_n, gin = b * s.y_b + n * s.y_n, dout = b * s.dx_b + n * s.dx_n;
+        Raw4<true> rxa[STEPS], rxb[STEPS];
+        Raw4<GRAD_BF16> rua[STEPS], rub[STEPS];
 #pragma unroll
-        for (int k = 0; k < kNrHeads / ROWS; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
+            const int h = h0 + k * ROWS + sub;
+            rxa[k].zero();
+            rxb[k].zero();
+            rua[k].zero();
+            rub[k].zero();
+            if (h < s.H) {
+                rxa[k].load(s.x, xin + h * s.x_h + sp.a);
+                rxb[k].load(s.x, xin + h * s.x_h + sp.b);
+                rua[k].load(s.y, gin + h * s.y_h + sp.a);
+                rub[k].load(s.y, gin + h * s.y_h + sp.b);
+            }
+        }
+        const Turn turn = load_turn(p, sp, b, n);
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
             const int h = h0 + k * ROWS + sub;
             const bool live = h < s.H;
-            float xa[4] = {0.f, 0.f, 0.f, 0.f}, xb[4] = {0.f, 0.f, 0.f, 0.f};
-            float ua[4] = {0.f, 0.f, 0.f, 0.f}, ub[4] = {0.f, 0.f, 0.f, 0.f};
-            if (live) {
-                load4(s.x, true, xin + h * s.x_h + sp.a, xa);
-                load4(s.x, true, xin + h * s.x_h + sp.b, xb);
-                load4(s.y, p.grad_bf16, gin + h * s.y_h + sp.a, ua);
-                load4(s.y, p.grad_bf16, gin + h * s.y_h + sp.b, ub);
-            }
-            if (sp.turned) rotate<true>(ua, ub, turn, p.interleaved);
+            float xa[4], xb[4], ua[4], ub[4];
+            rxa[k].get(xa);
+            rxb[k].get(xb);
+            rua[k].get(ua);
+            rub[k].get(ub);
+            if (sp.turned) rotate<true>(ua, ub, turn, INTERLEAVED);
             float q = 0.f, m = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -315,18 +365,33 @@ void norm_rope_bwd_ctas(const NormRopeParams& p, int sms, int* ctas_q, int* ctas
 cudaError_t launch_norm_rope_fwd(int d, const NormRopeParams& p, cudaStream_t stream) {
     const int64_t groups = (int64_t(p.B) * p.N + kNrTokens - 1) / kNrTokens;
     const int64_t ctas = groups * ((p.Hq + kNrHeads - 1) / kNrHeads + (p.Hk + kNrHeads - 1) / kNrHeads);
+    const unsigned grid = static_cast<unsigned>(ctas);
     if (d == 128)
-        norm_rope_fwd_kernel<128><<<static_cast<unsigned>(ctas), kNrThreads, 0, stream>>>(p);
+        p.interleaved ? norm_rope_fwd_kernel<128, true><<<grid, kNrThreads, 0, stream>>>(p)
+                      : norm_rope_fwd_kernel<128, false><<<grid, kNrThreads, 0, stream>>>(p);
     else
-        norm_rope_fwd_kernel<64><<<static_cast<unsigned>(ctas), kNrThreads, 0, stream>>>(p);
+        p.interleaved ? norm_rope_fwd_kernel<64, true><<<grid, kNrThreads, 0, stream>>>(p)
+                      : norm_rope_fwd_kernel<64, false><<<grid, kNrThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
+namespace {
+template <int D>
+void launch_bwd_d(const NormRopeParams& p, int ctas, cudaStream_t stream) {
+    if (p.interleaved)
+        p.grad_bf16 ? norm_rope_bwd_kernel<D, true, true><<<ctas, kNrThreads, 0, stream>>>(p)
+                    : norm_rope_bwd_kernel<D, true, false><<<ctas, kNrThreads, 0, stream>>>(p);
+    else
+        p.grad_bf16 ? norm_rope_bwd_kernel<D, false, true><<<ctas, kNrThreads, 0, stream>>>(p)
+                    : norm_rope_bwd_kernel<D, false, false><<<ctas, kNrThreads, 0, stream>>>(p);
+}
+}  // namespace
+
 cudaError_t launch_norm_rope_bwd(int d, const NormRopeParams& p, int ctas, cudaStream_t stream) {
     if (d == 128)
-        norm_rope_bwd_kernel<128><<<ctas, kNrThreads, 0, stream>>>(p);
+        launch_bwd_d<128>(p, ctas, stream);
     else
-        norm_rope_bwd_kernel<64><<<ctas, kNrThreads, 0, stream>>>(p);
+        launch_bwd_d<64>(p, ctas, stream);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!p.side[0].dw && !p.side[1].dw)) return e;
     norm_rope_dw_kernel<<<dim3(d / 32, 2), 256, 0, stream>>>(p, d, ctas);

@@ -426,6 +426,54 @@ class AttentionKL(torch.autograd.Function):
 # ---------------------------------------------------------------------------
 # Divergence of attentions with modified scores
 # ---------------------------------------------------------------------------
+# Calls whose arguments passed every check, by what the checks look at (shapes,
+# strides, types, devices, options -- never values or addresses): the structs
+# and sizes they led to.  Checking again and planning cost more host time than a
+# small call's kernels.
+_known = {}
+
+
+def _tensors(*tensors):
+    """What the checks look at of each tensor; None where something is no strided tensor, for them to refuse."""
+    try:
+        return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+    except (AttributeError, RuntimeError):
+        return None
+
+
+def _remember(key, entry):
+    if len(_known) >= 512:
+        _known.clear()
+    _known[key] = entry
+    return entry
+
+
+def _lookup(*key):
+    try:
+        return key, _known.get(key)
+    except TypeError:  # an argument that is not hashable is none that passes the checks
+        return key, None
+
+
+def _on(device, function, *args):
+    """function(*args, current stream of device) with the device current."""
+    if torch.cuda.current_device() == device.index:
+        return function(*args, torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return function(*args, torch.cuda.current_stream(device).cuda_stream)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, nbytes, device):
+    """A caller's workspace, checked, or a new one.  A new one is not cleared: its error word is never read."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _check_workspace(workspace, nbytes, device)
+
+
 class Scores:
     """How the raw products q.k of the teacher (1) and the student (2) become scores, and which keys each row sees:
 
@@ -443,7 +491,7 @@ class Scores:
     def tensors(self):
         return self.slopes1, self.slopes2, self.begin, self.end, self.offset
 
-    def _struct(self, Q1):
+    def check(self, Q1):
         B, H, Nq, _ = Q1.shape
         for name, shape, dtype in (("slopes1", (H,), torch.float32), ("slopes2", (H,), torch.float32),
                                    ("begin", (B, Nq), torch.int32), ("end", (B, Nq), torch.int32),
@@ -451,7 +499,6 @@ class Scores:
             t = getattr(self, name)
             if t is not None:
                 _check_tensor(name, t, shape, dtype, Q1.device)
-        return Score(self.cap1, self.cap2, *(None if t is None else t.data_ptr() for t in self.tensors()))
 
 
 def key_ranges(B, Nq, Nk, device, causal=True, window=0, prefix=None, docs=None, q_lengths=None, k_lengths=None):
@@ -509,23 +556,28 @@ def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0,
                  wait_limit_ns=0, debug_flags=0):
     """Per-row KL(P1 || P2), LSE1, LSE2 as float32 [B, H, Nq] for the scores that ``scores`` describes.  A row that
     sees no key has KL = 0 and LSE = -inf; what a row does not see (NaN included) has no effect on it."""
-    _check_qk(Q1, K1, Q2, K2)
-    lib, shape, opts, plan = load(), make_shape(Q1, K1), _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
-    score = _scores(scores)._struct(Q1)
-    B, H, Nq, _ = Q1.shape
-    with torch.cuda.device(Q1.device):
-        _raise(lib.streamkl_score_fwd_plan(ctypes.byref(shape), ctypes.byref(opts), ctypes.byref(plan)),
-               "streamkl_score_fwd_plan")
-        if out is None:
-            out = tuple(torch.empty((B, H, Nq), dtype=torch.float32, device=Q1.device) for _ in range(3))
+    given = _scores(scores).tensors()
+    key, known = _lookup("score_fwd", _tensors(Q1, K1, Q2, K2, *given), num_splits, wait_limit_ns, debug_flags)
+    if known is None:
+        _check_qk(Q1, K1, Q2, K2)
+        scores.check(Q1)
+        shape, opts, plan = make_shape(Q1, K1), _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
+        with torch.cuda.device(Q1.device):
+            _raise(load().streamkl_score_fwd_plan(ctypes.byref(shape), ctypes.byref(opts), ctypes.byref(plan)),
+                   "streamkl_score_fwd_plan")
+        known = _remember(key, (shape, opts, plan.workspace_bytes, tuple(Q1.shape[:3]), Q1.device))
+    shape, opts, nbytes, rows, device = known
+    if out is None:
+        out = tuple([torch.empty(rows, dtype=torch.float32, device=device) for _ in range(3)])
+    else:
         for name, t in zip(("KL", "LSE1", "LSE2"), out):
-            _check_tensor(name, t, (B, H, Nq), torch.float32, Q1.device)
-        workspace = _check_workspace(workspace, plan.workspace_bytes, Q1.device)
-        KL, L1, L2 = out
-        _raise(lib.streamkl_score_fwd(ctypes.byref(shape), ctypes.byref(score), _ptr(Q1), _ptr(K1), _ptr(Q2), _ptr(K2),
-                                      ctypes.c_float(0.0 if scale is None else float(scale)), int(bool(causal)),
-                                      _ptr(KL), _ptr(L1), _ptr(L2), _ptr(workspace), workspace.numel(),
-                                      ctypes.byref(opts), _stream(Q1.device)), "streamkl_score_fwd")
+            _check_tensor(name, t, rows, torch.float32, device)
+    workspace = _scratch(workspace, nbytes, device)
+    KL, L1, L2 = out
+    score = Score(scores.cap1, scores.cap2, *[_address(t) for t in given])
+    _raise(_on(device, load().streamkl_score_fwd, shape, score, Q1.data_ptr(), K1.data_ptr(), Q2.data_ptr(), K2.data_ptr(),
+               0.0 if scale is None else float(scale), 1 if causal else 0, KL.data_ptr(), L1.data_ptr(), L2.data_ptr(),
+               workspace.data_ptr(), workspace.numel(), opts), "streamkl_score_fwd")
     return KL, L1, L2
 
 
@@ -533,29 +585,33 @@ def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=Fals
                  wait_limit_ns=0, debug_flags=0, grad_dtype=torch.float32):
     """(dQ, dK) of the trainable side of kl_score_fwd: setting 1 -> (Q2, K2), 2 -> (Q1, K1), as kl_bwd.  dQ is added
     up in float32 in no fixed order (like kl_bwd's fused mode)."""
-    _check_qk(Q1, K1, Q2, K2)
-    lib, shape, plan = load(), make_shape(Q1, K1), Plan()
-    opts = _opts(0, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
-    score = _scores(scores)._struct(Q1)
-    B, H, Nq, d = Q1.shape
-    Hk, Nk = K1.shape[1], K1.shape[2]
-    with torch.cuda.device(Q1.device):
-        _raise(lib.streamkl_score_bwd_plan(ctypes.byref(shape), int(setting), ctypes.byref(opts), ctypes.byref(plan)),
-               "streamkl_score_bwd_plan")
+    given = _scores(scores).tensors()
+    key, known = _lookup("score_bwd", _tensors(Q1, K1, Q2, K2, g, KL, LSE1, LSE2, *given), setting, grad_dtype, wait_limit_ns,
+                         debug_flags)
+    if known is None:
+        _check_qk(Q1, K1, Q2, K2)
+        scores.check(Q1)
+        shape, plan = make_shape(Q1, K1), Plan()
+        opts = _opts(0, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
+        with torch.cuda.device(Q1.device):
+            _raise(load().streamkl_score_bwd_plan(ctypes.byref(shape), int(setting), ctypes.byref(opts), ctypes.byref(plan)),
+                   "streamkl_score_bwd_plan")
         for name, t in (("g", g), ("KL", KL), ("LSE1", LSE1), ("LSE2", LSE2)):
-            _check_tensor(name, t, (B, H, Nq), torch.float32, Q1.device)
-        if out is None:
-            out = (torch.empty((B, H, Nq, d), dtype=grad_dtype, device=Q1.device),
-                   torch.empty((B, Hk, Nk, d), dtype=grad_dtype, device=Q1.device))
-        _check_tensor("dQ", out[0], (B, H, Nq, d), grad_dtype, Q1.device)
-        _check_tensor("dK", out[1], (B, Hk, Nk, d), grad_dtype, Q1.device)
-        workspace = _check_workspace(workspace, plan.workspace_bytes, Q1.device)
-        dQ, dK = out
-        _raise(lib.streamkl_score_bwd(ctypes.byref(shape), ctypes.byref(score), int(setting), _ptr(g), _ptr(Q1), _ptr(K1),
-                                      _ptr(Q2), _ptr(K2), _ptr(KL), _ptr(LSE1), _ptr(LSE2),
-                                      ctypes.c_float(0.0 if scale is None else float(scale)), int(bool(causal)),
-                                      _ptr(dQ), _ptr(dK), _ptr(workspace), workspace.numel(), ctypes.byref(opts),
-                                      _stream(Q1.device)), "streamkl_score_bwd")
+            _check_tensor(name, t, Q1.shape[:3], torch.float32, Q1.device)
+        known = _remember(key, (shape, opts, plan.workspace_bytes, tuple(Q1.shape), tuple(K1.shape), Q1.device))
+    shape, opts, nbytes, q_shape, k_shape, device = known
+    if out is None:
+        out = (torch.empty(q_shape, dtype=grad_dtype, device=device), torch.empty(k_shape, dtype=grad_dtype, device=device))
+    else:
+        _check_tensor("dQ", out[0], q_shape, grad_dtype, device)
+        _check_tensor("dK", out[1], k_shape, grad_dtype, device)
+    workspace = _scratch(workspace, nbytes, device)
+    dQ, dK = out
+    score = Score(scores.cap1, scores.cap2, *[_address(t) for t in given])
+    _raise(_on(device, load().streamkl_score_bwd, shape, score, int(setting), g.data_ptr(), Q1.data_ptr(), K1.data_ptr(),
+               Q2.data_ptr(), K2.data_ptr(), KL.data_ptr(), LSE1.data_ptr(), LSE2.data_ptr(),
+               0.0 if scale is None else float(scale), 1 if causal else 0, dQ.data_ptr(), dK.data_ptr(),
+               workspace.data_ptr(), workspace.numel(), opts), "streamkl_score_bwd")
     return dQ, dK
 
 
@@ -623,6 +679,11 @@ def _heads(name, t, dtypes, device=None, shape=None):
     return Strides(*[t.stride(k) if t.shape[k] > 1 else 0 for k in range(3)])
 
 
+def _contiguous(shape) -> Strides:
+    _, H, N, d = shape
+    return Strides(H * max(N, 1) * d, max(N, 1) * d, d)
+
+
 def _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved):
     desc = NormRope()
     desc.q, desc.k = _heads("q", q, (torch.bfloat16,)), _heads("k", k, (torch.bfloat16,), q.device)
@@ -662,16 +723,22 @@ def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, ep
     its root mean square, times wq / wk ([d], float32 or bf16; None: ones), its first 2 * table.shape[1] values turned
     by the angles of its position (positions [B, N], else start + n; table from rope_table; None: no rotation).  out: two
     bf16 tensors of the same shapes, any strides (rows of a cache, or q and k themselves); new contiguous ones otherwise."""
-    desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+    key, known = _lookup("norm_rope", _tensors(q, k, wq, wk, table, positions, *(out or ())), start, eps, interleaved)
+    if known is None:
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+        if out is not None:
+            desc.yq = _heads("out[0]", out[0], (torch.bfloat16,), q.device, q.shape)
+            desc.yk = _heads("out[1]", out[1], (torch.bfloat16,), q.device, k.shape)
+        else:
+            desc.yq, desc.yk = _contiguous(q.shape), _contiguous(k.shape)
+        known = _remember(key, (desc, tuple(q.shape), tuple(k.shape), q.device))
+    desc, q_shape, k_shape, device = known
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k))
+        out = (torch.empty(q_shape, dtype=torch.bfloat16, device=device),
+               torch.empty(k_shape, dtype=torch.bfloat16, device=device))
     yq, yk = out
-    desc.yq = _heads("out[0]", yq, (torch.bfloat16,), q.device, q.shape)
-    desc.yk = _heads("out[1]", yk, (torch.bfloat16,), q.device, k.shape)
-    with torch.cuda.device(q.device):
-        _raise(load().streamkl_norm_rope_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(table),
-                                             _ptr(positions), _ptr(yq), _ptr(yk), _stream(q.device)),
-               "streamkl_norm_rope_fwd")
+    _raise(_on(device, load().streamkl_norm_rope_fwd, desc, q.data_ptr(), k.data_ptr(), _address(wq), _address(wk),
+               _address(table), _address(positions), yq.data_ptr(), yk.data_ptr()), "streamkl_norm_rope_fwd")
     return yq, yk
 
 
@@ -680,27 +747,31 @@ def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=Non
     """(dq, dk, dwq, dwk) of sum(dyq q') + sum(dyk k') for qk_norm_rope's arguments; dyq, dyk are both bf16 or both
     float32 (kl_bwd's gradients as they come), any strides with d contiguous.  dq, dk are bf16, dwq, dwk of the weights'
     type (None without weights).  out: (dq, dk) to write into.  Equal inputs give equal bits."""
-    desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
-    types = (torch.bfloat16, torch.float32)
-    desc.yq = _heads("dyq", dyq, types, q.device, q.shape)
-    desc.yk = _heads("dyk", dyk, (dyq.dtype,), q.device, k.shape)
-    desc.grad_bf16 = int(dyq.dtype == torch.bfloat16)
+    key, known = _lookup("norm_rope_bwd", _tensors(dyq, dyk, q, k, wq, wk, table, positions, *(out or ())), start, eps,
+                         interleaved)
+    if known is None:
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+        desc.yq = _heads("dyq", dyq, (torch.bfloat16, torch.float32), q.device, q.shape)
+        desc.yk = _heads("dyk", dyk, (dyq.dtype,), q.device, k.shape)
+        desc.grad_bf16 = int(dyq.dtype == torch.bfloat16)
+        if out is not None:
+            desc.dq = _heads("out[0]", out[0], (torch.bfloat16,), q.device, q.shape)
+            desc.dk = _heads("out[1]", out[1], (torch.bfloat16,), q.device, k.shape)
+        else:
+            desc.dq, desc.dk = _contiguous(q.shape), _contiguous(k.shape)
+        with torch.cuda.device(q.device):
+            nbytes = max(int(load().streamkl_norm_rope_workspace_bytes(ctypes.byref(desc))), 256)
+        known = _remember(key, (desc, nbytes, tuple(q.shape), tuple(k.shape), q.device))
+    desc, nbytes, q_shape, k_shape, device = known
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k))
+        out = (torch.empty(q_shape, dtype=torch.bfloat16, device=device),
+               torch.empty(k_shape, dtype=torch.bfloat16, device=device))
     dq, dk = out
-    desc.dq = _heads("out[0]", dq, (torch.bfloat16,), q.device, q.shape)
-    desc.dk = _heads("out[1]", dk, (torch.bfloat16,), q.device, k.shape)
     dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
-    lib = load()
-    with torch.cuda.device(q.device):
-        nbytes = int(lib.streamkl_norm_rope_workspace_bytes(ctypes.byref(desc)))
-        # nothing in this workspace is read before it is written: no need to clear a new one
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device) if workspace is None \
-            else _check_workspace(workspace, nbytes, q.device)
-        _raise(lib.streamkl_norm_rope_bwd(ctypes.byref(desc), _ptr(dyq), _ptr(dyk), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
-                                          _ptr(table), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
-                                          _ptr(workspace), workspace.numel(), _stream(q.device)),
-               "streamkl_norm_rope_bwd")
+    workspace = _scratch(workspace, nbytes, device)
+    _raise(_on(device, load().streamkl_norm_rope_bwd, desc, dyq.data_ptr(), dyk.data_ptr(), q.data_ptr(), k.data_ptr(),
+               _address(wq), _address(wk), _address(table), _address(positions), dq.data_ptr(), dk.data_ptr(),
+               _address(dwq), _address(dwk), workspace.data_ptr(), workspace.numel()), "streamkl_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
