@@ -88,6 +88,14 @@ bool options_ok(const streamkl_options* opt) {
                     !(opt->debug_flags & ~STREAMKL_DEBUG_INJECT_STALL));
 }
 
+// Key splits of the tile forward: those of the unmodified forward where they
+// save more than the combine launch costs, about three key tiles (256 x 256 keys,
+// 2 heads: 1 split 7.5 us, 2 splits 6.5 + 3.0 us).
+int tile_splits(int64_t units, int k_tiles, int sms) {
+    const int s = choose_splits(units, k_tiles, sms);
+    return (k_tiles + s - 1) / s + 3 < k_tiles ? s : 1;
+}
+
 struct ScoreFwdPlan {
     bool decode;
     int heads_per_cta, num_splits, ctas, num_q_tiles, num_k_tiles, group;
@@ -116,7 +124,7 @@ streamkl_status plan_score_fwd(const streamkl_shape* s, const streamkl_options* 
     const int64_t units = BH / pl->heads_per_cta * pl->num_q_tiles;
     int splits = opt && opt->num_splits > 0 ? std::min(opt->num_splits, pl->num_k_tiles)
                  : pl->decode               ? decode_splits(units, pl->num_k_tiles, sms)
-                                            : choose_splits(units, pl->num_k_tiles, sms);
+                                            : tile_splits(units, pl->num_k_tiles, sms);
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (units * splits > INT32_MAX || BH * s->Nq > (int64_t(1) << 38)) return STREAMKL_ERR_UNSUPPORTED;
     pl->num_splits = splits;
@@ -128,10 +136,30 @@ streamkl_status plan_score_fwd(const streamkl_shape* s, const streamkl_options* 
 }
 
 struct ScoreBwdPlan {
-    int ctas, num_q_tiles, num_k_tiles, group;
+    int ctas, num_q_tiles, num_k_tiles, group, splits, sms;
     bool bf16;
-    size_t row_bytes, key_bytes, ws_bytes;
+    size_t row_bytes, key_bytes, part_bytes, ws_bytes;
 };
+
+// Splits of a key tile's iterations (its query tiles, of every query head of its
+// group).  Without them few key tiles leave SMs idle, and the tile with the most
+// rows sets the time.  In units of an iteration, for a causal mask: a launch of u
+// tiles with up to n iterations each takes about the larger of the SMs' average
+// and the longest CTA, a CTA costs about 3 more (start, key tiles, dK), and
+// summing the parts about 4.  Splits are taken when they save a fifth: 64 CTAs of
+// up to 128 iterations (2 x 2 key heads, 4 query heads each, 2048 keys) 297 -> 98
+// us with 5, while at 512 CTAs of 512 the estimate stays with 1.
+int bwd_splits(int64_t units, int64_t iterations, int sms) {
+    auto cost = [&](int64_t s) {
+        const double mean = (units * iterations * 0.5 + double(units) * s * 3) / sms;
+        const double longest = double((iterations + s - 1) / s) + 3;
+        return std::max(mean, longest) + (s > 1 ? 4 : 0);
+    };
+    int best = 1;
+    for (int s = 2; s <= 16 && s <= iterations; ++s)
+        if (cost(s) < cost(best)) best = s;
+    return cost(best) < 0.8 * cost(1) ? best : 1;
+}
 
 streamkl_status plan_score_bwd(const streamkl_shape* s, int setting, const streamkl_options* opt, ScoreBwdPlan* pl) {
     streamkl_status st = check_shape(s, 0);
@@ -145,12 +173,18 @@ streamkl_status plan_score_bwd(const streamkl_shape* s, int setting, const strea
     // the iterations of a CTA are counted in 32 bits; the prepare kernel has a block per query tile and head
     if (ctas > INT32_MAX || int64_t(s->B) * s->H * pl->num_q_tiles > INT32_MAX || int64_t(pl->num_q_tiles) * (s->H / kv_heads(s)) > INT32_MAX)
         return STREAMKL_ERR_UNSUPPORTED;
-    pl->ctas = static_cast<int>(ctas);
+    pl->sms = sms;
+    pl->splits = opt && opt->num_splits > 0
+                     ? std::min(opt->num_splits, kMaxSplits)
+                     : bwd_splits(ctas, int64_t(pl->num_q_tiles) * (s->H / kv_heads(s)), sms);
+    if (ctas * pl->splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    pl->ctas = static_cast<int>(ctas * pl->splits);
     pl->group = order_group(int64_t(s->B) * kv_heads(s), pl->num_k_tiles, sms);
     pl->bf16 = opt && opt->grad_bf16 == 1;
     pl->row_bytes = (score_bwd_row_bytes(int64_t(s->B) * s->H, pl->num_q_tiles) + 255) / 256 * 256;
     pl->key_bytes = (score_bwd_key_bytes(s->B, pl->num_q_tiles) + 255) / 256 * 256;
-    pl->ws_bytes = kStatusBytes + pl->row_bytes + pl->key_bytes;
+    pl->part_bytes = pl->splits > 1 ? size_t(pl->splits) * s->B * kv_heads(s) * s->Nk * s->d * sizeof(float) : 0;
+    pl->ws_bytes = kStatusBytes + pl->row_bytes + pl->key_bytes + pl->part_bytes;
     if (pl->bf16) pl->ws_bytes += size_t(s->B) * s->H * s->Nq * s->d * sizeof(float);
     return STREAMKL_OK;
 }
@@ -232,9 +266,9 @@ streamkl_status streamkl_score_bwd_plan(const streamkl_shape* shape, int setting
     streamkl_status st = plan_score_bwd(shape, setting, opt, &pl);
     if (st != STREAMKL_OK) return st;
     plan->path = 2;
-    plan->num_splits = 1;
+    plan->num_splits = pl.splits;
     plan->num_ctas = pl.ctas;
-    plan->launches = pl.bf16 ? 3 : 2;  // prepare (zeros dQ), gradient kernel (+ bf16 conversion)
+    plan->launches = pl.bf16 || pl.splits > 1 ? 3 : 2;  // prepare (zeros dQ), gradient kernel (+ finish)
     plan->workspace_bytes = pl.ws_bytes;
     return STREAMKL_OK;
 }
@@ -267,6 +301,7 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     sp.rows = reinterpret_cast<float*>(ws + kStatusBytes);
     sp.keys = ws + kStatusBytes + pl.row_bytes;
+    sp.dk_parts = reinterpret_cast<float*>(ws + kStatusBytes + pl.row_bytes + pl.key_bytes);
     // Q boxes of 64 rows, K boxes of 128 rows
     CUtensorMap maps[4];
     if (!make_map(&maps[0], Q1, shape, true, 64) || !make_map(&maps[1], K1, shape, false, kBlockK) ||
@@ -281,7 +316,7 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     p.num_k_tiles = pl.num_k_tiles;
     p.H_kv = kv_heads(shape);
     p.kv_group = shape->H / p.H_kv;
-    p.num_splits = 1;
+    p.num_splits = pl.splits;
     p.order_group = pl.group;
     p.scale = sc;
     p.scale_log2e = sc * kLog2e;
@@ -292,19 +327,14 @@ streamkl_status streamkl_score_bwd(const streamkl_shape* shape, const streamkl_s
     p.dQ = dQ;
     p.dK = dK;
     p.grad_bf16 = pl.bf16 ? 1 : 0;
-    p.dQacc = pl.bf16 ? reinterpret_cast<float*>(ws + kStatusBytes + pl.row_bytes + pl.key_bytes) : static_cast<float*>(dQ);
+    p.dQacc = pl.bf16 ? reinterpret_cast<float*>(ws + kStatusBytes + pl.row_bytes + pl.key_bytes + pl.part_bytes)
+                        : static_cast<float*>(dQ);
     p.status = static_cast<unsigned int*>(workspace);
     p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
     p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t dq_elems = size_t(shape->B) * shape->H * shape->Nq * shape->d;
-    if (launch_score_bwd(shape->d, setting, mode, maps, p, sp, pl.ctas, s) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    if (pl.bf16) {
-        int sms = 0;
-        if (device_sms(&sms) != STREAMKL_OK) return STREAMKL_ERR_CUDA;
-        if (launch_to_bf16(p.dQacc, dQ, dq_elems, sms, s) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    }
-    return STREAMKL_OK;
+    return launch_score_bwd(shape->d, setting, mode, maps, p, sp, pl.ctas, pl.sms, s) == cudaSuccess ? STREAMKL_OK
+                                                                                                     : STREAMKL_ERR_CUDA;
 }
 
 streamkl_status streamkl_key_ranges(int32_t B, int32_t Nq, int32_t Nk, int causal, int32_t window,

@@ -39,7 +39,7 @@ cudaError_t launch_score_fwd(int d, int mode, bool decode, const CUtensorMap* ma
 size_t score_bwd_row_bytes(int64_t bh, int q_tiles);     // workspace of sp.rows and
 size_t score_bwd_key_bytes(int64_t batch, int q_tiles);  // of sp.keys
 cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
-                             const ScoreParams& sp, int ctas, cudaStream_t stream);
+                             const ScoreParams& sp, int ctas, int sms, cudaStream_t stream);
 
 cudaError_t launch_key_ranges(const KeyRangeParams& p, cudaStream_t stream);
 

@@ -51,6 +51,7 @@ struct ScoreParams {
     int causal;
     float* rows;            // backward: per-row constants and key ranges of the
     void* keys;             // query tiles (score_bwd.cu)
+    float* dk_parts;        // backward: float32 parts of dK, [splits][B*H_kv*Nk, d], when there are several
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;

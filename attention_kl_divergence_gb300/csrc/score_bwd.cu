@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     // rows see under a causal mask, come first.  (A key head serves kv_group query
     // heads: the CTA visits every query tile of each of them, so dK sums the group's
     // gradients without a second pass.)
-    const int2 at = grouped_order(blockIdx.x, p.num_k_tiles, p.B * p.H_kv, p.order_group);
+    const int unit = blockIdx.x / p.num_splits, split = blockIdx.x - unit * p.num_splits;
+    const int2 at = grouped_order(unit, p.num_k_tiles, p.B * p.H_kv, p.order_group);
     const int bkv = at.x, nt = at.y;  // flat (batch, key head), key tile
     const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
     const int n0 = nt * kBlockK;
@@ -261,10 +262,13 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     const WaitCtx wc{abort_flag, p.status, p.wait_ns};
     const int m_start = tile_span[1] >= 0 ? tile_span[0] : 0;
     const int per_head = tile_span[1] - m_start + 1;  // query tiles of one query head that see this key tile
-    const int n_tiles = per_head * p.kv_group;
+    // this split's share of the key tile's iterations, counted from m0
+    const int64_t all_tiles = static_cast<int64_t>(per_head) * p.kv_group;
+    const int m0 = static_cast<int>(all_tiles * split / p.num_splits);
+    const int n_tiles = static_cast<int>(all_tiles * (split + 1) / p.num_splits) - m0;
     // iteration m -> (query head, query tile)
-    auto qhead = [&](int m) { return p.kv_group == 1 ? hk : hk * p.kv_group + m / per_head; };
-    auto qtile = [&](int m) { return m_start + (p.kv_group == 1 ? m : m % per_head); };
+    auto qhead = [&](int m) { return p.kv_group == 1 ? hk : hk * p.kv_group + (m0 + m) / per_head; };
+    auto qtile = [&](int m) { return m_start + (p.kv_group == 1 ? m0 + m : (m0 + m) % per_head); };
 
     if (warp == 0) {
         // ------------------------------------------------ copies
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             int n_qt = 0, n_qn = 0, n_v = 0;  // tiles whose copies were issued, per ring
             int st = 0, sn = 0, sv = 0;
             uint32_t pt = 0, pn = 0, pv = 0;
-            int h = hk * p.kv_group, t = m_start;
+            int h = qhead(0), t = qtile(0);
             for (int m = 0; m < n_tiles; ++m) {
                 const int r0 = t * kBwdTile;
                 if (!mbar_wait(base + L::bar_qtempty + 8 * st, pt ^ 1, wc, kErrWaitOther)) break;
@@ -593,8 +597,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         // epilogue: dK row = scale * accumulator; each warpgroup writes half the columns
         if (ok && (n_tiles == 0 || wait_all(base + L::bar_done, 0, wc, kErrWaitOther))) {
             tc_fence_after();
-            void* out = reinterpret_cast<uint8_t*>(p.dK) +
-                        (static_cast<size_t>(bkv) * p.Nk + j) * D * (p.grad_bf16 ? 2 : 4);
+            // one split: the output; several: this split's float32 part of it, summed by score_finish_kernel
+            const size_t at_row = static_cast<size_t>(bkv) * p.Nk + j;
+            const bool parts = p.num_splits > 1, bf16 = !parts && p.grad_bf16 != 0;
+            void* out = parts ? static_cast<void*>(sp.dk_parts + (static_cast<size_t>(split) * p.B * p.H_kv * p.Nk + at_row) * D)
+                              : static_cast<void*>(reinterpret_cast<uint8_t*>(p.dK) + at_row * D * (bf16 ? 2 : 4));
 #pragma unroll 1
             for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
                 float v[32];
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;  // no row sees these keys: nothing was accumulated
                 }
-                if (key_ok) store_grad32(out, c0, v, 1.0f, p.grad_bf16 != 0);  // the scale is in dS
+                if (key_ok) store_grad32(out, c0, v, 1.0f, bf16);  // the scale is in dS
             }
         }
     } else {
@@ -691,6 +698,33 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     }
 }
 
+// 8 elements of dQ (float32 -> bf16, when asked for) or of dK (the sum of its
+// splits' parts, in order) per thread and step.
+__global__ void __launch_bounds__(256) score_finish_kernel(const float4* dq, uint4* dq_out, size_t nq8, const float4* dk_parts,
+                                                           void* dk_out, size_t nk8, int splits, bool bf16) {
+    for (size_t k = blockIdx.x * size_t(blockDim.x) + threadIdx.x; k < nq8 + nk8; k += size_t(gridDim.x) * blockDim.x) {
+        if (k < nq8) {
+            const float4 a = dq[2 * k], b = dq[2 * k + 1];
+            dq_out[k] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+            continue;
+        }
+        const size_t e = k - nq8;
+        float4 a = dk_parts[2 * e], b = dk_parts[2 * e + 1];
+        for (int s = 1; s < splits; ++s) {
+            const float4 u = dk_parts[2 * (s * nk8 + e)], v = dk_parts[2 * (s * nk8 + e) + 1];
+            a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+            b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
+        }
+        if (bf16) {
+            static_cast<uint4*>(dk_out)[e] =
+                make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+        } else {
+            static_cast<float4*>(dk_out)[2 * e] = a;
+            static_cast<float4*>(dk_out)[2 * e + 1] = b;
+        }
+    }
+}
+
 template <int D, int SETTING, int MODE>
 cudaError_t launch_impl(const CUtensorMap* m, const BwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
     constexpr int NST = D == 128 ? 4 : 8;  // trainable-side query ring; the other side's is half as deep
@@ -717,13 +751,22 @@ size_t score_bwd_row_bytes(int64_t bh, int q_tiles) { return static_cast<size_t>
 size_t score_bwd_key_bytes(int64_t batch, int q_tiles) { return static_cast<size_t>(batch) * q_tiles * sizeof(KeyBlock); }
 
 cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
-                             const ScoreParams& sp, int ctas, cudaStream_t stream) {
+                             const ScoreParams& sp, int ctas, int sms, cudaStream_t stream) {
     score_prepare_kernel<<<static_cast<unsigned>(p.B * p.H) * p.num_q_tiles, 256, 0, stream>>>(p, sp, setting, d);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return mode == kScorePlain     ? launch_mode<kScorePlain>(d, setting, maps, p, sp, ctas, stream)
-           : mode == kScoreBounded ? launch_mode<kScoreBounded>(d, setting, maps, p, sp, ctas, stream)
-                                   : launch_mode<kScoreGeneral>(d, setting, maps, p, sp, ctas, stream);
+    e = mode == kScorePlain     ? launch_mode<kScorePlain>(d, setting, maps, p, sp, ctas, stream)
+        : mode == kScoreBounded ? launch_mode<kScoreBounded>(d, setting, maps, p, sp, ctas, stream)
+                                : launch_mode<kScoreGeneral>(d, setting, maps, p, sp, ctas, stream);
+    const bool parts = p.num_splits > 1;
+    if (e != cudaSuccess || !(parts || p.grad_bf16)) return e;
+    const size_t nq8 = p.grad_bf16 ? static_cast<size_t>(p.B) * p.H * p.Nq * d / 8 : 0;
+    const size_t nk8 = parts ? static_cast<size_t>(p.B) * p.H_kv * p.Nk * d / 8 : 0;
+    const size_t blocks = std::min<size_t>((nq8 + nk8 + 255) / 256, static_cast<size_t>(sms) * 8);
+    score_finish_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+        reinterpret_cast<const float4*>(p.dQacc), static_cast<uint4*>(p.dQ), nq8,
+        reinterpret_cast<const float4*>(sp.dk_parts), p.dK, nk8, p.num_splits, p.grad_bf16 != 0);
+    return cudaGetLastError();
 }
 
 }  // namespace streamkl

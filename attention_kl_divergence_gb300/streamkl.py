@@ -455,10 +455,15 @@ def _lookup(*key):
         return key, None
 
 
+# the current stream's handle without a Stream object (2 us on the GPU's host CPU)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device, function, *args):
     """function(*args, current stream of device) with the device current."""
     if torch.cuda.current_device() == device.index:
-        return function(*args, torch.cuda.current_stream(device).cuda_stream)
+        return function(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
         return function(*args, torch.cuda.current_stream(device).cuda_stream)
 
@@ -543,11 +548,11 @@ def score_fwd_plan(Q1, K1, num_splits=0) -> Plan:
     return plan
 
 
-def score_bwd_plan(Q1, K1, setting, grad_dtype=torch.float32) -> Plan:
+def score_bwd_plan(Q1, K1, setting, grad_dtype=torch.float32, num_splits=0) -> Plan:
     plan = Plan()
     with torch.cuda.device(Q1.device):
         _raise(load().streamkl_score_bwd_plan(ctypes.byref(make_shape(Q1, K1)), int(setting),
-                                              ctypes.byref(_opts(grad_bf16=_grad_flag(grad_dtype))),
+                                              ctypes.byref(_opts(num_splits, grad_bf16=_grad_flag(grad_dtype))),
                                               ctypes.byref(plan)), "streamkl_score_bwd_plan")
     return plan
 
@@ -582,17 +587,18 @@ def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0,
 
 
 def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=False, scale=None, workspace=None, out=None,
-                 wait_limit_ns=0, debug_flags=0, grad_dtype=torch.float32):
+                 wait_limit_ns=0, debug_flags=0, grad_dtype=torch.float32, num_splits=0):
     """(dQ, dK) of the trainable side of kl_score_fwd: setting 1 -> (Q2, K2), 2 -> (Q1, K1), as kl_bwd.  dQ is added
-    up in float32 in no fixed order (like kl_bwd's fused mode)."""
+    up in float32 in no fixed order (like kl_bwd's fused mode); dK is the same on every run.  num_splits: CTAs that
+    share a key tile's query rows (0 = automatic)."""
     given = _scores(scores).tensors()
     key, known = _lookup("score_bwd", _tensors(Q1, K1, Q2, K2, g, KL, LSE1, LSE2, *given), setting, grad_dtype, wait_limit_ns,
-                         debug_flags)
+                         debug_flags, num_splits)
     if known is None:
         _check_qk(Q1, K1, Q2, K2)
         scores.check(Q1)
         shape, plan = make_shape(Q1, K1), Plan()
-        opts = _opts(0, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
+        opts = _opts(num_splits, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
         with torch.cuda.device(Q1.device):
             _raise(load().streamkl_score_bwd_plan(ctypes.byref(shape), int(setting), ctypes.byref(opts), ctypes.byref(plan)),
                    "streamkl_score_bwd_plan")

@@ -252,8 +252,9 @@ STREAMKL_API streamkl_status streamkl_noalloc_status(streamkl_stream_t stream, u
  *    and infinities included.  A visible one (or a product that overflows
  *    float32) makes the row NaN, capped or not.
  *  - A capped side needs 1e-5 <= scale / cap <= 1e5 (UNSUPPORTED otherwise).
- *  - The backward is the fused one (dQ added up in float32 in no fixed order);
- *    opt->bwd_mode must be 0.  Its gradients include the slope of the cap,
+ *  - The backward is the fused one (dQ added up in float32 in no fixed order, dK
+ *    the same on every run); opt->bwd_mode must be 0; opt->num_splits sets the
+ *    CTAs that share the query rows of a key tile (0 = automatic).  Its gradients include the slope of the cap,
  *    1 - tanh^2.  begin, end, offset, slopes, caps and scale as in the forward.
  *  - Layouts, strides, dtypes, shared keys, workspace and streams as above.
  * ------------------------------------------------------------------------- */

@@ -113,7 +113,7 @@ class Ref:
 
 
 def run_case(B, H, Hk, Nq, Nk, d, mask, cap1=0.0, cap2=0.0, bias=False, settings=(1, 2), peak=1.0, seed=0, scale=None,
-             grad_dtype=torch.float32, num_splits=0):
+             grad_dtype=torch.float32, num_splits=0, bwd_splits=0):
     Q1, K1, Q2, K2 = make_qk(B, H, Nq, Nk, d, 0.3, teacher_scale=peak, seed=seed, device=DEV, H_kv=Hk)
     begin, end, offset = mask(B, Nq, Nk)
     pos = torch.arange(Nq, device=DEV) + offset[:, None].long()
@@ -125,7 +125,7 @@ def run_case(B, H, Hk, Nq, Nk, d, mask, cap1=0.0, cap2=0.0, bias=False, settings
     ref.check_rows(*rows)
     g = torch.randn((B, H, Nq), device=DEV, generator=torch.Generator(device=DEV).manual_seed(seed))
     for setting in settings:
-        dQ, dK = sk.kl_score_bwd(setting, sc, g, Q1, K1, Q2, K2, *rows, scale=scale, grad_dtype=grad_dtype)
+        dQ, dK = sk.kl_score_bwd(setting, sc, g, Q1, K1, Q2, K2, *rows, scale=scale, grad_dtype=grad_dtype, num_splits=bwd_splits)
         assert dQ.dtype == dK.dtype == grad_dtype
         ref.check_grads(setting, g, dQ, dK)
     return ref
@@ -202,6 +202,15 @@ def test_bf16_gradients_and_other_scale(kind):
 def test_split_counts(Nq, splits):
     run_case(1, 4, 2, Nq, 900, 64, ranges(k_lengths=[770]), settings=(), num_splits=splits, cap1=30.0, cap2=30.0)
     run_case(1, 4, 2, Nq, 900, 64, random_ranges, settings=(), num_splits=splits, bias=True)
+
+
+@gpu
+@pytest.mark.parametrize("grad_dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("splits", [1, 3, 16, 64])
+def test_backward_split_counts(splits, grad_dtype):
+    """More splits than a key tile has iterations, too: some do nothing."""
+    run_case(2, 4, 1, 200, 300, 128, ranges(docs=[0, 190, 300]), cap1=30.0, cap2=30.0, bwd_splits=splits, grad_dtype=grad_dtype)
+    run_case(1, 2, 2, 130, 130, 64, random_ranges, bias=True, bwd_splits=splits, grad_dtype=grad_dtype)
 
 
 @gpu
