@@ -27,18 +27,21 @@ constexpr int kNrThreads = 256;
 constexpr int kNrHeads = 8;                  // heads of one token that a warp takes at a time
 constexpr int kNrTokens = kNrThreads / 32;   // neighbouring tokens of a CTA, one per warp
 
-// Offsets of a lane's two groups of 4 values within a head.
+// A lane's 8 values of a head lie in two groups of 4, at a and b, and are held
+// as 4 pairs (f[e], g[e]): f the first members, g the second.  With halves, f is
+// group a and g group b; interleaved, the members alternate through both groups.
 struct Span {
     int a, b;
     bool turned;  // the lane's values are rotated
-    int pair;     // its first pair
+    int pair;     // its first pair in the table
 };
 
-__device__ __forceinline__ Span lane_span(int t, int rot, bool interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ Span lane_span(int t, int rot) {
     Span s;
     s.turned = 8 * t < rot;
     s.pair = 4 * t;
-    if (s.turned && !interleaved) {
+    if (s.turned && !INTERLEAVED) {
         s.a = 4 * t;
         s.b = rot / 2 + 4 * t;
     } else {
@@ -48,103 +51,103 @@ __device__ __forceinline__ Span lane_span(int t, int rot, bool interleaved) {
     return s;
 }
 
-__device__ __forceinline__ void load4(const void* p, bool bf16, int64_t at, float (&v)[4]) {
-    if (bf16) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-        v[0] = __uint_as_float(u.x << 16);
-        v[1] = __uint_as_float(u.x & 0xffff0000u);
-        v[2] = __uint_as_float(u.y << 16);
-        v[3] = __uint_as_float(u.y & 0xffff0000u);
-    } else {
-        const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        v[0] = f.x;
-        v[1] = f.y;
-        v[2] = f.z;
-        v[3] = f.w;
-    }
-}
+struct Pairs {
+    float2 f[2], g[2];  // f[0], f[1] | f[2], f[3] and so on: packed float32 arithmetic
+};
 
-// 4 values as they lie in memory, so that a warp's loads can all be issued
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// A lane's 8 values as they lie in memory, so that a warp's loads are all issued
 // before the first of them is used.
 template <bool BF16>
-struct Raw4 {
-    uint2 u;
-    __device__ __forceinline__ void load(const void* p, int64_t at) {
-        u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+struct Raw {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const void* pa, const void* pb) {
+        a = *static_cast<const uint2*>(pa);
+        b = *static_cast<const uint2*>(pb);
     }
-    __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
-    __device__ __forceinline__ void get(float (&v)[4]) const {
-        v[0] = __uint_as_float(u.x << 16);
-        v[1] = __uint_as_float(u.x & 0xffff0000u);
-        v[2] = __uint_as_float(u.y << 16);
-        v[3] = __uint_as_float(u.y & 0xffff0000u);
+    __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
+    template <bool INTERLEAVED>
+    __device__ __forceinline__ Pairs get() const {
+        Pairs p;
+        if (INTERLEAVED) {
+            p.f[0] = make_float2(bf_lo(a.x), bf_lo(a.y));
+            p.f[1] = make_float2(bf_lo(b.x), bf_lo(b.y));
+            p.g[0] = make_float2(bf_hi(a.x), bf_hi(a.y));
+            p.g[1] = make_float2(bf_hi(b.x), bf_hi(b.y));
+        } else {
+            p.f[0] = make_float2(bf_lo(a.x), bf_hi(a.x));
+            p.f[1] = make_float2(bf_lo(a.y), bf_hi(a.y));
+            p.g[0] = make_float2(bf_lo(b.x), bf_hi(b.x));
+            p.g[1] = make_float2(bf_lo(b.y), bf_hi(b.y));
+        }
+        return p;
     }
 };
 template <>
-struct Raw4<false> {
-    float4 f;
-    __device__ __forceinline__ void load(const void* p, int64_t at) {
-        f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+struct Raw<false> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* pa, const void* pb) {
+        a = *static_cast<const float4*>(pa);
+        b = *static_cast<const float4*>(pb);
     }
-    __device__ __forceinline__ void zero() { f = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w; }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    template <bool INTERLEAVED>
+    __device__ __forceinline__ Pairs get() const {
+        Pairs p;
+        if (INTERLEAVED) {
+            p.f[0] = make_float2(a.x, a.z);
+            p.f[1] = make_float2(b.x, b.z);
+            p.g[0] = make_float2(a.y, a.w);
+            p.g[1] = make_float2(b.y, b.w);
+        } else {
+            p.f[0] = make_float2(a.x, a.y);
+            p.f[1] = make_float2(a.z, a.w);
+            p.g[0] = make_float2(b.x, b.y);
+            p.g[1] = make_float2(b.z, b.w);
+        }
+        return p;
+    }
 };
 
-__device__ __forceinline__ void store4(void* p, int64_t at, const float (&v)[4]) {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
-        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+template <bool INTERLEAVED>
+__device__ __forceinline__ void store_pairs(void* pa, void* pb, const Pairs& p) {
+    uint2 a, b;
+    if (INTERLEAVED) {
+        a = make_uint2(pack_bf16(p.f[0].x, p.g[0].x), pack_bf16(p.f[0].y, p.g[0].y));
+        b = make_uint2(pack_bf16(p.f[1].x, p.g[1].x), pack_bf16(p.f[1].y, p.g[1].y));
+    } else {
+        a = make_uint2(pack_bf16(p.f[0].x, p.f[0].y), pack_bf16(p.f[1].x, p.f[1].y));
+        b = make_uint2(pack_bf16(p.g[0].x, p.g[0].y), pack_bf16(p.g[1].x, p.g[1].y));
+    }
+    *static_cast<uint2*>(pa) = a;
+    *static_cast<uint2*>(pb) = b;
 }
 
 // Cosines and sines of a lane's 4 pairs; a position outside the table gives NaN.
 struct Turn {
-    float c[4], s[4];
+    float2 c[2], s[2];
 };
 
-__device__ __forceinline__ Turn load_turn(const NormRopeParams& p, const Span& sp, int b, int n) {
+__device__ __forceinline__ Turn load_turn(const NormRopeParams& p, const Span& sp, uint32_t token, uint32_t n) {
     Turn t;
-    if (!sp.turned) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t.c[e] = 1.f, t.s[e] = 0.f;
-        return t;
-    }
-    const int64_t at = static_cast<int64_t>(b) * p.N + n;
+    t.c[0] = t.c[1] = make_float2(1.f, 1.f);
+    t.s[0] = t.s[1] = make_float2(0.f, 0.f);
+    if (!sp.turned) return t;
     const int64_t pos = !p.positions ? p.start + n
-                        : p.pos_int64 ? static_cast<const int64_t*>(p.positions)[at]
-                                      : static_cast<const int32_t*>(p.positions)[at];
+                        : p.pos_int64 ? static_cast<const int64_t*>(p.positions)[token]
+                                      : static_cast<const int32_t*>(p.positions)[token];
     if (pos < 0 || pos >= p.table_rows) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t.c[e] = t.s[e] = __int_as_float(0x7fc00000);
+        const float nan = __int_as_float(0x7fc00000);
+        t.c[0] = t.c[1] = t.s[0] = t.s[1] = make_float2(nan, nan);
         return t;
     }
     const float4* f = reinterpret_cast<const float4*>(p.table + (pos * (p.rot / 2) + sp.pair) * 2);
     const float4 lo = __ldg(f), hi = __ldg(f + 1);
-    t.c[0] = lo.x, t.s[0] = lo.y, t.c[1] = lo.z, t.s[1] = lo.w;
-    t.c[2] = hi.x, t.s[2] = hi.y, t.c[3] = hi.z, t.s[3] = hi.w;
+    t.c[0] = make_float2(lo.x, lo.z), t.s[0] = make_float2(lo.y, lo.w);
+    t.c[1] = make_float2(hi.x, hi.z), t.s[1] = make_float2(hi.y, hi.w);
     return t;
-}
-
-// Turn a lane's pairs by the angles (inverse: by their negatives).
-template <bool INVERSE>
-__device__ __forceinline__ void rotate(float (&a)[4], float (&b)[4], const Turn& t, bool interleaved) {
-    if (interleaved) {  // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float& x = e < 2 ? a[2 * (e & 1)] : b[2 * (e & 1)];
-            float& y = e < 2 ? a[2 * (e & 1) + 1] : b[2 * (e & 1) + 1];
-            const float s = INVERSE ? -t.s[e] : t.s[e];
-            const float u = x * t.c[e] - y * s, v = y * t.c[e] + x * s;
-            x = u;
-            y = v;
-        }
-    } else {  // pairs (a_e, b_e)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float s = INVERSE ? -t.s[e] : t.s[e];
-            const float u = a[e] * t.c[e] - b[e] * s, v = b[e] * t.c[e] + a[e] * s;
-            a[e] = u;
-            b[e] = v;
-        }
-    }
 }
 
 template <int LANES>
@@ -154,66 +157,88 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void load_weights(const void* w, bool bf16, const Span& sp, float (&wa)[4], float (&wb)[4]) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pairs load_weights(const void* w, bool bf16, const Span& sp) {
     if (!w) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) wa[e] = wb[e] = 1.f;
-        return;
+        Pairs p;
+        p.f[0] = p.f[1] = p.g[0] = p.g[1] = make_float2(1.f, 1.f);
+        return p;
     }
-    load4(w, bf16, sp.a, wa);
-    load4(w, bf16, sp.b, wb);
+    if (bf16) {
+        Raw<true> r;
+        r.load(static_cast<const uint16_t*>(w) + sp.a, static_cast<const uint16_t*>(w) + sp.b);
+        return r.get<INTERLEAVED>();
+    }
+    Raw<false> r;
+    r.load(static_cast<const float*>(w) + sp.a, static_cast<const float*>(w) + sp.b);
+    return r.get<INTERLEAVED>();
 }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Sum over a lane's 8 products.
+__device__ __forceinline__ float dot(const Pairs& a, const Pairs& b) {
+    float2 u = mul2(a.f[0], b.f[0]), v = mul2(a.f[1], b.f[1]);
+    u = fma2(a.g[0], b.g[0], u);
+    v = fma2(a.g[1], b.g[1], v);
+    return (u.x + u.y) + (v.x + v.y);
+}
+
+__device__ __forceinline__ const char* at_bytes(const void* p, int64_t bytes) { return static_cast<const char*>(p) + bytes; }
 
 }  // namespace
 
 // One CTA: kNrTokens neighbouring tokens x kNrHeads heads of q or of k.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const NormRopeParams p) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kNrHeads / ROWS;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = lane % LANES, sub = lane / LANES;
-    const int chunks_q = (p.Hq + kNrHeads - 1) / kNrHeads, chunks = chunks_q + (p.Hk + kNrHeads - 1) / kNrHeads;
-    const int64_t token = static_cast<int64_t>(blockIdx.x / chunks) * kNrTokens + warp;
-    if (token >= static_cast<int64_t>(p.B) * p.N) return;
-    const int chunk = blockIdx.x % chunks;
+    const uint32_t chunks_q = (p.Hq + kNrHeads - 1) / kNrHeads, chunks = chunks_q + (p.Hk + kNrHeads - 1) / kNrHeads;
+    const uint32_t group = blockIdx.x / chunks, chunk = blockIdx.x - group * chunks;
+    const uint32_t token = group * kNrTokens + warp;  // B N < 2^28
+    if (token >= static_cast<uint32_t>(p.B) * p.N) return;
     const NormRopeSide& s = p.side[chunk >= chunks_q];
-    const int h0 = (chunk - (chunk >= chunks_q ? chunks_q : 0)) * kNrHeads;
-    const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-    const Span sp = lane_span(t, p.rot, INTERLEAVED);
-    const int64_t xin = b * s.x_b + n * s.x_n, yout = b * s.y_b + n * s.y_n;
-    constexpr int STEPS = kNrHeads / ROWS;
-    Raw4<true> ra[STEPS], rb[STEPS];
+    const int h0 = static_cast<int>(chunk - (chunk >= chunks_q ? chunks_q : 0)) * kNrHeads + sub;
+    const uint32_t b = token / static_cast<uint32_t>(p.N), n = token - b * p.N;
+    const Span sp = lane_span<INTERLEAVED>(t, p.rot);
+    const char* xp = at_bytes(s.x, 2 * (b * s.x_b + n * s.x_n + h0 * s.x_h + sp.a));
+    char* yp = const_cast<char*>(at_bytes(s.y, 2 * (b * s.y_b + n * s.y_n + h0 * s.y_h + sp.a)));
+    const int ab = 2 * (sp.b - sp.a);  // bytes from group a to group b
+    const int64_t xs = 2 * ROWS * s.x_h, ys = 2 * ROWS * s.y_h;
+    Raw<true> raw[STEPS];
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-        const int h = h0 + k * ROWS + sub;
-        ra[k].zero();
-        rb[k].zero();
-        if (h < s.H) {
-            ra[k].load(s.x, xin + h * s.x_h + sp.a);
-            rb[k].load(s.x, xin + h * s.x_h + sp.b);
-        }
+        raw[k].zero();
+        if (h0 + k * ROWS < s.H) raw[k].load(xp, xp + ab);
+        xp += xs;
     }
-    const Turn turn = load_turn(p, sp, b, n);
-    float wa[4], wb[4];
-    load_weights(s.w, p.weight_bf16, sp, wa, wb);
+    const Turn turn = load_turn(p, sp, token, n);
+    const Pairs w = load_weights<INTERLEAVED>(s.w, p.weight_bf16, sp);
+    // y_f = r (f (w_f c) - g (w_g s)),  y_g = r (g (w_g c) + f (w_f s))
+    float2 fc[2], gs[2], gc[2], fs[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        fc[e] = mul2(w.f[e], turn.c[e]);
+        fs[e] = mul2(w.f[e], turn.s[e]);
+        gc[e] = mul2(w.g[e], turn.c[e]);
+        gs[e] = neg2(mul2(w.g[e], turn.s[e]));
+    }
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-        const int h = h0 + k * ROWS + sub;
-        const bool live = h < s.H;
-        float xa[4], xb[4];
-        ra[k].get(xa);
-        rb[k].get(xb);
-        float q = 0.f;
+        const Pairs x = raw[k].template get<INTERLEAVED>();
+        const float2 r = both(rsqrtf(row_sum<LANES>(dot(x, x)) * (1.f / D) + p.eps));
+        Pairs y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], q));
-        const float r = rsqrtf(row_sum<LANES>(q) * (1.f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xa[e] = xa[e] * r * wa[e], xb[e] = xb[e] * r * wb[e];
-        if (sp.turned) rotate<false>(xa, xb, turn, INTERLEAVED);
-        if (live) {
-            store4(s.y, yout + h * s.y_h + sp.a, xa);
-            store4(s.y, yout + h * s.y_h + sp.b, xb);
+        for (int e = 0; e < 2; ++e) {
+            y.f[e] = mul2(r, fma2(x.f[e], fc[e], mul2(x.g[e], gs[e])));
+            y.g[e] = mul2(r, fma2(x.g[e], gc[e], mul2(x.f[e], fs[e])));
         }
+        if (h0 + k * ROWS < s.H) store_pairs<INTERLEAVED>(yp, yp + ab, y);
+        yp += ys;
     }
 }
 
@@ -221,95 +246,103 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const NormRop
 // each sums its rows' part of dw in registers, then over its warps, and writes
 // it to part[cta][D].  The order of every sum is fixed.
 template <int D, bool INTERLEAVED, bool GRAD_BF16>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeParams p) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kNrHeads / ROWS, GB = GRAD_BF16 ? 2 : 4;
     __shared__ float red[kNrThreads / 32][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = lane % LANES, sub = lane / LANES;
     const bool keys = static_cast<int>(blockIdx.x) >= p.ctas_q;
     const NormRopeSide& s = p.side[keys];
-    const int first = keys ? blockIdx.x - p.ctas_q : blockIdx.x;
-    const int step = keys ? static_cast<int>(gridDim.x) - p.ctas_q : p.ctas_q;
-    const int chunks = (s.H + kNrHeads - 1) / kNrHeads;
-    const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
-    const int64_t items = (tokens + kNrTokens - 1) / kNrTokens * chunks;
-    const Span sp = lane_span(t, p.rot, INTERLEAVED);
-    constexpr int STEPS = kNrHeads / ROWS;
-    float wa[4], wb[4], da[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
-    load_weights(s.w, p.weight_bf16, sp, wa, wb);
-    for (int64_t it = first; it < items; it += step) {
-        const int64_t token = it / chunks * kNrTokens + warp;
+    const uint32_t first = keys ? blockIdx.x - p.ctas_q : blockIdx.x;
+    const uint32_t step = keys ? gridDim.x - p.ctas_q : p.ctas_q;
+    const uint32_t chunks = (s.H + kNrHeads - 1) / kNrHeads;
+    const uint32_t tokens = static_cast<uint32_t>(p.B) * p.N;
+    const uint32_t items = (tokens + kNrTokens - 1) / kNrTokens * chunks;  // < 2^31, as the forward's CTAs
+    const Span sp = lane_span<INTERLEAVED>(t, p.rot);
+    const int ab = sp.b - sp.a;
+    const Pairs w = load_weights<INTERLEAVED>(s.w, p.weight_bf16, sp);
+    Pairs dw;
+    dw.f[0] = dw.f[1] = dw.g[0] = dw.g[1] = make_float2(0.f, 0.f);
+    for (uint32_t it = first; it < items; it += step) {
+        const uint32_t group = it / chunks, token = group * kNrTokens + warp;
         if (token >= tokens) continue;
-        const int h0 = static_cast<int>(it % chunks) * kNrHeads;
-        const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-        const int64_t xin = b * s.x_b + n * s.x_n, gin = b * s.y_b + n * s.y_n, dout = b * s.dx_b + n * s.dx_n;
-        Raw4<true> rxa[STEPS], rxb[STEPS];
-        Raw4<GRAD_BF16> rua[STEPS], rub[STEPS];
+        const int h0 = static_cast<int>(it - group * chunks) * kNrHeads + sub;
+        const uint32_t b = token / static_cast<uint32_t>(p.N), n = token - b * p.N;
+        const char* xp = at_bytes(s.x, 2 * (b * s.x_b + n * s.x_n + h0 * s.x_h + sp.a));
+        const char* gp = at_bytes(s.y, GB * (b * s.y_b + n * s.y_n + h0 * s.y_h + sp.a));
+        char* op = const_cast<char*>(at_bytes(s.dx, 2 * (b * s.dx_b + n * s.dx_n + h0 * s.dx_h + sp.a)));
+        const int64_t xs = 2 * ROWS * s.x_h, gs = GB * ROWS * s.y_h, os = 2 * ROWS * s.dx_h;
+        Raw<true> rx[STEPS];
+        Raw<GRAD_BF16> rg[STEPS];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int h = h0 + k * ROWS + sub;
-            rxa[k].zero();
-            rxb[k].zero();
-            rua[k].zero();
-            rub[k].zero();
-            if (h < s.H) {
-                rxa[k].load(s.x, xin + h * s.x_h + sp.a);
-                rxb[k].load(s.x, xin + h * s.x_h + sp.b);
-                rua[k].load(s.y, gin + h * s.y_h + sp.a);
-                rub[k].load(s.y, gin + h * s.y_h + sp.b);
+            rx[k].zero();
+            rg[k].zero();
+            if (h0 + k * ROWS < s.H) {
+                rx[k].load(xp, xp + 2 * ab);
+                rg[k].load(gp, gp + GB * ab);
             }
+            xp += xs;
+            gp += gs;
         }
-        const Turn turn = load_turn(p, sp, b, n);
+        const Turn turn = load_turn(p, sp, token, n);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int h = h0 + k * ROWS + sub;
-            const bool live = h < s.H;
-            float xa[4], xb[4], ua[4], ub[4];
-            rxa[k].get(xa);
-            rxb[k].get(xb);
-            rua[k].get(ua);
-            rub[k].get(ub);
-            if (sp.turned) rotate<true>(ua, ub, turn, INTERLEAVED);
-            float q = 0.f, m = 0.f;
+            const Pairs x = rx[k].template get<INTERLEAVED>(), g = rg[k].template get<INTERLEAVED>();
+            Pairs u, wu;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                q = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], q));
-                m = fmaf(ua[e] * wa[e], xa[e], fmaf(ub[e] * wb[e], xb[e], m));
+            for (int e = 0; e < 2; ++e) {  // u = R^T dy
+                u.f[e] = fma2(g.f[e], turn.c[e], mul2(g.g[e], turn.s[e]));
+                u.g[e] = fma2(g.g[e], turn.c[e], neg2(mul2(g.f[e], turn.s[e])));
+                wu.f[e] = mul2(w.f[e], u.f[e]);
+                wu.g[e] = mul2(w.g[e], u.g[e]);
             }
-            const float r = rsqrtf(row_sum<LANES>(q) * (1.f / D) + p.eps);
-            const float c = row_sum<LANES>(m) * r * (1.f / D);  // mean(w u n)
-            if (live) {
+            const float r = rsqrtf(row_sum<LANES>(dot(x, x)) * (1.f / D) + p.eps);
+            // dx = r wu - n mean(wu n),  n = x r
+            const float m = row_sum<LANES>(dot(wu, x)) * r * (1.f / D);
+            const float2 rr = both(r), mm = both(-m * r);
+            if (h0 + k * ROWS < s.H) {
+                Pairs dx;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float na = xa[e] * r, nb = xb[e] * r;
-                    da[e] = fmaf(ua[e], na, da[e]);
-                    db[e] = fmaf(ub[e], nb, db[e]);
-                    ua[e] = r * (ua[e] * wa[e] - na * c);
-                    ub[e] = r * (ub[e] * wb[e] - nb * c);
+                for (int e = 0; e < 2; ++e) {
+                    const float2 nf = mul2(x.f[e], rr), ng = mul2(x.g[e], rr);
+                    dw.f[e] = fma2(u.f[e], nf, dw.f[e]);
+                    dw.g[e] = fma2(u.g[e], ng, dw.g[e]);
+                    dx.f[e] = fma2(wu.f[e], rr, mul2(nf, mm));
+                    dx.g[e] = fma2(wu.g[e], rr, mul2(ng, mm));
                 }
-                store4(s.dx, dout + h * s.dx_h + sp.a, ua);
-                store4(s.dx, dout + h * s.dx_h + sp.b, ub);
+                store_pairs<INTERLEAVED>(op, op + 2 * ab, dx);
             }
+            op += os;
         }
     }
     if (!s.dw) return;
+    // back to the order of memory, then over the lanes that hold the same columns
+    float va[4], vb[4];
+    if (INTERLEAVED) {
+        va[0] = dw.f[0].x, va[1] = dw.g[0].x, va[2] = dw.f[0].y, va[3] = dw.g[0].y;
+        vb[0] = dw.f[1].x, vb[1] = dw.g[1].x, vb[2] = dw.f[1].y, vb[3] = dw.g[1].y;
+    } else {
+        va[0] = dw.f[0].x, va[1] = dw.f[0].y, va[2] = dw.f[1].x, va[3] = dw.f[1].y;
+        vb[0] = dw.g[0].x, vb[1] = dw.g[0].y, vb[2] = dw.g[1].x, vb[3] = dw.g[1].y;
+    }
 #pragma unroll
     for (int o = LANES; o < 32; o <<= 1) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
-            db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+            va[e] += __shfl_xor_sync(0xffffffffu, va[e], o);
+            vb[e] += __shfl_xor_sync(0xffffffffu, vb[e], o);
         }
     }
     if (lane < LANES) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[warp][sp.a + e] = da[e], red[warp][sp.b + e] = db[e];
+        for (int e = 0; e < 4; ++e) red[warp][sp.a + e] = va[e], red[warp][sp.b + e] = vb[e];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < D; e += blockDim.x) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNrThreads / 32; ++w) v += red[w][e];
+        for (int k = 0; k < kNrThreads / 32; ++k) v += red[k][e];
         p.part[static_cast<size_t>(blockIdx.x) * D + e] = v;
     }
 }
