@@ -25,6 +25,10 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrHeads = 8;                  // heads of one token that a warp takes at a time
+// CTAs of the gradient pass per SM, all resident: 16 KB of loads in flight each.
+// 64K tokens of 32 + 8 heads: 2 CTAs 371 us, 3 341 us, 4 (half the heads at a
+// time, to fit the registers) 415 us.
+constexpr int kNrBwdCtas = 3;
 constexpr int kNrTokens = kNrThreads / 32;   // neighbouring tokens of a CTA, one per warp
 
 // A lane's 8 values of a head lie in two groups of 4, at a and b, and are held
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const __grid_
 // each sums its rows' part of dw in registers, then over its warps, and writes
 // it to part[cta][D].  The order of every sum is fixed.
 template <int D, bool INTERLEAVED, bool GRAD_BF16>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kNrHeads / ROWS, GB = GRAD_BF16 ? 2 : 4;
     __shared__ float red[kNrThreads / 32][D];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq,
 void norm_rope_bwd_ctas(const NormRopeParams& p, int sms, int* ctas_q, int* ctas) {
     const int64_t groups = (int64_t(p.B) * p.N + kNrTokens - 1) / kNrTokens;
     const int64_t iq = groups * ((p.Hq + kNrHeads - 1) / kNrHeads), ik = groups * ((p.Hk + kNrHeads - 1) / kNrHeads);
-    const int64_t slots = int64_t(sms) * 4;
+    const int64_t slots = int64_t(sms) * kNrBwdCtas;
     if (iq + ik <= slots) {
         *ctas_q = static_cast<int>(iq);
         *ctas = static_cast<int>(iq + ik);

@@ -130,6 +130,32 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
 }
 
 // ---------------------------------------------------------------------------
+// Cluster launch control: a running CTA takes over a CTA of its grid that has
+// not started yet.  The 16-byte response lands at `dst` (16-byte aligned) and
+// completes 16 bytes on the mbarrier.  No request may follow a refused one.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+
+// blockIdx.x of the CTA taken over, or -1 when none was left.
+__device__ __forceinline__ int clc_response(uint32_t src) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.s32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(x)
+        : "r"(src)
+        : "memory");
+    return x;
+}
+
+// ---------------------------------------------------------------------------
 // tcgen05: tensor memory and the 5th-generation tensor core
 // ---------------------------------------------------------------------------
 

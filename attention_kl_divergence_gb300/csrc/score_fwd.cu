@@ -25,9 +25,18 @@ constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 sta
 #define SFG 4
 #endif
 constexpr int sf_groups(int mode) { return mode == kScorePlain ? SFP : mode == kScoreBounded ? SFB : SFG; }
-// warp 0 TMA, warp 1 the S1 MMAs, the update warpgroups, and a last warp for the S2 MMAs
+// warp 0 work items and copies, warp 1 the S1 MMAs, the update warpgroups, and a last warp for the S2 MMAs
 constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 32; }
 constexpr uint64_t kSfDrainNs = 200000000ull;  // in-flight copies and MMAs retire before a CTA exits
+
+// A 128-row query tile of one head, and a share of its key tiles.
+struct WorkItem {
+    int bh, q0, split;
+    int kt_begin, n_tiles;
+    int valid;  // 0: no further items
+    int pad[2];
+};
+static_assert(sizeof(WorkItem) == 32, "packed");
 
 template <int D, int NST, int GROUPS>
 struct ScoreTileSmem {
@@ -41,11 +50,18 @@ struct ScoreTileSmem {
     static constexpr int bar_kempty = bar_kfull + 8 * NST;
     static constexpr int bar_sfull = bar_kempty + 8 * NST;
     static constexpr int bar_sempty = bar_sfull + 16;
-    static constexpr int bar_done = bar_sempty + 16;  // drain barriers of aborted MMA issuers (S1, S2)
-    static constexpr int misc = bar_done + 16;    // tmem base (4 B), abort flag (4 B)
-    static constexpr int span = misc + 16;        // [4 warps]{lowest begin, highest end}
-    static constexpr int red = span + 32;         // [groups - 1][5][128] floats: the other groups' row states
-    static constexpr int total = red + (GROUPS - 1) * 5 * 128 * 4;
+    static constexpr int bar_done = bar_sempty + 16;      // drain barriers of aborted MMA issuers (S1, S2)
+    static constexpr int bar_qempty = bar_done + 16;
+    static constexpr int bar_ifull = bar_qempty + 8;      // [2] work items
+    static constexpr int bar_iempty = bar_ifull + 16;
+    static constexpr int bar_clc = bar_iempty + 16;
+    static constexpr int misc = bar_clc + 8;              // tmem base (4 B), abort flag (4 B)
+    static constexpr int clc = (misc + 8 + 15) / 16 * 16; // [2] launch-control responses
+    static constexpr int items = clc + 32;                // [2] WorkItem
+    static constexpr int ranges = items + 64;             // [2][128] int2: the rows' key ranges
+    static constexpr int red = ranges + 2 * kBlockQ * 8;  // [2][groups - 1][5][128] floats: the other groups' states
+    static constexpr int kRed = (GROUPS - 1) * 5 * 128;
+    static constexpr int total = red + 2 * kRed * 4;
     static constexpr int alloc = total + 1024;    // slack for 1024-byte alignment
 };
 
@@ -162,54 +178,50 @@ __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_s
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Tile forward.  The CTA first takes the union of its rows' key ranges and
-// visits only the tiles inside it.  Warp 0 TMA, warp 1 the S1 MMAs and TMEM, the
-// last warp the S2 MMAs, the others the update (one query row per thread).
+// Tile forward.  A work item is a 128-row query tile of one head; a CTA starts
+// with its own and then takes over CTAs that have not started, one after the
+// other.  Short rows (documents, windows) make short items: their start (row
+// ranges, first copies) and end (merge, outputs) run while the neighbouring items'
+// tiles are computed.  Every role walks the same items:
+//   warp 0       fetches the items, works out the union of the rows' key ranges
+//                (only tiles inside it are visited) and issues the copies
+//   warp 1, last S1 and S2 MMAs (warp 1 owns TMEM)
+//   the others   the update, one query row per thread
+// Rings (key tiles, score buffers) run on through the items.  8192 keys in 8 heads
+// of documents of 1000 to 2000 tokens: one item per CTA 258 us, as here @DOCS us.
 // ---------------------------------------------------------------------------
 template <int D, int NST, int MODE>
 __global__ void __launch_bounds__(sf_threads(MODE), 1)
     score_fwd_tile_kernel(const __grid_constant__ CUtensorMap tQ1, const __grid_constant__ CUtensorMap tK1,
                           const __grid_constant__ CUtensorMap tQ2, const __grid_constant__ CUtensorMap tK2,
                           const __grid_constant__ FwdParams p, const __grid_constant__ ScoreParams sp) {
-    constexpr int kGroups = sf_groups(MODE), kS2Warp = sf_threads(MODE) / 32 - 1;
-    using L = ScoreTileSmem<D, NST, sf_groups(MODE)>;
+    constexpr int kGroups = sf_groups(MODE), kS2Warp = sf_threads(MODE) / 32 - 1, kUpdate = 128 * kGroups;
+    using L = ScoreTileSmem<D, NST, kGroups>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
-    int2* span = reinterpret_cast<int2*>(gbase + L::span);
-
+    WorkItem* items = reinterpret_cast<WorkItem*>(gbase + L::items);
+    int2* ranges = reinterpret_cast<int2*>(gbase + L::ranges);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // Groups of heads, a few waves of CTAs each, so that resident CTAs share key
-    // tiles through L2; in a group the last query tiles of every head, which see
-    // the most keys under a causal mask, come first.
-    const int unit = blockIdx.x / p.num_splits, split = blockIdx.x - unit * p.num_splits;
-    const int2 at = grouped_order(unit, p.num_q_tiles, p.B * p.H, p.order_group);
-    const int bh = at.x, qt = p.num_q_tiles - 1 - at.y;
-    const int b = bh / p.H, h = bh - b * p.H;
-    const int hk = h / p.kv_group;
-    const int q0 = qt * kBlockQ;
-
-    if (threadIdx.x < 128) {
-        const int2 r = row_range(sp, p.Nq, p.Nk, b, q0 + threadIdx.x);
-        const int low = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT32_MAX);
-        const int high = __reduce_max_sync(0xffffffffu, r.y);
-        if (lane == 0) span[warp] = make_int2(low, high);
-    }
     if (threadIdx.x == 0) {
         mbar_init(base + L::bar_q, 1);
+        mbar_init(base + L::bar_qempty, 2);  // both issuers' last MMAs of the item
         for (int s = 0; s < NST; ++s) {
             mbar_init(base + L::bar_kfull + 8 * s, 1);
             mbar_init(base + L::bar_kempty + 8 * s, 2);  // both issuers' MMAs have read the stage
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(base + L::bar_sfull + 8 * s, 2);  // S1 and S2 of the buffer are complete
-            mbar_init(base + L::bar_sempty + 8 * s, 128 * kGroups);
+            mbar_init(base + L::bar_sempty + 8 * s, kUpdate);
+            mbar_init(base + L::bar_ifull + 8 * s, 1);
+            mbar_init(base + L::bar_iempty + 8 * s, 2 + kUpdate / 32);  // the issuers and the update warps
         }
         mbar_init(base + L::bar_done, 1);
         mbar_init(base + L::bar_done + 8, 1);
+        mbar_init(base + L::bar_clc, 1);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -220,78 +232,150 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wc{abort_flag, p.status, p.wait_ns};
-    const int lo = min(min(span[0].x, span[1].x), min(span[2].x, span[3].x));
-    const int hi = max(max(span[0].y, span[1].y), max(span[2].y, span[3].y));
-    const int2 mine = lo < hi ? split_tiles(lo / kBlockK, (hi + kBlockK - 1) / kBlockK, split, p.num_splits)
-                              : make_int2(0, 0);
-    const int kt_begin = mine.x, n_tiles = mine.y;
 
     if (warp == 0) {
-        // ------------------------------------------------------------ TMA
-        if (lane == 0 && n_tiles > 0) {
+        // ------------------------------------------------------------ work items and copies
+        if (lane == 0) {
             prefetch_tensormap(&tQ1);
             prefetch_tensormap(&tK1);
             prefetch_tensormap(&tQ2);
             prefetch_tensormap(&tK2);
-            const uint64_t keep = policy_evict_last();  // K tiles are re-read by every query tile
-            mbar_arrive_expect_tx(base + L::bar_q, 2 * L::kQBytes);
+        }
+        const uint64_t keep = policy_evict_last();  // key tiles are read again by other query tiles
+        // Groups of heads, a few waves of CTAs each, so that CTAs running at a time share
+        // key tiles through L2; in a group the last query tiles of every head, which see
+        // the most keys under a causal mask, come first.
+        auto place = [&](int unit) {
+            const int u = unit / p.num_splits;
+            const int2 at = grouped_order(u, p.num_q_tiles, p.B * p.H, p.order_group);
+            return make_int4(at.x, (p.num_q_tiles - 1 - at.y) * kBlockQ, unit - u * p.num_splits, at.x / p.H);
+        };
+        auto row_ranges = [&](const int4& at, int2 (&r)[4]) {
 #pragma unroll
-            for (int c = 0; c < D / kSwizzleCols; ++c) {
-                tma_load_4d(base + L::q1 + c * kBlockQ * 128, &tQ1, base + L::bar_q, c * kSwizzleCols, q0, h, b);
-                tma_load_4d(base + L::q2 + c * kBlockQ * 128, &tQ2, base + L::bar_q, c * kSwizzleCols, q0, h, b);
-            }
-            int it = 0;
-            for (; it < n_tiles; ++it) {
-                const int s = it % NST;
-                if (!mbar_wait(base + L::bar_kempty + 8 * s, ((it / NST) & 1) ^ 1, wc, kErrWaitK)) break;
-                const uint32_t fb = base + L::bar_kfull + 8 * s;
-                mbar_arrive_expect_tx(fb, 2 * L::kKBytes);
-                const int k0 = (kt_begin + it) * kBlockK;
-                const uint32_t k1s = base + L::k + 2 * s * L::kKBytes, k2s = k1s + L::kKBytes;
+            for (int k = 0; k < 4; ++k) r[k] = row_range(sp, p.Nq, p.Nk, at.w, at.y + lane + 32 * k);
+        };
+        int unit = blockIdx.x, requests = 0, it = 0, n_q = 0;
+        int4 at = place(unit);
+        int2 rr[4];
+        row_ranges(at, rr);
+        bool pending = true, ok = true;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(base + L::bar_clc, 16);
+            clc_request(base + L::clc, base + L::bar_clc);
+        }
+        for (int k = 0;; ++k) {
+            const int slot = k & 1;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * slot, ((k >> 1) & 1) ^ 1, wc, kErrWaitOther))))
+                break;
+            int kt_begin = 0, n_tiles = 0;
+            if (unit >= 0) {
+                int lo = INT32_MAX, hi = 0;
 #pragma unroll
-                for (int c = 0; c < D / kSwizzleCols; ++c) {
-                    tma_load_4d_hint(k1s + c * kBlockK * 128, &tK1, fb, c * kSwizzleCols, k0, hk, b, keep);
-                    tma_load_4d_hint(k2s + c * kBlockK * 128, &tK2, fb, c * kSwizzleCols, k0, hk, b, keep);
+                for (int r = 0; r < 4; ++r) {
+                    ranges[slot * kBlockQ + lane + 32 * r] = rr[r];
+                    if (rr[r].x < rr[r].y) lo = min(lo, rr[r].x), hi = max(hi, rr[r].y);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                if (lo < hi) {
+                    const int2 mine = split_tiles(lo / kBlockK, (hi + kBlockK - 1) / kBlockK, at.z, p.num_splits);
+                    kt_begin = mine.x;
+                    n_tiles = mine.y;
                 }
             }
-            // drain: every issued copy has landed and every stage was released
-            score_drain(base + L::bar_q, 0, kSfDrainNs);  // the query tiles' copies have landed
+            if (lane == 0) items[slot] = WorkItem{at.x, at.y, at.z, kt_begin, n_tiles, unit >= 0, {0, 0}};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);
+            if (unit < 0) break;
+            const int b = at.w, h = at.x - b * p.H, hk = h / p.kv_group, q0 = at.y;
+            auto load_keys = [&](int from, int to) {  // key tiles [from, to) of the item
+                for (int t = from; t < to; ++t, ++it) {
+                    const int s = it % NST;
+                    if (!mbar_wait(base + L::bar_kempty + 8 * s, ((it / NST) & 1) ^ 1, wc, kErrWaitK)) return false;
+                    const uint32_t fb = base + L::bar_kfull + 8 * s;
+                    mbar_arrive_expect_tx(fb, 2 * L::kKBytes);
+                    const int k0 = (kt_begin + t) * kBlockK;
+                    const uint32_t k1s = base + L::k + 2 * s * L::kKBytes, k2s = k1s + L::kKBytes;
+#pragma unroll
+                    for (int c = 0; c < D / kSwizzleCols; ++c) {
+                        tma_load_4d_hint(k1s + c * kBlockK * 128, &tK1, fb, c * kSwizzleCols, k0, hk, b, keep);
+                        tma_load_4d_hint(k2s + c * kBlockK * 128, &tK2, fb, c * kSwizzleCols, k0, hk, b, keep);
+                    }
+                }
+                return true;
+            };
+            const int head = min(n_tiles, NST);
+            if (lane == 0 && n_tiles > 0) {
+                // the previous item's last MMAs have read its query tiles
+                ok = mbar_wait(base + L::bar_qempty, (n_q & 1) ^ 1, wc, kErrWaitQ);
+                if (ok) {
+                    mbar_arrive_expect_tx(base + L::bar_q, 2 * L::kQBytes);
+#pragma unroll
+                    for (int c = 0; c < D / kSwizzleCols; ++c) {
+                        tma_load_4d(base + L::q1 + c * kBlockQ * 128, &tQ1, base + L::bar_q, c * kSwizzleCols, q0, h, b);
+                        tma_load_4d(base + L::q2 + c * kBlockQ * 128, &tQ2, base + L::bar_q, c * kSwizzleCols, q0, h, b);
+                    }
+                    ++n_q;
+                    ok = load_keys(0, head);
+                }
+            }
+            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+            // the next item, while this one's tiles are under way
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, requests & 1, wc, kErrWaitOther)))) break;
+            pending = false;
+            unit = clc_response(base + L::clc + 16 * (requests & 1));
+            ++requests;
+            fence_proxy_async_smem();  // the response is read before the slot's next one is written
+            __syncwarp();
+            if (unit >= 0) {
+                pending = true;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(base + L::bar_clc, 16);
+                    clc_request(base + L::clc + 16 * (requests & 1), base + L::bar_clc);
+                }
+                at = place(unit);
+                row_ranges(at, rr);
+            }
+            if (lane == 0 && n_tiles > head) ok = load_keys(head, n_tiles);
+            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+        }
+        if (lane == 0) {  // every issued copy has landed, every stage was released
+            if (pending) score_drain(base + L::bar_clc, requests & 1, kSfDrainNs);
+            if (n_q > 0) score_drain(base + L::bar_q, (n_q - 1) & 1, kSfDrainNs);
             for (int j = max(0, it - NST); j < it; ++j) {
                 score_drain(base + L::bar_kfull + 8 * (j % NST), (j / NST) & 1, kSfDrainNs);
                 if (!*abort_flag) score_drain(base + L::bar_kempty + 8 * (j % NST), (j / NST) & 1, kSfDrainNs);
             }
         }
     } else if (warp == 1 || warp == kS2Warp) {
-        // ------------------------------------------------------------ MMA
-        // Two threads issue the MMAs, S1 = Q1 K1^T (warp 1) and S2 = Q2 K2^T
-        // (the last warp), each committing its own arrival on the shared
-        // barriers: the update warpgroups share their schedulers and keep them
-        // busy, and two issuers keep the tensor pipe fed when one is held up.
-        if (lane == 0 && n_tiles > 0) {
+        // ------------------------------------------------------------ MMA: S1 (warp 1), S2 (last warp)
+        if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16_f32(kBlockQ, kBlockK);
             const bool second = warp != 1;
             const uint32_t done_bar = base + L::bar_done + (second ? 8 : 0);
-            int issued = 0;
-            // test aid: a wait on a barrier that nothing arrives on (bar_done is
-            // only committed on the abort path below) gives up after wait_ns
-            const bool stalled = p.inject_stall && blockIdx.x == 0 && !second &&
-                                 !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther);
-            if (!stalled && mbar_wait(base + L::bar_q, 0, wc, kErrWaitQ)) {
+            const uint32_t dhi = smem_desc_hi();
+            const uint32_t q_lo = smem_desc_lo_k128(base + (second ? L::q2 : L::q1));
+            const uint32_t k_lo0 = smem_desc_lo_k128(base + L::k) + (second ? (L::kKBytes >> 4) : 0u);
+            constexpr uint32_t kStageLo = (2 * L::kKBytes) >> 4;
+            const uint32_t dcol = second ? kBlockK : 0u;
+            int it = 0, n_q = 0, s = 0;
+            uint32_t kph = 0, k_lo = k_lo0;
+            // test aid: a wait on a barrier that nothing arrives on gives up after wait_ns
+            bool ok = !(p.inject_stall && blockIdx.x == 0 && !second && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther));
+            for (int k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!mbar_wait(base + L::bar_ifull + 8 * slot, (k >> 1) & 1, wc, kErrWaitOther)) break;
+                const int n_tiles = items[slot].n_tiles, valid = items[slot].valid;
+                mbar_arrive(base + L::bar_iempty + 8 * slot);
+                if (!valid) break;
+                if (n_tiles == 0) continue;
+                if (!mbar_wait(base + L::bar_q, n_q & 1, wc, kErrWaitQ)) break;
+                ++n_q;
                 tc_fence_after();
-                // few instructions per MMA: descriptor low words advance by
-                // compile-time offsets (the high word is one constant) and ring
-                // positions are counters rather than divisions
-                const uint32_t dhi = smem_desc_hi();
-                const uint32_t q_lo = smem_desc_lo_k128(base + (second ? L::q2 : L::q1));
-                const uint32_t k_lo0 = smem_desc_lo_k128(base + L::k) + (second ? (L::kKBytes >> 4) : 0u);
-                constexpr uint32_t kStageLo = (2 * L::kKBytes) >> 4;
-                const uint32_t dcol = second ? kBlockK : 0u;
-                int s = 0;
-                uint32_t kph = 0, k_lo = k_lo0;
-                for (int it = 0; it < n_tiles; ++it) {
+                for (int t = 0; t < n_tiles; ++t, ++it) {
                     const int buf = it & 1;
-                    if (!mbar_wait(base + L::bar_kfull + 8 * s, kph, wc, kErrWaitK)) break;
-                    if (!mbar_wait(base + L::bar_sempty + 8 * buf, ((it >> 1) & 1) ^ 1, wc, kErrWaitS)) break;
+                    if (!(ok = mbar_wait(base + L::bar_kfull + 8 * s, kph, wc, kErrWaitK))) break;
+                    if (!(ok = mbar_wait(base + L::bar_sempty + 8 * buf, ((it >> 1) & 1) ^ 1, wc, kErrWaitS))) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * 2 * kBlockK + dcol;
 #pragma unroll
@@ -302,7 +386,6 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                     }
                     tc_commit(base + L::bar_sfull + 8 * buf);
                     tc_commit(base + L::bar_kempty + 8 * s);
-                    ++issued;
                     if (++s == NST) {
                         s = 0;
                         kph ^= 1;
@@ -311,104 +394,117 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         k_lo += kStageLo;
                     }
                 }
+                if (ok) tc_commit(base + L::bar_qempty);
             }
-            if (*abort_flag && issued > 0) {  // let the issued MMAs retire before TMEM is freed
+            if (*abort_flag && it > 0) {  // let the issued MMAs retire before TMEM is freed
                 tc_commit(done_bar);
                 score_drain(done_bar, 0, kSfDrainNs);
             }
         }
     } else {
-        // ------------------------------------------------------------ online update (warps 2 .. 2 + 4 groups)
-        // kGroups warpgroups split every tile's 128 columns; each keeps its
-        // own running state per row, and the states of a row are merged at the
-        // end (the same log-sum-exp merge as the Split-K combine).
+        // ------------------------------------------------------------ online update
         constexpr int kChunks = 4 / kGroups;  // 32-column chunks per group and tile
         const int wg = (warp - 2) >> 2;
         const int wq = warp & 3;
         const int row = wq * 32 + lane;
-        const int i = q0 + row;
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float c = MODE == kScorePlain ? p.scale_log2e : 1.f;
         const float tau = kScoreTau / c;
-        const int2 range = row_range(sp, p.Nq, p.Nk, b, i);
-        // keys [warp_lo, warp_hi) are seen by some row of the warp, [whole_lo, whole_hi) by all of them
-        const int warp_lo = __reduce_min_sync(0xffffffffu, range.x < range.y ? range.x : INT32_MAX);
-        const int warp_hi = __reduce_max_sync(0xffffffffu, range.y);
-        const int whole_lo = __reduce_max_sync(0xffffffffu, range.x);
-        const int whole_hi = __reduce_min_sync(0xffffffffu, range.y);
-        const int64_t pos = row_position(sp, p.Nq, p.Nk, b, i);
-        float sl1 = 0.f, sl2 = 0.f;
-        if (MODE == kScoreGeneral) {
-            if (sp.side[0].slopes) sl1 = sp.side[0].slopes[h] * kLog2e;
-            if (sp.side[1].slopes) sl2 = sp.side[1].slopes[h] * kLog2e;
-        }
-        RowState st{-INFINITY, 0.f, 0.f, -INFINITY, 0.f};
-        bool ok = true;
-        for (int it = 0; it < n_tiles; ++it) {
-            const int buf = it & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_sfull + 8 * buf, (it >> 1) & 1, wc, kErrWaitS))) {
-                ok = false;
-                break;
+        int it = 0;
+        // All update warps leave together: each pass ends in one barrier that also says whether every warp goes on.
+        for (int k = 0;; ++k) {
+            const int slot = k & 1;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_ifull + 8 * slot, (k >> 1) & 1, wc, kErrWaitOther));
+            const WorkItem item = items[slot];
+            const int2 range = ranges[slot * kBlockQ + row];
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(base + L::bar_iempty + 8 * slot);
+            const bool live = ok && item.valid;
+            const int n_tiles = live ? item.n_tiles : 0;
+            const int bh = item.bh, b = bh / p.H, i = item.q0 + row;
+            // keys [warp_lo, warp_hi) are seen by some row of the warp, [whole_lo, whole_hi) by all of them
+            const int warp_lo = __reduce_min_sync(0xffffffffu, range.x < range.y ? range.x : INT32_MAX);
+            const int warp_hi = __reduce_max_sync(0xffffffffu, range.y);
+            const int whole_lo = __reduce_max_sync(0xffffffffu, range.x);
+            const int whole_hi = __reduce_min_sync(0xffffffffu, range.y);
+            int64_t pos = 0;
+            float sl1 = 0.f, sl2 = 0.f;
+            if (MODE == kScoreGeneral && live) {
+                const int h = bh - b * p.H;
+                pos = row_position(sp, p.Nq, p.Nk, b, i);
+                if (sp.side[0].slopes) sl1 = sp.side[0].slopes[h] * kLog2e;
+                if (sp.side[1].slopes) sl2 = sp.side[1].slopes[h] * kLog2e;
             }
-            tc_fence_after();
-            const int j0 = (kt_begin + it) * kBlockK;
-            const uint32_t t1 = tl + buf * 2 * kBlockK, t2 = t1 + kBlockK;
+            RowState st{-INFINITY, 0.f, 0.f, -INFINITY, 0.f};
+            for (int t = 0; t < n_tiles; ++t, ++it) {
+                const int buf = it & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_sfull + 8 * buf, (it >> 1) & 1, wc, kErrWaitS))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int j0 = (item.kt_begin + t) * kBlockK;
+                const uint32_t t1 = tl + buf * 2 * kBlockK, t2 = t1 + kBlockK;
 #pragma unroll 1
-            for (int cc = 0; cc < kChunks; ++cc) {
-                const int ch = kChunks * wg + cc;
-                const int c0 = j0 + ch * 32;  // the chunk's first key
-                const bool any = c0 < warp_hi && c0 + 32 > warp_lo;
-                const bool whole = c0 >= whole_lo && c0 + 32 <= whole_hi;
-                const int first = range.x - c0, last = range.y - 1 - c0;  // columns that the row sees
-                if (!any) {
+                for (int cc = 0; cc < kChunks; ++cc) {
+                    const int ch = kChunks * wg + cc;
+                    const int c0 = j0 + ch * 32;  // the chunk's first key
+                    const bool any = c0 < warp_hi && c0 + 32 > warp_lo;
+                    const bool whole = c0 >= whole_lo && c0 + 32 <= whole_hi;
+                    const int first = range.x - c0, last = range.y - 1 - c0;  // columns that the row sees
+                    if (!any) {
+                        if (cc == kChunks - 1) {
+                            tc_fence_before();
+                            mbar_arrive(base + L::bar_sempty + 8 * buf);
+                        }
+                        continue;
+                    }
+                    float z1[32], z2[32];
+                    tmem_ld32(t1 + ch * 32, z1);
+                    tmem_ld32(t2 + ch * 32, z2);
+                    tc_wait_ld();
                     if (cc == kChunks - 1) {
                         tc_fence_before();
                         mbar_arrive(base + L::bar_sempty + 8 * buf);
                     }
-                    continue;
+                    if (!whole) {
+                        hide(z1, first, last);
+                        hide(z2, first, last);
+                    }
+                    cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
+                    if (MODE == kScoreGeneral) {
+                        const float d0 = static_cast<float>(pos - c0);
+                        if (sl1 != 0.f) add_bias(z1, sl1, d0);
+                        if (sl2 != 0.f) add_bias(z2, sl2, d0);
+                    }
+                    if (whole)
+                        update_scored<false, MODE == kScoreBounded>(z1, z2, 0, 31, st, c, tau);
+                    else
+                        update_scored<true, MODE == kScoreBounded>(z1, z2, first, last, st, c, tau);
                 }
-                float z1[32], z2[32];
-                tmem_ld32(t1 + ch * 32, z1);
-                tmem_ld32(t2 + ch * 32, z2);
-                tc_wait_ld();
-                if (cc == kChunks - 1) {
-                    tc_fence_before();
-                    mbar_arrive(base + L::bar_sempty + 8 * buf);
-                }
-                if (!whole) {
-                    hide(z1, first, last);
-                    hide(z2, first, last);
-                }
-                cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
-                if (MODE == kScoreGeneral) {
-                    const float d0 = static_cast<float>(pos - c0);
-                    if (sl1 != 0.f) add_bias(z1, sl1, d0);
-                    if (sl2 != 0.f) add_bias(z2, sl2, d0);
-                }
-                if (whole)
-                    update_scored<false, MODE == kScoreBounded>(z1, z2, 0, 31, st, c, tau);
-                else
-                    update_scored<true, MODE == kScoreBounded>(z1, z2, first, last, st, c, tau);
             }
-        }
-        float* red = reinterpret_cast<float*>(gbase + L::red);
-        if (wg > 0) {
-            float* r = red + (wg - 1) * 5 * 128;
-            r[row] = st.m1;
-            r[128 + row] = st.l1;
-            r[256 + row] = st.acc;
-            r[384 + row] = st.m2;
-            r[512 + row] = st.l2;
-        }
-        asm volatile("bar.sync 1, %0;" ::"r"(128 * kGroups) : "memory");  // the update warps only
-        if (wg == 0) {
-            for (int k = 0; k < kGroups - 1; ++k) {
-                const float* r = red + k * 5 * 128;
-                const RowState o{r[row], r[128 + row], r[256 + row], r[384 + row], r[512 + row]};
-                merge_state(st, o, c);
+            // the groups' states of a row; two buffers, so that one barrier per item keeps them apart
+            float* red = reinterpret_cast<float*>(gbase + L::red) + slot * L::kRed;
+            if (wg > 0) {
+                float* r = red + (wg - 1) * 5 * 128;
+                r[row] = st.m1;
+                r[128 + row] = st.l1;
+                r[256 + row] = st.acc;
+                r[384 + row] = st.m2;
+                r[512 + row] = st.l2;
             }
-            if (i < p.Nq)
-                store_scored(p, static_cast<size_t>(bh) * p.Nq + i, split, st, range.x >= range.y, !ok || *abort_flag);
+            const bool go_on = bar_sync_and(1, kUpdate, live && ok);
+            if (wg == 0 && live) {
+                for (int g = 0; g < kGroups - 1; ++g) {
+                    const float* r = red + g * 5 * 128;
+                    const RowState o{r[row], r[128 + row], r[256 + row], r[384 + row], r[512 + row]};
+                    merge_state(st, o, c);
+                }
+                if (i < p.Nq)
+                    store_scored(p, static_cast<size_t>(bh) * p.Nq + i, item.split, st, range.x >= range.y,
+                                 !go_on || *abort_flag);
+            }
+            if (!go_on) break;
         }
     }
 

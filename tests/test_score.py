@@ -14,6 +14,7 @@ add 2^-8 of the value.
 """
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -372,6 +373,36 @@ def test_autograd_function_settings():
     assert bool(((dQ.double() - want).abs() <= tol + 2.0 ** -8 * want.abs()).all())
     with pytest.raises(ValueError):
         sk.ScoredAttentionKL.apply(*leaves, sk.Scores(slopes1=torch.ones(4, device=DEV, requires_grad=True)))
+
+
+@gpu
+def test_first_call_of_a_host_thread():
+    """A thread that has made no CUDA call yet, with every buffer at hand: nothing before the library's own calls
+    binds the device's context to it."""
+    qk = make_qk(1, 2, 64, 64, 64, 0.3, seed=2, device=DEV)
+    g = torch.ones(1, 2, 64, device=DEV)
+    ws = sk.new_workspace(1 << 20, DEV)
+    rows = [torch.empty(1, 2, 64, device=DEV) for _ in range(3)]
+    grads = [torch.empty(1, 2, 64, 64, device=DEV) for _ in range(2)]
+    calls = [lambda: sk.kl_score_fwd(sk.Scores(), *qk, workspace=ws, out=rows),
+             lambda: sk.kl_score_bwd(1, sk.Scores(), g, *qk, *rows, workspace=ws, out=grads),
+             lambda: sk.kl_fwd(*qk, workspace=ws, out=rows)]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        failed = []
+
+        def work():
+            try:
+                call()
+            except Exception as e:
+                failed.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not failed, failed
 
 
 @gpu
