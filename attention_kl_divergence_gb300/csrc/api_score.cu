@@ -71,7 +71,10 @@ streamkl_status make_score(const streamkl_score* s, float scale, int causal, Sco
     const bool bias = s->slopes1 || s->slopes2;
     const bool bounded = capped(s->cap1) && capped(s->cap2) && out->side[0].lim <= kBoundedMax &&
                          out->side[1].lim <= kBoundedMax;
-    *mode = !bias && !capped(s->cap1) && !capped(s->cap2) ? kScorePlain : !bias && bounded ? kScoreBounded : kScoreGeneral;
+    *mode = bias                                        ? kScoreBias
+            : !capped(s->cap1) && !capped(s->cap2) ? kScorePlain
+            : bounded                              ? kScoreBounded
+                                                   : kScoreGeneral;
     return STREAMKL_OK;
 }
 
@@ -98,7 +101,7 @@ int tile_splits(int64_t units, int k_tiles, int sms) {
 
 struct ScoreFwdPlan {
     bool decode;
-    int heads_per_cta, num_splits, ctas, num_q_tiles, num_k_tiles, group;
+    int heads_per_cta, num_splits, ctas, num_q_tiles, num_k_tiles, group, sms;
     size_t ws_bytes;
 };
 
@@ -130,6 +133,7 @@ streamkl_status plan_score_fwd(const streamkl_shape* s, const streamkl_options* 
     pl->num_splits = splits;
     pl->ctas = static_cast<int>(units * splits);
     pl->group = order_group(BH, pl->num_q_tiles, sms);
+    pl->sms = sms;
     pl->ws_bytes = kStatusBytes;
     if (splits > 1) pl->ws_bytes += size_t(5) * splits * size_t(BH) * s->Nq * sizeof(float);
     return STREAMKL_OK;
@@ -244,6 +248,7 @@ streamkl_status streamkl_score_fwd(const streamkl_shape* shape, const streamkl_s
     p.kv_group = shape->H / kv_heads(shape);
     p.heads_per_cta = pl.heads_per_cta;
     p.order_group = pl.group;
+    p.take_over = pl.ctas > pl.sms ? 1 : 0;
     p.scale = mode == kScorePlain ? sc : kLn2;  // unit of the running state: raw products, or log2(e) S
     p.scale_log2e = sc * kLog2e;
     p.KL = KL;

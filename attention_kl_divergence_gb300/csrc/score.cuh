@@ -18,8 +18,9 @@ namespace streamkl {
 //   kScorePlain    no cap, no bias: x = c z, applied inside the exponent's FMA
 //   kScoreBounded  both sides capped, |x| <= kBoundedMax: sums of 2^x of any
 //                  length fit float32, so no running maximum is needed
-//   kScoreGeneral  any cap and bias, running maxima
-constexpr int kScorePlain = 0, kScoreBounded = 1, kScoreGeneral = 2;
+//   kScoreGeneral  any caps, no bias, running maxima
+//   kScoreBias     any caps and a bias, running maxima
+constexpr int kScorePlain = 0, kScoreBounded = 1, kScoreGeneral = 2, kScoreBias = 3;
 // 2^x with |x| <= 80: a sum of 2^31 of them is at most 2^111, times a score
 // difference (2^8) at most 2^119; the smallest one, 2^-80, is a normal number.
 constexpr float kBoundedMax = 80.f;
@@ -134,12 +135,14 @@ __device__ __forceinline__ void cap_mid(float (&z)[W], const ScoreSide& s) {
 }
 
 // z -> x in place for both sides, without the bias.  A warp takes the shortest
-// form that fits every score of its lanes.
+// form that fits every score of its lanes (those with `use`: the others' results
+// are not used).
 template <int MODE, int W>
-__device__ __forceinline__ void cap_scores(float (&z1)[W], float (&z2)[W], const ScoreSide& s1, const ScoreSide& s2) {
+__device__ __forceinline__ void cap_scores(float (&z1)[W], float (&z2)[W], const ScoreSide& s1, const ScoreSide& s2,
+                                           bool use = true) {
     if (MODE == kScorePlain) return;
-    const float top1 = abs_max(z1), top2 = abs_max(z2);
-    if (MODE == kScoreGeneral) {  // a side may have no cap
+    const float top1 = use ? abs_max(z1) : 0.f, top2 = use ? abs_max(z2) : 0.f;
+    if (MODE >= kScoreGeneral) {  // a side may have no cap
         if (s1.lim == 0.f) {
 #pragma unroll
             for (int e = 0; e < W; ++e) z1[e] *= s1.c;

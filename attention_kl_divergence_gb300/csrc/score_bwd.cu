@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             }
             cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
             float sl1 = 0.f, sl2 = 0.f, d0 = 0.f;
-            if (MODE == kScoreGeneral) {
+            if (MODE == kScoreBias) {
                 const int h = qhead(m);
                 if (sp.side[0].slopes) sl1 = -kLog2e * sp.side[0].slopes[h];
                 if (sp.side[1].slopes) sl2 = -kLog2e * sp.side[1].slopes[h];
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                         d = dscore2<SETTING>(u1, u2, cc, sc2, nla, nxb, gs);
                     } else {
                         float2 x1 = u1, x2 = u2;
-                        if (MODE == kScoreGeneral) {
+                        if (MODE == kScoreBias) {
                             const float2 away = make_float2(fabsf(d0 + static_cast<float>(e)),
                                                             fabsf(d0 + static_cast<float>(e + 1)));
                             x1 = __ffma2_rn(away, splat(sl1), x1);
@@ -757,7 +757,8 @@ cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* ma
     if (e != cudaSuccess) return e;
     e = mode == kScorePlain     ? launch_mode<kScorePlain>(d, setting, maps, p, sp, ctas, stream)
         : mode == kScoreBounded ? launch_mode<kScoreBounded>(d, setting, maps, p, sp, ctas, stream)
-                                : launch_mode<kScoreGeneral>(d, setting, maps, p, sp, ctas, stream);
+        : mode == kScoreGeneral ? launch_mode<kScoreGeneral>(d, setting, maps, p, sp, ctas, stream)
+                                : launch_mode<kScoreBias>(d, setting, maps, p, sp, ctas, stream);
     const bool parts = p.num_splits > 1;
     if (e != cudaSuccess || !(parts || p.grad_bf16)) return e;
     const size_t nq8 = p.grad_bf16 ? static_cast<size_t>(p.B) * p.H * p.Nq * d / 8 : 0;

@@ -19,14 +19,15 @@ namespace {
 
 constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 stale
 // Update warpgroups of the tile kernel, each taking its share of a tile's columns.
-#ifndef SFP
-#define SFP 2
-#define SFB 4
-#define SFG 4
-#endif
-constexpr int sf_groups(int mode) { return mode == kScorePlain ? SFP : mode == kScoreBounded ? SFB : SFG; }
+// The cap's polynomial makes the update the slowest part, and its dependent steps
+// need more warps to overlap (8K causal, 32 heads: 2 groups 985 us, 4 765); the
+// plain update does better with the registers of 2 (documents of 8K: 197 against
+// 206 us).
+constexpr int sf_groups(int mode) { return mode == kScorePlain ? 2 : 4; }
 // warp 0 work items and copies, warp 1 the S1 MMAs, the update warpgroups, and a last warp for the S2 MMAs
 constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 32; }
+constexpr int kSfAhead = 4;  // key tiles between a tile's fetch into L2 and its copy into shared memory
+constexpr int kSfLead = 4;   // key tiles left to issue when the next work item is asked for
 constexpr uint64_t kSfDrainNs = 200000000ull;  // in-flight copies and MMAs retire before a CTA exits
 
 // A 128-row query tile of one head, and a share of its key tiles.
@@ -73,11 +74,26 @@ __device__ __noinline__ bool score_drain(uint32_t bar, uint32_t parity, uint64_t
     return true;
 }
 
-// x -= slope |distance| for columns at distance d0, d0 - 1, ...
+// The bias -slope |d0 - e| of column e.  Of a chunk that lies wholly before the
+// warp's rows (where > 0) or behind them (where < 0) it is linear in e; its part
+// without e is returned, for update_scored to add to the running maximum instead
+// of to every score.
 template <int W>
-__device__ __forceinline__ void add_bias(float (&x)[W], float slope, float d0) {
+__device__ __forceinline__ float add_bias(float (&x)[W], float slope, float d0, int where) {
+    if (where == 0) {
 #pragma unroll
-    for (int e = 0; e < W; ++e) x[e] = fmaf(-slope, fabsf(d0 - static_cast<float>(e)), x[e]);
+        for (int e = 0; e < W; ++e) x[e] = fmaf(-slope, fabsf(d0 - static_cast<float>(e)), x[e]);
+        return 0.f;
+    }
+    const float s = where > 0 ? slope : -slope;
+#pragma unroll
+    for (int e = 0; e < W; e += 2) {
+        const float2 v = __ffma2_rn(splat(s), make_float2(static_cast<float>(e), static_cast<float>(e + 1)),
+                                    make_float2(x[e], x[e + 1]));
+        x[e] = v.x;
+        x[e + 1] = v.y;
+    }
+    return -s * d0;
 }
 
 // Hidden products become 0: whatever they were (NaN, infinities) has no effect,
@@ -90,10 +106,15 @@ __device__ __forceinline__ void hide(float (&z)[W], int first, int last) {
 }
 
 // Online update with columns [first, last] visible (the hidden ones finite).
-// c = 1 when z holds x.
-template <bool MASKED, bool BOUNDED, int W>
+// c = 1 when z holds x; the scores are z + base1 and z + base2 (kScoreBias).
+template <int MODE, bool MASKED, int W>
 __device__ __forceinline__ void update_scored(const float (&z1)[W], const float (&z2)[W], int first, int last,
-                                              RowState& st, float c, float tau) {
+                                              RowState& st, float c, float tau, float base1, float base2) {
+    constexpr bool BOUNDED = MODE == kScoreBounded;
+    if (MODE == kScoreBias) {
+        st.m1 -= base1;
+        st.m2 -= base2;
+    }
     float2 s1[2] = {splat(0.f), splat(0.f)}, s2[2] = {splat(0.f), splat(0.f)}, sa[2] = {splat(0.f), splat(0.f)};
     const float2 neg = splat(-1.f);
     if (BOUNDED) {
@@ -145,9 +166,15 @@ __device__ __forceinline__ void update_scored(const float (&z1)[W], const float 
         s2[k] = __fadd2_rn(s2[k], p2);
         sa[k] = __ffma2_rn(p1, df, sa[k]);
     }
-    st.l1 += (s1[0].x + s1[0].y) + (s1[1].x + s1[1].y);
+    const float sum = (s1[0].x + s1[0].y) + (s1[1].x + s1[1].y);
+    st.l1 += sum;
     st.l2 += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
     st.acc += (sa[0].x + sa[0].y) + (sa[1].x + sa[1].y);
+    if (MODE == kScoreBias) {
+        st.acc = fmaf(sum, base1 - base2, st.acc);
+        st.m1 += base1;
+        st.m2 += base2;
+    }
 }
 
 __device__ __forceinline__ void store_scored(const FwdParams& p, size_t row, int split, const RowState& st, bool empty,
@@ -187,8 +214,8 @@ __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_s
 //                (only tiles inside it are visited) and issues the copies
 //   warp 1, last S1 and S2 MMAs (warp 1 owns TMEM)
 //   the others   the update, one query row per thread
-// Rings (key tiles, score buffers) run on through the items.  8192 keys in 8 heads
-// of documents of 1000 to 2000 tokens: one item per CTA 258 us, as here @DOCS us.
+// Rings (key tiles, score buffers) run on through the items.  8192 tokens, 32
+// heads, documents of a few hundred to 3000 tokens: one item per CTA 258 us, as here 197 us.
 // ---------------------------------------------------------------------------
 template <int D, int NST, int MODE>
 __global__ void __launch_bounds__(sf_threads(MODE), 1)
@@ -258,11 +285,17 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         int4 at = place(unit);
         int2 rr[4];
         row_ranges(at, rr);
-        bool pending = true, ok = true;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(base + L::bar_clc, 16);
-            clc_request(base + L::clc, base + L::bar_clc);
-        }
+        bool pending = false, ok = true;
+        // One request at a time, made when the copies of all but an item's last kSfLead key
+        // tiles are issued: early enough for the next item's start to hide behind those tiles,
+        // late enough to leave the items to CTAs that end sooner.
+        auto request = [&] {
+            pending = true;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(base + L::bar_clc, 16);
+                clc_request(base + L::clc + 16 * (requests & 1), base + L::bar_clc);
+            }
+        };
         for (int k = 0;; ++k) {
             const int slot = k & 1;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * slot, ((k >> 1) & 1) ^ 1, wc, kErrWaitOther))))
@@ -301,10 +334,18 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         tma_load_4d_hint(k1s + c * kBlockK * 128, &tK1, fb, c * kSwizzleCols, k0, hk, b, keep);
                         tma_load_4d_hint(k2s + c * kBlockK * 128, &tK2, fb, c * kSwizzleCols, k0, hk, b, keep);
                     }
+                    // the ring is shorter than HBM's latency: a tile is fetched into L2 some tiles earlier
+                    if (t + kSfAhead < n_tiles) {
+#pragma unroll
+                        for (int c = 0; c < D / kSwizzleCols; ++c) {
+                            tma_prefetch_4d(&tK1, c * kSwizzleCols, k0 + kSfAhead * kBlockK, hk, b);
+                            tma_prefetch_4d(&tK2, c * kSwizzleCols, k0 + kSfAhead * kBlockK, hk, b);
+                        }
+                    }
                 }
                 return true;
             };
-            const int head = min(n_tiles, NST);
+            const int early = max(0, n_tiles - kSfLead);  // tiles issued before the next item is asked for
             if (lane == 0 && n_tiles > 0) {
                 // the previous item's last MMAs have read its query tiles
                 ok = mbar_wait(base + L::bar_qempty, (n_q & 1) ^ 1, wc, kErrWaitQ);
@@ -316,28 +357,34 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         tma_load_4d(base + L::q2 + c * kBlockQ * 128, &tQ2, base + L::bar_q, c * kSwizzleCols, q0, h, b);
                     }
                     ++n_q;
-                    ok = load_keys(0, head);
+                    ok = load_keys(0, early);
                 }
             }
             if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
-            // the next item, while this one's tiles are under way
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, requests & 1, wc, kErrWaitOther)))) break;
-            pending = false;
-            unit = clc_response(base + L::clc + 16 * (requests & 1));
-            ++requests;
-            fence_proxy_async_smem();  // the response is read before the slot's next one is written
-            __syncwarp();
+            if (p.take_over) request();
+            if (lane == 0 && n_tiles > 0) ok = load_keys(early, n_tiles);
+            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+            unit = -1;
+            if (p.take_over) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, requests & 1, wc, kErrWaitOther)))) break;
+                pending = false;
+                unit = clc_response(base + L::clc + 16 * (requests & 1));
+                ++requests;
+                fence_proxy_async_smem();  // the response is read before its slot is written again
+                __syncwarp();
+            }
             if (unit >= 0) {
-                pending = true;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(base + L::bar_clc, 16);
-                    clc_request(base + L::clc + 16 * (requests & 1), base + L::bar_clc);
-                }
                 at = place(unit);
+                if (lane == 0) {  // its query tiles on their way while the current item ends
+                    const int pb = at.w, ph = at.x - pb * p.H;
+#pragma unroll
+                    for (int c = 0; c < D / kSwizzleCols; ++c) {
+                        tma_prefetch_4d(&tQ1, c * kSwizzleCols, at.y, ph, pb);
+                        tma_prefetch_4d(&tQ2, c * kSwizzleCols, at.y, ph, pb);
+                    }
+                }
                 row_ranges(at, rr);
             }
-            if (lane == 0 && n_tiles > head) ok = load_keys(head, n_tiles);
-            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
         }
         if (lane == 0) {  // every issued copy has landed, every stage was released
             if (pending) score_drain(base + L::bar_clc, requests & 1, kSfDrainNs);
@@ -429,7 +476,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             const int whole_hi = __reduce_min_sync(0xffffffffu, range.y);
             int64_t pos = 0;
             float sl1 = 0.f, sl2 = 0.f;
-            if (MODE == kScoreGeneral && live) {
+            if (MODE == kScoreBias && live) {
                 const int h = bh - b * p.H;
                 pos = row_position(sp, p.Nq, p.Nk, b, i);
                 if (sp.side[0].slopes) sl1 = sp.side[0].slopes[h] * kLog2e;
@@ -451,7 +498,6 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                     const int c0 = j0 + ch * 32;  // the chunk's first key
                     const bool any = c0 < warp_hi && c0 + 32 > warp_lo;
                     const bool whole = c0 >= whole_lo && c0 + 32 <= whole_hi;
-                    const int first = range.x - c0, last = range.y - 1 - c0;  // columns that the row sees
                     if (!any) {
                         if (cc == kChunks - 1) {
                             tc_fence_before();
@@ -467,20 +513,33 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         tc_fence_before();
                         mbar_arrive(base + L::bar_sempty + 8 * buf);
                     }
+                    const int first = range.x - c0, last = range.y - 1 - c0;  // columns that the row sees
+                    bool masked = false, take = true;
                     if (!whole) {
-                        hide(z1, first, last);
-                        hide(z2, first, last);
+                        // Rows of two documents in one warp: each sees all of most chunks or nothing
+                        // of them, which needs no mask, only the rows that take part.
+                        take = first <= 0 && last >= 31;
+                        const bool none = first > 31 || last < 0 || range.x >= range.y;
+                        masked = !__all_sync(0xffffffffu, take || none);
+                        if (masked) {
+                            hide(z1, first, last);
+                            hide(z2, first, last);
+                            take = true;
+                        }
                     }
-                    cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1]);
-                    if (MODE == kScoreGeneral) {
-                        const float d0 = static_cast<float>(pos - c0);
-                        if (sl1 != 0.f) add_bias(z1, sl1, d0);
-                        if (sl2 != 0.f) add_bias(z2, sl2, d0);
+                    cap_scores<MODE>(z1, z2, sp.side[0], sp.side[1], take);
+                    float base1 = 0.f, base2 = 0.f;
+                    if (MODE == kScoreBias) {
+                        const int64_t away = pos - c0;  // distance of the chunk's first key
+                        const int where = away - lane >= 31 ? 1 : away - lane + 31 <= 0 ? -1 : 0;
+                        const float d0 = static_cast<float>(away);
+                        if (sl1 != 0.f) base1 = add_bias(z1, sl1, d0, where);
+                        if (sl2 != 0.f) base2 = add_bias(z2, sl2, d0, where);
                     }
-                    if (whole)
-                        update_scored<false, MODE == kScoreBounded>(z1, z2, 0, 31, st, c, tau);
-                    else
-                        update_scored<true, MODE == kScoreBounded>(z1, z2, first, last, st, c, tau);
+                    if (masked)
+                        update_scored<MODE, true>(z1, z2, first, last, st, c, tau, base1, base2);
+                    else if (take)
+                        update_scored<MODE, false>(z1, z2, 0, 31, st, c, tau, base1, base2);
                 }
             }
             // the groups' states of a row; two buffers, so that one barrier per item keeps them apart
@@ -578,8 +637,8 @@ __global__ void __launch_bounds__(192, 1)
         if (r.x < r.y) lo = r.x, hi = r.y;
         full_lo = r.x, full_hi = r.y;
         if (warp == 0) {
-            const float a1 = MODE == kScoreGeneral && sp.side[0].slopes ? sp.side[0].slopes[h] * kLog2e : 0.f;
-            const float a2 = MODE == kScoreGeneral && sp.side[1].slopes ? sp.side[1].slopes[h] * kLog2e : 0.f;
+            const float a1 = MODE == kScoreBias && sp.side[0].slopes ? sp.side[0].slopes[h] * kLog2e : 0.f;
+            const float a2 = MODE == kScoreBias && sp.side[1].slopes ? sp.side[1].slopes[h] * kLog2e : 0.f;
             cols[lane] = make_int4(r.x, r.y, __float_as_int(a1), __float_as_int(a2));
             at[lane] = row_position(sp, p.Nq, p.Nk, b, i);
         }
@@ -739,7 +798,7 @@ __global__ void __launch_bounds__(192, 1)
             for (int q = 0; q < NQ; ++q) {
                 if (q < nq) {
                     float x1 = z1[q], x2 = z2[q];
-                    if (MODE == kScoreGeneral) {
+                    if (MODE == kScoreBias) {
                         const float dist = fabsf(static_cast<float>(at[q] - j));
                         x1 = fmaf(-__int_as_float(cols[q].z), dist, x1);
                         x2 = fmaf(-__int_as_float(cols[q].w), dist, x2);
@@ -873,7 +932,8 @@ cudaError_t launch_score_fwd(int d, int mode, bool decode, const CUtensorMap* ma
                              const ScoreParams& sp, int ctas, cudaStream_t stream) {
     cudaError_t e = mode == kScorePlain     ? launch_mode<kScorePlain>(d, decode, maps, p, sp, ctas, stream)
                     : mode == kScoreBounded ? launch_mode<kScoreBounded>(d, decode, maps, p, sp, ctas, stream)
-                                            : launch_mode<kScoreGeneral>(d, decode, maps, p, sp, ctas, stream);
+                    : mode == kScoreGeneral ? launch_mode<kScoreGeneral>(d, decode, maps, p, sp, ctas, stream)
+                                            : launch_mode<kScoreBias>(d, decode, maps, p, sp, ctas, stream);
     if (e != cudaSuccess || p.num_splits == 1) return e;
     const int64_t rows = int64_t(p.B) * p.H * p.Nq;
     score_combine_kernel<<<static_cast<unsigned>((rows + 127) / 128), 128, 0, stream>>>(
