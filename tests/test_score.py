@@ -8,7 +8,8 @@ A = max scale |q|.|k| and M = max |S| that is  del = (d + 32) 2^-24 A + 2^-20 M.
 LSE is off by at most del + a rounding; KL = E[S1 - S2] + LSE2 - LSE1 by
 del (4 + 4 max |S1 - S2|) (each P is off by a factor 1 +- 2 del).  dS is off by
 g (P1 + P2) 4 del (setting 1) or g P1 6 del (1 + |ratio - KL|) (setting 2) and
-enters the gradient products as two bf16 terms (2^-16 of it); the products
+enters the gradient products as two bf16 terms (2^-16 of it) for float32
+gradients and as one (rounded: 2^-8 of it) for bf16 gradients; the products
 accumulate in float32 ((N + 128) 2^-24 of the sum of magnitudes).  bf16 outputs
 add 2^-8 of the value.
 """
@@ -76,8 +77,8 @@ class Ref:
         self.delta = (Q1.shape[3] + 32) * 2.0 ** -24 * A + 2.0 ** -20 * max(m(s1), m(s2))
         self.spread = m(s1 - s2)
 
-    def grads(self, setting, g):
-        """(dQ, dK) and the bounds of their errors in float32."""
+    def grads(self, setting, g, dtype=torch.float32):
+        """(dQ, dK) and the bounds of their errors before the output's rounding."""
         Q1, K1, Q2, K2 = self.qk
         B, H, Nq, d = Q1.shape
         Hk, Nk = K1.shape[1], K1.shape[2]
@@ -88,7 +89,7 @@ class Ref:
         else:
             dz, err, f, Q, K = g * self.p1 * dev, g.abs() * self.p1 * (1 + dev.abs()) * 6 * self.delta, self.f1, Q1, K1
         dz = dz * f * self.scale
-        err = err * self.scale + dz.abs() * (2.0 ** -16 + 2.0 ** -18)
+        err = err * self.scale + dz.abs() * (2.0 ** -16 + 2.0 ** -18 if dtype == torch.float32 else 2.0 ** -8)
         kx = K.repeat_interleave(H // Hk, 1)
         back = lambda t, q: (t.transpose(2, 3) @ q).reshape(B, Hk, H // Hk, Nk, d).sum(2)  # noqa: E731
         acc = 2.0 ** -24 * (max(Nk, Nq * (H // Hk)) + 128)
@@ -106,7 +107,7 @@ class Ref:
         assert bool((err <= self.delta * (4 + 4 * self.spread)).all()), (float(err.max()), self.delta)
 
     def check_grads(self, setting, g, dQ, dK):
-        for name, got, want, tol in zip(("dQ", "dK"), (dQ, dK), *self.grads(setting, g)):
+        for name, got, want, tol in zip(("dQ", "dK"), (dQ, dK), *self.grads(setting, g, dQ.dtype)):
             if got.dtype == BF16:
                 tol = tol + 2.0 ** -8 * want.abs()
             err = (got.double() - want).abs()
@@ -369,7 +370,7 @@ def test_autograd_function_settings():
     ref.check_grads(1, g, *grads[2:])
     student = [qk[0], qk[1], leaves[2], qk[3]]
     (dQ,) = torch.autograd.grad(sk.ScoredAttentionKL.apply(*student, sc).sum(), leaves[2])  # a broadcast upstream gradient
-    (want, _), (tol, _) = ref.grads(1, torch.ones_like(g))
+    (want, _), (tol, _) = ref.grads(1, torch.ones_like(g), BF16)
     assert bool(((dQ.double() - want).abs() <= tol + 2.0 ** -8 * want.abs()).all())
     with pytest.raises(ValueError):
         sk.ScoredAttentionKL.apply(*leaves, sk.Scores(slopes1=torch.ones(4, device=DEV, requires_grad=True)))
