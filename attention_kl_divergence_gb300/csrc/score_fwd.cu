@@ -110,11 +110,7 @@ __device__ __forceinline__ void hide(float (&z)[W], int first, int last) {
 template <int MODE, bool MASKED, int W>
 __device__ __forceinline__ void update_scored(const float (&z1)[W], const float (&z2)[W], int first, int last,
                                               RowState& st, float c, float tau, float base1, float base2) {
-    constexpr bool BOUNDED = MODE == kScoreBounded;
-    if (MODE == kScoreBias) {
-        st.m1 -= base1;
-        st.m2 -= base2;
-    }
+    constexpr bool BOUNDED = MODE == kScoreBounded, BIAS = MODE == kScoreBias;
     float2 s1[2] = {splat(0.f), splat(0.f)}, s2[2] = {splat(0.f), splat(0.f)}, sa[2] = {splat(0.f), splat(0.f)};
     const float2 neg = splat(-1.f);
     if (BOUNDED) {
@@ -135,7 +131,7 @@ __device__ __forceinline__ void update_scored(const float (&z1)[W], const float 
             a2 = max3f(a2, v2[0], v2[1]);
             b2 = max3f(b2, v2[2], v2[3]);
         }
-        const float cm1 = fmaxf(a1, b1), cm2 = fmaxf(a2, b2);
+        const float cm1 = fmaxf(a1, b1) + (BIAS ? base1 : 0.f), cm2 = fmaxf(a2, b2) + (BIAS ? base2 : 0.f);
         if (cm1 > st.m1 + tau) {
             const float a = ex2(c * (st.m1 - cm1));  // 0 on the first visible chunk (m1 = -inf)
             st.l1 *= a;
@@ -148,7 +144,11 @@ __device__ __forceinline__ void update_scored(const float (&z1)[W], const float 
         }
     }
     // a row that has seen no key yet keeps m = -inf: a reference of 0 makes its masked terms 2^-inf = 0
-    const float r1 = MASKED && st.m1 == -INFINITY ? 0.f : st.m1, r2 = MASKED && st.m2 == -INFINITY ? 0.f : st.m2;
+    float r1 = MASKED && st.m1 == -INFINITY ? 0.f : st.m1, r2 = MASKED && st.m2 == -INFINITY ? 0.f : st.m2;
+    if (BIAS) {  // relative to the base; the running maximum itself stays as it is, so that a far base costs it no bits
+        r1 -= base1;
+        r2 -= base2;
+    }
     const float2 cc = splat(c), n1 = splat(-c * r1), n2 = splat(-c * r2);
 #pragma unroll
     for (int e = 0; e < W; e += 2) {
@@ -170,11 +170,7 @@ __device__ __forceinline__ void update_scored(const float (&z1)[W], const float 
     st.l1 += sum;
     st.l2 += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
     st.acc += (sa[0].x + sa[0].y) + (sa[1].x + sa[1].y);
-    if (MODE == kScoreBias) {
-        st.acc = fmaf(sum, base1 - base2, st.acc);
-        st.m1 += base1;
-        st.m2 += base2;
-    }
+    if (BIAS) st.acc = fmaf(sum, base1 - base2, st.acc);
 }
 
 __device__ __forceinline__ void store_scored(const FwdParams& p, size_t row, int split, const RowState& st, bool empty,

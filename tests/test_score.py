@@ -5,6 +5,8 @@ Tolerances, from the arithmetic.  A product z is a float32 sum of d exact
 products, in any order off by at most d 2^-24 of the sum of their magnitudes; a
 score adds a polynomial's 2^-23 and a few roundings of |S|.  With
 A = max scale |q|.|k| and M = max |S| that is  del = (d + 32) 2^-24 A + 2^-20 M.
+A key's error counts by its probability: for the rows' outputs M is the largest
+sum over a row of P |S| (a bias makes far scores large and their P nothing).
 LSE is off by at most del + a rounding; KL = E[S1 - S2] + LSE2 - LSE1 by
 del (4 + 4 max |S1 - S2|) (each P is off by a factor 1 +- 2 del).  dS is off by
 g (P1 + P2) 4 del (setting 1) or g P1 6 del (1 + |ratio - KL|) (setting 2) and
@@ -76,6 +78,10 @@ class Ref:
         A = max(m(q.abs() @ k.abs().repeat_interleave(G, 1).transpose(2, 3)) for q, k in ((Q1, K1), (Q2, K2))) * self.scale
         self.delta = (Q1.shape[3] + 32) * 2.0 ** -24 * A + 2.0 ** -20 * max(m(s1), m(s2))
         self.spread = m(s1 - s2)
+        near = max(float((p * s.abs()).masked_fill(~self.vis, 0.0).sum(-1).max()) for p, s in ((self.p1, s1), (self.p2, s2)))
+        weighted = float((self.p1 * (s1 - s2).abs()).masked_fill(~self.vis, 0.0).sum(-1).max())
+        self.delta_row = (Q1.shape[3] + 32) * 2.0 ** -24 * A + 2.0 ** -20 * near
+        self.spread_row = weighted
 
     def grads(self, setting, g, dtype=torch.float32):
         """(dQ, dK) and the bounds of their errors before the output's rounding."""
@@ -101,10 +107,12 @@ class Ref:
             got = got.double()
             assert torch.equal(got == -math.inf, ~self.live)
             err = (got - want)[self.live].abs()
-            assert bool((err <= self.delta + 2.0 ** -23 * want[self.live].abs()).all()), float(err.max())
+            assert bool((err <= self.delta_row + 2.0 ** -23 * want[self.live].abs()).all()), float(err.max())
         err = (KL.double() - self.KL).abs()
         assert bool((KL[~self.live] == 0).all())
-        assert bool((err <= self.delta * (4 + 4 * self.spread)).all()), (float(err.max()), self.delta)
+        # dKL = sum P1 (dS1 (ratio - KL) + dS1 - dS2) + dLSE: the spread counts by P1 too
+        bound = self.delta_row * (4 + 4 * self.spread_row)
+        assert bool((err <= bound).all()), (float(err.max()), bound)
 
     def check_grads(self, setting, g, dQ, dK):
         for name, got, want, tol in zip(("dQ", "dK"), (dQ, dK), *self.grads(setting, g, dQ.dtype)):
@@ -190,6 +198,16 @@ SCORES = {
 def test_forward_and_gradients(problem, kind):
     B, H, Hk, Nq, Nk, d, mask = PROBLEMS[problem]
     run_case(B, H, Hk, Nq, Nk, d, mask, seed=Nq + Nk, **SCORES[kind])
+
+
+@gpu
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_far_keys_cost_a_biased_row_no_precision(d, mask):
+    """Steep and shallow slopes over a long row: scores of far keys reach -3000."""
+    make = {"causal": CAUSAL, "full": FULL, "prefix": ranges(prefix=[1300])}[mask]
+    run_case(1, 4, 2, 2100, 2100, d, make, bias=True, seed=5, settings=(1,), peak=1.6)
+    run_case(1, 4, 2, 3, 2500, d, FULL if mask == "full" else CAUSAL, bias=True, seed=6, settings=(2,), cap1=30.0)
 
 
 @gpu
