@@ -468,6 +468,19 @@ def _on(device, function, *args):
         return function(*args, torch.cuda.current_stream(device).cuda_stream)
 
 
+def _guard_capture(*inputs):
+    """Refuse to record a graph in a CUDA-graph capture on leaves that an earlier, still living eager graph uses: the
+    leaves' gradient accumulators belong to that graph's stream, and running them inside the capture breaks it (at
+    worst the process ends).  Eager calls mark the accumulators; the marks die with the graphs."""
+    for t in inputs:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad and t.grad_fn is None:
+            stream = _raw_stream(t.device.index)
+            made_on = torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault("streamkl stream", stream)
+            if made_on != stream and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("an eager autograd graph of these leaves, made on another stream, is still alive: "
+                                   "drop it (or make it on the capturing stream) before the capture")
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -629,6 +642,7 @@ class ScoredAttentionKL(torch.autograd.Function):
     def forward(ctx, Q1, K1, Q2, K2, scores, causal=False, scale=None):
         if any(t is not None and t.requires_grad for t in _scores(scores).tensors()):
             raise ValueError("the tensors of scores are constants: they get no gradient")
+        _guard_capture(Q1, K1, Q2, K2)
         KL, L1, L2 = kl_score_fwd(scores, Q1, K1, Q2, K2, causal=causal, scale=scale)
         ctx.save_for_backward(Q1, K1, Q2, K2, KL, L1, L2, *scores.tensors())
         ctx.caps, ctx.causal, ctx.scale = (scores.cap1, scores.cap2), causal, scale
@@ -787,6 +801,7 @@ class QKNormRope(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False):
+        _guard_capture(q, k, wq, wk)
         ctx.save_for_backward(q, k, wq, wk, table, positions)
         ctx.how = dict(start=start, eps=eps, interleaved=interleaved)
         return qk_norm_rope(q, k, wq, wk, table, positions, **ctx.how)
