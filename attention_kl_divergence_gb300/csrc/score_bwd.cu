@@ -791,7 +791,7 @@ cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* ma
     if (e != cudaSuccess || !(parts || p.grad_bf16)) return e;
     const size_t nq8 = p.grad_bf16 ? static_cast<size_t>(p.B) * p.H * p.Nq * d / 8 : 0;
     const size_t nk8 = parts ? static_cast<size_t>(p.B) * p.H_kv * p.Nk * d / 8 : 0;
-    const size_t blocks = std::min<size_t>((nq8 + nk8 + 255) / 256, static_cast<size_t>(sms) * 8);
+    const size_t blocks = std::min<size_t>((nq8 + nk8 + 255) / 256, static_cast<size_t>(sms) * 16);
     score_finish_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
         reinterpret_cast<const float4*>(p.dQacc), static_cast<uint4*>(p.dQ), nq8,
         reinterpret_cast<const float4*>(sp.dk_parts), p.dK, nk8, p.num_splits, p.grad_bf16 != 0);
