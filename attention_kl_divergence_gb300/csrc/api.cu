@@ -255,7 +255,7 @@ streamkl_status plan_bwd(const streamkl_shape* s, int setting, int causal, const
 
 extern "C" {
 
-int streamkl_version(void) { return 200; }  // 0.2.0: joint backward, size queries, allocation-free status
+int streamkl_version(void) { return 300; }  // 0.3.0: score-modified divergence, norm with rotation
 
 const char* streamkl_status_string(streamkl_status s) {
     switch (s) {

@@ -225,6 +225,34 @@ def test_split_counts(Nq, splits):
 
 
 @gpu
+@pytest.mark.parametrize("splits", [0, 5])
+@pytest.mark.parametrize("kind", ["plain", "capped", "bias"])
+def test_more_work_items_than_ctas_that_fit(kind, splits):
+    """CTAs that take over the items of CTAs not started, most of them empty or short."""
+    run_case(2, 32, 8, 300, 400, 64, random_ranges, seed=splits, num_splits=splits, settings=(1,), **SCORES[kind])
+    lengths = [(37 * b) % 131 for b in range(24)]
+    run_case(24, 16, 4, 130, 130, 64, ranges(q_lengths=lengths, k_lengths=lengths), num_splits=splits, settings=(2,), **SCORES[kind])
+
+
+@gpu
+def test_many_items_replay_from_a_graph_and_run_beside_another_stream():
+    qk = make_qk(4, 32, 256, 256, 64, 0.3, seed=9, device=DEV, H_kv=8)
+    begin, end, _ = ranges(docs=[0, 100, 256])(4, 256, 256)
+    sc = sk.Scores(50.0, 50.0, begin=begin, end=end)
+    want = sk.kl_score_fwd(sc, *qk)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = sk.kl_score_fwd(sc, *qk)
+    for _ in range(3):
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = sk.kl_score_fwd(sc, *qk)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, other))
+
+
+@gpu
 @pytest.mark.parametrize("grad_dtype", [torch.float32, BF16])
 @pytest.mark.parametrize("splits", [1, 3, 16, 64])
 def test_backward_split_counts(splits, grad_dtype):
@@ -251,6 +279,20 @@ def test_agrees_with_the_unmodified_divergence():
         for x, y in zip(sk.kl_bwd(setting, g, Q1, K1, Q2, K2, *a, causal=True),
                         sk.kl_score_bwd(setting, sk.Scores(), g, Q1, K1, Q2, K2, *b, causal=True)):
             assert float((x - y).abs().max()) <= 1e-3 * float(x.abs().max())
+
+
+@gpu
+def test_agrees_with_the_unmodified_divergence_over_a_long_sequence():
+    """20000 keys, shared by two query heads: windows of the whole length are the causal mask."""
+    N = 20000
+    qk = make_qk(1, 4, N, N, 128, 0.3, seed=12, device=DEV, H_kv=2)
+    begin, end, _ = sk.key_ranges(1, N, N, DEV, window=N)
+    a, b = sk.kl_fwd(*qk, causal=True), sk.kl_score_fwd(sk.Scores(begin=begin, end=end), *qk)
+    for x, y in zip(a, b):
+        assert float((x - y).abs().max()) <= 1e-4
+    g = torch.rand(1, 4, N, device=DEV) / N
+    for x, y in zip(sk.kl_bwd(1, g, *qk, *a, causal=True), sk.kl_score_bwd(1, sk.Scores(begin=begin, end=end), g, *qk, *b)):
+        assert float((x - y).norm()) <= 1e-4 * float(x.norm())
 
 
 @gpu
@@ -454,10 +496,11 @@ def test_replays_from_a_graph_on_another_stream():
 
 
 @gpu
-@pytest.mark.parametrize("Nq", [8, 300])
-def test_bounded_waits_give_up_and_are_reported(Nq):
-    """Test aid: the first CTA waits on a barrier that nothing arrives on, for 20 ms."""
-    qk = make_qk(1, 2, Nq, 300, 128, 0.3, seed=5, device=DEV)
+@pytest.mark.parametrize("H,Nq", [(2, 8), (2, 300), (128, 300)])
+def test_bounded_waits_give_up_and_are_reported(H, Nq):
+    """Test aid: the first CTA waits on a barrier that nothing arrives on, for 20 ms.  128 heads: more work items than
+    fit at a time, which the other CTAs take over."""
+    qk = make_qk(1, H, Nq, 300, 128, 0.3, seed=5, device=DEV)
     sc = sk.Scores(50.0, 50.0)
     ws = sk.new_workspace(max(sk.score_fwd_plan(qk[0], qk[1]).workspace_bytes,
                               sk.score_bwd_plan(qk[0], qk[1], 1).workspace_bytes), DEV)
@@ -465,7 +508,7 @@ def test_bounded_waits_give_up_and_are_reported(Nq):
     assert sk.workspace_status(ws) != 0 and bool(torch.isnan(rows[0]).any())
     rows = sk.kl_score_fwd(sc, *qk, workspace=ws)
     assert sk.workspace_status(ws) == 0 and bool(torch.isfinite(rows[0]).all())
-    g = torch.rand(1, 2, Nq, device=DEV)
+    g = torch.rand(1, H, Nq, device=DEV)
     sk.kl_score_bwd(1, sc, g, *qk, *rows, workspace=ws, wait_limit_ns=20_000_000, debug_flags=sk.DEBUG_INJECT_STALL)
     assert sk.workspace_status(ws) != 0
     want = sk.kl_score_bwd(1, sc, g, *qk, *rows)
