@@ -149,14 +149,14 @@ struct ScoreBwdPlan {
 // group).  Without them few key tiles leave SMs idle, and the tile with the most
 // rows sets the time.  In units of an iteration, for a causal mask: a launch of u
 // tiles with up to n iterations each takes about the larger of the SMs' average
-// and the longest CTA, a CTA costs about 3 more (start, key tiles, dK), and
-// summing the parts about 4.  Splits are taken when they save a fifth: 64 CTAs of
-// up to 128 iterations (2 x 2 key heads, 4 query heads each, 2048 keys) 297 -> 98
-// us with 5, while at 512 CTAs of 512 the estimate stays with 1.
+// and the longest CTA, a CTA costs about 5 more (start, key tiles, dK), and
+// summing the parts about 4.  Splits are taken when they save a fifth.  Measured
+// (us): 64 key tiles of up to 128 iterations, 1 split 277, 3 112, 4 90, 5 96,
+// 8 107; 114 of up to 38, 1 78, 2 48, 3 56; 192 of up to 16, 1 37, 2 41.
 int bwd_splits(int64_t units, int64_t iterations, int sms) {
     auto cost = [&](int64_t s) {
-        const double mean = (units * iterations * 0.5 + double(units) * s * 3) / sms;
-        const double longest = double((iterations + s - 1) / s) + 3;
+        const double mean = (units * iterations * 0.5 + double(units) * s * 5) / sms;
+        const double longest = double((iterations + s - 1) / s) + 5;
         return std::max(mean, longest) + (s > 1 ? 4 : 0);
     };
     int best = 1;
