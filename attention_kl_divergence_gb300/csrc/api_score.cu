@@ -248,7 +248,7 @@ streamkl_status streamkl_score_fwd(const streamkl_shape* shape, const streamkl_s
     p.kv_group = shape->H / kv_heads(shape);
     p.heads_per_cta = pl.heads_per_cta;
     p.order_group = pl.group;
-    p.take_over = pl.ctas > pl.sms ? 1 : 0;
+    p.take_over = pl.ctas > pl.sms ? pl.sms : 0;
     p.scale = mode == kScorePlain ? sc : kLn2;  // unit of the running state: raw products, or log2(e) S
     p.scale_log2e = sc * kLog2e;
     p.KL = KL;

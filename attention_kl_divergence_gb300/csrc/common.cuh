@@ -33,7 +33,7 @@ struct FwdParams {
     int kv_group;        // query heads per key head (1 = no sharing)
     int heads_per_cta;   // decode: query heads of one key head packed into a CTA's query columns
     int order_group;     // score tile forward: heads whose tiles are interleaved, see grouped_order
-    int take_over;       // score tile forward: more CTAs than can run at a time
+    int take_over;       // score tile forward: SMs when there are more CTAs than can run at a time, else 0
     float scale;         // softmax scale
     float scale_log2e;   // scale * log2(e): raw dot product -> base-2 exponent
     float* KL;           // [B*H*Nq]

@@ -24,10 +24,10 @@ constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 sta
 // plain update does better with the registers of 2 (documents of 8K: 197 against
 // 206 us).
 constexpr int sf_groups(int mode) { return mode == kScorePlain ? 2 : 4; }
-// warp 0 work items and copies, warp 1 the S1 MMAs, the update warpgroups, and a last warp for the S2 MMAs
-constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 32; }
+// warp 0 copies, warp 1 the S1 MMAs, the update warpgroups, the S2 MMAs, and the work items
+constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 64; }
 constexpr int kSfAhead = 4;  // key tiles between a tile's fetch into L2 and its copy into shared memory
-constexpr int kSfLead = 4;   // key tiles left to issue when the next work item is asked for
+constexpr int kSfNear = 4;   // key tiles left to issue when an item counts as nearly done
 constexpr uint64_t kSfDrainNs = 200000000ull;  // in-flight copies and MMAs retire before a CTA exits
 
 // A 128-row query tile of one head, and a share of its key tiles.
@@ -56,7 +56,8 @@ struct ScoreTileSmem {
     static constexpr int bar_ifull = bar_qempty + 8;      // [2] work items
     static constexpr int bar_iempty = bar_ifull + 16;
     static constexpr int bar_clc = bar_iempty + 16;
-    static constexpr int misc = bar_clc + 8;              // tmem base (4 B), abort flag (4 B)
+    static constexpr int bar_near = bar_clc + 8;          // an item's copies are all but issued
+    static constexpr int misc = bar_near + 8;             // tmem base (4 B), abort flag (4 B)
     static constexpr int clc = (misc + 8 + 15) / 16 * 16; // [2] launch-control responses
     static constexpr int items = clc + 32;                // [2] WorkItem
     static constexpr int ranges = items + 64;             // [2][128] int2: the rows' key ranges
@@ -173,6 +174,27 @@ __device__ __forceinline__ void update_scored(const float (&z1)[W], const float 
     if (BIAS) st.acc = fmaf(sum, base1 - base2, st.acc);
 }
 
+// States of one row over disjoint keys, merged at once.
+template <int MODE, int N>
+__device__ __forceinline__ RowState merge_groups(const RowState (&o)[N], float c) {
+    RowState s = o[0];
+#pragma unroll
+    for (int g = 1; g < N; ++g) {
+        s.m1 = fmaxf(s.m1, o[g].m1);
+        s.m2 = fmaxf(s.m2, o[g].m2);
+    }
+    s.l1 = s.acc = s.l2 = 0.f;
+#pragma unroll
+    for (int g = 0; g < N; ++g) {  // a group that saw nothing has m = -inf and l = acc = 0
+        const float w1 = MODE == kScoreBounded ? 1.f : o[g].m1 == -INFINITY ? 0.f : ex2(c * (o[g].m1 - s.m1));
+        const float w2 = MODE == kScoreBounded ? 1.f : o[g].m2 == -INFINITY ? 0.f : ex2(c * (o[g].m2 - s.m2));
+        s.l1 = fmaf(o[g].l1, w1, s.l1);
+        s.acc = fmaf(o[g].acc, w1, s.acc);
+        s.l2 = fmaf(o[g].l2, w2, s.l2);
+    }
+    return s;
+}
+
 __device__ __forceinline__ void store_scored(const FwdParams& p, size_t row, int split, const RowState& st, bool empty,
                                              bool failed) {
     if (p.num_splits == 1) {
@@ -206,19 +228,21 @@ __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_s
 // other.  Short rows (documents, windows) make short items: their start (row
 // ranges, first copies) and end (merge, outputs) run while the neighbouring items'
 // tiles are computed.  Every role walks the same items:
-//   warp 0       fetches the items, works out the union of the rows' key ranges
-//                (only tiles inside it are visited) and issues the copies
-//   warp 1, last S1 and S2 MMAs (warp 1 owns TMEM)
-//   the others   the update, one query row per thread
+//   the last warp fetches the items and works out the union of the rows' key ranges
+//                 (only tiles inside it are visited)
+//   warp 0        issues the copies
+//   warp 1, S2    the MMAs (warp 1 owns TMEM)
+//   the others    the update, one query row per thread
 // Rings (key tiles, score buffers) run on through the items.  8192 tokens, 32
-// heads, documents of a few hundred to 3000 tokens: one item per CTA 258 us, as here 197 us.
+// heads, documents of a few hundred to 3000 tokens: one item per CTA 258 us, as here 175 us.
 // ---------------------------------------------------------------------------
 template <int D, int NST, int MODE>
 __global__ void __launch_bounds__(sf_threads(MODE), 1)
     score_fwd_tile_kernel(const __grid_constant__ CUtensorMap tQ1, const __grid_constant__ CUtensorMap tK1,
                           const __grid_constant__ CUtensorMap tQ2, const __grid_constant__ CUtensorMap tK2,
                           const __grid_constant__ FwdParams p, const __grid_constant__ ScoreParams sp) {
-    constexpr int kGroups = sf_groups(MODE), kS2Warp = sf_threads(MODE) / 32 - 1, kUpdate = 128 * kGroups;
+    constexpr int kGroups = sf_groups(MODE), kUpdate = 128 * kGroups;
+    constexpr int kS2Warp = 2 + kUpdate / 32, kItemWarp = kS2Warp + 1;
     using L = ScoreTileSmem<D, NST, kGroups>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -240,11 +264,12 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             mbar_init(base + L::bar_sfull + 8 * s, 2);  // S1 and S2 of the buffer are complete
             mbar_init(base + L::bar_sempty + 8 * s, kUpdate);
             mbar_init(base + L::bar_ifull + 8 * s, 1);
-            mbar_init(base + L::bar_iempty + 8 * s, 2 + kUpdate / 32);  // the issuers and the update warps
+            mbar_init(base + L::bar_iempty + 8 * s, 3 + kUpdate / 32);  // the copies, the issuers, the update warps
         }
         mbar_init(base + L::bar_done, 1);
         mbar_init(base + L::bar_done + 8, 1);
         mbar_init(base + L::bar_clc, 1);
+        mbar_init(base + L::bar_near, 1);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -257,73 +282,42 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
     const WaitCtx wc{abort_flag, p.status, p.wait_ns};
 
     if (warp == 0) {
-        // ------------------------------------------------------------ work items and copies
+        // ------------------------------------------------------------ copies
         if (lane == 0) {
             prefetch_tensormap(&tQ1);
             prefetch_tensormap(&tK1);
             prefetch_tensormap(&tQ2);
             prefetch_tensormap(&tK2);
-        }
-        const uint64_t keep = policy_evict_last();  // key tiles are read again by other query tiles
-        // Groups of heads, a few waves of CTAs each, so that CTAs running at a time share
-        // key tiles through L2; in a group the last query tiles of every head, which see
-        // the most keys under a causal mask, come first.
-        auto place = [&](int unit) {
-            const int u = unit / p.num_splits;
-            const int2 at = grouped_order(u, p.num_q_tiles, p.B * p.H, p.order_group);
-            return make_int4(at.x, (p.num_q_tiles - 1 - at.y) * kBlockQ, unit - u * p.num_splits, at.x / p.H);
-        };
-        auto row_ranges = [&](const int4& at, int2 (&r)[4]) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = row_range(sp, p.Nq, p.Nk, at.w, at.y + lane + 32 * k);
-        };
-        int unit = blockIdx.x, requests = 0, it = 0, n_q = 0;
-        int4 at = place(unit);
-        int2 rr[4];
-        row_ranges(at, rr);
-        bool pending = false, ok = true;
-        // One request at a time, made when the copies of all but an item's last kSfLead key
-        // tiles are issued: early enough for the next item's start to hide behind those tiles,
-        // late enough to leave the items to CTAs that end sooner.
-        auto request = [&] {
-            pending = true;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(base + L::bar_clc, 16);
-                clc_request(base + L::clc + 16 * (requests & 1), base + L::bar_clc);
-            }
-        };
-        for (int k = 0;; ++k) {
-            const int slot = k & 1;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * slot, ((k >> 1) & 1) ^ 1, wc, kErrWaitOther))))
-                break;
-            int kt_begin = 0, n_tiles = 0;
-            if (unit >= 0) {
-                int lo = INT32_MAX, hi = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    ranges[slot * kBlockQ + lane + 32 * r] = rr[r];
-                    if (rr[r].x < rr[r].y) lo = min(lo, rr[r].x), hi = max(hi, rr[r].y);
+            const uint64_t keep = policy_evict_last();  // key tiles are read again by other query tiles
+            int it = 0, n_q = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!mbar_wait(base + L::bar_ifull + 8 * slot, (k >> 1) & 1, wc, kErrWaitOther)) break;
+                const WorkItem item = items[slot];
+                mbar_arrive(base + L::bar_iempty + 8 * slot);
+                if (!item.valid) break;
+                if (item.n_tiles == 0) {
+                    mbar_arrive(base + L::bar_near);
+                    continue;
                 }
-                lo = __reduce_min_sync(0xffffffffu, lo);
-                hi = __reduce_max_sync(0xffffffffu, hi);
-                if (lo < hi) {
-                    const int2 mine = split_tiles(lo / kBlockK, (hi + kBlockK - 1) / kBlockK, at.z, p.num_splits);
-                    kt_begin = mine.x;
-                    n_tiles = mine.y;
+                const int b = item.bh / p.H, h = item.bh - b * p.H, hk = h / p.kv_group;
+                // the previous item's last MMAs have read its query tiles
+                if (!mbar_wait(base + L::bar_qempty, (n_q & 1) ^ 1, wc, kErrWaitQ)) break;
+                mbar_arrive_expect_tx(base + L::bar_q, 2 * L::kQBytes);
+#pragma unroll
+                for (int c = 0; c < D / kSwizzleCols; ++c) {
+                    tma_load_4d(base + L::q1 + c * kBlockQ * 128, &tQ1, base + L::bar_q, c * kSwizzleCols, item.q0, h, b);
+                    tma_load_4d(base + L::q2 + c * kBlockQ * 128, &tQ2, base + L::bar_q, c * kSwizzleCols, item.q0, h, b);
                 }
-            }
-            if (lane == 0) items[slot] = WorkItem{at.x, at.y, at.z, kt_begin, n_tiles, unit >= 0, {0, 0}};
-            __syncwarp();
-            if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);
-            if (unit < 0) break;
-            const int b = at.w, h = at.x - b * p.H, hk = h / p.kv_group, q0 = at.y;
-            auto load_keys = [&](int from, int to) {  // key tiles [from, to) of the item
-                for (int t = from; t < to; ++t, ++it) {
+                ++n_q;
+                for (int t = 0; t < item.n_tiles; ++t, ++it) {
+                    if (t == max(0, item.n_tiles - kSfNear)) mbar_arrive(base + L::bar_near);
                     const int s = it % NST;
-                    if (!mbar_wait(base + L::bar_kempty + 8 * s, ((it / NST) & 1) ^ 1, wc, kErrWaitK)) return false;
+                    if (!(ok = mbar_wait(base + L::bar_kempty + 8 * s, ((it / NST) & 1) ^ 1, wc, kErrWaitK))) break;
                     const uint32_t fb = base + L::bar_kfull + 8 * s;
                     mbar_arrive_expect_tx(fb, 2 * L::kKBytes);
-                    const int k0 = (kt_begin + t) * kBlockK;
+                    const int k0 = (item.kt_begin + t) * kBlockK;
                     const uint32_t k1s = base + L::k + 2 * s * L::kKBytes, k2s = k1s + L::kKBytes;
 #pragma unroll
                     for (int c = 0; c < D / kSwizzleCols; ++c) {
@@ -331,7 +325,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         tma_load_4d_hint(k2s + c * kBlockK * 128, &tK2, fb, c * kSwizzleCols, k0, hk, b, keep);
                     }
                     // the ring is shorter than HBM's latency: a tile is fetched into L2 some tiles earlier
-                    if (t + kSfAhead < n_tiles) {
+                    if (t + kSfAhead < item.n_tiles) {
 #pragma unroll
                         for (int c = 0; c < D / kSwizzleCols; ++c) {
                             tma_prefetch_4d(&tK1, c * kSwizzleCols, k0 + kSfAhead * kBlockK, hk, b);
@@ -339,56 +333,85 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         }
                     }
                 }
-                return true;
-            };
-            const int early = max(0, n_tiles - kSfLead);  // tiles issued before the next item is asked for
-            if (lane == 0 && n_tiles > 0) {
-                // the previous item's last MMAs have read its query tiles
-                ok = mbar_wait(base + L::bar_qempty, (n_q & 1) ^ 1, wc, kErrWaitQ);
-                if (ok) {
-                    mbar_arrive_expect_tx(base + L::bar_q, 2 * L::kQBytes);
-#pragma unroll
-                    for (int c = 0; c < D / kSwizzleCols; ++c) {
-                        tma_load_4d(base + L::q1 + c * kBlockQ * 128, &tQ1, base + L::bar_q, c * kSwizzleCols, q0, h, b);
-                        tma_load_4d(base + L::q2 + c * kBlockQ * 128, &tQ2, base + L::bar_q, c * kSwizzleCols, q0, h, b);
-                    }
-                    ++n_q;
-                    ok = load_keys(0, early);
-                }
             }
-            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
-            if (p.take_over) request();
-            if (lane == 0 && n_tiles > 0) ok = load_keys(early, n_tiles);
-            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
-            unit = -1;
-            if (p.take_over) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, requests & 1, wc, kErrWaitOther)))) break;
-                pending = false;
-                unit = clc_response(base + L::clc + 16 * (requests & 1));
-                ++requests;
-                fence_proxy_async_smem();  // the response is read before its slot is written again
-                __syncwarp();
-            }
-            if (unit >= 0) {
-                at = place(unit);
-                if (lane == 0) {  // its query tiles on their way while the current item ends
-                    const int pb = at.w, ph = at.x - pb * p.H;
-#pragma unroll
-                    for (int c = 0; c < D / kSwizzleCols; ++c) {
-                        tma_prefetch_4d(&tQ1, c * kSwizzleCols, at.y, ph, pb);
-                        tma_prefetch_4d(&tQ2, c * kSwizzleCols, at.y, ph, pb);
-                    }
-                }
-                row_ranges(at, rr);
-            }
-        }
-        if (lane == 0) {  // every issued copy has landed, every stage was released
-            if (pending) score_drain(base + L::bar_clc, requests & 1, kSfDrainNs);
+            // every issued copy has landed, every stage was released
             if (n_q > 0) score_drain(base + L::bar_q, (n_q - 1) & 1, kSfDrainNs);
             for (int j = max(0, it - NST); j < it; ++j) {
                 score_drain(base + L::bar_kfull + 8 * (j % NST), (j / NST) & 1, kSfDrainNs);
                 if (!*abort_flag) score_drain(base + L::bar_kempty + 8 * (j % NST), (j / NST) & 1, kSfDrainNs);
             }
+        }
+    } else if (warp == kItemWarp) {
+        // ------------------------------------------------------------ work items
+        // The next item is asked for once every role has taken up the one before, so that its start
+        // hides behind that one's tiles; of the last three items per SM only when that one is nearly
+        // done, so that they go to the CTAs that end first (256 items of 1 to 16 tiles: 67 us when
+        // always early, 53 us so; 2048 items of 1 to 23 tiles: 197 us when always late, 175 so).
+        int unit = blockIdx.x;
+        for (int k = 0;; ++k) {
+            const int slot = k & 1;
+            if (k > 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * (slot ^ 1), ((k - 1) >> 1) & 1, wc, kErrWaitOther)))
+                    break;
+                const bool late = unit >= static_cast<int>(gridDim.x) - 3 * p.take_over;
+                if (p.take_over && late &&
+                    !__all_sync(0xffffffffu, mbar_wait(base + L::bar_near, (k - 1) & 1, wc, kErrWaitOther)))
+                    break;
+                unit = -1;
+                if (p.take_over) {
+                    const uint32_t response = base + L::clc + 16 * slot;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(base + L::bar_clc, 16);
+                        clc_request(response, base + L::bar_clc);
+                    }
+                    if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, (k - 1) & 1, wc, kErrWaitOther))) {
+                        if (lane == 0) score_drain(base + L::bar_clc, (k - 1) & 1, kSfDrainNs);
+                        break;
+                    }
+                    unit = clc_response(response);
+                    fence_proxy_async_smem();  // the response is read before its slot is written again
+                    __syncwarp();
+                }
+            }
+            WorkItem item{0, 0, 0, 0, 0, unit >= 0, {0, 0}};
+            if (unit >= 0) {
+                // Groups of heads, a few waves of CTAs each, so that CTAs running at a time share
+                // key tiles through L2; in a group the last query tiles of every head, which see
+                // the most keys under a causal mask, come first.
+                const int u = unit / p.num_splits;
+                const int2 at = grouped_order(u, p.num_q_tiles, p.B * p.H, p.order_group);
+                const int b = at.x / p.H, h = at.x - b * p.H;
+                item.bh = at.x;
+                item.q0 = (p.num_q_tiles - 1 - at.y) * kBlockQ;
+                item.split = unit - u * p.num_splits;
+                if (lane == 0 && k > 0) {  // its query tiles on their way while the current item ends
+#pragma unroll
+                    for (int c = 0; c < D / kSwizzleCols; ++c) {
+                        tma_prefetch_4d(&tQ1, c * kSwizzleCols, item.q0, h, b);
+                        tma_prefetch_4d(&tQ2, c * kSwizzleCols, item.q0, h, b);
+                    }
+                }
+                int2 r[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) r[n] = row_range(sp, p.Nq, p.Nk, b, item.q0 + lane + 32 * n);
+                int lo = INT32_MAX, hi = 0;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    ranges[slot * kBlockQ + lane + 32 * n] = r[n];
+                    if (r[n].x < r[n].y) lo = min(lo, r[n].x), hi = max(hi, r[n].y);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                if (lo < hi) {
+                    const int2 mine = split_tiles(lo / kBlockK, (hi + kBlockK - 1) / kBlockK, item.split, p.num_splits);
+                    item.kt_begin = mine.x;
+                    item.n_tiles = mine.y;
+                }
+            }
+            if (lane == 0) items[slot] = item;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);
+            if (unit < 0) break;
         }
     } else if (warp == 1 || warp == kS2Warp) {
         // ------------------------------------------------------------ MMA: S1 (warp 1), S2 (last warp)
@@ -550,11 +573,14 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             }
             const bool go_on = bar_sync_and(1, kUpdate, live && ok);
             if (wg == 0 && live) {
-                for (int g = 0; g < kGroups - 1; ++g) {
-                    const float* r = red + g * 5 * 128;
-                    const RowState o{r[row], r[128 + row], r[256 + row], r[384 + row], r[512 + row]};
-                    merge_state(st, o, c);
+                RowState o[kGroups];
+                o[0] = st;
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g) {
+                    const float* r = red + (g - 1) * 5 * 128;
+                    o[g] = RowState{r[row], r[128 + row], r[256 + row], r[384 + row], r[512 + row]};
                 }
+                st = merge_groups<MODE>(o, c);
                 if (i < p.Nq)
                     store_scored(p, static_cast<size_t>(bh) * p.Nq + i, item.split, st, range.x >= range.y,
                                  !go_on || *abort_flag);
