@@ -26,7 +26,6 @@ constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 sta
 constexpr int sf_groups(int mode) { return mode == kScorePlain ? 2 : 4; }
 // warp 0 copies, warp 1 the S1 MMAs, the update warpgroups, the S2 MMAs, and the work items
 constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 64; }
-constexpr int kSfAhead = 4;  // key tiles between a tile's fetch into L2 and its copy into shared memory
 constexpr int kSfNear = 4;   // key tiles left to issue when an item counts as nearly done
 constexpr uint64_t kSfDrainNs = 200000000ull;  // in-flight copies and MMAs retire before a CTA exits
 
@@ -324,14 +323,6 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         tma_load_4d_hint(k1s + c * kBlockK * 128, &tK1, fb, c * kSwizzleCols, k0, hk, b, keep);
                         tma_load_4d_hint(k2s + c * kBlockK * 128, &tK2, fb, c * kSwizzleCols, k0, hk, b, keep);
                     }
-                    // the ring is shorter than HBM's latency: a tile is fetched into L2 some tiles earlier
-                    if (t + kSfAhead < item.n_tiles) {
-#pragma unroll
-                        for (int c = 0; c < D / kSwizzleCols; ++c) {
-                            tma_prefetch_4d(&tK1, c * kSwizzleCols, k0 + kSfAhead * kBlockK, hk, b);
-                            tma_prefetch_4d(&tK2, c * kSwizzleCols, k0 + kSfAhead * kBlockK, hk, b);
-                        }
-                    }
                 }
             }
             // every issued copy has landed, every stage was released
@@ -380,17 +371,10 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                 // the most keys under a causal mask, come first.
                 const int u = unit / p.num_splits;
                 const int2 at = grouped_order(u, p.num_q_tiles, p.B * p.H, p.order_group);
-                const int b = at.x / p.H, h = at.x - b * p.H;
+                const int b = at.x / p.H;
                 item.bh = at.x;
                 item.q0 = (p.num_q_tiles - 1 - at.y) * kBlockQ;
                 item.split = unit - u * p.num_splits;
-                if (lane == 0 && k > 0) {  // its query tiles on their way while the current item ends
-#pragma unroll
-                    for (int c = 0; c < D / kSwizzleCols; ++c) {
-                        tma_prefetch_4d(&tQ1, c * kSwizzleCols, item.q0, h, b);
-                        tma_prefetch_4d(&tQ2, c * kSwizzleCols, item.q0, h, b);
-                    }
-                }
                 int2 r[4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) r[n] = row_range(sp, p.Nq, p.Nk, b, item.q0 + lane + 32 * n);
