@@ -8,6 +8,10 @@
 // Roles, rings and the five-scalar state are those of the unmodified forward;
 // what differs is the update: z -> x (score.cuh), the range of each row, and for
 // bounded scores a sum of 2^x without a running maximum.
+//
+// 8192 causal rows, 32 heads: plain 542 us (1015 TFLOP/s), caps of 50 734 us (750):
+// the update bounds both, the cap's polynomials add 10 operations a pair to the
+// FMA pipe's 6 (60% busy, issue slots 61%, tensor pipe 31%).
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -585,8 +589,9 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
 // ---------------------------------------------------------------------------
 // Decode forward, Nq <= 16: S^T = K Q^T with 128 keys on the TMEM lanes and up
 // to 16 query columns (heads_per_cta heads of one key head x Nq rows), so a key
-// byte is streamed once for all of them.  Bound by HBM.  Each split takes its
-// share of the tiles that the CTA's rows see, not of the whole cache.
+// byte is streamed once for all of them.  Bound by HBM: 4 caches of up to 131072
+// keys, 8 key heads, caps of 50, 1.93 GB in 282 us with the combine.  Each split
+// takes its share of the tiles that the CTA's rows see, not of the whole cache.
 // ---------------------------------------------------------------------------
 template <int D, int NST>
 struct ScoreDecodeSmem {
