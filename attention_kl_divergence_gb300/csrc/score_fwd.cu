@@ -342,15 +342,18 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         // hides behind that one's tiles; of the last three items per SM only when that one is nearly
         // done, so that they go to the CTAs that end first (256 items of 1 to 16 tiles: 67 us when
         // always early, 53 us so; 2048 items of 1 to 23 tiles: 197 us when always late, 175 so).
-        int unit = blockIdx.x;
+        // These two waits last as long as whole items do: the limit of a wait is theirs per key tile.
+        int unit = blockIdx.x, last_tiles = 0, before_tiles = 0;
+        WaitCtx wi = wc;
         for (int k = 0;; ++k) {
             const int slot = k & 1;
             if (k > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * (slot ^ 1), ((k - 1) >> 1) & 1, wc, kErrWaitOther)))
+                wi.limit_ns = max(p.wait_ns, min(p.wait_ns, 1ull << 38) * (1ull + last_tiles + before_tiles));
+                if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_iempty + 8 * (slot ^ 1), ((k - 1) >> 1) & 1, wi, kErrWaitOther)))
                     break;
                 const bool late = unit >= static_cast<int>(gridDim.x) - 3 * p.take_over;
                 if (p.take_over && late &&
-                    !__all_sync(0xffffffffu, mbar_wait(base + L::bar_near, (k - 1) & 1, wc, kErrWaitOther)))
+                    !__all_sync(0xffffffffu, mbar_wait(base + L::bar_near, (k - 1) & 1, wi, kErrWaitOther)))
                     break;
                 unit = -1;
                 if (p.take_over) {
@@ -396,6 +399,8 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                     item.n_tiles = mine.y;
                 }
             }
+            before_tiles = last_tiles;
+            last_tiles = item.n_tiles;
             if (lane == 0) items[slot] = item;
             __syncwarp();
             if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);

@@ -442,6 +442,8 @@ def _tensors(*tensors):
 
 
 def _remember(key, entry):
+    if key[1] is None:  # nothing to know the call by
+        return entry
     if len(_known) >= 512:
         _known.clear()
     _known[key] = entry

@@ -437,6 +437,23 @@ def test_autograd_function_settings():
 
 
 @gpu
+def test_wait_limit_is_shorter_than_a_work_item():
+    """The limit holds for a step of the pipeline, not for a row's whole length: 320 work items of 8192 key tiles
+    take several milliseconds each, with a limit of 2."""
+    B, H, N, M, d = 1, 320, 17, 1 << 20, 64
+    x = [0.3 * torch.randn(B, h, n, d, device=DEV).to(BF16) for h, n in ((H, N), (1, M), (H, N), (1, M))]
+    for sc in (sk.Scores(), sk.Scores(50.0, 50.0)):
+        plan = sk.score_fwd_plan(x[0], x[1], num_splits=1)
+        assert plan.num_ctas > torch.cuda.get_device_properties(0).multi_processor_count
+        ws = sk.new_workspace(plan.workspace_bytes, DEV)
+        got = sk.kl_score_fwd(sc, *x, num_splits=1, workspace=ws, wait_limit_ns=2_000_000)
+        assert sk.workspace_status(ws) == 0
+        want = sk.kl_score_fwd(sc, *x, num_splits=1)
+        for a, b in zip(got, want):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
+@gpu
 def test_first_call_of_a_host_thread():
     """A thread that has made no CUDA call yet, with every buffer at hand: nothing before the library's own calls
     binds the device's context to it."""
