@@ -13,10 +13,10 @@
 // out by the copying warp they took longer than a tile's matrix work.
 //
 // 8192 causal rows, 32 heads on 8 key heads, caps of 50, bf16 gradients: prepare
-// 21 us, gradients 1262 us, finish 30 us.  Without caps the 28 MMAs of a tile
-// (16 of N = 64, each about 58 cycles whatever N <= 128 is) set its 2130 cycles;
-// with them the update's dependent steps do (2800 cycles; more update warps,
-// polling waits, K^T in tensor memory and a second S1 buffer changed nothing).
+// 21 us, gradients 1260 us, finish 30 us.  Without caps the 28 MMAs of a tile
+// (about 60 cycles each, whatever N <= 128 is) and their handoffs take 2130
+// cycles; with caps the update's dependent steps take 2800 (twice the update
+// warps, or a second buffer for the scores, changed nothing).
 #include <algorithm>
 
 #include "bwd_common.cuh"

@@ -9,9 +9,9 @@
 // what differs is the update: z -> x (score.cuh), the range of each row, and for
 // bounded scores a sum of 2^x without a running maximum.
 //
-// 8192 causal rows, 32 heads: plain 542 us (1015 TFLOP/s), caps of 50 734 us (750):
-// the update bounds both, the cap's polynomials add 10 operations a pair to the
-// FMA pipe's 6 (60% busy, issue slots 61%, tensor pipe 31%).
+// 8192 causal rows, 32 heads: plain scores 519 to 531 us (1.05 PFLOP/s), caps of
+// 50 730 us (0.75).  The update bounds both; with caps the FMA pipe is busy 62% of
+// the cycles, issue slots 65%, the tensor pipe 33%.
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -25,8 +25,8 @@ constexpr float kScoreTau = 8.0f;  // lazy rescale: running maxima up to 2^8 sta
 // Update warpgroups of the tile kernel, each taking its share of a tile's columns.
 // The cap's polynomial makes the update the slowest part, and its dependent steps
 // need more warps to overlap (8K causal, 32 heads: 2 groups 985 us, 4 765); the
-// plain update does better with the registers of 2 (documents of 8K: 197 against
-// 206 us).
+// plain update does better with the registers of 2 (8K tokens in documents: 197
+// against 206 us).
 constexpr int sf_groups(int mode) { return mode == kScorePlain ? 2 : 4; }
 // warp 0 copies, warp 1 the S1 MMAs, the update warpgroups, the S2 MMAs, and the work items
 constexpr int sf_threads(int mode) { return 64 + 128 * sf_groups(mode) + 64; }
@@ -237,7 +237,7 @@ __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_s
 //   warp 1, S2    the MMAs (warp 1 owns TMEM)
 //   the others    the update, one query row per thread
 // Rings (key tiles, score buffers) run on through the items.  8192 tokens, 32
-// heads, documents of a few hundred to 3000 tokens: one item per CTA 258 us, as here 175 us.
+// heads, documents of 468 to 2741 tokens: one item per CTA 258 us, as here 174 us.
 // ---------------------------------------------------------------------------
 template <int D, int NST, int MODE>
 __global__ void __launch_bounds__(sf_threads(MODE), 1)
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         // ------------------------------------------------------------ work items
         // The next item is asked for once every role has taken up the one before, so that its start
         // hides behind that one's tiles; of the last three items per SM only when that one is nearly
-        // done, so that they go to the CTAs that end first (256 items of 1 to 16 tiles: 67 us when
+        // done, so that they go to the CTAs that end first (256 items of 4 to 16 tiles: 67 us when
         // always early, 53 us so; 2048 items of 1 to 23 tiles: 197 us when always late, 175 so).
         // These two waits last as long as whole items do: the limit of a wait is theirs per key tile.
         int unit = blockIdx.x, last_tiles = 0, before_tiles = 0;
