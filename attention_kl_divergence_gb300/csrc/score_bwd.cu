@@ -219,6 +219,10 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     const uint32_t kt_tile = base + (SETTING == 1 ? L::k2 : L::k1);  // trainable keys
 
     if (threadIdx.x == 0) {
+        prefetch_tensormap(&tK1);
+        prefetch_tensormap(&tK2);
+        prefetch_tensormap(&tQ1);
+        prefetch_tensormap(&tQ2);
         mbar_init(base + L::bar_k, 1);
         for (int s = 0; s < L::kQt; ++s) {
             mbar_init(base + L::bar_qtfull + 8 * s, 1);
@@ -247,6 +251,13 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         tile_span[1] = -1;
         fence_barrier_init();
         fence_proxy_async_smem();
+        // the key tiles are on their way while the query tiles are looked up
+        mbar_arrive_expect_tx(base + L::bar_k, 2 * L::kKBytes);
+#pragma unroll
+        for (int c = 0; c < D / kSwizzleCols; ++c) {
+            tma_load_4d(base + L::k1 + c * kBlockK * 128, &tK1, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
+            tma_load_4d(base + L::k2 + c * kBlockK * 128, &tK2, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
+        }
     }
     if (L::kZeroBytes > 0) {
         for (int k = threadIdx.x; k < L::kZeroBytes / 16; k += blockDim.x)
@@ -254,7 +265,6 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         fence_proxy_async_smem();  // the tensor core reads it through the async proxy
     }
     if (warp == 1) tmem_alloc(base + L::misc, 512);
-    __syncthreads();
     // the query tiles with a row that sees one of these keys: from the first to the last of them
     {
         const KeyBlock* blocks = static_cast<const KeyBlock*>(sp.keys) + static_cast<size_t>(b) * p.num_q_tiles;
@@ -269,6 +279,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         }
         first = __reduce_min_sync(0xffffffffu, first);
         last = __reduce_max_sync(0xffffffffu, last);
+        __syncthreads();  // tile_span is set up
         if (lane == 0 && last >= 0) {
             atomicMin(&tile_span[0], first);
             atomicMax(&tile_span[1], last);
@@ -292,16 +303,6 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------ copies
         if (lane == 0 && n_tiles > 0) {
-            prefetch_tensormap(&tQ1);
-            prefetch_tensormap(&tK1);
-            prefetch_tensormap(&tQ2);
-            prefetch_tensormap(&tK2);
-            mbar_arrive_expect_tx(base + L::bar_k, 2 * L::kKBytes);
-#pragma unroll
-            for (int c = 0; c < D / kSwizzleCols; ++c) {
-                tma_load_4d(base + L::k1 + c * kBlockK * 128, &tK1, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
-                tma_load_4d(base + L::k2 + c * kBlockK * 128, &tK2, base + L::bar_k, c * kSwizzleCols, n0, hk, b);
-            }
             const uint64_t keep = policy_evict_last();
             const CUtensorMap* tqt = SETTING == 1 ? &tQ2 : &tQ1;  // the trainable side's queries
             const CUtensorMap* tqn = SETTING == 1 ? &tQ1 : &tQ2;
@@ -342,7 +343,6 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 }
             }
             // every issued copy has landed (and, unless aborting, been consumed)
-            drain_wait_b(base + L::bar_k, 0, kDrainNs);
             for (int j = max(0, n_qt - L::kQt); j < n_qt; ++j) {
                 const uint32_t bo = 8 * (j % L::kQt), ph = (j / L::kQt) & 1;
                 drain_wait_b(base + L::bar_qtfull + bo, ph, kDrainNs);
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 if (!*abort_flag) drain_wait_b(base + L::bar_vempty + bo, ph, kDrainNs);
             }
         }
+        if (lane == 0) drain_wait_b(base + L::bar_k, 0, kDrainNs);
     } else if (warp == 1) {
         // ------------------------------------------------ score MMAs
         // Two threads issue the MMAs: this one the scores of tile m, the
