@@ -12,6 +12,13 @@
 // the row constants, which a first kernel prepares and bulk copies fetch: worked
 // out by the copying warp they took longer than a tile's matrix work.
 //
+// dS enters the gradient products as two bf16 terms (2^-17 of it is lost),
+// whatever the gradients' type.  One term rounds each dS by up to 2^-8: what all
+// keys have in common cancels in dQ, where the dS of a row sum to zero, and those
+// roundings do not.  Keys with an offset of 16 beside a noise of 1 in an eighth of
+// the channels: dQ off by 0.0085 of its norm with one term, by the output's own
+// rounding, 0.0017, with two.
+//
 // 8192 causal rows, 32 heads on 8 key heads, caps of 50, bf16 gradients: prepare
 // 21 us, gradients 1260 us, finish 30 us.  Without caps the 28 MMAs of a tile
 // (about 60 cycles each, whatever N <= 128 is) and their handoffs take 2130
@@ -39,17 +46,6 @@ struct KeyBlock {
 };
 constexpr int kRowBlockBytes = 3 * kBwdTile * 4;
 static_assert(sizeof(KeyBlock) == 2 * kBwdTile * 4 + 32, "packed");
-
-// 32 dS values rounded to bf16: four 16-byte chunks of a 128-byte swizzled row.
-__device__ __forceinline__ void store_ds_term(uint32_t tile, int row, int chunk0, const float (&v)[32]) {
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = pack_bf16(v[cc * 8 + 2 * k], v[cc * 8 + 2 * k + 1]);
-        st_shared_v4(tile + row * 128 + (((chunk0 + cc) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-    }
-}
 
 __device__ __forceinline__ bool has_nonfinite_bf16(uint32_t u) {
     return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(256) score_prepare_kernel(const __grid_constan
 // (cols 0-127), S1^T|S2^T (128-255), dK (256-383), dQ^T of the hi|lo halves of dS
 // (384-511).
 // ---------------------------------------------------------------------------
-template <int D, int NST, int TERMS>
+template <int D, int NST>
 struct ScoreKvSmem {
     static constexpr int kKBytes = kBlockK * D * 2;    // 128 keys
     static constexpr int kQBytes = kBwdTile * D * 2;   // 64 query rows of one tensor
@@ -154,9 +150,9 @@ struct ScoreKvSmem {
     static constexpr int qt = 2 * kKBytes;
     static constexpr int qn = qt + kQt * kQBytes;
     static constexpr int kNumDs = 2;                   // dS buffers (hi + lo each)
-    static constexpr int ds = qn + kQn * kQBytes;      // buffer b: its TERMS terms at ds + b*TERMS*kDsBytes
+    static constexpr int ds = qn + kQn * kQBytes;      // buffer b: hi at ds + 2*b*kDsBytes, lo right after
     // d = 64: a zero 64-feature atom pads the dQ^T MMA's A operand (K_t^T) to M = 128
-    static constexpr int zero = ds + TERMS * kNumDs * kDsBytes;
+    static constexpr int zero = ds + 2 * kNumDs * kDsBytes;
     static constexpr int kZeroBytes = D < 128 ? kBlockK * 128 : 0;
     static constexpr int vec = zero + kZeroBytes;      // [kNv][3][64] floats
     static constexpr int keys = vec + kNv * kRowBlockBytes;  // [kNv] KeyBlock
@@ -183,12 +179,12 @@ struct ScoreKvSmem {
 
 constexpr int kSbThreads = 480;
 
-template <int D, int NST, int SETTING, int MODE, int TERMS>
+template <int D, int NST, int SETTING, int MODE>
 __global__ void __launch_bounds__(kSbThreads, 1)
     score_bwd_kernel(const __grid_constant__ CUtensorMap tQ1, const __grid_constant__ CUtensorMap tK1,
                      const __grid_constant__ CUtensorMap tQ2, const __grid_constant__ CUtensorMap tK2,
                      const __grid_constant__ BwdParams p, const __grid_constant__ ScoreParams sp) {
-    using L = ScoreKvSmem<D, NST, TERMS>;
+    using L = ScoreKvSmem<D, NST>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // The layout uses every byte it asked for, so the dynamic shared memory
     // base itself must be 1024-byte aligned (128-byte swizzle atoms); if it is
@@ -437,12 +433,12 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         // existed, so these commits also cover the score MMAs that read the stage.)
         if (lane == 0) {
             constexpr uint32_t id_dk = idesc_bf16_f32(kBlockK, D, 0, 1);
-            constexpr uint32_t id_dq = idesc_bf16_f32(128, TERMS * kBwdTile, 1, 1);  // M = 128 features (d = 64: padded)
+            constexpr uint32_t id_dq = idesc_bf16_f32(128, 2 * kBwdTile, 1, 1);  // M = 128 features (d = 64: padded)
             // A = K_t^T as 64-feature atoms: the tile's second block, or the zero atom when d = 64
             const uint32_t a_atom = D == 128 ? kBlockK * 128 : base + L::zero - kt_tile;
             const uint32_t t_dk = tmem + 256, t_dq = tmem + 384;
             const uint32_t dhi = smem_desc_hi();
-            constexpr uint32_t kSlotLo = L::kQBytes >> 4, kDsLo = (TERMS * L::kDsBytes) >> 4;
+            constexpr uint32_t kSlotLo = L::kQBytes >> 4, kDsLo = (2 * L::kDsBytes) >> 4;
             const uint32_t qt_lo0 = smem_desc_lo_mn128(base + L::qt, kBwdTile * 128);
             const uint32_t ds_lo0 = smem_desc_lo_k128(base + L::ds);
             const uint32_t dsmn_lo0 = smem_desc_lo_mn128(base + L::ds, L::kDsBytes);
@@ -457,7 +453,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                     const uint32_t ds_lo = ds_lo0 + (dsb ? kDsLo : 0u);
                     // dK += dS^T Q_t : A = dS^T (K-major over queries), B = Q_t (MN-major); dS = hi + lo
 #pragma unroll
-                    for (int part = 0; part < TERMS; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int kk = 0; kk < kBwdTile / 16; ++kk)
                             tc_mma_bf16_w(t_dk, ds_lo + ((part * L::kDsBytes + kk * 32) >> 4), dhi,
@@ -521,7 +517,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             const int r0 = qtile(m) * kBwdTile + wg * 32;  // first query row of this chunk
             const uint32_t t1 = tl + 128 + wg * 32, t2 = t1 + 64;
             const int dsb = m % L::kNumDs;
-            const uint32_t dss = base + L::ds + TERMS * dsb * L::kDsBytes;
+            const uint32_t dss = base + L::ds + 2 * dsb * L::kDsBytes;
             float z1[32], z2[32];
             tmem_ld32(t1, z1);
             tmem_ld32(t2, z2);
@@ -610,10 +606,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 ok = false;
                 break;
             }
-            if (TERMS == 2)
-                store_ds_chunk(dss, dss + L::kDsBytes, row, wg * 4, dsv);
-            else
-                store_ds_term(dss, row, wg * 4, dsv);
+            store_ds_chunk(dss, dss + L::kDsBytes, row, wg * 4, dsv);
             fence_proxy_async_smem();
             mbar_arrive(base + L::bar_dsfull + 8 * dsb);
         }
@@ -656,27 +649,25 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             tc_fence_after();
             float v0[32], v1[32];
             if (wq * 32 < D) {  // d = 64: TMEM lanes 64-127 hold the zero padding
-                tmem_ld32(tl + 384, v0);  // first term, query rows 0-31
+                tmem_ld32(tl + 384, v0);  // hi, query rows 0-31
                 tmem_ld32(tl + 416, v1);  // and 32-63
                 tc_wait_ld();
-                if (TERMS == 2) {
-                    float lo[32];
-                    tmem_ld32(tl + 448, lo);
-                    tc_wait_ld();
+                float lo[32];
+                tmem_ld32(tl + 448, lo);
+                tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 t = __fadd2_rn(make_float2(v0[e], v0[e + 1]), make_float2(lo[e], lo[e + 1]));
-                        v0[e] = t.x;
-                        v0[e + 1] = t.y;
-                    }
-                    tmem_ld32(tl + 480, lo);
-                    tc_wait_ld();
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 t = __fadd2_rn(make_float2(v0[e], v0[e + 1]), make_float2(lo[e], lo[e + 1]));
+                    v0[e] = t.x;
+                    v0[e + 1] = t.y;
+                }
+                tmem_ld32(tl + 480, lo);
+                tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 t = __fadd2_rn(make_float2(v1[e], v1[e + 1]), make_float2(lo[e], lo[e + 1]));
-                        v1[e] = t.x;
-                        v1[e + 1] = t.y;
-                    }
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 t = __fadd2_rn(make_float2(v1[e], v1[e + 1]), make_float2(lo[e], lo[e + 1]));
+                    v1[e] = t.x;
+                    v1[e + 1] = t.y;
                 }
             }
             tc_fence_before();
@@ -751,27 +742,16 @@ __global__ void __launch_bounds__(256) score_finish_kernel(const float4* dq, uin
     }
 }
 
-template <int D, int SETTING, int MODE, int TERMS>
-cudaError_t launch_terms(const CUtensorMap* m, const BwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
+template <int D, int SETTING, int MODE>
+cudaError_t launch_impl(const CUtensorMap* m, const BwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
     constexpr int NST = D == 128 ? 4 : 8;  // trainable-side query ring; the other side's is half as deep
-    constexpr int bytes = ScoreKvSmem<D, NST, TERMS>::alloc;
+    constexpr int bytes = ScoreKvSmem<D, NST>::alloc;
     static_assert(bytes <= 232448, "shared memory");
-    auto k = score_bwd_kernel<D, NST, SETTING, MODE, TERMS>;
+    auto k = score_bwd_kernel<D, NST, SETTING, MODE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k<<<ctas, kSbThreads, bytes, st>>>(m[0], m[1], m[2], m[3], p, sp);
     return cudaGetLastError();
-}
-
-// dS enters the gradient products as one bf16 term for bf16 gradients: its
-// roundings, each up to 2^-8 of a term and independent of one another, add less
-// error than the output's own rounding, up to 2^-8 of the sum, as long as the
-// products do not mostly cancel; the second term would be a third of the kernel's
-// matrix work.  float32 gradients take two (2^-17 of each term).
-template <int D, int SETTING, int MODE>
-cudaError_t launch_impl(const CUtensorMap* m, const BwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
-    return p.grad_bf16 ? launch_terms<D, SETTING, MODE, 1>(m, p, sp, ctas, st)
-                       : launch_terms<D, SETTING, MODE, 2>(m, p, sp, ctas, st);
 }
 
 template <int MODE>
