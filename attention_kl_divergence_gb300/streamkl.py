@@ -427,9 +427,9 @@ class AttentionKL(torch.autograd.Function):
 # Divergence of attentions with modified scores
 # ---------------------------------------------------------------------------
 # Calls whose arguments passed every check, by what the checks look at (shapes,
-# strides, types, devices, options -- never values or addresses): the structs
-# and sizes they led to.  Checking again and planning cost more host time than a
-# small call's kernels.
+# strides, types, devices, and options as plain numbers -- never the tensors, their
+# values or addresses): the structs and sizes they led to.  Checking again and
+# planning cost more host time than a small call's kernels.
 _known = {}
 
 
@@ -444,9 +444,10 @@ def _tensors(*tensors):
 def _remember(key, entry):
     if key[1] is None:  # nothing to know the call by
         return entry
-    if len(_known) >= 512:
-        _known.clear()
-    _known[key] = entry
+    with _lock:
+        while len(_known) >= 512:
+            del _known[next(iter(_known))]  # the oldest
+        _known[key] = entry
     return entry
 
 
@@ -577,6 +578,7 @@ def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0,
     """Per-row KL(P1 || P2), LSE1, LSE2 as float32 [B, H, Nq] for the scores that ``scores`` describes.  A row that
     sees no key has KL = 0 and LSE = -inf; what a row does not see (NaN included) has no effect on it."""
     given = _scores(scores).tensors()
+    num_splits, wait_limit_ns, debug_flags = int(num_splits), int(wait_limit_ns), int(debug_flags)
     key, known = _lookup("score_fwd", _tensors(Q1, K1, Q2, K2, *given), num_splits, wait_limit_ns, debug_flags)
     if known is None:
         _check_qk(Q1, K1, Q2, K2)
@@ -607,6 +609,7 @@ def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=Fals
     up in float32 in no fixed order (like kl_bwd's fused mode); dK is the same on every run.  num_splits: CTAs that
     share a key tile's query rows (0 = automatic)."""
     given = _scores(scores).tensors()
+    setting, num_splits, wait_limit_ns, debug_flags = int(setting), int(num_splits), int(wait_limit_ns), int(debug_flags)
     key, known = _lookup("score_bwd", _tensors(Q1, K1, Q2, K2, g, KL, LSE1, LSE2, *given), setting, grad_dtype, wait_limit_ns,
                          debug_flags, num_splits)
     if known is None:
@@ -615,7 +618,7 @@ def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=Fals
         shape, plan = make_shape(Q1, K1), Plan()
         opts = _opts(num_splits, 0, wait_limit_ns, debug_flags, _grad_flag(grad_dtype))
         with torch.cuda.device(Q1.device):
-            _raise(load().streamkl_score_bwd_plan(ctypes.byref(shape), int(setting), ctypes.byref(opts), ctypes.byref(plan)),
+            _raise(load().streamkl_score_bwd_plan(ctypes.byref(shape), setting, ctypes.byref(opts), ctypes.byref(plan)),
                    "streamkl_score_bwd_plan")
         for name, t in (("g", g), ("KL", KL), ("LSE1", LSE1), ("LSE2", LSE2)):
             _check_tensor(name, t, Q1.shape[:3], torch.float32, Q1.device)
@@ -629,7 +632,7 @@ def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=Fals
     workspace = _scratch(workspace, nbytes, device)
     dQ, dK = out
     score = Score(scores.cap1, scores.cap2, *[_address(t) for t in given])
-    _raise(_on(device, load().streamkl_score_bwd, shape, score, int(setting), g.data_ptr(), Q1.data_ptr(), K1.data_ptr(),
+    _raise(_on(device, load().streamkl_score_bwd, shape, score, setting, g.data_ptr(), Q1.data_ptr(), K1.data_ptr(),
                Q2.data_ptr(), K2.data_ptr(), KL.data_ptr(), LSE1.data_ptr(), LSE2.data_ptr(),
                0.0 if scale is None else float(scale), 1 if causal else 0, dQ.data_ptr(), dK.data_ptr(),
                workspace.data_ptr(), workspace.numel(), opts), "streamkl_score_bwd")
@@ -645,6 +648,7 @@ class ScoredAttentionKL(torch.autograd.Function):
         if any(t is not None and t.requires_grad for t in _scores(scores).tensors()):
             raise ValueError("the tensors of scores are constants: they get no gradient")
         _guard_capture(Q1, K1, Q2, K2)
+        causal, scale = bool(causal), None if scale is None else float(scale)  # the backward's are the forward's
         KL, L1, L2 = kl_score_fwd(scores, Q1, K1, Q2, K2, causal=causal, scale=scale)
         ctx.save_for_backward(Q1, K1, Q2, K2, KL, L1, L2, *scores.tensors())
         ctx.caps, ctx.causal, ctx.scale = (scores.cap1, scores.cap2), causal, scale
@@ -706,7 +710,7 @@ def _contiguous(shape) -> Strides:
     return Strides(H * max(N, 1) * d, max(N, 1) * d, d)
 
 
-def _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved):
+def _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved):
     desc = NormRope()
     desc.q, desc.k = _heads("q", q, (torch.bfloat16,)), _heads("k", k, (torch.bfloat16,), q.device)
     B, Hq, N, d = q.shape
@@ -733,10 +737,26 @@ def _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved):
             raise ValueError("positions must be an int32 or int64 tensor")
         _check_tensor("positions", positions, (B, N), positions.dtype, q.device)
     desc.B, desc.Hq, desc.Hk, desc.N, desc.d, desc.rot = B, Hq, k.shape[1], N, d, rot
-    desc.interleaved, desc.eps = int(bool(interleaved)), float(eps)
+    desc.interleaved, desc.eps = int(interleaved), eps
     desc.weight_bf16 = int(torch.bfloat16 in types)
     desc.pos_int64 = int(positions is not None and positions.dtype == torch.int64)
-    desc.table_rows, desc.start = (table.shape[0] if table is not None else 0), int(start)
+    desc.table_rows = table.shape[0] if table is not None else 0
+    return desc
+
+
+def _plain(start, eps, interleaved):
+    """Plain numbers, read now: a program may hand in a tensor or an array and change it in place."""
+    start = int(start)
+    if not -2 ** 63 <= start < 2 ** 63:
+        raise ValueError(f"start must fit 64 bits, got {start}")
+    return start, float(eps), bool(interleaved)
+
+
+def _at(desc, start):
+    """The description of a known call (whose start is 0: no check looks at it) from position ``start``."""
+    if start:
+        desc = NormRope.from_buffer_copy(desc)  # another thread may be using the known one
+        desc.start = start
     return desc
 
 
@@ -745,9 +765,10 @@ def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, ep
     its root mean square, times wq / wk ([d], float32 or bf16; None: ones), its first 2 * table.shape[1] values turned
     by the angles of its position (positions [B, N], else start + n; table from rope_table; None: no rotation).  out: two
     bf16 tensors of the same shapes, any strides (rows of a cache, or q and k themselves); new contiguous ones otherwise."""
-    key, known = _lookup("norm_rope", _tensors(q, k, wq, wk, table, positions, *(out or ())), start, eps, interleaved)
+    start, eps, interleaved = _plain(start, eps, interleaved)
+    key, known = _lookup("norm_rope", _tensors(q, k, wq, wk, table, positions, *(out or ())), eps, interleaved)
     if known is None:
-        desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved)
         if out is not None:
             desc.yq = _heads("out[0]", out[0], (torch.bfloat16,), q.device, q.shape)
             desc.yk = _heads("out[1]", out[1], (torch.bfloat16,), q.device, k.shape)
@@ -759,8 +780,8 @@ def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, ep
         out = (torch.empty(q_shape, dtype=torch.bfloat16, device=device),
                torch.empty(k_shape, dtype=torch.bfloat16, device=device))
     yq, yk = out
-    _raise(_on(device, load().streamkl_norm_rope_fwd, desc, q.data_ptr(), k.data_ptr(), _address(wq), _address(wk),
-               _address(table), _address(positions), yq.data_ptr(), yk.data_ptr()), "streamkl_norm_rope_fwd")
+    _raise(_on(device, load().streamkl_norm_rope_fwd, _at(desc, start), q.data_ptr(), k.data_ptr(), _address(wq),
+               _address(wk), _address(table), _address(positions), yq.data_ptr(), yk.data_ptr()), "streamkl_norm_rope_fwd")
     return yq, yk
 
 
@@ -769,10 +790,10 @@ def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=Non
     """(dq, dk, dwq, dwk) of sum(dyq q') + sum(dyk k') for qk_norm_rope's arguments; dyq, dyk are both bf16 or both
     float32 (kl_bwd's gradients as they come), any strides with d contiguous.  dq, dk are bf16, dwq, dwk of the weights'
     type (None without weights).  out: (dq, dk) to write into.  Equal inputs give equal bits."""
-    key, known = _lookup("norm_rope_bwd", _tensors(dyq, dyk, q, k, wq, wk, table, positions, *(out or ())), start, eps,
-                         interleaved)
+    start, eps, interleaved = _plain(start, eps, interleaved)
+    key, known = _lookup("norm_rope_bwd", _tensors(dyq, dyk, q, k, wq, wk, table, positions, *(out or ())), eps, interleaved)
     if known is None:
-        desc = _norm_rope_desc(q, k, wq, wk, table, positions, start, eps, interleaved)
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved)
         desc.yq = _heads("dyq", dyq, (torch.bfloat16, torch.float32), q.device, q.shape)
         desc.yk = _heads("dyk", dyk, (dyq.dtype,), q.device, k.shape)
         desc.grad_bf16 = int(dyq.dtype == torch.bfloat16)
@@ -791,8 +812,8 @@ def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=Non
     dq, dk = out
     dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
     workspace = _scratch(workspace, nbytes, device)
-    _raise(_on(device, load().streamkl_norm_rope_bwd, desc, dyq.data_ptr(), dyk.data_ptr(), q.data_ptr(), k.data_ptr(),
-               _address(wq), _address(wk), _address(table), _address(positions), dq.data_ptr(), dk.data_ptr(),
+    _raise(_on(device, load().streamkl_norm_rope_bwd, _at(desc, start), dyq.data_ptr(), dyk.data_ptr(), q.data_ptr(),
+               k.data_ptr(), _address(wq), _address(wk), _address(table), _address(positions), dq.data_ptr(), dk.data_ptr(),
                _address(dwq), _address(dwk), workspace.data_ptr(), workspace.numel()), "streamkl_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -805,7 +826,7 @@ class QKNormRope(torch.autograd.Function):
     def forward(ctx, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False):
         _guard_capture(q, k, wq, wk)
         ctx.save_for_backward(q, k, wq, wk, table, positions)
-        ctx.how = dict(start=start, eps=eps, interleaved=interleaved)
+        ctx.how = dict(zip(("start", "eps", "interleaved"), _plain(start, eps, interleaved)))
         return qk_norm_rope(q, k, wq, wk, table, positions, **ctx.how)
 
     @staticmethod
