@@ -60,8 +60,8 @@ struct ScoreTileSmem {
     static constexpr int bar_iempty = bar_ifull + 16;
     static constexpr int bar_clc = bar_iempty + 16;
     static constexpr int bar_near = bar_clc + 8;          // an item's copies are all but issued
-    static constexpr int misc = bar_near + 8;             // tmem base (4 B), abort flag (4 B)
-    static constexpr int clc = (misc + 8 + 15) / 16 * 16; // [2] launch-control responses
+    static constexpr int misc = bar_near + 8;             // tmem base, abort flag, items finished, items claimed (4 B each)
+    static constexpr int clc = (misc + 16 + 15) / 16 * 16;  // [2] launch-control responses
     static constexpr int items = clc + 32;                // [2] WorkItem
     static constexpr int ranges = items + 64;             // [2][128] int2: the rows' key ranges
     static constexpr int red = ranges + 2 * kBlockQ * 8;  // [2][groups - 1][5][128] floats: the other groups' states
@@ -216,6 +216,15 @@ __device__ __forceinline__ void store_scored(const FwdParams& p, size_t row, int
     }
 }
 
+// Rows of a work item that nobody will finish: their outputs, or this split's
+// parts of them, become NaN.
+__device__ __forceinline__ void mark_item(const FwdParams& p, const WorkItem& item) {
+    const float nan = __int_as_float(0x7fc00000);
+    for (int r = threadIdx.x; r < kBlockQ && item.q0 + r < p.Nq; r += blockDim.x)
+        store_scored(p, static_cast<size_t>(item.bh) * p.Nq + item.q0 + r, item.split, RowState{nan, nan, nan, nan, nan},
+                     false, true);
+}
+
 // This split's share of key tiles [lo, hi).
 __device__ __forceinline__ int2 split_tiles(int lo, int hi, int split, int num_splits) {
     const int n = max(0, hi - lo), per = (n + num_splits - 1) / num_splits;
@@ -252,6 +261,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
+    int* progress = reinterpret_cast<int*>(gbase + L::misc + 8);  // work items finished, and claimed
     WorkItem* items = reinterpret_cast<WorkItem*>(gbase + L::items);
     int2* ranges = reinterpret_cast<int2*>(gbase + L::ranges);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -274,6 +284,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         mbar_init(base + L::bar_clc, 1);
         mbar_init(base + L::bar_near, 1);
         *abort_flag = 0;
+        progress[0] = progress[1] = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -343,7 +354,10 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         // done, so that they go to the CTAs that end first (256 items of 4 to 16 tiles: 67 us when
         // always early, 53 us so; 2048 items of 1 to 23 tiles: 197 us when always late, 175 so).
         // These two waits last as long as whole items do: the limit of a wait is theirs per key tile.
-        int unit = blockIdx.x, last_tiles = 0, before_tiles = 0;
+        // After a give-up `claimed` says which items the CTA answers for: the last one of them may be
+        // one whose response came late and that no role has seen.
+        int unit = blockIdx.x, last_tiles = 0, before_tiles = 0, claimed = 0;
+        bool gave_up = false;
         WaitCtx wi = wc;
         for (int k = 0;; ++k) {
             const int slot = k & 1;
@@ -362,10 +376,8 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                         mbar_arrive_expect_tx(base + L::bar_clc, 16);
                         clc_request(response, base + L::bar_clc);
                     }
-                    if (!__all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, (k - 1) & 1, wc, kErrWaitOther))) {
-                        if (lane == 0) score_drain(base + L::bar_clc, (k - 1) & 1, kSfDrainNs);
-                        break;
-                    }
+                    gave_up = !__all_sync(0xffffffffu, mbar_wait(base + L::bar_clc, (k - 1) & 1, wc, kErrWaitOther));
+                    if (gave_up && !__all_sync(0xffffffffu, score_drain(base + L::bar_clc, (k - 1) & 1, kSfDrainNs))) break;
                     unit = clc_response(response);
                     fence_proxy_async_smem();  // the response is read before its slot is written again
                     __syncwarp();
@@ -402,10 +414,13 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             before_tiles = last_tiles;
             last_tiles = item.n_tiles;
             if (lane == 0) items[slot] = item;
+            claimed = k + 1;
             __syncwarp();
+            if (gave_up) break;
             if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);
             if (unit < 0) break;
         }
+        if (lane == 0) progress[1] = claimed;
     } else if (warp == 1 || warp == kS2Warp) {
         // ------------------------------------------------------------ MMA: S1 (warp 1), S2 (last warp)
         if (lane == 0) {
@@ -419,14 +434,17 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             const uint32_t dcol = second ? kBlockK : 0u;
             int it = 0, n_q = 0, s = 0;
             uint32_t kph = 0, k_lo = k_lo0;
-            // test aid: a wait on a barrier that nothing arrives on gives up after wait_ns
-            bool ok = !(p.inject_stall && blockIdx.x == 0 && !second && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther));
+            bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
                 if (!mbar_wait(base + L::bar_ifull + 8 * slot, (k >> 1) & 1, wc, kErrWaitOther)) break;
                 const int n_tiles = items[slot].n_tiles, valid = items[slot].valid;
                 mbar_arrive(base + L::bar_iempty + 8 * slot);
                 if (!valid) break;
+                // test aid: with its first item taken up, so that the CTA goes on to claim the next one,
+                // a wait on a barrier that nothing arrives on gives up after wait_ns
+                if (p.inject_stall && blockIdx.x == 0 && !second && k == 0 && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther))
+                    break;
                 if (n_tiles == 0) continue;
                 if (!mbar_wait(base + L::bar_q, n_q & 1, wc, kErrWaitQ)) break;
                 ++n_q;
@@ -578,7 +596,10 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                     store_scored(p, static_cast<size_t>(bh) * p.Nq + i, item.split, st, range.x >= range.y,
                                  !go_on || *abort_flag);
             }
-            if (!go_on) break;
+            if (!go_on) {
+                if (wg == 0 && row == 0) progress[0] = k;
+                break;
+            }
         }
     }
 
@@ -588,6 +609,12 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+    // A give-up leaves the item in progress and up to one more that was claimed; both are still in the ring
+    // (an item is claimed once every role has taken up the one before).
+    if (*abort_flag) {
+        for (int k = progress[0]; k < progress[1]; ++k)
+            if (items[k & 1].valid) mark_item(p, items[k & 1]);
     }
 }
 
