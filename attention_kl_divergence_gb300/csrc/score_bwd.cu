@@ -127,6 +127,30 @@ __global__ void __launch_bounds__(256) score_prepare_kernel(const __grid_constan
     if ((r & 31) == 0) kb.bounds[r >> 5] = make_int4(lo, hi, in_lo, in_hi);
 }
 
+// After a give-up: NaN in this CTA's rows of dK (or of its part) and in the dQ
+// rows of iterations [m0, m0 + n), the query tiles [t0, t0 + per_head) of each of
+// the key head's query heads in turn.  Other CTAs' reductions keep a NaN.
+__device__ __forceinline__ void mark_gradients(const BwdParams& p, const ScoreParams& sp, int d, int b, int hk, int n0,
+                                               int split, int t0, int per_head, int64_t m0, int64_t n) {
+    const float nan = __int_as_float(0x7fc00000);
+    const size_t row = (static_cast<size_t>(b) * p.H_kv + hk) * p.Nk + n0;
+    const int keys = min(kBlockK, p.Nk - n0) * d;
+    float* part = sp.dk_parts + static_cast<size_t>(split) * p.B * p.H_kv * p.Nk * d + row * d;
+    for (int e = threadIdx.x; e < keys; e += blockDim.x) {
+        if (p.num_splits > 1)
+            part[e] = nan;
+        else if (p.grad_bf16)
+            static_cast<uint16_t*>(p.dK)[row * d + e] = 0x7fc0;
+        else
+            static_cast<float*>(p.dK)[row * d + e] = nan;
+    }
+    for (int64_t m = m0; m < m0 + n; ++m) {
+        const int h = hk * p.kv_group + static_cast<int>(m / per_head), r0 = (t0 + static_cast<int>(m % per_head)) * kBwdTile;
+        float* dq = p.dQacc + ((static_cast<size_t>(b) * p.H + h) * p.Nq + r0) * d;
+        for (int e = threadIdx.x; e < min(kBwdTile, p.Nq - r0) * d; e += blockDim.x) dq[e] = nan;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // CTA = 128 keys; 64-row query tiles.  Warps: 0 copies, 1 TMEM +
 // score MMAs, 2-9 recompute/dS (two warpgroups, one key per thread, each taking
@@ -188,12 +212,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // The layout uses every byte it asked for, so the dynamic shared memory
     // base itself must be 1024-byte aligned (128-byte swizzle atoms); if it is
-    // not, report it and leave before touching any barrier or tensor memory.
+    // not, report it and leave (below) before touching any barrier or tensor memory.
     const uint32_t base = smem_u32(smem_raw);
-    if (base & 1023u) {
-        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kErrSmemAlign);
-        return;
-    }
     uint8_t* gbase = smem_raw;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
@@ -213,6 +233,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
     const int n0 = nt * kBlockK;
     const uint32_t kt_tile = base + (SETTING == 1 ? L::k2 : L::k1);  // trainable keys
+    if (base & 1023u) {
+        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kErrSmemAlign);
+        mark_gradients(p, sp, D, b, hk, n0, split, 0, p.num_q_tiles, 0, static_cast<int64_t>(p.num_q_tiles) * p.kv_group);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tK1);
@@ -713,6 +738,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (*abort_flag) mark_gradients(p, sp, D, b, hk, n0, split, m_start, per_head, m0, n_tiles);
 }
 
 // 8 elements of dQ (float32 -> bf16, when asked for) or of dK (the sum of its

@@ -50,3 +50,30 @@ def test_forward_rows_are_right_or_marked(H, Nq, splits, kind):
     assert bool(torch.isnan(sk.kl_score_fwd(sc, *qk, num_splits=splits, **STALL)[0]).any())
     got = sk.kl_score_fwd(sc, *qk, num_splits=splits, workspace=ws, out=out)
     assert sk.workspace_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# H, Nq, splits, type: one part of dK, several; bf16 goes through float32 sums of dQ
+@pytest.mark.parametrize("setting", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("d,Nq,splits", [(64, 8, 1), (64, 300, 1), (128, 300, 3), (128, 600, 2)])
+def test_gradients_are_right_or_marked(d, Nq, splits, dtype, setting):
+    qk = make_qk(1, 4, Nq, 600, d, 0.3, seed=5, device=DEV, H_kv=2)
+    sc = sk.Scores(50.0, 50.0)
+    rows = sk.kl_score_fwd(sc, *qk)
+    g = torch.rand(1, 4, Nq, device=DEV)
+    want = sk.kl_score_bwd(setting, sc, g, *qk, *rows, num_splits=splits, grad_dtype=dtype)
+    ws = stale_workspace(sk.score_bwd_plan(*qk[:2], setting, grad_dtype=dtype, num_splits=splits).workspace_bytes)
+    out = tuple(torch.full_like(t, STALE) for t in want)
+    sk.kl_score_bwd(setting, sc, g, *qk, *rows, num_splits=splits, grad_dtype=dtype, workspace=ws, out=out, **STALL)
+    assert sk.workspace_status(ws) != 0
+    # the first CTA: the first key tile of the first key head, and rows of its two query heads
+    lost = right_or_nan(out[1], want[1])
+    assert bool(lost[0, 0, :128].all()) and not bool(lost[0, 0, 128:].any()) and not bool(lost[0, 1].any())
+    lost = torch.isnan(out[0])
+    assert bool(lost.any()) and not bool(lost[0, 2:].any()) and bool(lost.eq(lost[..., :1]).all())
+    # sums of up to 5 key tiles in another order: 2 * 5 * 2^-24 of the magnitudes, taken as the largest value; one step of bf16
+    near = (out[0].double() - want[0].double()).abs() <= 1e-5 * want[0].double().abs().max() + \
+        (2.0 ** -7 * want[0].double().abs() if dtype == BF16 else 0)
+    assert bool((lost | near).all())
+    got = sk.kl_score_bwd(setting, sc, g, *qk, *rows, num_splits=splits, grad_dtype=dtype, workspace=ws, out=out)
+    assert sk.workspace_status(ws) == 0 and torch.equal(got[1], want[1]) and bool(torch.isfinite(got[0].float()).all())
