@@ -395,6 +395,7 @@ class AttentionKL(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, Q1, K1, Q2, K2, causal=False, scale=None):
+        _guard_capture(Q1, K1, Q2, K2)
         KL, L1, L2 = kl_fwd(Q1, K1, Q2, K2, causal=causal, scale=scale)
         ctx.save_for_backward(Q1, K1, Q2, K2, KL, L1, L2)
         ctx.causal, ctx.scale = causal, scale
@@ -472,16 +473,21 @@ def _on(device, function, *args):
 
 
 def _guard_capture(*inputs):
-    """Refuse to record a graph in a CUDA-graph capture on leaves that an earlier, still living eager graph uses: the
-    leaves' gradient accumulators belong to that graph's stream, and running them inside the capture breaks it (at
-    worst the process ends).  Eager calls mark the accumulators; the marks die with the graphs."""
+    """Refuse to record a graph in a CUDA-graph capture on leaves (or views of leaves) that a still living graph made on
+    the default stream uses: the leaves' gradient accumulators belong to that stream, which cannot be captured, and
+    running them inside the capture breaks it (at worst the process ends).  An accumulator of any other stream, a
+    warm-up's, joins the capture.  Calls mark the accumulators with the stream they found current; the marks die with
+    the graphs."""
     for t in inputs:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad and t.grad_fn is None:
-            stream = _raw_stream(t.device.index)
-            made_on = torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault("streamkl stream", stream)
-            if made_on != stream and torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("an eager autograd graph of these leaves, made on another stream, is still alive: "
-                                   "drop it (or make it on the capturing stream) before the capture")
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad:
+            leaf = t if t.grad_fn is None else t._base
+            if leaf is None or leaf.grad_fn is not None or not leaf.requires_grad:
+                continue
+            made_on = torch.autograd.graph.get_gradient_edge(leaf).node.metadata.setdefault(
+                "streamkl stream", _raw_stream(t.device.index))
+            if made_on == 0 and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("an autograd graph of these leaves, made on the default stream, is still alive: drop it "
+                                   "(or make it on a stream of its own) before the capture")
 
 
 def _address(t):
