@@ -352,7 +352,7 @@ streamkl_status streamkl_key_ranges(int32_t B, int32_t Nq, int32_t Nk, int causa
     const void* ptrs[7] = {q_lengths, k_lengths, prefix, docs, begin, end, offset};
     for (const void* p : ptrs)
         if (!aligned4(p)) return STREAMKL_ERR_INVALID_ARG;
-    if (B > 65535) return STREAMKL_ERR_UNSUPPORTED;
+    if (B > 65535 || Nq > INT32_MAX - 255) return STREAMKL_ERR_UNSUPPORTED;  // the grid, counted in blocks of 256 rows
     KeyRangeParams p{};
     p.B = B;
     p.Nq = Nq;

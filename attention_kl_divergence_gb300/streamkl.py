@@ -534,6 +534,10 @@ def key_ranges(B, Nq, Nk, device, causal=True, window=0, prefix=None, docs=None,
     k_lengths with j <= p (causal), p - window < j < p + window (window > 0), any j < prefix[b] (int32 [B], not with
     window or docs), and of p's document alone (docs: nondecreasing int32 bounds, [M] for every batch or [B, M]; document
     m is docs[m] <= j < docs[m + 1])."""
+    B, Nq, Nk, window = int(B), int(Nq), int(Nk), int(window)
+    for name, v in (("B", B), ("Nq", Nq), ("Nk", Nk), ("window", window)):
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, got {v}")
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError("device must be a CUDA device")
@@ -550,7 +554,7 @@ def key_ranges(B, Nq, Nk, device, causal=True, window=0, prefix=None, docs=None,
             _check_tensor("docs", docs, (B, bounds) if per_batch else (bounds,), torch.int32, device)
         begin, end = (torch.empty((B, Nq), dtype=torch.int32, device=device) for _ in range(2))
         offset = torch.empty((B,), dtype=torch.int32, device=device)
-        _raise(load().streamkl_key_ranges(B, Nq, Nk, int(bool(causal)), int(window), _ptr(q_lengths), _ptr(k_lengths),
+        _raise(load().streamkl_key_ranges(B, Nq, Nk, int(bool(causal)), window, _ptr(q_lengths), _ptr(k_lengths),
                                           _ptr(prefix), _ptr(docs), bounds, per_batch, _ptr(begin), _ptr(end),
                                           _ptr(offset), _stream(device)), "streamkl_key_ranges")
     return begin, end, offset
