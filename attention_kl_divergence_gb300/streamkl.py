@@ -685,7 +685,9 @@ class ScoredAttentionKL(torch.autograd.Function):
 def rope_table(rows, rot, device, base=10000.0, inv_freq=None) -> torch.Tensor:
     """Cosines and sines of the positions below ``rows`` as float32 [rows, rot/2, 2],
     from angles in float64.  inv_freq (rot/2 values) replaces base^(-2e/rot), for
-    scaled frequencies.  Made once and kept; it synchronises nothing."""
+    scaled frequencies.  Made once and kept.  Frequencies from the host (the default's
+    too) are copied to the device first, which waits for the current stream and cannot
+    be captured; a float64 tensor on the device is read as it is."""
     rot, rows = int(rot), int(rows)
     if rot < 8 or rot % 8 or rot > 128 or rows < 1:
         raise ValueError(f"rot must be a multiple of 8 up to 128 and rows at least 1, got {rot} and {rows}")
