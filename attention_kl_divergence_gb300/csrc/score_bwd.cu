@@ -497,12 +497,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                     }
                     tc_commit(base + L::bar_dsempty + 8 * dsb);
                     tc_commit(base + L::bar_qtempty + 8 * s2);
-                    if (L::kNumDs == 1) {
-                        dsph ^= 1;
-                    } else {
-                        dsph ^= dsb;  // a buffer's phase flips each time it comes round again
-                        dsb ^= 1;
-                    }
+                    dsph ^= dsb;  // a buffer's phase flips each time it comes round again
+                    dsb ^= 1;
                     if (++s2 == L::kQt) {
                         s2 = 0;
                         qt_lo = qt_lo0;
