@@ -60,7 +60,7 @@ struct ScoreTileSmem {
     static constexpr int bar_iempty = bar_ifull + 16;
     static constexpr int bar_clc = bar_iempty + 16;
     static constexpr int bar_near = bar_clc + 8;          // an item's copies are all but issued
-    static constexpr int misc = bar_near + 8;             // tmem base, abort flag, items finished, items claimed (4 B each)
+    static constexpr int misc = bar_near + 8;             // tmem base, abort flag, items claimed (4 B each)
     static constexpr int clc = (misc + 16 + 15) / 16 * 16;  // [2] launch-control responses
     static constexpr int items = clc + 32;                // [2] WorkItem
     static constexpr int ranges = items + 64;             // [2][128] int2: the rows' key ranges
@@ -216,13 +216,17 @@ __device__ __forceinline__ void store_scored(const FwdParams& p, size_t row, int
     }
 }
 
-// Rows of a work item that nobody will finish: their outputs, or this split's
-// parts of them, become NaN.
-__device__ __forceinline__ void mark_item(const FwdParams& p, const WorkItem& item) {
+// Rows of the last two claimed work items: their outputs, or their split's parts
+// of them, become NaN.
+__device__ __noinline__ void mark_claimed(const FwdParams& p, const WorkItem* items, int claims) {
     const float nan = __int_as_float(0x7fc00000);
-    for (int r = threadIdx.x; r < kBlockQ && item.q0 + r < p.Nq; r += blockDim.x)
-        store_scored(p, static_cast<size_t>(item.bh) * p.Nq + item.q0 + r, item.split, RowState{nan, nan, nan, nan, nan},
-                     false, true);
+    for (int k = max(0, claims - 2); k < claims; ++k) {
+        const WorkItem& item = items[k & 1];
+        if (!item.valid) continue;
+        for (int r = threadIdx.x; r < kBlockQ && item.q0 + r < p.Nq; r += blockDim.x)
+            store_scored(p, static_cast<size_t>(item.bh) * p.Nq + item.q0 + r, item.split, RowState{nan, nan, nan, nan, nan},
+                         false, true);
+    }
 }
 
 // This split's share of key tiles [lo, hi).
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
-    int* progress = reinterpret_cast<int*>(gbase + L::misc + 8);  // work items finished, and claimed
+    int* claims = reinterpret_cast<int*>(gbase + L::misc + 8);  // work items claimed
     WorkItem* items = reinterpret_cast<WorkItem*>(gbase + L::items);
     int2* ranges = reinterpret_cast<int2*>(gbase + L::ranges);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         mbar_init(base + L::bar_clc, 1);
         mbar_init(base + L::bar_near, 1);
         *abort_flag = 0;
-        progress[0] = progress[1] = 0;
+        *claims = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -354,9 +358,9 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         // done, so that they go to the CTAs that end first (256 items of 4 to 16 tiles: 67 us when
         // always early, 53 us so; 2048 items of 1 to 23 tiles: 197 us when always late, 175 so).
         // These two waits last as long as whole items do: the limit of a wait is theirs per key tile.
-        // After a give-up `claimed` says which items the CTA answers for: the last one of them may be
+        // After a give-up `claims` says which items the CTA answers for: the last one of them may be
         // one whose response came late and that no role has seen.
-        int unit = blockIdx.x, last_tiles = 0, before_tiles = 0, claimed = 0;
+        int unit = blockIdx.x, last_tiles = 0, before_tiles = 0;
         bool gave_up = false;
         WaitCtx wi = wc;
         for (int k = 0;; ++k) {
@@ -413,14 +417,12 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             }
             before_tiles = last_tiles;
             last_tiles = item.n_tiles;
-            if (lane == 0) items[slot] = item;
-            claimed = k + 1;
+            if (lane == 0) items[slot] = item, *claims = k + 1;
             __syncwarp();
             if (gave_up) break;
             if (lane == 0) mbar_arrive(base + L::bar_ifull + 8 * slot);
             if (unit < 0) break;
         }
-        if (lane == 0) progress[1] = claimed;
     } else if (warp == 1 || warp == kS2Warp) {
         // ------------------------------------------------------------ MMA: S1 (warp 1), S2 (last warp)
         if (lane == 0) {
@@ -434,17 +436,17 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
             const uint32_t dcol = second ? kBlockK : 0u;
             int it = 0, n_q = 0, s = 0;
             uint32_t kph = 0, k_lo = k_lo0;
-            bool ok = true;
+            // test aid: a wait on a barrier that nothing arrives on gives up after wait_ns; the first item counts as
+            // taken up, so that the CTA goes on to claim the next one
+            const bool stall = p.inject_stall && blockIdx.x == 0 && !second;
+            if (stall) mbar_arrive(base + L::bar_iempty);
+            bool ok = !(stall && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther));
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
                 if (!mbar_wait(base + L::bar_ifull + 8 * slot, (k >> 1) & 1, wc, kErrWaitOther)) break;
                 const int n_tiles = items[slot].n_tiles, valid = items[slot].valid;
                 mbar_arrive(base + L::bar_iempty + 8 * slot);
                 if (!valid) break;
-                // test aid: with its first item taken up, so that the CTA goes on to claim the next one,
-                // a wait on a barrier that nothing arrives on gives up after wait_ns
-                if (p.inject_stall && blockIdx.x == 0 && !second && k == 0 && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther))
-                    break;
                 if (n_tiles == 0) continue;
                 if (!mbar_wait(base + L::bar_q, n_q & 1, wc, kErrWaitQ)) break;
                 ++n_q;
@@ -596,10 +598,7 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
                     store_scored(p, static_cast<size_t>(bh) * p.Nq + i, item.split, st, range.x >= range.y,
                                  !go_on || *abort_flag);
             }
-            if (!go_on) {
-                if (wg == 0 && row == 0) progress[0] = k;
-                break;
-            }
+            if (!go_on) break;
         }
     }
 
@@ -610,12 +609,9 @@ __global__ void __launch_bounds__(sf_threads(MODE), 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    // A give-up leaves the item in progress and up to one more that was claimed; both are still in the ring
-    // (an item is claimed once every role has taken up the one before).
-    if (*abort_flag) {
-        for (int k = progress[0]; k < progress[1]; ++k)
-            if (items[k & 1].valid) mark_item(p, items[k & 1]);
-    }
+    // An item is claimed once every role has taken up the one before: after a give-up the unfinished ones
+    // are among the last two, which are still in the ring.
+    if (*abort_flag) mark_claimed(p, items, *claims);
 }
 
 // ---------------------------------------------------------------------------
