@@ -57,7 +57,9 @@ streamkl_status check_score(const streamkl_score* s) {
     return STREAMKL_OK;
 }
 
-// Kernel variant and parameters.
+// Kernel variant and parameters.  The variant is that of the worse side: a side
+// that needs running maxima, or no cap, takes the other along (8192 causal rows, 32
+// heads: both sides capped at 50 729 us, one of them 773, both at 60 885; plain 511).
 streamkl_status make_score(const streamkl_score* s, float scale, int causal, ScoreParams* out, int* mode) {
     *out = ScoreParams{};
     const streamkl_score none{};
@@ -151,8 +153,13 @@ struct ScoreBwdPlan {
 // tiles with up to n iterations each takes about the larger of the SMs' average
 // and the longest CTA, a CTA costs about 5 more (start, key tiles, dK), and
 // summing the parts about 4.  Splits are taken when they save a fifth.  Measured
-// (us): 64 key tiles of up to 128 iterations, 1 split 277, 3 112, 4 90, 5 96,
-// 8 107; 114 of up to 38, 1 78, 2 48, 3 56; 192 of up to 16, 1 37, 2 41.
+// (whole backward, us): 64 key tiles of up to 128 iterations, 1 split 296, 2 161,
+// 3 117, 4 94, 5 105, 8 113; 114 of up to 38, 1 73, 2 49, 3 58; 192 of up to 16,
+// 1 44, 2 56.  The ranges lie on the device, so every mask counts as causal.  What
+// that costs (chosen splits first, the best ones second): full masks 167 at 4
+// against 165 at 2, 96 at 2 against 88 at 4, 85 at 1 against 76 at 2; windows of a
+// sixteenth 52 at 4 against 44 at 2, 37 at 2 against 27 at 1; documents of an
+// eighth to three eighths within 8% in all three.
 int bwd_splits(int64_t units, int64_t iterations, int sms) {
     auto cost = [&](int64_t s) {
         const double mean = (units * iterations * 0.5 + double(units) * s * 5) / sms;

@@ -27,7 +27,8 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrHeads = 8;                  // heads of one token that a warp takes at a time
-// CTAs of the gradient pass per SM, all resident: 16 KB of loads in flight each.
+// CTAs of the gradient pass per SM, all resident.  Loads in flight of each: 32 KB
+// for d = 128 and bf16 gradients, 48 KB for float32 ones, half of it for d = 64.
 // 64K tokens of 32 + 8 heads: 2 CTAs 371 us, 3 341 us, 4 (half the heads at a
 // time, to fit the registers) 415 us.
 constexpr int kNrBwdCtas = 3;

@@ -136,7 +136,9 @@ __device__ __forceinline__ void cap_mid(float (&z)[W], const ScoreSide& s) {
 
 // z -> x in place for both sides, without the bias.  A warp takes the shortest
 // form that fits every score of its lanes (those with `use`: the others' results
-// are not used).
+// are not used), of both sides: one vote, one branch.  8192 causal rows, caps of 50:
+// 730 us where the 4 terms do, 1040 where a teacher of nine times the scores takes
+// the student along to the longer forms.  A vote per side has not been measured.
 template <int MODE, int W>
 __device__ __forceinline__ void cap_scores(float (&z1)[W], float (&z2)[W], const ScoreSide& s1, const ScoreSide& s2,
                                            bool use = true) {

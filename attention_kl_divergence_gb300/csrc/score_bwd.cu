@@ -17,13 +17,15 @@
 // keys have in common cancels in dQ, where the dS of a row sum to zero, and those
 // roundings do not.  Keys with an offset of 16 beside a noise of 1 in an eighth of
 // the channels: dQ off by 0.0085 of its norm with one term, by the output's own
-// rounding, 0.0017, with two.
+// rounding, 0.0017, with two.  With one term the kernel took 1260 us instead of
+// 1411; with two in dQ and one in dK as long as with two in both.
 //
 // 8192 causal rows, 32 heads on 8 key heads, caps of 50, bf16 gradients: prepare
-// 21 us, gradients 1260 us, finish 30 us.  Without caps the 28 MMAs of a tile
-// (about 60 cycles each, whatever N <= 128 is) and their handoffs take 2130
-// cycles; with caps the update's dependent steps take 2800 (twice the update
-// warps, or a second buffer for the scores, changed nothing).
+// 21 us, gradients 1411 us, finish 30 us: about 3100 cycles of an SM per tile, and
+// 2900 without caps.  Without caps the 32 MMAs of a tile (about 60 cycles each,
+// whatever N <= 128 is) and their handoffs are the bound, with caps the update's
+// dependent steps (the tensor pipe is busy half of the cycles; with one dS term
+// twice the update warps or a second buffer for the scores changed nothing).
 #include <algorithm>
 
 #include "bwd_common.cuh"

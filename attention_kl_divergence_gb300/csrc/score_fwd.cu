@@ -9,9 +9,9 @@
 // what differs is the update: z -> x (score.cuh), the range of each row, and for
 // bounded scores a sum of 2^x without a running maximum.
 //
-// 8192 causal rows, 32 heads: plain scores 519 to 531 us (1.05 PFLOP/s), caps of
-// 50 730 us (0.75).  The update bounds both; with caps the FMA pipe is busy 62% of
-// the cycles, issue slots 65%, the tensor pipe 33%.
+// 8192 causal rows, 32 heads: plain scores 511 us (1.08 PFLOP/s), caps of 50 730
+// us (0.75).  The update bounds both; with caps the FMA pipe is busy 62% of the
+// cycles, issue slots 65%, the tensor pipe 33%.
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"

@@ -495,7 +495,8 @@ def _address(t):
 
 
 def _scratch(workspace, nbytes, device):
-    """A caller's workspace, checked, or a new one.  A new one is not cleared: its error word is never read."""
+    """A caller's workspace, checked, or a new one.  A new one is not cleared: its error word is never read (the score
+    kernels mark with NaN what a give-up leaves undone; the norm's wait for nothing)."""
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     return _check_workspace(workspace, nbytes, device)
@@ -586,7 +587,8 @@ def score_bwd_plan(Q1, K1, setting, grad_dtype=torch.float32, num_splits=0) -> P
 def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0, workspace=None, out=None,
                  wait_limit_ns=0, debug_flags=0):
     """Per-row KL(P1 || P2), LSE1, LSE2 as float32 [B, H, Nq] for the scores that ``scores`` describes.  A row that
-    sees no key has KL = 0 and LSE = -inf; what a row does not see (NaN included) has no effect on it."""
+    sees no key has KL = 0 and LSE = -inf; what a row does not see (NaN included) has no effect on it.  Rows that a
+    give-up of a bounded wait left unfinished are NaN."""
     given = _scores(scores).tensors()
     num_splits, wait_limit_ns, debug_flags = int(num_splits), int(wait_limit_ns), int(debug_flags)
     key, known = _lookup("score_fwd", _tensors(Q1, K1, Q2, K2, *given), num_splits, wait_limit_ns, debug_flags)
@@ -616,8 +618,9 @@ def kl_score_fwd(scores, Q1, K1, Q2, K2, causal=False, scale=None, num_splits=0,
 def kl_score_bwd(setting, scores, g, Q1, K1, Q2, K2, KL, LSE1, LSE2, causal=False, scale=None, workspace=None, out=None,
                  wait_limit_ns=0, debug_flags=0, grad_dtype=torch.float32, num_splits=0):
     """(dQ, dK) of the trainable side of kl_score_fwd: setting 1 -> (Q2, K2), 2 -> (Q1, K1), as kl_bwd.  dQ is added
-    up in float32 in no fixed order (like kl_bwd's fused mode); dK is the same on every run.  num_splits: CTAs that
-    share a key tile's query rows (0 = automatic)."""
+    up in float32 in no fixed order (like kl_bwd's fused mode); dK is the same on every run.  bf16 gradients are the
+    float32 ones, rounded once.  num_splits: CTAs that share a key tile's query rows (0 = automatic).  Rows of either
+    gradient that a give-up of a bounded wait left without some of their terms are NaN."""
     given = _scores(scores).tensors()
     setting, num_splits, wait_limit_ns, debug_flags = int(setting), int(num_splits), int(wait_limit_ns), int(debug_flags)
     key, known = _lookup("score_bwd", _tensors(Q1, K1, Q2, K2, g, KL, LSE1, LSE2, *given), setting, grad_dtype, wait_limit_ns,

@@ -256,6 +256,9 @@ STREAMKL_API streamkl_status streamkl_noalloc_status(streamkl_stream_t stream, u
  *    the same on every run); opt->bwd_mode must be 0; opt->num_splits sets the
  *    CTAs that share the query rows of a key tile (0 = automatic).  Its gradients include the slope of the cap,
  *    1 - tanh^2.  begin, end, offset, slopes, caps and scale as in the forward.
+ *    bf16 gradients are the float32 ones, rounded once.
+ *  - After a bounded wait has given up (the workspace's error word says so), the
+ *    rows of KL and LSE, of dK and of dQ that lack anything are NaN.
  *  - Layouts, strides, dtypes, shared keys, workspace and streams as above.
  * ------------------------------------------------------------------------- */
 typedef struct {
@@ -288,7 +291,8 @@ STREAMKL_API streamkl_status streamkl_score_bwd(const streamkl_shape* shape, con
 
 /* Key ranges (begin, end, offset of streamkl_score) from the usual masks.  Query
  * row i < q_lengths[b] stands at key position p = i + offset[b], offset[b] =
- * k_lengths[b] - q_lengths[b] (lengths NULL: Nq, Nk; clamped to them); later
+ * k_lengths[b] - q_lengths[b] (lengths NULL: Nq, Nk; clamped to them; B up to
+ * 65535 and Nq up to 2^31 - 256, UNSUPPORTED beyond); later
  * rows see nothing.  It sees the keys j < k_lengths[b] with
  *   causal:      j <= p;
  *   window > 0:  p - window < j < p + window;
