@@ -94,18 +94,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 }  // namespace
 
-// 4-D map over [B, H, N, d] bf16 with a (64 x rows x heads) box, 128-byte
+// 4-D map over [B, heads, N, d] bf16 with a (64 x rows x heads) box, 128-byte
 // swizzle; rows outside [0, N) read as zero.  A box of several heads lands
 // in shared memory as heads * rows consecutive 128-byte rows, head-major.
-bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads) {
+bool make_map_strided(CUtensorMap* m, const void* ptr, int d, int64_t N, int heads, int B, const streamkl_strides& st,
+                      int box_rows, int box_heads) {
     auto enc = encode_fn();
     if (!enc) return false;
-    const int64_t N = is_q ? s->Nq : s->Nk;
-    const int64_t sb = is_q ? s->q_stride_b : s->k_stride_b;
-    const int64_t sh = is_q ? s->q_stride_h : s->k_stride_h;
-    const int64_t sn = is_q ? s->q_stride_n : s->k_stride_n;
-    cuuint64_t dims[4] = {cuuint64_t(s->d), cuuint64_t(N), cuuint64_t(is_q ? s->H : kv_heads(s)), cuuint64_t(s->B)};
-    cuuint64_t strides[3] = {cuuint64_t(sn * 2), cuuint64_t(sh * 2), cuuint64_t(sb * 2)};
+    cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(N), cuuint64_t(heads), cuuint64_t(B)};
+    cuuint64_t strides[3] = {cuuint64_t(st.n * 2), cuuint64_t(st.h * 2), cuuint64_t(st.b * 2)};
     cuuint32_t box[4] = {cuuint32_t(kSwizzleCols), cuuint32_t(box_rows), cuuint32_t(box_heads), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     auto encode = [&] {
@@ -122,6 +119,12 @@ bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_
         r = encode();
     }
     return r == CUDA_SUCCESS;
+}
+
+bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads) {
+    const streamkl_strides q{s->q_stride_b, s->q_stride_h, s->q_stride_n}, k{s->k_stride_b, s->k_stride_h, s->k_stride_n};
+    return make_map_strided(m, ptr, s->d, is_q ? s->Nq : s->Nk, is_q ? s->H : kv_heads(s), s->B, is_q ? q : k, box_rows,
+                            box_heads);
 }
 
 float resolve_scale(float scale, int d) {

@@ -1,0 +1,176 @@
+// api_attn.cu -- C ABI of the attention over whole prompts: argument validation,
+// launch planning and launches on the caller's stream.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "attn.cuh"
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+
+using namespace streamkl;
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Element strides of a [B, heads, N, d] tensor: multiples of 8 (16 bytes), rows
+// that do not overlap; an axis with one entry has a stride that is never used.
+bool strides_ok(const streamkl_strides& s, int B, int heads, int N, int d) {
+    const int64_t st[3] = {s.b, s.h, s.n};
+    const int n[3] = {B, heads, N};
+    for (int k = 0; k < 3; ++k)
+        if (n[k] > 1 && (st[k] < d || st[k] % 8 != 0 || st[k] > (int64_t(1) << 38))) return false;
+    return true;
+}
+
+// The strides that a tensor map gets: those of unused axes are any valid ones.
+streamkl_strides used(const streamkl_strides& s, int B, int heads, int N, int d) {
+    return {B > 1 ? s.b : d, heads > 1 ? s.h : d, N > 1 ? s.n : d};
+}
+
+streamkl_status check_desc(const streamkl_attn* s, bool backward) {
+    if (!s) return STREAMKL_ERR_INVALID_ARG;
+    if (s->B < 1 || s->H < 1 || s->H_kv < 1 || s->Nq < 1 || s->Nk < 1 || s->H % s->H_kv != 0) return STREAMKL_ERR_INVALID_ARG;
+    if (s->d != 64 && s->d != 128) return STREAMKL_ERR_UNSUPPORTED;
+    if (!strides_ok(s->q, s->B, s->H, s->Nq, s->d) || !strides_ok(s->k, s->B, s->H_kv, s->Nk, s->d) ||
+        !strides_ok(s->v, s->B, s->H_kv, s->Nk, s->d) || !strides_ok(s->o, s->B, s->H, s->Nq, s->d) ||
+        (backward && !strides_ok(s->d_o, s->B, s->H, s->Nq, s->d)))
+        return STREAMKL_ERR_INVALID_ARG;
+    if (int64_t(s->B) * s->H > (int64_t(1) << 24) || int64_t(s->B) * s->H * s->Nq > (int64_t(1) << 38))
+        return STREAMKL_ERR_UNSUPPORTED;
+    return STREAMKL_OK;
+}
+
+bool options_ok(const streamkl_options* opt) {
+    return !opt || (opt->num_splits >= 0 && opt->grad_bf16 == 0 && opt->bwd_mode == 0 &&
+                    !(opt->debug_flags & ~STREAMKL_DEBUG_INJECT_STALL));
+}
+
+struct AttnFwdPlan {
+    AttnFwdParams p;  // the layout of the work
+    int ctas;
+    size_t ws_bytes;
+};
+
+streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* opt, AttnFwdPlan* pl) {
+    streamkl_status st = check_desc(s, false);
+    if (st != STREAMKL_OK) return st;
+    if (!options_ok(opt)) return STREAMKL_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    AttnFwdParams& p = pl->p;
+    p = AttnFwdParams{};
+    p.B = s->B;
+    p.H = s->H;
+    p.H_kv = s->H_kv;
+    p.Nq = s->Nq;
+    p.Nk = s->Nk;
+    p.group = s->H / s->H_kv;
+    // few rows: as many heads of a key head in a tile as fit (a divisor of the group, so that no tile is ragged)
+    p.heads = 1;
+    p.rows = std::min(s->Nq, kBlockQ);
+    for (int c = p.group; c > 1; --c)
+        if (p.group % c == 0 && int64_t(c) * s->Nq <= kBlockQ) {
+            p.heads = c;
+            break;
+        }
+    p.blocks = p.group / p.heads;
+    p.q_tiles = (s->Nq - 1) / kBlockQ + 1;
+    // two head blocks have the same keys to see; where they do not pair up, neighbouring query tiles do
+    p.pair_heads = p.blocks > 1 && (p.blocks % 2 == 0 || p.q_tiles == 1);
+    p.units_h = p.pair_heads ? (p.blocks + 1) / 2 : p.blocks;
+    p.units_q = p.pair_heads ? p.q_tiles : (p.q_tiles + 1) / 2;
+    const int64_t heads = int64_t(s->B) * s->H_kv * p.units_h, units = heads * p.units_q;
+    if (units > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    const int k_tiles = (s->Nk - 1) / kBlockK + 1;
+    int splits = 1;
+    if (opt && opt->num_splits > 0) {
+        splits = std::min({opt->num_splits, k_tiles, kMaxSplits});
+    } else {
+        const int n = choose_splits(units, k_tiles, sms);
+        if ((k_tiles + n - 1) / n + 3 < k_tiles) splits = n;
+    }
+    if (units * splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    p.num_splits = splits;
+    pl->ctas = static_cast<int>(units * splits);
+    // heads whose tiles are interleaved: about four waves of CTAs, so that their keys stay in L2
+    p.order_group = static_cast<int>(std::min<int64_t>(heads, (4LL * sms + p.units_q - 1) / p.units_q));
+    pl->ws_bytes = kStatusBytes;
+    if (splits > 1) pl->ws_bytes += size_t(splits) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
+    return STREAMKL_OK;
+}
+
+ScoreParams ranges_of(const int32_t* begin, const int32_t* end, const int32_t* offset, int causal) {
+    ScoreParams sp{};
+    sp.begin = begin;
+    sp.end = end;
+    sp.offset = offset;
+    sp.causal = causal ? 1 : 0;
+    return sp;
+}
+
+}  // namespace
+
+extern "C" {
+
+streamkl_status streamkl_attn_fwd_plan(const streamkl_attn* desc, const streamkl_options* opt, streamkl_plan* plan) {
+    if (!plan) return STREAMKL_ERR_INVALID_ARG;
+    AttnFwdPlan pl{};
+    streamkl_status st = plan_attn_fwd(desc, opt, &pl);
+    if (st != STREAMKL_OK) return st;
+    plan->path = 0;
+    plan->num_splits = pl.p.num_splits;
+    plan->num_ctas = pl.ctas;
+    plan->launches = pl.p.num_splits > 1 ? 2 : 1;
+    plan->workspace_bytes = pl.ws_bytes;
+    return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, const void* K, const void* V,
+                                  const int32_t* begin, const int32_t* end, const int32_t* offset, float scale, int causal,
+                                  void* O, void* rest, float* LSE, void* workspace, size_t workspace_bytes,
+                                  const streamkl_options* opt, streamkl_stream_t stream) {
+    streamkl_status st = check_desc(desc, false);
+    if (st != STREAMKL_OK) return st;
+    const void* need[4] = {Q, K, V, O};
+    for (const void* q : need)
+        if (!q || !aligned16(q)) return STREAMKL_ERR_INVALID_ARG;
+    if (!aligned16(rest) || !LSE || !aligned4(LSE) || !aligned4(begin) || !aligned4(end) || !aligned4(offset))
+        return STREAMKL_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
+    AttnFwdPlan pl{};
+    if ((st = plan_attn_fwd(desc, opt, &pl)) != STREAMKL_OK) return st;
+    if (workspace_bytes < pl.ws_bytes) return STREAMKL_ERR_WORKSPACE;
+
+    AttnFwdParams& p = pl.p;
+    CUtensorMap maps[3];
+    const streamkl_attn& s = *desc;
+    if (!make_map_strided(&maps[0], Q, s.d, s.Nq, s.H, s.B, used(s.q, s.B, s.H, s.Nq, s.d), p.rows, p.heads) ||
+        !make_map_strided(&maps[1], K, s.d, s.Nk, s.H_kv, s.B, used(s.k, s.B, s.H_kv, s.Nk, s.d), kBlockK) ||
+        !make_map_strided(&maps[2], V, s.d, s.Nk, s.H_kv, s.B, used(s.v, s.B, s.H_kv, s.Nk, s.d), kBlockK))
+        return STREAMKL_ERR_CUDA;
+    p.c = resolve_scale(scale, s.d) * kLog2e;
+    p.O = O;
+    p.o_b = s.o.b;
+    p.o_h = s.o.h;
+    p.o_n = s.o.n;
+    p.rest = rest;
+    p.LSE = LSE;
+    if (p.num_splits > 1) {
+        p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+        p.part_ml = reinterpret_cast<float2*>(p.part + size_t(p.num_splits) * s.B * s.H * s.Nq * s.d);
+    }
+    p.status = static_cast<unsigned int*>(workspace);
+    p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
+    p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
+    return launch_attn_fwd(s.d, maps, p, ranges_of(begin, end, offset, causal), pl.ctas,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? STREAMKL_OK
+               : STREAMKL_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,37 @@
+// attn.cuh -- parameter blocks of the attention over whole prompts (attn_fwd.cu,
+// attn_bwd.cu).
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "score.cuh"
+
+namespace streamkl {
+
+// Forward.  A 128-row tile holds `heads` query heads of one key head with `rows`
+// rows each (few rows: several heads share a tile; else one head and 128 rows).  A
+// work item is a pair of tiles that read the same keys: two head blocks, or two
+// neighbouring query tiles.
+struct AttnFwdParams {
+    int B, H, H_kv, Nq, Nk;
+    int group;               // query heads per key head
+    int heads, rows;         // of a tile
+    int blocks, q_tiles;     // tiles of a key head: head blocks x query tiles
+    int pair_heads;          // a pair is two head blocks (else two query tiles)
+    int units_h, units_q;    // pairs of a key head
+    int num_splits;
+    int order_group;         // see grouped_order
+    float c;                 // softmax scale * log2(e)
+    void* O;                 // bf16, strided
+    int64_t o_b, o_h, o_n;
+    void* rest;              // bf16 [B, H, Nq, d] or null: O before its rounding, less O
+    float* LSE;              // [B, H, Nq]
+    float* part;             // several splits: [splits][B*H*Nq][d] sums of 2^(x - m) v
+    float2* part_ml;         // [splits][B*H*Nq]: m (log2) and the sum of 2^(x - m)
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int inject_stall;
+};
+
+}  // namespace streamkl

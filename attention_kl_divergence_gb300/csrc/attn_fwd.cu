@@ -1,0 +1,532 @@
+// attn_fwd.cu -- attention over whole prompts on sm_103a, forward.
+//
+//   O_i = sum_j 2^(x_ij - m_i) v_j / l_i,  l_i = sum_j 2^(x_ij - m_i),  x = log2(e) scale q k
+//
+// over the keys of row i's range, one pass over the keys.  m_i is a whole number
+// near the running maximum (at most 2^8 below it): every rescale is by a power of
+// two, exact in the sums, in O and in probabilities already rounded to bf16.
+#include "attn.cuh"
+#include "bwd_common.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "score.cuh"
+
+namespace streamkl {
+
+namespace {
+
+constexpr float kAttnTau = 8.f;  // m may stay this far (log2) below the largest score
+// warps 0-7 softmax (a warpgroup per tile of the pair, a row per thread), 8 copies,
+// 9 MMAs, 10 and 11 look for NaN and infinities in values that some row must not see
+constexpr int kAfThreads = 384;
+
+template <int D>
+struct AttnSmem {
+    static constexpr int kNst = D == 128 ? 5 : 8;      // ring of key and value tiles, alternating
+    static constexpr int kTile = kBlockQ * D * 2;      // 128 rows of q, k or v
+    static constexpr int q = 0;                        // the pair's query tiles
+    static constexpr int kv = 2 * kTile;
+    static constexpr int bar_q = kv + kNst * kTile;    // [2]
+    static constexpr int bar_full = bar_q + 16;        // [kNst]
+    static constexpr int bar_empty = bar_full + 8 * kNst;
+    static constexpr int bar_clean = bar_empty + 8 * kNst;  // [kNst] checks, in turn
+    static constexpr int bar_s = bar_clean + 8 * kNst;      // [2] scores complete
+    static constexpr int bar_p = bar_s + 16;                // [2] probabilities stored
+    static constexpr int bar_o = bar_p + 16;                // [2] output complete
+    static constexpr int bar_done = bar_o + 16;             // drain of an aborted issuer
+    static constexpr int misc = bar_done + 8;               // tmem base, abort flag
+    static constexpr int spans = (misc + 8 + 15) / 16 * 16; // [2] int4: union and common range of a tile's rows
+    static constexpr int bad = spans + 32;                  // [kNst][4] keys whose values are not finite
+    static constexpr int total = bad + 16 * kNst;
+    static constexpr int alloc = total + 1024;              // slack for 1024-byte alignment
+};
+
+// The key tiles [lo, hi) of a range of keys.
+__device__ __forceinline__ int2 tiles_of(int4 span) {
+    return span.x < span.y ? make_int2(span.x / kBlockK, (span.y + kBlockK - 1) / kBlockK) : make_int2(0, 0);
+}
+
+// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs; their float32 sum is added to la, lb.
+__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, uint32_t (&w)[16]) {
+    const float2 cc = splat(c), nr = splat(-ref);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), cc, nr), b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), cc, nr);
+        const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
+        la = __fadd2_rn(la, pa);
+        lb = __fadd2_rn(lb, pb);
+        w[e / 2] = pack_bf16(pa.x, pa.y);
+        w[e / 2 + 1] = pack_bf16(pb.x, pb.y);
+    }
+}
+
+__device__ __forceinline__ float max_chunk(const float (&z)[32]) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        a = max3f(a, z[e], z[e + 1]);
+        b = max3f(b, z[e + 2], z[e + 3]);
+    }
+    return fmaxf(a, b);
+}
+
+// O (d columns at t_o) and the tile's probabilities in front of chunk `ch` times f.
+template <int D>
+__device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int ch, float f) {
+    if (has_o) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            float v[32];
+            tmem_ld32(t_o + k, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= f;
+            tmem_st32(t_o + k, v);
+        }
+    }
+#pragma unroll 1
+    for (int k = 0; k < ch; ++k) {
+        float v[16];
+        tmem_ld16(t_p + 16 * k, v);
+        tc_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t u = __float_as_uint(v[e]);
+            w[e] = pack_bf16(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+        }
+        tmem_st16(t_p + 16 * k, w);
+    }
+    tc_wait_st();
+}
+
+// Not finite: any of a word's two bf16.
+__device__ __forceinline__ bool not_finite2(uint32_t u) {
+    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kAfThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                    const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnFwdParams p,
+                    const __grid_constant__ ScoreParams sp) {
+    using L = AttnSmem<D>;
+    constexpr int NST = L::kNst;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
+    int4* spans = reinterpret_cast<int4*>(gbase + L::spans);
+    uint32_t* bad = reinterpret_cast<uint32_t*>(gbase + L::bad);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the pair's tiles; in a group of heads the last query tiles of every head come first
+    const int unit = blockIdx.x / p.num_splits, split = blockIdx.x - unit * p.num_splits;
+    const int2 at = grouped_order(unit, p.units_q, p.B * p.H_kv * p.units_h, p.order_group);
+    const int bkv = at.x / p.units_h, hb = at.x - bkv * p.units_h, qu = p.units_q - 1 - at.y;
+    const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
+    auto block_of = [&](int s) { return p.pair_heads ? 2 * hb + s : hb; };
+    auto qtile_of = [&](int s) { return p.pair_heads ? qu : 2 * qu + s; };
+    auto exists = [&](int s) { return block_of(s) < p.blocks && qtile_of(s) < p.q_tiles; };
+
+    // a softmax thread's row: its keys, and whether there is such a row
+    const int sub = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
+    const int in_block = row / p.rows, i = qtile_of(sub) * kBlockQ + row - in_block * p.rows;
+    const bool valid = warp < 8 && exists(sub) && in_block < p.heads && i < p.Nq;
+    const int2 range = valid ? row_range(sp, p.Nq, p.Nk, b, i) : make_int2(0, 0);
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tQ);
+        prefetch_tensormap(&tK);
+        prefetch_tensormap(&tV);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(base + L::bar_q + 8 * s, 1);
+            mbar_init(base + L::bar_s + 8 * s, 1);
+            mbar_init(base + L::bar_p + 8 * s, 128);
+            mbar_init(base + L::bar_o + 8 * s, 1);
+            spans[s] = make_int4(INT32_MAX, 0, 0, INT32_MAX);
+        }
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(base + L::bar_full + 8 * s, 1);
+            mbar_init(base + L::bar_empty + 8 * s, 1);
+            mbar_init(base + L::bar_clean + 8 * s, 2);
+        }
+        mbar_init(base + L::bar_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 9) tmem_alloc(base + L::misc, 512);
+    __syncthreads();
+    // keys that some row of the warp sees, and those that all of its rows see
+    int4 mine = make_int4(0, 0, 0, 0);
+    if (warp < 8) {
+        const bool live = range.x < range.y;
+        mine.x = __reduce_min_sync(0xffffffffu, live ? range.x : INT32_MAX);
+        mine.y = __reduce_max_sync(0xffffffffu, live ? range.y : 0);
+        mine.z = __reduce_max_sync(0xffffffffu, !valid ? 0 : live ? range.x : INT32_MAX);
+        mine.w = __reduce_min_sync(0xffffffffu, valid ? range.y : INT32_MAX);
+        if (lane == 0) {
+            int* s = reinterpret_cast<int*>(spans + sub);
+            atomicMin(s, mine.x);
+            atomicMax(s + 1, mine.y);
+            atomicMax(s + 2, mine.z);
+            atomicMin(s + 3, mine.w);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{abort_flag, p.status, p.wait_ns};
+
+    // key tiles: this split's share [t0, t1) of the pair's, and each tile's own part of it
+    const int2 ta = tiles_of(spans[0]), tb = tiles_of(spans[1]);
+    int t0, t1;
+    {
+        const int lo = ta.x < ta.y ? (tb.x < tb.y ? min(ta.x, tb.x) : ta.x) : tb.x, hi = max(ta.y, tb.y);
+        const int n = max(0, hi - lo), per = (n + p.num_splits - 1) / p.num_splits;
+        t0 = lo + split * per;
+        t1 = max(t0, min(hi, t0 + per));
+    }
+    auto active = [&](int s, int t) { return s == 0 ? t >= ta.x && t < ta.y : t >= tb.x && t < tb.y; };
+    // a value tile is checked when some row of an active tile does not see all of its keys
+    auto checked = [&](int t) {
+        const int j0 = t * kBlockK;
+        return (active(0, t) && !(j0 >= spans[0].z && j0 + kBlockK <= spans[0].w)) ||
+               (active(1, t) && !(j0 >= spans[1].z && j0 + kBlockK <= spans[1].w));
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0 && t1 > t0) {
+            const uint64_t keep = policy_evict_last();  // key and value tiles are read again by other query tiles
+            for (int s = 0; s < 2; ++s) {
+                if (!exists(s)) continue;
+                const uint32_t fb = base + L::bar_q + 8 * s, dst = base + L::q + s * L::kTile;
+                const int box = p.heads * p.rows;  // rows that a copy writes
+                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(box) * D * 2);
+#pragma unroll
+                for (int c = 0; c < D / kSwizzleCols; ++c)
+                    tma_load_4d(dst + c * kBlockQ * 128, &tQ, fb, c * kSwizzleCols, qtile_of(s) * kBlockQ,
+                                hk * p.group + block_of(s) * p.heads, b);
+            }
+            int n = 0;
+            for (; n < 2 * (t1 - t0); ++n) {  // key tile, value tile, key tile, ...
+                const int s = n % NST;
+                if (!mbar_wait(base + L::bar_empty + 8 * s, ((n / NST) & 1) ^ 1, wc, kErrWaitK)) break;
+                const uint32_t fb = base + L::bar_full + 8 * s, dst = base + L::kv + s * L::kTile;
+                mbar_arrive_expect_tx(fb, L::kTile);
+#pragma unroll
+                for (int c = 0; c < D / kSwizzleCols; ++c)
+                    tma_load_4d_hint(dst + c * kBlockK * 128, n & 1 ? &tV : &tK, fb, c * kSwizzleCols,
+                                     (t0 + (n >> 1)) * kBlockK, hk, b, keep);
+            }
+            // every issued copy has landed, every stage was released
+            for (int s = 0; s < 2; ++s)
+                if (exists(s)) drain_wait_b(base + L::bar_q + 8 * s, 0, kDrainNs);
+            for (int j = max(0, n - NST); j < n; ++j) {
+                drain_wait_b(base + L::bar_full + 8 * (j % NST), (j / NST) & 1, kDrainNs);
+                if (!*abort_flag) drain_wait_b(base + L::bar_empty + 8 * (j % NST), (j / NST) & 1, kDrainNs);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMAs
+        // S_s(t) = Q_s K(t)^T, then O_s += P_s(t) V(t) with P_s over S_s in tensor memory.  While one tile's
+        // softmax runs, the tensor core works for the other.  The MMAs of a thread run in order: S_s(t + 1)
+        // does not overwrite P_s(t) before O_s has taken it, and S_s(t + 1) complete means that O_s is too.
+        if (lane == 0 && t1 > t0) {
+            constexpr uint32_t id_s = idesc_bf16_f32(kBlockQ, kBlockK), id_o = idesc_bf16_f32(kBlockQ, D, 0, 1);
+            const uint32_t dhi = smem_desc_hi();
+            int issued = 0, n_p[2] = {0, 0};
+            bool ok = !(p.inject_stall && blockIdx.x == 0 && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther));
+            auto scores = [&](int s, int t) {
+                const int st = (2 * (t - t0)) % NST;
+                const uint32_t q_lo = smem_desc_lo_k128(base + L::q + s * L::kTile);
+                const uint32_t k_lo = smem_desc_lo_k128(base + L::kv + st * L::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * kBlockQ * 128 + (kk & 3) * 32) >> 4;
+                    tc_mma_bf16_w(tmem + s * 128, q_lo + o, dhi, k_lo + o, dhi, id_s, kk > 0);
+                }
+                tc_commit(base + L::bar_s + 8 * s);
+                ++issued;
+            };
+            for (int t = t0 - 1; ok && t < t1; ++t) {
+                const int nv = 2 * (t - t0) + 1, nk = nv + 1;  // ring positions of V(t) and K(t + 1)
+                bool have_v = false, have_k = false;
+                for (int s = 0; ok && s < 2; ++s) {
+                    if (t >= t0 && active(s, t)) {
+                        if (!have_v && !(ok = mbar_wait(base + L::bar_full + 8 * (nv % NST), (nv / NST) & 1, wc, kErrWaitK))) break;
+                        have_v = true;
+                        if (!(ok = mbar_wait(base + L::bar_p + 8 * s, n_p[s] & 1, wc, kErrWaitS))) break;
+                        tc_fence_after();
+                        const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + (nv % NST) * L::kTile, kBlockK * 128);
+#pragma unroll
+                        for (int kk = 0; kk < kBlockK / 16; ++kk)
+                            tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi, id_o,
+                                             (n_p[s] | kk) != 0);
+                        ++n_p[s];
+                        if (t + 1 == t1 || !active(s, t + 1)) tc_commit(base + L::bar_o + 8 * s);
+                    }
+                    if (t + 1 < t1 && active(s, t + 1)) {
+                        if (t + 1 == t0 || !active(s, t))
+                            if (!(ok = mbar_wait(base + L::bar_q + 8 * s, 0, wc, kErrWaitQ))) break;
+                        if (!have_k && !(ok = mbar_wait(base + L::bar_full + 8 * (nk % NST), (nk / NST) & 1, wc, kErrWaitK))) break;
+                        have_k = true;
+                        tc_fence_after();
+                        scores(s, t + 1);
+                    }
+                }
+                if (!ok) break;
+                // tiles between two separate ranges are read by no MMA: their copies have to land first
+                if (t >= t0 && !have_v && !(ok = mbar_wait(base + L::bar_full + 8 * (nv % NST), (nv / NST) & 1, wc, kErrWaitK))) break;
+                if (t + 1 < t1 && !have_k && !(ok = mbar_wait(base + L::bar_full + 8 * (nk % NST), (nk / NST) & 1, wc, kErrWaitK))) break;
+                if (t >= t0) tc_commit(base + L::bar_empty + 8 * (nv % NST));
+                if (t + 1 < t1) tc_commit(base + L::bar_empty + 8 * (nk % NST));
+            }
+            if (*abort_flag && issued > 0) {  // let the issued MMAs retire before TMEM is freed
+                tc_commit(base + L::bar_done);
+                drain_wait_b(base + L::bar_done, 0, kDrainNs);
+            }
+        }
+    } else if (warp >= 10) {
+        // ------------------------------------------------------------ value check
+        // A probability of 0 does not hide a NaN or an infinity in the value that it meets in the MMA.  In tiles
+        // that some row does not see all of, keys with such values get zeros, and rows that see them become NaN.
+        // The k-th check uses slot k % NST; a tile's stage is released only after its check, and the ring holds
+        // fewer value tiles than there are slots.
+        const int w = warp - 10;
+        int k_check = 0;
+        for (int t = t0; t < t1; ++t) {
+            if (!checked(t)) continue;
+            const int n = 2 * (t - t0) + 1, st = n % NST, slot = k_check++ % NST;
+            if (!wait_all(base + L::bar_full + 8 * st, (n / NST) & 1, wc, kErrWaitK)) break;
+            const uint8_t* tile = gbase + L::kv + st * L::kTile;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = 64 * half + 32 * w + lane;
+                bool any = false;
+#pragma unroll 1
+                for (int c = 0; c < D / kSwizzleCols; ++c)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(tile + c * kBlockK * 128 + r * 128 + ((k ^ (lane & 7)) << 4));
+                        any |= not_finite2(u.x) | not_finite2(u.y) | not_finite2(u.z) | not_finite2(u.w);
+                    }
+                const uint32_t rows = __ballot_sync(0xffffffffu, any);
+                if (lane == 0) bad[4 * slot + 2 * half + w] = rows;
+                if (any) {
+#pragma unroll 1
+                    for (int c = 0; c < D / kSwizzleCols; ++c)
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k)
+                            st_shared_v4(base + L::kv + st * L::kTile + c * kBlockK * 128 + r * 128 + 16 * k, 0u, 0u, 0u, 0u);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + L::bar_clean + 8 * slot);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const uint32_t t_s = tl + sub * 128, t_o = tl + 256 + sub * 128;
+        const float c = p.c;
+        float ref = -INFINITY;  // m
+        float2 la = splat(0.f), lb = splat(0.f);
+        bool broken = false;
+        bool ok = true;
+        int n = 0, k_check = 0;
+        for (int t = t0; t < t1; ++t) {
+            const bool check = checked(t);
+            const int slot = k_check % NST, phase = (k_check / NST) & 1;
+            k_check += check;
+            if (!active(sub, t)) continue;
+            if (!wait_all(base + L::bar_s + 8 * sub, n & 1, wc, kErrWaitS)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int j0 = t * kBlockK;
+            const int first = range.x - j0, last = range.y - 1 - j0;  // columns that the row sees
+            const bool whole = j0 >= mine.z && j0 + kBlockK <= mine.w;
+            if (check) {
+                if (!wait_all(base + L::bar_clean + 8 * slot, phase, wc, kErrWaitOther)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t u = bad[4 * slot + k];
+                    if (u) {
+                        const int lo = max(first - 32 * k, 0), hi = min(last - 32 * k, 31);
+                        if (lo <= hi) broken |= ((u >> lo) << lo & (0xffffffffu >> (31 - hi))) != 0u;
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t w[16];
+                const int c0 = j0 + 32 * ch;
+                if (c0 >= mine.y || c0 + 32 <= mine.x) {  // no row of the warp sees any of these keys
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = 0u;
+                } else {
+                    float z[32];
+                    tmem_ld32(t_s + 32 * ch, z);
+                    tc_wait_ld();
+                    if (!whole) {
+                        const int lo = first - 32 * ch, hi = last - 32 * ch;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e < lo || e > hi) z[e] = -INFINITY;
+                    }
+                    const float top = c * max_chunk(z);
+                    const bool raise = valid && top > ref + kAttnTau;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float next = raise ? ceilf(top) : ref, f = raise ? ex2(ref - next) : 1.f;
+                        la = __fmul2_rn(la, splat(f));
+                        lb = __fmul2_rn(lb, splat(f));
+                        ref = next;
+                        if (n > 0 || ch > 0) rescale<D>(t_o, n > 0, t_s, ch, f);
+                    }
+                    exp_chunk(z, c, ref == -INFINITY ? 0.f : ref, la, lb, w);
+                }
+                tmem_st16(t_s + 16 * ch, w);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(base + L::bar_p + 8 * sub);
+            ++n;
+        }
+        if (ok && n > 0) ok = wait_all(base + L::bar_o + 8 * sub, 0, wc, kErrWaitOther);
+        tc_fence_after();
+        const float nan = __int_as_float(0x7fc00000);
+        const bool fail = __any_sync(0xffffffffu, !ok || *abort_flag);
+        const int h = hk * p.group + block_of(sub) * p.heads + in_block;
+        const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
+        float l = (la.x + la.y) + (lb.x + lb.y);
+        if (fail || broken) l = nan;
+        const bool empty = range.x >= range.y;
+        if (p.num_splits == 1) {
+            const float inv = empty ? 0.f : 1.f / l;
+            uint8_t* out = static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                float v[32];
+                if (n > 0 && !fail) {
+                    tmem_ld32(t_o + k, v);
+                    tc_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : n > 0 && !fail ? v[e] * inv : nan;
+                if (valid) store_grad32(out, k, v, 1.f, true);
+                if (valid && p.rest) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint32_t u = pack_bf16(v[e], v[e + 1]);
+                        v[e] -= __uint_as_float(u << 16);
+                        v[e + 1] -= __uint_as_float(u & 0xffff0000u);
+                    }
+                    store_grad32(static_cast<uint8_t*>(p.rest) + flat * (2 * D), k, v, 1.f, true);
+                }
+                __syncwarp();
+            }
+            if (valid) p.LSE[flat] = empty ? -INFINITY : fmaf(ref, kLn2, logf(l));
+        } else {
+            const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq, at_row = split * R + flat;
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                float v[32];
+                if (n > 0 && !fail) {
+                    tmem_ld32(t_o + k, v);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (valid) store_grad32(p.part + at_row * D, k, v, 1.f, false);
+                __syncwarp();
+            }
+            if (valid) p.part_ml[at_row] = make_float2(ref, l);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// One warp per row: the splits' sums, brought to the largest m.
+template <int D>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnFwdParams p,
+                                                           const __grid_constant__ ScoreParams sp) {
+    const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq;
+    const size_t row = blockIdx.x * size_t(8) + (threadIdx.x >> 5);
+    if (row >= R) return;
+    const int lane = threadIdx.x & 31, V = D / 32;
+    const int i = static_cast<int>(row % p.Nq), h = static_cast<int>(row / p.Nq % p.H), b = static_cast<int>(row / p.Nq / p.H);
+    const int2 range = row_range(sp, p.Nq, p.Nk, b, i);
+    float m = -INFINITY;
+    for (int s = lane; s < p.num_splits; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
+    for (int s = 0; s < p.num_splits; ++s) {
+        const float2 ml = p.part_ml[s * R + row];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this split's keys are hidden from the row
+        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+        l = fmaf(ml.y, f, l);
+        const float* part = p.part + (s * R + row) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
+    }
+    const bool empty = range.x >= range.y;
+    const float inv = empty ? 0.f : 1.f / l;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + i * p.o_n) + lane * V);
+    uint32_t* rest = p.rest ? reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.rest) + row * D + lane * V) : nullptr;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        const float a = empty ? 0.f : v[e] * inv, c = empty ? 0.f : v[e + 1] * inv;
+        const uint32_t u = pack_bf16(a, c);
+        out[e / 2] = u;
+        if (rest) rest[e / 2] = pack_bf16(a - __uint_as_float(u << 16), c - __uint_as_float(u & 0xffff0000u));
+    }
+    if (lane == 0) p.LSE[row] = empty ? -INFINITY : fmaf(m, kLn2, logf(l));
+}
+
+namespace {
+template <int D>
+cudaError_t launch_attn_d(const CUtensorMap* m, const AttnFwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
+    constexpr int bytes = AttnSmem<D>::alloc;
+    static_assert(bytes <= 232448, "shared memory");
+    auto k = attn_fwd_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<ctas, kAfThreads, bytes, st>>>(m[0], m[1], m[2], p, sp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.num_splits == 1) return e;
+    const int64_t rows = int64_t(p.B) * p.H * p.Nq;
+    attn_combine_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(p, sp);
+    return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_attn_fwd(int d, const CUtensorMap* maps, const AttnFwdParams& p, const ScoreParams& sp, int ctas,
+                            cudaStream_t stream) {
+    return d == 128 ? launch_attn_d<128>(maps, p, sp, ctas, stream) : launch_attn_d<64>(maps, p, sp, ctas, stream);
+}
+
+}  // namespace streamkl

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "attn.cuh"
 #include "common.cuh"
 #include "score.cuh"
 
@@ -40,6 +41,11 @@ size_t score_bwd_row_bytes(int64_t bh, int q_tiles);     // workspace of sp.rows
 size_t score_bwd_key_bytes(int64_t batch, int q_tiles);  // of sp.keys
 cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* maps, const BwdParams& p,
                              const ScoreParams& sp, int ctas, int sms, cudaStream_t stream);
+
+// Attention over whole prompts.  maps = {Q, K, V}: Q boxes of p.rows rows x
+// p.heads heads, K and V boxes of 128 rows.
+cudaError_t launch_attn_fwd(int d, const CUtensorMap* maps, const AttnFwdParams& p, const ScoreParams& sp, int ctas,
+                            cudaStream_t stream);
 
 cudaError_t launch_key_ranges(const KeyRangeParams& p, cudaStream_t stream);
 

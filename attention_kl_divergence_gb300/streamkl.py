@@ -77,6 +77,11 @@ class NormRope(ctypes.Structure):
         [(n, Strides) for n in ("q", "k", "yq", "yk", "dq", "dk")]
 
 
+class Attn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "H_kv", "Nq", "Nk", "d")] + \
+        [(n, Strides) for n in ("q", "k", "v", "o", "d_o")]
+
+
 class StreamKLError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -88,7 +93,8 @@ EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_
             "streamkl_fwd_workspace_bytes", "streamkl_bwd_workspace_bytes", "streamkl_bwd_joint_plan",
             "streamkl_bwd_joint", "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd",
             "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table", "streamkl_score_fwd_plan", "streamkl_score_fwd",
-            "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges")
+            "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges", "streamkl_attn_fwd_plan",
+            "streamkl_attn_fwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -137,6 +143,9 @@ def load(build_if_stale: bool = True):
         lib.streamkl_norm_rope_workspace_bytes.argtypes = [nr]
         lib.streamkl_norm_rope_workspace_bytes.restype = Z
         lib.streamkl_rope_table.argtypes = [P, ctypes.c_int64, ctypes.c_int32, P, P]
+        at = ctypes.POINTER(Attn)
+        lib.streamkl_attn_fwd_plan.argtypes = [at, op, pp]
+        lib.streamkl_attn_fwd.argtypes = [at, *[P] * 6, F, I, P, P, P, P, Z, op, P]
         lib.streamkl_status_string.argtypes = [I]
         lib.streamkl_status_string.restype = ctypes.c_char_p
         for name in ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd",
@@ -144,7 +153,7 @@ def load(build_if_stale: bool = True):
                      "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint",
                      "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table",
                      "streamkl_score_fwd_plan", "streamkl_score_fwd", "streamkl_score_bwd_plan", "streamkl_score_bwd",
-                     "streamkl_key_ranges"):
+                     "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -852,3 +861,78 @@ class QKNormRope(torch.autograd.Function):
                     for g, x in ((dyq, q), (dyk, k)))
         grads = qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, table, positions, **ctx.how)
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None, None, None)
+
+
+# ---------------------------------------------------------------------------
+# Attention over whole prompts
+# ---------------------------------------------------------------------------
+def _attn_desc(Q, K, V):
+    desc = Attn()
+    desc.q = _heads("Q", Q, (torch.bfloat16,))
+    desc.k, desc.v = _heads("K", K, (torch.bfloat16,), Q.device), _heads("V", V, (torch.bfloat16,), Q.device)
+    B, H, Nq, d = Q.shape
+    if K.shape != V.shape or K.shape[0] != B or K.shape[3] != d:
+        raise ValueError("K and V must have one shape, and share B and d with Q")
+    if K.shape[1] < 1 or H % K.shape[1] != 0:
+        raise ValueError("the key head count must divide the query head count")
+    desc.B, desc.H, desc.H_kv, desc.Nq, desc.Nk, desc.d = B, H, K.shape[1], Nq, K.shape[2], d
+    return desc
+
+
+def _ranges(ranges, Q):
+    """(begin, end, offset) of key_ranges, checked; None: every key."""
+    if ranges is None:
+        return None, None, None
+    if not isinstance(ranges, (tuple, list)) or len(ranges) != 3:
+        raise ValueError("ranges must be (begin, end, offset) (see key_ranges)")
+    B, _, Nq, _ = Q.shape
+    for name, t, shape in zip(("begin", "end", "offset"), ranges, ((B, Nq), (B, Nq), (B,))):
+        if t is not None:
+            _check_tensor(name, t, shape, torch.int32, Q.device)
+    return tuple(ranges)
+
+
+def _given_ranges(ranges):
+    return tuple(ranges) if isinstance(ranges, (tuple, list)) else (ranges,)
+
+
+def attn_fwd_plan(Q, K, V, num_splits=0) -> Plan:
+    plan, desc = Plan(), _attn_desc(Q, K, V)
+    desc.o = _contiguous(Q.shape)
+    with torch.cuda.device(Q.device):
+        _raise(load().streamkl_attn_fwd_plan(ctypes.byref(desc), ctypes.byref(_opts(num_splits)), ctypes.byref(plan)),
+               "streamkl_attn_fwd_plan")
+    return plan
+
+
+def attn_fwd(Q, K, V, ranges=None, causal=False, scale=None, rest=False, out=None, num_splits=0, workspace=None,
+             wait_limit_ns=0, debug_flags=0):
+    """(O, LSE): softmax attention of Q [B, H, Nq, d] over K, V [B, Hk, Nk, d] (bf16, any strides with d contiguous; Hk
+    divides H), O bf16 like Q, LSE float32 [B, H, Nq].  ranges: (begin, end, offset) of key_ranges (None: every key);
+    causal: row i also sees no key behind i + offset (None: Nk - Nq).  A row that sees no key has O = 0 and LSE = -inf;
+    what a row does not see (NaN included) has no effect on it.  out: a bf16 tensor for O, any strides; a new contiguous
+    one otherwise.  rest=True returns (O, LSE, rest): rest, contiguous, is what O's rounding left; attn_bwd takes it."""
+    given = _given_ranges(ranges)
+    num_splits, wait_limit_ns, debug_flags, rest = int(num_splits), int(wait_limit_ns), int(debug_flags), bool(rest)
+    key, known = _lookup("attn_fwd", _tensors(Q, K, V, *given, *(() if out is None else (out,))), num_splits, wait_limit_ns,
+                         debug_flags, out is None)
+    if known is None:
+        desc = _attn_desc(Q, K, V)
+        _ranges(ranges, Q)
+        desc.o = _contiguous(Q.shape) if out is None else _heads("out", out, (torch.bfloat16,), Q.device, Q.shape)
+        opts, plan = _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
+        with torch.cuda.device(Q.device):
+            _raise(load().streamkl_attn_fwd_plan(ctypes.byref(desc), ctypes.byref(opts), ctypes.byref(plan)),
+                   "streamkl_attn_fwd_plan")
+        known = _remember(key, (desc, opts, plan.workspace_bytes, tuple(Q.shape), Q.device))
+    desc, opts, nbytes, shape, device = known
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    left = torch.empty(shape, dtype=torch.bfloat16, device=device) if rest else None
+    LSE = torch.empty(shape[:3], dtype=torch.float32, device=device)
+    workspace = _scratch(workspace, nbytes, device)
+    begin, end, offset = given if len(given) == 3 else (None, None, None)
+    _raise(_on(device, load().streamkl_attn_fwd, desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _address(begin),
+               _address(end), _address(offset), 0.0 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
+               _address(left), LSE.data_ptr(), workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_fwd")
+    return (out, LSE, left) if rest else (out, LSE)

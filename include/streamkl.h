@@ -378,6 +378,46 @@ STREAMKL_API streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* de
 STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t rows, int32_t half, float* table,
                                                  streamkl_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over whole prompts, and its gradients.
+ *
+ * For every query row i of every (batch b, head h), over the keys j of its
+ * range (begin[b, i] <= j < end[b, i]; NULL: 0 and Nk; with causal != 0 also
+ * j <= i + offset[b], NULL: Nk - Nq):
+ *
+ *     S = scale * Q K^T,  LSE[i] = log sum_j exp(S[i,j]),
+ *     O[i] = sum_j exp(S[i,j] - LSE[i]) V[j]
+ *
+ *  - Q, O, dO [B, H, Nq, d] and K, V [B, H_kv, Nk, d] are bf16 with d
+ *    contiguous (64 or 128) and strides of their own, multiples of 8 elements,
+ *    that keep rows apart; H_kv divides H, and query head h uses key head
+ *    h / (H / H_kv).  Base pointers are 16-byte aligned.
+ *  - A row that sees no key has O = 0 and LSE = -inf, and no effect on any
+ *    gradient.  What a row does not see (NaN and infinities included) has no
+ *    effect on it; a row that sees a NaN or an infinite value of V gets NaN, at
+ *    least where that value counts and at most in the whole row.
+ *  - rest (NULL or bf16 [B, H, Nq, d], contiguous): what the rounding of O to
+ *    bf16 left, for the backward's row sums of dO * O.
+ *  - Probabilities enter the product with V rounded to bf16; sums, maxima and
+ *    outputs are float32 until their one rounding.
+ *  - Equal inputs give equal bits.  A give-up of a bounded wait leaves NaN in
+ *    the rows that it left unfinished.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B, H, H_kv, Nq, Nk, d;
+    streamkl_strides q, k, v, o;
+    streamkl_strides d_o; /* backward only: dO */
+} streamkl_attn;
+
+STREAMKL_API streamkl_status streamkl_attn_fwd_plan(const streamkl_attn* desc, const streamkl_options* opt,
+                                                    streamkl_plan* plan);
+STREAMKL_API streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, const void* K, const void* V,
+                                               const int32_t* begin, const int32_t* end, const int32_t* offset,
+                                               float scale, int causal, void* O, void* rest, float* LSE,
+                                               void* workspace, size_t workspace_bytes, const streamkl_options* opt,
+                                               streamkl_stream_t stream);
+
 /* Synchronises `stream`, reads the workspace's device error word into
  * *device_error (if not NULL), clears it, and returns STREAMKL_ERR_TIMEOUT if
  * it was set, STREAMKL_OK otherwise (or CUDA on a failed copy). */

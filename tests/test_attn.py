@@ -1,0 +1,114 @@
+"""Attention over whole prompts and its gradients against the definition in float64.
+
+Tolerances, from the arithmetic.  A product z is a float32 sum of d exact
+products, off by at most d 2^-24 of the sum of their magnitudes; the exponent
+adds a few roundings of |S|.  With A = max scale |q|.|k| and M = max |S| over
+the visible pairs a score is off by  del = (d + 32) 2^-24 A + 2^-20 (M + 1).
+LSE is off by at most del + N 2^-24 (the sum of up to N terms) + its rounding.
+A probability enters the product with V rounded to bf16 (2^-8 of it) from a
+value off by a factor 1 +- 2 del, the product accumulates in float32, and O is
+rounded once:  (2^-8 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|.
+"""
+import math
+
+import pytest
+import torch
+
+from attention_kl_divergence_gb300 import streamkl as sk
+
+gpu = pytest.mark.gpu
+F64, F32, BF16 = torch.float64, torch.float32, torch.bfloat16
+DEV = "cuda"
+
+
+def inputs(B, H, Hk, Nq, Nk, d, seed=0, peak=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    new = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    return (new(B, H, Nq, d) * peak).to(BF16), (new(B, Hk, Nk, d) * peak).to(BF16), new(B, Hk, Nk, d).to(BF16)
+
+
+class Ref:
+    """The definition in 64 bits, and the bounds of the errors."""
+
+    def __init__(self, Q, K, V, ranges=None, causal=False, scale=None):
+        B, H, Nq, d = Q.shape
+        Hk, Nk = K.shape[1], K.shape[2]
+        self.G, self.Hk = H // Hk, Hk
+        self.scale = d ** -0.5 if scale is None else scale
+        j = torch.arange(Nk, device=DEV)
+        begin, end, offset = ranges if ranges is not None else (None, None, None)
+        lo = torch.zeros((B, Nq), dtype=torch.int64, device=DEV) if begin is None else begin.long()
+        hi = torch.full((B, Nq), Nk, dtype=torch.int64, device=DEV) if end is None else end.long()
+        if causal:
+            off = torch.full((B,), Nk - Nq, device=DEV) if offset is None else offset.long()
+            hi = torch.minimum(hi, torch.arange(Nq, device=DEV) + off[:, None] + 1)
+        self.vis = ((j >= lo[..., None]) & (j < hi[..., None]))[:, None]
+        rep = lambda t: t.double().repeat_interleave(self.G, 1)  # noqa: E731
+        self.q, self.k, self.v = Q.double(), rep(K), rep(V)
+        s = (self.q @ self.k.transpose(2, 3) * self.scale).masked_fill(~self.vis, -math.inf)
+        self.LSE = torch.logsumexp(s, -1)
+        self.live = self.vis.any(-1).expand_as(self.LSE)
+        self.p = torch.exp(s - torch.where(self.live, self.LSE, 0.0)[..., None]).masked_fill(~self.vis, 0.0)
+        v = self.v if bool(torch.isfinite(self.v).all()) else torch.nan_to_num(self.v, 0.0, 0.0, 0.0)
+        self.O = self.p @ v
+        big = lambda t: float(torch.nan_to_num(t).masked_fill(~self.vis, 0.0).abs().max())  # noqa: E731
+        A = big(self.q.abs() @ self.k.abs().transpose(2, 3)) * self.scale
+        self.delta = (d + 32) * 2.0 ** -24 * A + 2.0 ** -20 * (big(s) + 1)
+        self.acc = (Nk + 128) * 2.0 ** -24
+        self.o_tol = (2.0 ** -8 + 4 * self.delta + self.acc) * (self.p @ v.abs()) + 2.0 ** -8 * self.O.abs() + 1e-30
+
+    def check(self, O, LSE):
+        assert torch.equal(LSE == -math.inf, ~self.live)
+        err = (LSE.double() - self.LSE)[self.live].abs()
+        tol = self.delta + self.acc + 2.0 ** -23 * self.LSE[self.live].abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
+        assert bool((O[~self.live] == 0).all())
+        err = (O.double() - self.O).abs()
+        assert bool((err <= self.o_tol).all()), float((err / self.o_tol).max())
+
+
+def masks(kind, B, Nq, Nk):
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    if kind == "full":
+        return sk.key_ranges(B, Nq, Nk, DEV, causal=False)
+    if kind == "causal":
+        return sk.key_ranges(B, Nq, Nk, DEV)
+    if kind == "window":
+        return sk.key_ranges(B, Nq, Nk, DEV, window=max(1, Nk // 5))
+    if kind == "docs":
+        bounds = sorted({0, Nk // 7, Nk // 7 + 1, Nk // 2, Nk - Nk // 9, Nk})
+        return sk.key_ranges(B, Nq, Nk, DEV, docs=i32(*bounds))
+    if kind == "padded":
+        n = [max(1, Nk - b * (Nk // 3) - (b > 0)) for b in range(B)]
+        return sk.key_ranges(B, Nq, Nk, DEV, q_lengths=i32(*[min(Nq, x) for x in n]), k_lengths=i32(*n))
+    assert kind == "two ends"  # rows in turn see keys at the start and at the end; every fifth row nothing
+    row = torch.arange(Nq, device=DEV)
+    begin = torch.where(row % 2 == 0, 0, max(0, Nk - 3)).int().repeat(B, 1)
+    end = torch.where(row % 2 == 0, min(2, Nk), Nk).int().repeat(B, 1)
+    end[:, ::5] = 0
+    return begin, end, None
+
+
+SHAPES = [
+    # B, H, Hk, Nq, Nk, d
+    (1, 1, 1, 1, 1, 64), (1, 4, 2, 1, 300, 128), (2, 8, 2, 5, 777, 64), (1, 6, 2, 33, 129, 128), (2, 3, 1, 128, 128, 64),
+    (1, 4, 4, 129, 129, 128), (1, 2, 1, 257, 1000, 128), (2, 6, 2, 300, 300, 64), (1, 16, 2, 16, 4097, 128),
+    (1, 5, 1, 200, 513, 64), (1, 2, 2, 1024, 1024, 128), (3, 3, 3, 64, 640, 64),
+]
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["full", "causal", "window", "docs", "padded", "two ends"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape, kind):
+    B, H, Hk, Nq, Nk, d = shape
+    Q, K, V = inputs(*shape, seed=Nk)
+    ranges = masks(kind, B, Nq, Nk)
+    O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True)
+    ref = Ref(Q, K, V, ranges)
+    ref.check(O, LSE)
+    # the rest is what the rounding left: O + rest has 16 bits
+    err = (O.double() + rest.double() - ref.O).abs()
+    assert bool((err <= ref.o_tol - 2.0 ** -8 * ref.O.abs() + 2.0 ** -16 * ref.O.abs()).all())
+    again = sk.attn_fwd(Q, K, V, ranges=ranges)
+    assert torch.equal(again[0], O) and torch.equal(again[1], LSE)
