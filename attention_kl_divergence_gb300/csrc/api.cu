@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -76,6 +77,39 @@ int decode_splits(int64_t units, int k_tiles, int sms) {
     if (s > k_tiles) s = k_tiles;
     if (s > kMaxSplits) s = kMaxSplits;
     return s < 1 ? 1 : static_cast<int>(s);
+}
+
+// Heads of a group of the CTAs' order: four waves of CTAs, so that the CTAs with
+// the most work of a group start before the lighter ones end, and no more: a
+// group's tiles are to stay in L2.
+int order_group(int64_t heads, int tiles, int sms) {
+    const int64_t g = (4LL * sms + tiles - 1) / tiles;
+    return static_cast<int>(std::min(heads, g));
+}
+
+// Splits of a key tile's iterations (its query tiles, of every query head of its
+// group).  Without them few key tiles leave SMs idle, and the tile with the most
+// rows sets the time.  In units of an iteration, for a causal mask: a launch of u
+// tiles with up to n iterations each takes about the larger of the SMs' average
+// and the longest CTA, a CTA costs about 5 more (start, key tiles, dK), and
+// summing the parts about 4.  Splits are taken when they save a fifth.  Measured
+// (whole backward, us): 64 key tiles of up to 128 iterations, 1 split 296, 2 161,
+// 3 117, 4 94, 5 105, 8 113; 114 of up to 38, 1 73, 2 49, 3 58; 192 of up to 16,
+// 1 44, 2 56.  The ranges lie on the device, so every mask counts as causal.  What
+// that costs (chosen splits first, the best ones second): full masks 167 at 4
+// against 165 at 2, 96 at 2 against 88 at 4, 85 at 1 against 76 at 2; windows of a
+// sixteenth 52 at 4 against 44 at 2, 37 at 2 against 27 at 1; documents of an
+// eighth to three eighths within 8% in all three.
+int bwd_splits(int64_t units, int64_t iterations, int sms) {
+    auto cost = [&](int64_t s) {
+        const double mean = (units * iterations * 0.5 + double(units) * s * 5) / sms;
+        const double longest = double((iterations + s - 1) / s) + 5;
+        return std::max(mean, longest) + (s > 1 ? 4 : 0);
+    };
+    int best = 1;
+    for (int s = 2; s <= 16 && s <= iterations; ++s)
+        if (cost(s) < cost(best)) best = s;
+    return cost(best) < 0.8 * cost(1) ? best : 1;
 }
 
 namespace {

@@ -97,10 +97,40 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
     if (units * splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     p.num_splits = splits;
     pl->ctas = static_cast<int>(units * splits);
-    // heads whose tiles are interleaved: about four waves of CTAs, so that their keys stay in L2
-    p.order_group = static_cast<int>(std::min<int64_t>(heads, (4LL * sms + p.units_q - 1) / p.units_q));
+    p.order_group = order_group(heads, p.units_q, sms);
     pl->ws_bytes = kStatusBytes;
     if (splits > 1) pl->ws_bytes += size_t(splits) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
+    return STREAMKL_OK;
+}
+
+struct AttnBwdPlan {
+    int ctas, num_q_tiles, num_k_tiles, group, splits, sms;
+    size_t row_bytes, key_bytes, part_bytes, ws_bytes;
+};
+
+streamkl_status plan_attn_bwd(const streamkl_attn* s, const streamkl_options* opt, AttnBwdPlan* pl) {
+    streamkl_status st = check_desc(s, true);
+    if (st != STREAMKL_OK) return st;
+    if (!options_ok(opt)) return STREAMKL_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    pl->sms = sms;
+    pl->num_q_tiles = (s->Nq - 1) / 64 + 1;
+    pl->num_k_tiles = (s->Nk - 1) / kBlockK + 1;
+    const int64_t key_heads = int64_t(s->B) * s->H_kv, ctas = key_heads * pl->num_k_tiles;
+    const int64_t iterations = int64_t(pl->num_q_tiles) * (s->H / s->H_kv);
+    // the iterations of a CTA are counted in 32 bits; the prepare kernel has a block per query tile and head
+    if (ctas > INT32_MAX || int64_t(s->B) * s->H * pl->num_q_tiles > INT32_MAX || iterations > INT32_MAX)
+        return STREAMKL_ERR_UNSUPPORTED;
+    pl->splits = opt && opt->num_splits > 0 ? std::min(opt->num_splits, kMaxSplits) : bwd_splits(ctas, iterations, sms);
+    if (ctas * pl->splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    pl->ctas = static_cast<int>(ctas * pl->splits);
+    pl->group = order_group(key_heads, pl->num_k_tiles, sms);
+    const size_t heads = size_t(s->B) * s->H;
+    pl->row_bytes = (attn_bwd_row_bytes(heads, pl->num_q_tiles) + 255) / 256 * 256;
+    pl->key_bytes = (attn_bwd_key_bytes(s->B, pl->num_q_tiles) + 255) / 256 * 256;
+    pl->part_bytes = pl->splits > 1 ? 2 * size_t(pl->splits) * key_heads * s->Nk * s->d * sizeof(float) : 0;
+    pl->ws_bytes = kStatusBytes + pl->row_bytes + pl->key_bytes + pl->part_bytes + heads * s->Nq * s->d * sizeof(float);
     return STREAMKL_OK;
 }
 
@@ -168,6 +198,79 @@ streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, cons
     p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
     p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
     return launch_attn_fwd(s.d, maps, p, ranges_of(begin, end, offset, causal), pl.ctas,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? STREAMKL_OK
+               : STREAMKL_ERR_CUDA;
+}
+
+streamkl_status streamkl_attn_bwd_plan(const streamkl_attn* desc, const streamkl_options* opt, streamkl_plan* plan) {
+    if (!plan) return STREAMKL_ERR_INVALID_ARG;
+    AttnBwdPlan pl{};
+    streamkl_status st = plan_attn_bwd(desc, opt, &pl);
+    if (st != STREAMKL_OK) return st;
+    plan->path = 2;
+    plan->num_splits = pl.splits;
+    plan->num_ctas = pl.ctas;
+    plan->launches = 3;  // prepare, gradients, finish
+    plan->workspace_bytes = pl.ws_bytes;
+    return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const void* dO, const void* Q, const void* K, const void* V,
+                                  const void* O, const void* rest, const float* LSE, const int32_t* begin,
+                                  const int32_t* end, const int32_t* offset, float scale, int causal, void* dQ, void* dK,
+                                  void* dV, void* workspace, size_t workspace_bytes, const streamkl_options* opt,
+                                  streamkl_stream_t stream) {
+    streamkl_status st = check_desc(desc, true);
+    if (st != STREAMKL_OK) return st;
+    const void* need[8] = {dO, Q, K, V, O, dQ, dK, dV};
+    for (const void* q : need)
+        if (!q || !aligned16(q)) return STREAMKL_ERR_INVALID_ARG;
+    if (!aligned16(rest) || !LSE || !aligned4(LSE) || !aligned4(begin) || !aligned4(end) || !aligned4(offset))
+        return STREAMKL_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
+    AttnBwdPlan pl{};
+    if ((st = plan_attn_bwd(desc, opt, &pl)) != STREAMKL_OK) return st;
+    if (workspace_bytes < pl.ws_bytes) return STREAMKL_ERR_WORKSPACE;
+
+    const streamkl_attn& s = *desc;
+    CUtensorMap maps[4];
+    if (!make_map_strided(&maps[0], Q, s.d, s.Nq, s.H, s.B, used(s.q, s.B, s.H, s.Nq, s.d), 64) ||
+        !make_map_strided(&maps[1], K, s.d, s.Nk, s.H_kv, s.B, used(s.k, s.B, s.H_kv, s.Nk, s.d), kBlockK) ||
+        !make_map_strided(&maps[2], V, s.d, s.Nk, s.H_kv, s.B, used(s.v, s.B, s.H_kv, s.Nk, s.d), kBlockK) ||
+        !make_map_strided(&maps[3], dO, s.d, s.Nq, s.H, s.B, used(s.d_o, s.B, s.H, s.Nq, s.d), 64))
+        return STREAMKL_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    AttnBwdParams p{};
+    p.B = s.B;
+    p.H = s.H;
+    p.H_kv = s.H_kv;
+    p.Nq = s.Nq;
+    p.Nk = s.Nk;
+    p.group = s.H / s.H_kv;
+    p.num_q_tiles = pl.num_q_tiles;
+    p.num_k_tiles = pl.num_k_tiles;
+    p.num_splits = pl.splits;
+    p.order_group = pl.group;
+    p.scale = resolve_scale(scale, s.d);
+    p.c = p.scale * kLog2e;
+    p.dO = dO;
+    p.g_b = s.d_o.b, p.g_h = s.d_o.h, p.g_n = s.d_o.n;
+    p.O = O;
+    p.o_b = s.o.b, p.o_h = s.o.h, p.o_n = s.o.n;
+    p.rest = rest;
+    p.LSE = LSE;
+    p.dQ = dQ;
+    p.dK = dK;
+    p.dV = dV;
+    p.rows = reinterpret_cast<float*>(ws);
+    p.keys = ws + pl.row_bytes;
+    p.parts = reinterpret_cast<float*>(ws + pl.row_bytes + pl.key_bytes);
+    p.dQacc = reinterpret_cast<float*>(ws + pl.row_bytes + pl.key_bytes + pl.part_bytes);
+    p.status = static_cast<unsigned int*>(workspace);
+    p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
+    p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
+    return launch_attn_bwd(s.d, maps, p, ranges_of(begin, end, offset, causal), pl.ctas, pl.sms,
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? STREAMKL_OK
                : STREAMKL_ERR_CUDA;

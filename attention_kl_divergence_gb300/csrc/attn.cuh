@@ -34,4 +34,30 @@ struct AttnFwdParams {
     int inject_stall;
 };
 
+// Backward.  Query tiles of 64 rows, key tiles of 128.
+struct AttnBwdParams {
+    int B, H, H_kv, Nq, Nk;
+    int group;
+    int num_q_tiles, num_k_tiles;
+    int num_splits;          // CTAs that share a key tile's query tiles
+    int order_group;
+    float scale, c;          // softmax scale; times log2(e)
+    const void* dO;          // bf16, strided
+    int64_t g_b, g_h, g_n;
+    const void* O;           // bf16, strided
+    int64_t o_b, o_h, o_n;
+    const void* rest;        // bf16 [B, H, Nq, d] or null
+    const float* LSE;
+    void* dQ;                // bf16 [B, H, Nq, d]
+    void* dK;                // bf16 [B, H_kv, Nk, d]
+    void* dV;
+    float* dQacc;            // float32 [B, H, Nq, d]: the key tiles' terms are added here
+    float* rows;             // [B*H][q tiles][2][64]: -LSE (log2) and -scale sum(dO O) of each row
+    void* keys;              // [B][q tiles] KeyBlock
+    float* parts;            // several splits: [2 (dK, dV)][splits][B*H_kv*Nk][d]
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int inject_stall;
+};
+
 }  // namespace streamkl

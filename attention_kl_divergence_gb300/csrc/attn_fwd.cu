@@ -101,11 +101,6 @@ __device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int
     tc_wait_st();
 }
 
-// Not finite: any of a word's two bf16.
-__device__ __forceinline__ bool not_finite2(uint32_t u) {
-    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-}
-
 }  // namespace
 
 template <int D>
@@ -316,7 +311,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint4 u = *reinterpret_cast<const uint4*>(tile + c * kBlockK * 128 + r * 128 + ((k ^ (lane & 7)) << 4));
-                        any |= not_finite2(u.x) | not_finite2(u.y) | not_finite2(u.z) | not_finite2(u.w);
+                        any |= has_nonfinite_bf16(u.x) | has_nonfinite_bf16(u.y) | has_nonfinite_bf16(u.z) | has_nonfinite_bf16(u.w);
                     }
                 const uint32_t rows = __ballot_sync(0xffffffffu, any);
                 if (lane == 0) bad[4 * slot + 2 * half + w] = rows;

@@ -130,6 +130,60 @@ __device__ __forceinline__ void store_ds_chunk(uint32_t tile_hi, uint32_t tile_l
     }
 }
 
+// The key ranges of a 64-row query tile, prepared once and fetched by bulk copies.
+struct KeyBlock {
+    int32_t begin[kBwdTile], end[kBwdTile];
+    int4 bounds[2];  // per half: lowest begin, highest end of a row with keys; highest begin, lowest end of all rows
+};
+static_assert(sizeof(KeyBlock) == 2 * kBwdTile * 4 + 32, "packed");
+
+__device__ __forceinline__ bool has_nonfinite_bf16(uint32_t u) {
+    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
+    uint32_t u;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+    return u;
+}
+
+// Zero every row with a NaN or an infinity among rows [r0, r0 + 32) of the 64-row
+// tile at `tile`.  Several warps may find the same row: they all write zeros.
+template <int D>
+__device__ __forceinline__ void clear_query_rows(uint32_t tile, int r0, int lane) {
+#pragma unroll 1
+    for (int r = r0; r < r0 + 32; ++r) {
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < D / kSwizzleCols; ++c)
+            bad |= has_nonfinite_bf16(ld_shared_u32(tile + c * kBwdTile * 128 + r * 128 + lane * 4));
+        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+            for (int c = 0; c < D / kSwizzleCols; ++c)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(tile + c * kBwdTile * 128 + r * 128 + lane * 4), "r"(0u)
+                             : "memory");
+        }
+    }
+    __syncwarp();
+}
+
+// Zero this thread's row of the 128-key tile at `kt` if it holds a NaN or an infinity.
+template <int D>
+__device__ __forceinline__ void clear_key_row(uint32_t kt, int key_row) {
+    bool bad = false;
+#pragma unroll 1
+    for (int k = 0; k < D / 2; ++k)
+        bad |= has_nonfinite_bf16(ld_shared_u32(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4));
+    if (bad) {
+#pragma unroll 1
+        for (int k = 0; k < D / 2; ++k)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4),
+                         "r"(0u)
+                         : "memory");
+    }
+    __syncwarp();
+}
+
 // Store 32 gradient values (scaled) at columns [c0, c0 + 32) of a row, as
 // float32 or as bf16 (round to nearest even).  Each thread writes its own
 // row, so a warp's store instruction touches 32 rows: whole 32-byte sectors

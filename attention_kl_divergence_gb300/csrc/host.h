@@ -18,6 +18,8 @@ int kv_heads(const streamkl_shape* s);
 streamkl_status device_sms(int* sms);
 int choose_splits(int64_t units, int k_tiles, int slots);
 int decode_splits(int64_t units, int k_tiles, int sms);
+int order_group(int64_t heads, int tiles, int sms);
+int bwd_splits(int64_t units, int64_t iterations, int sms);
 bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads = 1);
 bool make_map_strided(CUtensorMap* m, const void* ptr, int d, int64_t N, int heads, int B, const streamkl_strides& st,
                       int box_rows, int box_heads = 1);

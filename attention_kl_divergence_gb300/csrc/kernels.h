@@ -47,6 +47,12 @@ cudaError_t launch_score_bwd(int d, int setting, int mode, const CUtensorMap* ma
 cudaError_t launch_attn_fwd(int d, const CUtensorMap* maps, const AttnFwdParams& p, const ScoreParams& sp, int ctas,
                             cudaStream_t stream);
 
+// Its gradients.  maps = {Q, K, V, dO}: Q and dO boxes of 64 rows, K and V boxes of 128.
+size_t attn_bwd_row_bytes(int64_t bh, int q_tiles);     // workspace of p.rows and
+size_t attn_bwd_key_bytes(int64_t batch, int q_tiles);  // of p.keys
+cudaError_t launch_attn_bwd(int d, const CUtensorMap* maps, const AttnBwdParams& p, const ScoreParams& sp, int ctas, int sms,
+                            cudaStream_t stream);
+
 cudaError_t launch_key_ranges(const KeyRangeParams& p, cudaStream_t stream);
 
 // Norm and rotation of query and key heads.  norm_rope_bwd_ctas plans the

@@ -42,54 +42,7 @@ namespace {
 //   rows   [B*H][q tiles][3][64] floats: -LSE1 (log2), -xb and g * scale of each row
 //   keys   [B][q tiles] KeyBlock: the ranges of the tile's rows and their bounds
 // Both are read by bulk copies of a tile's block.
-struct KeyBlock {
-    int32_t begin[kBwdTile], end[kBwdTile];
-    int4 bounds[2];  // per half: lowest begin, highest end of a row with keys; highest begin, lowest end of all rows
-};
 constexpr int kRowBlockBytes = 3 * kBwdTile * 4;
-static_assert(sizeof(KeyBlock) == 2 * kBwdTile * 4 + 32, "packed");
-
-__device__ __forceinline__ bool has_nonfinite_bf16(uint32_t u) {
-    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-}
-
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
-    uint32_t u;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
-    return u;
-}
-
-// Zero every row with a NaN or an infinity among query rows [r0, r0 + 32) of
-// the tile at `qt`, and this thread's row of the key tile at `kt`.  Several
-// warps may find the same row: they all write zeros.
-template <int D>
-__device__ __forceinline__ void clear_nonfinite(uint32_t qt, int r0, uint32_t kt, int key_row, int lane) {
-#pragma unroll 1
-    for (int r = r0; r < r0 + 32; ++r) {
-        bool bad = false;
-#pragma unroll
-        for (int c = 0; c < D / kSwizzleCols; ++c)
-            bad |= has_nonfinite_bf16(ld_shared_u32(qt + c * kBwdTile * 128 + r * 128 + lane * 4));
-        if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-            for (int c = 0; c < D / kSwizzleCols; ++c)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(qt + c * kBwdTile * 128 + r * 128 + lane * 4), "r"(0u)
-                             : "memory");
-        }
-    }
-    bool bad = false;
-#pragma unroll 1
-    for (int k = 0; k < D / 2; ++k)
-        bad |= has_nonfinite_bf16(ld_shared_u32(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4));
-    if (bad) {
-#pragma unroll 1
-        for (int k = 0; k < D / 2; ++k)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(kt + (k >> 5) * kBlockK * 128 + key_row * 128 + (k & 31) * 4),
-                         "r"(0u)
-                         : "memory");
-    }
-    __syncwarp();
-}
 
 // One block per (64-row query tile, batch and head): the constants of its rows,
 // the ranges of the tile (the first head's block) and zeros in its rows of dQ.
@@ -622,8 +575,10 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 // A zero dS does not hide a NaN or an infinity in the operand it meets in the
                 // gradient MMAs: rows with one, of either operand, become zero rows (where such a
                 // row is visible, dS is NaN and the gradient with it).
-                if (__any_sync(0xffffffffu, bad))
-                    clear_nonfinite<D>(base + L::qt + (m % L::kQt) * L::kQBytes, wg * 32, kt_tile, row, lane);
+                if (__any_sync(0xffffffffu, bad)) {
+                    clear_query_rows<D>(base + L::qt + (m % L::kQt) * L::kQBytes, wg * 32, lane);
+                    clear_key_row<D>(kt_tile, row);
+                }
             }
             if (!wait_all(base + L::bar_dsempty + 8 * dsb, ((m / L::kNumDs) & 1) ^ 1, wc, kErrWaitOther)) {
                 ok = false;

@@ -94,7 +94,7 @@ EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_
             "streamkl_bwd_joint", "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd",
             "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table", "streamkl_score_fwd_plan", "streamkl_score_fwd",
             "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges", "streamkl_attn_fwd_plan",
-            "streamkl_attn_fwd")
+            "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -146,6 +146,8 @@ def load(build_if_stale: bool = True):
         at = ctypes.POINTER(Attn)
         lib.streamkl_attn_fwd_plan.argtypes = [at, op, pp]
         lib.streamkl_attn_fwd.argtypes = [at, *[P] * 6, F, I, P, P, P, P, Z, op, P]
+        lib.streamkl_attn_bwd_plan.argtypes = [at, op, pp]
+        lib.streamkl_attn_bwd.argtypes = [at, *[P] * 10, F, I, P, P, P, P, Z, op, P]
         lib.streamkl_status_string.argtypes = [I]
         lib.streamkl_status_string.restype = ctypes.c_char_p
         for name in ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd",
@@ -153,7 +155,7 @@ def load(build_if_stale: bool = True):
                      "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint",
                      "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table",
                      "streamkl_score_fwd_plan", "streamkl_score_fwd", "streamkl_score_bwd_plan", "streamkl_score_bwd",
-                     "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd"):
+                     "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -936,3 +938,75 @@ def attn_fwd(Q, K, V, ranges=None, causal=False, scale=None, rest=False, out=Non
                _address(end), _address(offset), 0.0 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
                _address(left), LSE.data_ptr(), workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_fwd")
     return (out, LSE, left) if rest else (out, LSE)
+
+
+def attn_bwd_plan(Q, K, V, num_splits=0) -> Plan:
+    plan, desc = Plan(), _attn_desc(Q, K, V)
+    desc.o = desc.d_o = _contiguous(Q.shape)
+    with torch.cuda.device(Q.device):
+        _raise(load().streamkl_attn_bwd_plan(ctypes.byref(desc), ctypes.byref(_opts(num_splits)), ctypes.byref(plan)),
+               "streamkl_attn_bwd_plan")
+    return plan
+
+
+def attn_bwd(dO, Q, K, V, O, LSE, rest=None, ranges=None, causal=False, scale=None, out=None, num_splits=0,
+             workspace=None, wait_limit_ns=0, debug_flags=0):
+    """(dQ, dK, dV), bf16 and contiguous, of sum(dO O) for attn_fwd's arguments and outputs; dO and O are bf16 with any
+    strides with d contiguous.  rest: attn_fwd's third output; without it the row sums of dO O carry O's rounding, which
+    shows in dQ where a row's keys have much in common.  dK and dV sum over the query heads of a key head and are the
+    same on every run; dQ is added up in float32 in no fixed order.  out: (dQ, dK, dV) to write into.  num_splits: CTAs
+    that share a key tile's query rows (0 = automatic)."""
+    given = _given_ranges(ranges)
+    num_splits, wait_limit_ns, debug_flags = int(num_splits), int(wait_limit_ns), int(debug_flags)
+    key, known = _lookup("attn_bwd", _tensors(dO, Q, K, V, O, LSE, rest, *given), num_splits, wait_limit_ns, debug_flags)
+    if known is None:
+        desc = _attn_desc(Q, K, V)
+        _ranges(ranges, Q)
+        desc.d_o = _heads("dO", dO, (torch.bfloat16,), Q.device, Q.shape)
+        desc.o = _heads("O", O, (torch.bfloat16,), Q.device, Q.shape)
+        _check_tensor("LSE", LSE, Q.shape[:3], torch.float32, Q.device)
+        if rest is not None:
+            _check_tensor("rest", rest, Q.shape, torch.bfloat16, Q.device)
+        opts, plan = _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
+        with torch.cuda.device(Q.device):
+            _raise(load().streamkl_attn_bwd_plan(ctypes.byref(desc), ctypes.byref(opts), ctypes.byref(plan)),
+                   "streamkl_attn_bwd_plan")
+        known = _remember(key, (desc, opts, plan.workspace_bytes, tuple(Q.shape), tuple(K.shape), Q.device))
+    desc, opts, nbytes, q_shape, k_shape, device = known
+    if out is None:
+        out = tuple([torch.empty(s, dtype=torch.bfloat16, device=device) for s in (q_shape, k_shape, k_shape)])
+    else:
+        for name, t, s in zip(("dQ", "dK", "dV"), out, (q_shape, k_shape, k_shape)):
+            _check_tensor(name, t, s, torch.bfloat16, device)
+    dQ, dK, dV = out
+    workspace = _scratch(workspace, nbytes, device)
+    begin, end, offset = given if len(given) == 3 else (None, None, None)
+    _raise(_on(device, load().streamkl_attn_bwd, desc, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+               _address(rest), LSE.data_ptr(), _address(begin), _address(end), _address(offset),
+               0.0 if scale is None else float(scale), 1 if causal else 0, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+               workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_bwd")
+    return dQ, dK, dV
+
+
+class Attention(torch.autograd.Function):
+    """O of attn_fwd with gradients to Q, K and V, in bf16 like the inputs.  Saves its inputs, O, what O's rounding left
+    and LSE, and recomputes the probabilities in the backward."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, ranges=None, causal=False, scale=None):
+        _guard_capture(Q, K, V)
+        causal, scale = bool(causal), None if scale is None else float(scale)  # the backward's are the forward's
+        O, LSE, rest = attn_fwd(Q, K, V, ranges, causal, scale, rest=True)
+        ctx.save_for_backward(Q, K, V, O, LSE, rest, *(ranges if ranges is not None else ()))
+        ctx.how = dict(causal=causal, scale=scale)
+        return O
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, LSE, rest, *ranges = ctx.saved_tensors
+        if dO.dtype != torch.bfloat16 or dO.stride(3) != 1 or any(s % 8 or s < dO.shape[3] for s in dO.stride()[:3]) or dO.data_ptr() % 16:
+            dO = dO.to(torch.bfloat16).contiguous()  # a broadcast or oddly strided gradient
+            dO = dO.clone() if dO.data_ptr() % 16 else dO
+        grads = attn_bwd(dO, Q, K, V, O, LSE, rest, tuple(ranges) if ranges else None, **ctx.how)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None)

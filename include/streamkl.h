@@ -418,6 +418,21 @@ STREAMKL_API streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const 
                                                void* workspace, size_t workspace_bytes, const streamkl_options* opt,
                                                streamkl_stream_t stream);
 
+/* Gradients of sum(dO * O): dQ [B, H, Nq, d], dK, dV [B, H_kv, Nk, d], bf16 and
+ * contiguous, sums in float32 rounded once; dK and dV sum over the query heads
+ * of a key head.  O, rest and LSE are the forward's for the same inputs; without
+ * rest (NULL) the row sums of dO * O carry O's rounding, which shows in dQ where
+ * keys have much in common.  dQ is added up in no fixed order; dK and dV are the
+ * same on every run. */
+STREAMKL_API streamkl_status streamkl_attn_bwd_plan(const streamkl_attn* desc, const streamkl_options* opt,
+                                                    streamkl_plan* plan);
+STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const void* dO, const void* Q, const void* K,
+                                               const void* V, const void* O, const void* rest, const float* LSE,
+                                               const int32_t* begin, const int32_t* end, const int32_t* offset,
+                                               float scale, int causal, void* dQ, void* dK, void* dV, void* workspace,
+                                               size_t workspace_bytes, const streamkl_options* opt,
+                                               streamkl_stream_t stream);
+
 /* Synchronises `stream`, reads the workspace's device error word into
  * *device_error (if not NULL), clears it, and returns STREAMKL_ERR_TIMEOUT if
  * it was set, STREAMKL_OK otherwise (or CUDA on a failed copy). */

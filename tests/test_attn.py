@@ -8,6 +8,13 @@ LSE is off by at most del + N 2^-24 (the sum of up to N terms) + its rounding.
 A probability enters the product with V rounded to bf16 (2^-8 of it) from a
 value off by a factor 1 +- 2 del, the product accumulates in float32, and O is
 rounded once:  (2^-8 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|.
+
+Gradients.  P is off by a factor 1 +- 2 del and enters dV rounded (2^-8 of it).
+dP is a float32 sum, off by (d + 32) 2^-24 of |dO| |V|^T; D is a float32 sum of
+products with O + rest, which is off from O by o_tol - 2^-8 |O| + 2^-16 |O|
+(o_tol's first part).  dS = P (dP - D) takes its share of all of these; it
+enters dK rounded to bf16 (2^-8) and dQ as two terms (2^-16), sums are float32
+((N + 128) 2^-24 of the magnitudes), outputs are rounded once (2^-8).
 """
 import math
 
@@ -56,6 +63,27 @@ class Ref:
         self.delta = (d + 32) * 2.0 ** -24 * A + 2.0 ** -20 * (big(s) + 1)
         self.acc = (Nk + 128) * 2.0 ** -24
         self.o_tol = (2.0 ** -8 + 4 * self.delta + self.acc) * (self.p @ v.abs()) + 2.0 ** -8 * self.O.abs() + 1e-30
+
+    def check_grads(self, dO, dQ, dK, dV):
+        B, H, Nq, d = self.q.shape
+        Nk = self.k.shape[2]
+        g = dO.double().masked_fill(~self.live[..., None], 0.0)
+        back = lambda t: t.reshape(B, self.Hk, self.G, Nk, d).sum(2)  # noqa: E731
+        mag = g.abs() @ self.v.abs().transpose(2, 3)
+        dP = g @ self.v.transpose(2, 3)
+        D = (g * self.O).sum(-1, keepdim=True)
+        d_err = ((self.o_tol - 2.0 ** -8 * self.O.abs() + (2.0 ** -16 + (d + 32) * 2.0 ** -24) * self.O.abs()) * g.abs()).sum(-1, keepdim=True)
+        dS = self.p * (dP - D) * self.scale
+        err = self.p * self.scale * (2 * self.delta * (dP - D).abs() + (d + 32) * 2.0 ** -24 * mag + d_err)
+        acc = 2.0 ** -24 * (max(Nk, Nq * self.G) + 128)
+        want = dS @ self.k, back(dS.transpose(2, 3) @ self.q), back(self.p.transpose(2, 3) @ g)
+        tol = ((err + (2.0 ** -16 + acc) * dS.abs()) @ self.k.abs(),
+               back((err + (2.0 ** -8 + acc) * dS.abs()).transpose(2, 3) @ self.q.abs()),
+               back((self.p * (2.0 ** -8 + 2 * self.delta + acc)).transpose(2, 3) @ g.abs()))
+        for name, got, w, t in zip(("dQ", "dK", "dV"), (dQ, dK, dV), want, tol):
+            bound = t * 1.01 + 2.0 ** -8 * w.abs() + 1e-30  # 1.01: products of the terms above
+            e = (got.double() - w).abs()
+            assert bool((e <= bound).all()), (name, float((e / bound).max()))
 
     def check(self, O, LSE):
         assert torch.equal(LSE == -math.inf, ~self.live)
@@ -112,3 +140,18 @@ def test_forward(shape, kind):
     assert bool((err <= ref.o_tol - 2.0 ** -8 * ref.O.abs() + 2.0 ** -16 * ref.O.abs()).all())
     again = sk.attn_fwd(Q, K, V, ranges=ranges)
     assert torch.equal(again[0], O) and torch.equal(again[1], LSE)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["full", "causal", "window", "docs", "padded", "two ends"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gradients(shape, kind):
+    B, H, Hk, Nq, Nk, d = shape
+    Q, K, V = inputs(*shape, seed=Nk + 1)
+    dO = torch.randn((B, H, Nq, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).to(BF16)
+    ranges = masks(kind, B, Nq, Nk)
+    O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True)
+    grads = sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges)
+    Ref(Q, K, V, ranges).check_grads(dO, *grads)
+    again = sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges)
+    assert torch.equal(again[1], grads[1]) and torch.equal(again[2], grads[2])
