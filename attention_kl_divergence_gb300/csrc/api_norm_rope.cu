@@ -84,6 +84,21 @@ NormRopeParams make_params(const streamkl_norm_rope* s, const void* q, const voi
     return p;
 }
 
+// Several axes: every pair's axis is one of them.  A description without is one position per token.
+bool axes_ok(const streamkl_norm_rope* s, const streamkl_rope_axes* a, const void* positions) {
+    if (!a) return true;
+    if (a->axes < 1 || a->axes > 4 || s->rot < 8 || (!positions && s->N > 0)) return false;
+    for (int e = 0; e < s->rot / 2; ++e)
+        if (a->axis_of[e] >= a->axes) return false;
+    return true;
+}
+
+void set_axes(NormRopeParams* p, const streamkl_norm_rope* s, const streamkl_rope_axes* a) {
+    if (!a) return;
+    p->axes = a->axes;
+    for (int e = 0; e < s->rot / 2; ++e) p->axis_of[e >> 4] |= uint32_t(a->axis_of[e]) << (2 * (e & 15));
+}
+
 // Pointers shared by both directions; weights and positions may be absent.
 bool pointers_ok(const streamkl_norm_rope* s, const void* q, const void* k, const void* wq, const void* wk,
                  const float* table, const void* positions) {
@@ -105,19 +120,17 @@ streamkl_status plan_bwd_norm(const streamkl_norm_rope* s, int* ctas_q, int* cta
     return STREAMKL_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-streamkl_status streamkl_norm_rope_fwd(const streamkl_norm_rope* desc, const void* q, const void* k, const void* wq,
-                                       const void* wk, const float* table, const void* positions, void* yq, void* yk,
-                                       streamkl_stream_t stream) {
+streamkl_status norm_rope_fwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes, const void* q,
+                              const void* k, const void* wq, const void* wk, const float* table,
+                              const void* positions, void* yq, void* yk, streamkl_stream_t stream) {
     streamkl_status st = check_desc(desc, false);
     if (st != STREAMKL_OK) return st;
+    if (!axes_ok(desc, axes, positions)) return STREAMKL_ERR_INVALID_ARG;
     if (desc->N == 0) return STREAMKL_OK;
     if (!pointers_ok(desc, q, k, wq, wk, table, positions)) return STREAMKL_ERR_INVALID_ARG;
     if (!yq || !yk || !aligned16(yq) || !aligned16(yk)) return STREAMKL_ERR_INVALID_ARG;
     NormRopeParams p = make_params(desc, q, k, wq, wk, table, positions);
+    set_axes(&p, desc, axes);
     p.side[0].y = yq;
     p.side[1].y = yk;
     return launch_norm_rope_fwd(desc->d, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -125,19 +138,13 @@ streamkl_status streamkl_norm_rope_fwd(const streamkl_norm_rope* desc, const voi
                : STREAMKL_ERR_CUDA;
 }
 
-size_t streamkl_norm_rope_workspace_bytes(const streamkl_norm_rope* desc) {
-    int cq = 0, c = 0;
-    size_t bytes = 0;
-    if (check_desc(desc, true) != STREAMKL_OK || plan_bwd_norm(desc, &cq, &c, &bytes) != STREAMKL_OK) return 0;
-    return bytes;
-}
-
-streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* desc, const void* dyq, const void* dyk, const void* q,
-                                       const void* k, const void* wq, const void* wk, const float* table,
-                                       const void* positions, void* dq, void* dk, void* dwq, void* dwk,
-                                       void* workspace, size_t workspace_bytes, streamkl_stream_t stream) {
+streamkl_status norm_rope_bwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes, const void* dyq,
+                              const void* dyk, const void* q, const void* k, const void* wq, const void* wk,
+                              const float* table, const void* positions, void* dq, void* dk, void* dwq, void* dwk,
+                              void* workspace, size_t workspace_bytes, streamkl_stream_t stream) {
     streamkl_status st = check_desc(desc, true);
     if (st != STREAMKL_OK) return st;
+    if (!axes_ok(desc, axes, positions)) return STREAMKL_ERR_INVALID_ARG;
     if ((dwq && !wq) || (dwk && !wk) || !aligned16(dwq) || !aligned16(dwk)) return STREAMKL_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t wbytes = size_t(desc->d) * (desc->weight_bf16 ? 2 : 4);
@@ -156,6 +163,7 @@ streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* desc, const voi
     if ((st = plan_bwd_norm(desc, &ctas_q, &ctas, &bytes)) != STREAMKL_OK) return st;
     if (workspace_bytes < bytes) return STREAMKL_ERR_WORKSPACE;
     NormRopeParams p = make_params(desc, q, k, wq, wk, table, positions);
+    set_axes(&p, desc, axes);
     p.side[0].y = const_cast<void*>(dyq);
     p.side[1].y = const_cast<void*>(dyk);
     p.side[0].dx = dq;
@@ -165,6 +173,49 @@ streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* desc, const voi
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
     p.ctas_q = ctas_q;
     return launch_norm_rope_bwd(desc->d, p, ctas, s) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+streamkl_status streamkl_norm_rope_fwd(const streamkl_norm_rope* desc, const void* q, const void* k, const void* wq,
+                                       const void* wk, const float* table, const void* positions, void* yq, void* yk,
+                                       streamkl_stream_t stream) {
+    return norm_rope_fwd(desc, nullptr, q, k, wq, wk, table, positions, yq, yk, stream);
+}
+
+streamkl_status streamkl_norm_rope_axes_fwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes,
+                                            const void* q, const void* k, const void* wq, const void* wk,
+                                            const float* table, const void* positions, void* yq, void* yk,
+                                            streamkl_stream_t stream) {
+    if (!axes) return STREAMKL_ERR_INVALID_ARG;
+    return norm_rope_fwd(desc, axes, q, k, wq, wk, table, positions, yq, yk, stream);
+}
+
+size_t streamkl_norm_rope_workspace_bytes(const streamkl_norm_rope* desc) {
+    int cq = 0, c = 0;
+    size_t bytes = 0;
+    if (check_desc(desc, true) != STREAMKL_OK || plan_bwd_norm(desc, &cq, &c, &bytes) != STREAMKL_OK) return 0;
+    return bytes;
+}
+
+streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* desc, const void* dyq, const void* dyk,
+                                       const void* q, const void* k, const void* wq, const void* wk,
+                                       const float* table, const void* positions, void* dq, void* dk, void* dwq,
+                                       void* dwk, void* workspace, size_t workspace_bytes, streamkl_stream_t stream) {
+    return norm_rope_bwd(desc, nullptr, dyq, dyk, q, k, wq, wk, table, positions, dq, dk, dwq, dwk, workspace,
+                         workspace_bytes, stream);
+}
+
+streamkl_status streamkl_norm_rope_axes_bwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes,
+                                            const void* dyq, const void* dyk, const void* q, const void* k,
+                                            const void* wq, const void* wk, const float* table, const void* positions,
+                                            void* dq, void* dk, void* dwq, void* dwk, void* workspace,
+                                            size_t workspace_bytes, streamkl_stream_t stream) {
+    if (!axes) return STREAMKL_ERR_INVALID_ARG;
+    return norm_rope_bwd(desc, axes, dyq, dyk, q, k, wq, wk, table, positions, dq, dk, dwq, dwk, workspace,
+                         workspace_bytes, stream);
 }
 
 streamkl_status streamkl_rope_table(const double* inv_freq, int64_t rows, int32_t half, float* table,

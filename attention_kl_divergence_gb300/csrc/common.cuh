@@ -121,7 +121,9 @@ struct NormRopeParams {
     float eps;
     const float* table;     // [table_rows][rot / 2][2]: cosine, sine
     int64_t table_rows;
-    const void* positions;  // [B, N] int32 or int64, or null: start + n
+    const void* positions;  // [B, N] int32 or int64, or null: start + n; several axes: [axes, B, N]
+    int axes;               // 0: one position per token
+    uint32_t axis_of[4];    // several axes: 2 bits per pair
     int64_t start;
     float* part;            // backward: [ctas][d] parts of dw
     int ctas_q;             // backward: CTAs of the query heads

@@ -137,14 +137,47 @@ struct Turn {
     float2 c[2], s[2];
 };
 
+__device__ __forceinline__ int64_t position_at(const NormRopeParams& p, int64_t k) {
+    return p.pos_int64 ? static_cast<const int64_t*>(p.positions)[k] : static_cast<const int32_t*>(p.positions)[k];
+}
+
+// AXES: each pair is turned by the token's position on an axis of its own.  Sections
+// of four pairs or more put a lane's pairs on one axis: one row of the table; else
+// four loads from as many rows.
+template <bool AXES>
 __device__ __forceinline__ Turn load_turn(const NormRopeParams& p, const Span& sp, uint32_t token, uint32_t n) {
     Turn t;
     t.c[0] = t.c[1] = make_float2(1.f, 1.f);
     t.s[0] = t.s[1] = make_float2(0.f, 0.f);
     if (!sp.turned) return t;
-    const int64_t pos = !p.positions ? p.start + n
-                        : p.pos_int64 ? static_cast<const int64_t*>(p.positions)[token]
-                                      : static_cast<const int32_t*>(p.positions)[token];
+    if (AXES) {
+        const float nan = __int_as_float(0x7fc00000);
+        const uint32_t axes = p.axis_of[sp.pair >> 4] >> (2 * (sp.pair & 15)) & 255u;  // of pairs pair .. pair + 3
+        const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
+        if (axes == (axes & 3u) * 0x55u) {
+            const int64_t pos = position_at(p, (axes & 3u) * tokens + token);
+            if (pos < 0 || pos >= p.table_rows) {
+                t.c[0] = t.c[1] = t.s[0] = t.s[1] = make_float2(nan, nan);
+                return t;
+            }
+            const float4* f = reinterpret_cast<const float4*>(p.table + (pos * (p.rot / 2) + sp.pair) * 2);
+            const float4 lo = __ldg(f), hi = __ldg(f + 1);
+            t.c[0] = make_float2(lo.x, lo.z), t.s[0] = make_float2(lo.y, lo.w);
+            t.c[1] = make_float2(hi.x, hi.z), t.s[1] = make_float2(hi.y, hi.w);
+            return t;
+        }
+        float2 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t pos = position_at(p, (axes >> (2 * e) & 3u) * tokens + token);
+            v[e] = make_float2(nan, nan);
+            if (pos >= 0 && pos < p.table_rows) v[e] = __ldg(reinterpret_cast<const float2*>(p.table) + pos * (p.rot / 2) + sp.pair + e);
+        }
+        t.c[0] = make_float2(v[0].x, v[1].x), t.s[0] = make_float2(v[0].y, v[1].y);
+        t.c[1] = make_float2(v[2].x, v[3].x), t.s[1] = make_float2(v[2].y, v[3].y);
+        return t;
+    }
+    const int64_t pos = !p.positions ? p.start + n : position_at(p, token);
     if (pos < 0 || pos >= p.table_rows) {
         const float nan = __int_as_float(0x7fc00000);
         t.c[0] = t.c[1] = t.s[0] = t.s[1] = make_float2(nan, nan);
@@ -199,7 +232,7 @@ __device__ __forceinline__ const char* at_bytes(const void* p, int64_t bytes) { 
 }  // namespace
 
 // One CTA: kNrTokens neighbouring tokens x kNrHeads heads of q or of k.
-template <int D, bool INTERLEAVED>
+template <int D, bool INTERLEAVED, bool AXES>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kNrHeads / ROWS;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -223,7 +256,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const __grid_
         if (h0 + k * ROWS < s.H) raw[k].load(xp, xp + ab);
         xp += xs;
     }
-    const Turn turn = load_turn(p, sp, token, n);
+    const Turn turn = load_turn<AXES>(p, sp, token, n);
     const Pairs w = load_weights<INTERLEAVED>(s.w, p.weight_bf16, sp);
     // y_f = r (f (w_f c) - g (w_g s)),  y_g = r (g (w_g c) + f (w_f s))
     float2 fc[2], gs[2], gc[2], fs[2];
@@ -252,7 +285,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_fwd_kernel(const __grid_
 // Gradient.  CTAs [0, ctas_q) walk the query heads, the others the key heads;
 // each sums its rows' part of dw in registers, then over its warps, and writes
 // it to part[cta][D].  The order of every sum is fixed.
-template <int D, bool INTERLEAVED, bool GRAD_BF16>
+template <int D, bool INTERLEAVED, bool GRAD_BF16, bool AXES>
 __global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kNrHeads / ROWS, GB = GRAD_BF16 ? 2 : 4;
     __shared__ float red[kNrThreads / 32][D];
@@ -292,7 +325,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) norm_rope_bwd_kernel(c
             xp += xs;
             gp += gs;
         }
-        const Turn turn = load_turn(p, sp, token, n);
+        const Turn turn = load_turn<AXES>(p, sp, token, n);
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             const Pairs x = rx[k].template get<INTERLEAVED>(), g = rg[k].template get<INTERLEAVED>();
@@ -402,36 +435,40 @@ void norm_rope_bwd_ctas(const NormRopeParams& p, int sms, int* ctas_q, int* ctas
     *ctas = *ctas_q + static_cast<int>(std::min(slots - q, ik));
 }
 
+namespace {
+template <int D, bool AXES>
+void launch_fwd_d(const NormRopeParams& p, unsigned grid, cudaStream_t stream) {
+    p.interleaved ? norm_rope_fwd_kernel<D, true, AXES><<<grid, kNrThreads, 0, stream>>>(p)
+                  : norm_rope_fwd_kernel<D, false, AXES><<<grid, kNrThreads, 0, stream>>>(p);
+}
+
+template <int D, bool AXES>
+void launch_bwd_d(const NormRopeParams& p, int ctas, cudaStream_t stream) {
+    if (p.interleaved)
+        p.grad_bf16 ? norm_rope_bwd_kernel<D, true, true, AXES><<<ctas, kNrThreads, 0, stream>>>(p)
+                    : norm_rope_bwd_kernel<D, true, false, AXES><<<ctas, kNrThreads, 0, stream>>>(p);
+    else
+        p.grad_bf16 ? norm_rope_bwd_kernel<D, false, true, AXES><<<ctas, kNrThreads, 0, stream>>>(p)
+                    : norm_rope_bwd_kernel<D, false, false, AXES><<<ctas, kNrThreads, 0, stream>>>(p);
+}
+}  // namespace
+
 cudaError_t launch_norm_rope_fwd(int d, const NormRopeParams& p, cudaStream_t stream) {
     const int64_t groups = (int64_t(p.B) * p.N + kNrTokens - 1) / kNrTokens;
     const int64_t ctas = groups * ((p.Hq + kNrHeads - 1) / kNrHeads + (p.Hk + kNrHeads - 1) / kNrHeads);
     const unsigned grid = static_cast<unsigned>(ctas);
     if (d == 128)
-        p.interleaved ? norm_rope_fwd_kernel<128, true><<<grid, kNrThreads, 0, stream>>>(p)
-                      : norm_rope_fwd_kernel<128, false><<<grid, kNrThreads, 0, stream>>>(p);
+        p.axes ? launch_fwd_d<128, true>(p, grid, stream) : launch_fwd_d<128, false>(p, grid, stream);
     else
-        p.interleaved ? norm_rope_fwd_kernel<64, true><<<grid, kNrThreads, 0, stream>>>(p)
-                      : norm_rope_fwd_kernel<64, false><<<grid, kNrThreads, 0, stream>>>(p);
+        p.axes ? launch_fwd_d<64, true>(p, grid, stream) : launch_fwd_d<64, false>(p, grid, stream);
     return cudaGetLastError();
 }
 
-namespace {
-template <int D>
-void launch_bwd_d(const NormRopeParams& p, int ctas, cudaStream_t stream) {
-    if (p.interleaved)
-        p.grad_bf16 ? norm_rope_bwd_kernel<D, true, true><<<ctas, kNrThreads, 0, stream>>>(p)
-                    : norm_rope_bwd_kernel<D, true, false><<<ctas, kNrThreads, 0, stream>>>(p);
-    else
-        p.grad_bf16 ? norm_rope_bwd_kernel<D, false, true><<<ctas, kNrThreads, 0, stream>>>(p)
-                    : norm_rope_bwd_kernel<D, false, false><<<ctas, kNrThreads, 0, stream>>>(p);
-}
-}  // namespace
-
 cudaError_t launch_norm_rope_bwd(int d, const NormRopeParams& p, int ctas, cudaStream_t stream) {
     if (d == 128)
-        launch_bwd_d<128>(p, ctas, stream);
+        p.axes ? launch_bwd_d<128, true>(p, ctas, stream) : launch_bwd_d<128, false>(p, ctas, stream);
     else
-        launch_bwd_d<64>(p, ctas, stream);
+        p.axes ? launch_bwd_d<64, true>(p, ctas, stream) : launch_bwd_d<64, false>(p, ctas, stream);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!p.side[0].dw && !p.side[1].dw)) return e;
     norm_rope_dw_kernel<<<dim3(d / 32, 2), 256, 0, stream>>>(p, d, ctas);

@@ -77,6 +77,10 @@ class NormRope(ctypes.Structure):
         [(n, Strides) for n in ("q", "k", "yq", "yk", "dq", "dk")]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("axis_of", ctypes.c_uint8 * 64)]
+
+
 class Attn(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "H_kv", "Nq", "Nk", "d")] + \
         [(n, Strides) for n in ("q", "k", "v", "o", "d_o")]
@@ -94,7 +98,8 @@ EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_
             "streamkl_bwd_joint", "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd",
             "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table", "streamkl_score_fwd_plan", "streamkl_score_fwd",
             "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges", "streamkl_attn_fwd_plan",
-            "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd")
+            "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd",
+            "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -143,6 +148,9 @@ def load(build_if_stale: bool = True):
         lib.streamkl_norm_rope_workspace_bytes.argtypes = [nr]
         lib.streamkl_norm_rope_workspace_bytes.restype = Z
         lib.streamkl_rope_table.argtypes = [P, ctypes.c_int64, ctypes.c_int32, P, P]
+        ra = ctypes.POINTER(RopeAxes)
+        lib.streamkl_norm_rope_axes_fwd.argtypes = [nr, ra, *[P] * 9]
+        lib.streamkl_norm_rope_axes_bwd.argtypes = [nr, ra, *[P] * 13, Z, P]
         at = ctypes.POINTER(Attn)
         lib.streamkl_attn_fwd_plan.argtypes = [at, op, pp]
         lib.streamkl_attn_fwd.argtypes = [at, *[P] * 6, F, I, P, P, P, P, Z, op, P]
@@ -155,7 +163,8 @@ def load(build_if_stale: bool = True):
                      "streamkl_noalloc_status", "streamkl_bwd_joint_plan", "streamkl_bwd_joint",
                      "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table",
                      "streamkl_score_fwd_plan", "streamkl_score_fwd", "streamkl_score_bwd_plan", "streamkl_score_bwd",
-                     "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd"):
+                     "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd",
+                     "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -736,7 +745,34 @@ def _contiguous(shape) -> Strides:
     return Strides(H * max(N, 1) * d, max(N, 1) * d, d)
 
 
-def _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved):
+def rope_axes(sections, spread=False) -> tuple:
+    """The axis that turns each pair, for qk_norm_rope's axes: sections[a] pairs of axis a, one axis after the other, or
+    (spread) the axes in turn, each as long as it has pairs left."""
+    left = [int(n) for n in sections]
+    if not left or any(n < 0 for n in left):
+        raise ValueError(f"sections must be numbers of pairs, got {tuple(sections)}")
+    if not spread:
+        return tuple([a for a, n in enumerate(left) for _ in range(n)])
+    return tuple([a for k in range(max(left)) for a, n in enumerate(left) if k < n])
+
+
+def _axes(axes, table, positions):
+    """None or (struct, number of axes); axes is a tuple of whole numbers."""
+    if axes is None:
+        return None
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 3 or not 1 <= positions.shape[0] <= 4:
+        raise ValueError("positions on several axes must be [axes, B, N], up to 4 axes")
+    if not isinstance(table, torch.Tensor) or table.dim() != 3 or len(axes) != table.shape[1]:
+        raise ValueError("axes must name the axis of each of the table's pairs (see rope_axes)")
+    if any(not 0 <= a < positions.shape[0] for a in axes):
+        raise ValueError(f"axes must be below {positions.shape[0]}, the axes of positions")
+    out = RopeAxes(positions.shape[0])
+    for e, a in enumerate(axes):
+        out.axis_of[e] = a
+    return out
+
+
+def _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved, axes=None):
     desc = NormRope()
     desc.q, desc.k = _heads("q", q, (torch.bfloat16,)), _heads("k", k, (torch.bfloat16,), q.device)
     B, Hq, N, d = q.shape
@@ -761,13 +797,20 @@ def _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved):
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
             raise ValueError("positions must be an int32 or int64 tensor")
-        _check_tensor("positions", positions, (B, N), positions.dtype, q.device)
+        _check_tensor("positions", positions, (B, N) if axes is None else (positions.shape[0], B, N), positions.dtype, q.device)
     desc.B, desc.Hq, desc.Hk, desc.N, desc.d, desc.rot = B, Hq, k.shape[1], N, d, rot
     desc.interleaved, desc.eps = int(interleaved), eps
     desc.weight_bf16 = int(torch.bfloat16 in types)
     desc.pos_int64 = int(positions is not None and positions.dtype == torch.int64)
     desc.table_rows = table.shape[0] if table is not None else 0
     return desc
+
+
+def _plain_axes(axes):
+    """A tuple of whole numbers that no program can change."""
+    if axes is None or (type(axes) is tuple and set(map(type, axes)) <= {int}):
+        return axes
+    return tuple([int(a) for a in axes])
 
 
 def _plain(start, eps, interleaved):
@@ -786,40 +829,52 @@ def _at(desc, start):
     return desc
 
 
-def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False, out=None):
+def qk_norm_rope(q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False, out=None,
+                 axes=None):
     """(q', k'): every head of q [B, Hq, N, d] and k [B, Hk, N, d] (bf16, any strides with d contiguous) divided by
     its root mean square, times wq / wk ([d], float32 or bf16; None: ones), its first 2 * table.shape[1] values turned
     by the angles of its position (positions [B, N], else start + n; table from rope_table; None: no rotation).  out: two
-    bf16 tensors of the same shapes, any strides (rows of a cache, or q and k themselves); new contiguous ones otherwise."""
+    bf16 tensors of the same shapes, any strides (rows of a cache, or q and k themselves); new contiguous ones otherwise.
+    axes: several positions per token, positions [A, B, N] (time, height and width of a patch, say): pair e is turned by
+    the position on axis axes[e] (see rope_axes)."""
     start, eps, interleaved = _plain(start, eps, interleaved)
-    key, known = _lookup("norm_rope", _tensors(q, k, wq, wk, table, positions, *(out or ())), eps, interleaved)
+    axes = _plain_axes(axes)
+    key, known = _lookup("norm_rope", _tensors(q, k, wq, wk, table, positions, *(out or ())), eps, interleaved, axes)
     if known is None:
-        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved)
+        more = _axes(axes, table, positions)
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved, axes)
         if out is not None:
             desc.yq = _heads("out[0]", out[0], (torch.bfloat16,), q.device, q.shape)
             desc.yk = _heads("out[1]", out[1], (torch.bfloat16,), q.device, k.shape)
         else:
             desc.yq, desc.yk = _contiguous(q.shape), _contiguous(k.shape)
-        known = _remember(key, (desc, tuple(q.shape), tuple(k.shape), q.device))
-    desc, q_shape, k_shape, device = known
+        known = _remember(key, (desc, tuple(q.shape), tuple(k.shape), q.device, more))
+    desc, q_shape, k_shape, device, more = known
     if out is None:
         out = (torch.empty(q_shape, dtype=torch.bfloat16, device=device),
                torch.empty(k_shape, dtype=torch.bfloat16, device=device))
     yq, yk = out
-    _raise(_on(device, load().streamkl_norm_rope_fwd, _at(desc, start), q.data_ptr(), k.data_ptr(), _address(wq),
-               _address(wk), _address(table), _address(positions), yq.data_ptr(), yk.data_ptr()), "streamkl_norm_rope_fwd")
+    args = (q.data_ptr(), k.data_ptr(), _address(wq), _address(wk), _address(table), _address(positions), yq.data_ptr(),
+            yk.data_ptr())
+    if more is None:
+        _raise(_on(device, load().streamkl_norm_rope_fwd, _at(desc, start), *args), "streamkl_norm_rope_fwd")
+    else:
+        _raise(_on(device, load().streamkl_norm_rope_axes_fwd, desc, more, *args), "streamkl_norm_rope_axes_fwd")
     return yq, yk
 
 
 def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6,
-                     interleaved=False, workspace=None, out=None):
+                     interleaved=False, workspace=None, out=None, axes=None):
     """(dq, dk, dwq, dwk) of sum(dyq q') + sum(dyk k') for qk_norm_rope's arguments; dyq, dyk are both bf16 or both
     float32 (kl_bwd's gradients as they come), any strides with d contiguous.  dq, dk are bf16, dwq, dwk of the weights'
     type (None without weights).  out: (dq, dk) to write into.  Equal inputs give equal bits."""
     start, eps, interleaved = _plain(start, eps, interleaved)
-    key, known = _lookup("norm_rope_bwd", _tensors(dyq, dyk, q, k, wq, wk, table, positions, *(out or ())), eps, interleaved)
+    axes = _plain_axes(axes)
+    key, known = _lookup("norm_rope_bwd", _tensors(dyq, dyk, q, k, wq, wk, table, positions, *(out or ())), eps, interleaved,
+                         axes)
     if known is None:
-        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved)
+        more = _axes(axes, table, positions)
+        desc = _norm_rope_desc(q, k, wq, wk, table, positions, eps, interleaved, axes)
         desc.yq = _heads("dyq", dyq, (torch.bfloat16, torch.float32), q.device, q.shape)
         desc.yk = _heads("dyk", dyk, (dyq.dtype,), q.device, k.shape)
         desc.grad_bf16 = int(dyq.dtype == torch.bfloat16)
@@ -830,17 +885,21 @@ def qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, table=None, positions=Non
             desc.dq, desc.dk = _contiguous(q.shape), _contiguous(k.shape)
         with torch.cuda.device(q.device):
             nbytes = max(int(load().streamkl_norm_rope_workspace_bytes(ctypes.byref(desc))), 256)
-        known = _remember(key, (desc, nbytes, tuple(q.shape), tuple(k.shape), q.device))
-    desc, nbytes, q_shape, k_shape, device = known
+        known = _remember(key, (desc, nbytes, tuple(q.shape), tuple(k.shape), q.device, more))
+    desc, nbytes, q_shape, k_shape, device, more = known
     if out is None:
         out = (torch.empty(q_shape, dtype=torch.bfloat16, device=device),
                torch.empty(k_shape, dtype=torch.bfloat16, device=device))
     dq, dk = out
     dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
     workspace = _scratch(workspace, nbytes, device)
-    _raise(_on(device, load().streamkl_norm_rope_bwd, _at(desc, start), dyq.data_ptr(), dyk.data_ptr(), q.data_ptr(),
-               k.data_ptr(), _address(wq), _address(wk), _address(table), _address(positions), dq.data_ptr(), dk.data_ptr(),
-               _address(dwq), _address(dwk), workspace.data_ptr(), workspace.numel()), "streamkl_norm_rope_bwd")
+    args = (dyq.data_ptr(), dyk.data_ptr(), q.data_ptr(), k.data_ptr(), _address(wq), _address(wk), _address(table),
+            _address(positions), dq.data_ptr(), dk.data_ptr(), _address(dwq), _address(dwk), workspace.data_ptr(),
+            workspace.numel())
+    if more is None:
+        _raise(_on(device, load().streamkl_norm_rope_bwd, _at(desc, start), *args), "streamkl_norm_rope_bwd")
+    else:
+        _raise(_on(device, load().streamkl_norm_rope_axes_bwd, desc, more, *args), "streamkl_norm_rope_axes_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -849,10 +908,10 @@ class QKNormRope(torch.autograd.Function):
     inputs and recomputes the norms in the backward."""
 
     @staticmethod
-    def forward(ctx, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False):
+    def forward(ctx, q, k, wq=None, wk=None, table=None, positions=None, start=0, eps=1e-6, interleaved=False, axes=None):
         _guard_capture(q, k, wq, wk)
         ctx.save_for_backward(q, k, wq, wk, table, positions)
-        ctx.how = dict(zip(("start", "eps", "interleaved"), _plain(start, eps, interleaved)))
+        ctx.how = dict(zip(("start", "eps", "interleaved"), _plain(start, eps, interleaved)), axes=_plain_axes(axes))
         return qk_norm_rope(q, k, wq, wk, table, positions, **ctx.how)
 
     @staticmethod
@@ -862,7 +921,7 @@ class QKNormRope(torch.autograd.Function):
         dyq, dyk = (torch.zeros_like(x, memory_format=torch.contiguous_format) if g is None else g.contiguous()
                     for g, x in ((dyq, q), (dyk, k)))
         grads = qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, table, positions, **ctx.how)
-        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None, None, None)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None, None, None, None)
 
 
 # ---------------------------------------------------------------------------

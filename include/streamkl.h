@@ -372,6 +372,26 @@ STREAMKL_API streamkl_status streamkl_norm_rope_bwd(const streamkl_norm_rope* de
                                                     void* dwq, void* dwk, void* workspace, size_t workspace_bytes,
                                                     streamkl_stream_t stream);
 
+/* The same with positions on several axes (time, height and width of a patch):
+ * positions is [axes, B, N] (not NULL), and pair e of a head is turned by the
+ * token's position on axis axis_of[e], e < rot / 2 (axes up to 4), through the
+ * table's row of that position.  Errors as above; INVALID_ARG for axes NULL. */
+typedef struct {
+    int32_t axes;
+    uint8_t axis_of[64];
+} streamkl_rope_axes;
+
+STREAMKL_API streamkl_status streamkl_norm_rope_axes_fwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes,
+                                                         const void* q, const void* k, const void* wq, const void* wk,
+                                                         const float* table, const void* positions, void* yq, void* yk,
+                                                         streamkl_stream_t stream);
+STREAMKL_API streamkl_status streamkl_norm_rope_axes_bwd(const streamkl_norm_rope* desc, const streamkl_rope_axes* axes,
+                                                         const void* dyq, const void* dyk, const void* q, const void* k,
+                                                         const void* wq, const void* wk, const float* table,
+                                                         const void* positions, void* dq, void* dk, void* dwq, void* dwk,
+                                                         void* workspace, size_t workspace_bytes,
+                                                         streamkl_stream_t stream);
+
 /* table[n][e] = (cos, sin) of n * inv_freq[e] for n < rows, e < half, from
  * angles in float64 (at position 10^6 a float32 angle is off by 0.03).
  * inv_freq: device float64 [half].  Errors: INVALID_ARG, CUDA. */
