@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.cuh"
+#include "cache8.cuh"
 #include "common.cuh"
 #include "score.cuh"
 
@@ -52,6 +53,11 @@ size_t attn_bwd_row_bytes(int64_t bh, int q_tiles);     // workspace of p.rows a
 size_t attn_bwd_key_bytes(int64_t batch, int q_tiles);  // of p.keys
 cudaError_t launch_attn_bwd(int d, const CUtensorMap* maps, const AttnBwdParams& p, const ScoreParams& sp, int ctas, int sms,
                             cudaStream_t stream);
+
+// 8-bit cache: new tokens in, tokens out, and attention of a few new tokens over it.
+cudaError_t launch_cache8_append(const CacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache8_read(const CacheReadParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_cache8_attn(const CacheAttnParams& p, cudaStream_t stream);
 
 cudaError_t launch_key_ranges(const KeyRangeParams& p, cudaStream_t stream);
 

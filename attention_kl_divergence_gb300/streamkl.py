@@ -86,6 +86,11 @@ class Attn(ctypes.Structure):
         [(n, Strides) for n in ("q", "k", "v", "o", "d_o")]
 
 
+class CacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("pages", "H_kv", "T", "d", "B", "M", "H", "N")] + \
+        [(n, Strides) for n in ("x", "y")]
+
+
 class StreamKLError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -99,7 +104,8 @@ EXPORTED = ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_
             "streamkl_norm_rope_workspace_bytes", "streamkl_rope_table", "streamkl_score_fwd_plan", "streamkl_score_fwd",
             "streamkl_score_bwd_plan", "streamkl_score_bwd", "streamkl_key_ranges", "streamkl_attn_fwd_plan",
             "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd",
-            "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd")
+            "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd", "streamkl_cache8_append", "streamkl_cache8_read",
+            "streamkl_attn_cache8_plan", "streamkl_attn_cache8")
 
 _lock = threading.Lock()
 _lib = None
@@ -156,6 +162,11 @@ def load(build_if_stale: bool = True):
         lib.streamkl_attn_fwd.argtypes = [at, *[P] * 6, F, I, P, P, P, P, Z, op, P]
         lib.streamkl_attn_bwd_plan.argtypes = [at, op, pp]
         lib.streamkl_attn_bwd.argtypes = [at, *[P] * 10, F, I, P, P, P, P, Z, op, P]
+        cd = ctypes.POINTER(CacheDesc)
+        lib.streamkl_cache8_append.argtypes = [cd, *[P] * 10]
+        lib.streamkl_cache8_read.argtypes = [cd, *[P] * 9]
+        lib.streamkl_attn_cache8_plan.argtypes = [cd, op, pp]
+        lib.streamkl_attn_cache8.argtypes = [cd, *[P] * 7, F, P, P, P, Z, op, P]
         lib.streamkl_status_string.argtypes = [I]
         lib.streamkl_status_string.restype = ctypes.c_char_p
         for name in ("streamkl_fwd_plan", "streamkl_fwd", "streamkl_bwd_plan", "streamkl_bwd",
@@ -164,7 +175,8 @@ def load(build_if_stale: bool = True):
                      "streamkl_norm_rope_fwd", "streamkl_norm_rope_bwd", "streamkl_rope_table",
                      "streamkl_score_fwd_plan", "streamkl_score_fwd", "streamkl_score_bwd_plan", "streamkl_score_bwd",
                      "streamkl_key_ranges", "streamkl_attn_fwd_plan", "streamkl_attn_fwd", "streamkl_attn_bwd_plan", "streamkl_attn_bwd",
-                     "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd"):
+                     "streamkl_norm_rope_axes_fwd", "streamkl_norm_rope_axes_bwd", "streamkl_cache8_append",
+                     "streamkl_cache8_read", "streamkl_attn_cache8_plan", "streamkl_attn_cache8"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -1069,3 +1081,153 @@ class Attention(torch.autograd.Function):
             dO = dO.clone() if dO.data_ptr() % 16 else dO
         grads = attn_bwd(dO, Q, K, V, O, LSE, rest, tuple(ranges) if ranges else None, **ctx.how)
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None)
+
+
+# ---------------------------------------------------------------------------
+# A paged cache of keys and values in 8 bits, and attention over it
+# ---------------------------------------------------------------------------
+class Cache8:
+    """k, v [pages, Hk, T, d] in float8_e4m3fn (or uint8, the same bytes) and k_scale, v_scale float32 [pages, Hk]: a
+    stored value stands for itself times the scale of its page and head.  T is 16, 32, 64 or 128, d is 64 or 128.  Token
+    j of sequence b stands in row j % T of page table[b, j // T], table int32 [B, M] being an argument of each call;
+    a page may be listed by several sequences as long as none of them appends to it."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    @classmethod
+    def empty(cls, pages, heads, tokens, d, device):
+        """A cache of ``pages`` pages of ``tokens`` tokens, all zeros."""
+        new = lambda: torch.zeros((int(pages), int(heads), int(tokens), int(d)), dtype=torch.uint8, device=device)  # noqa: E731
+        one = lambda: torch.ones((int(pages), int(heads)), dtype=torch.float32, device=device)  # noqa: E731
+        return cls(new().view(torch.float8_e4m3fn), new().view(torch.float8_e4m3fn), one(), one())
+
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+
+def _cache(cache):
+    if not isinstance(cache, Cache8):
+        raise ValueError("cache must be a Cache8")
+    return cache.tensors()
+
+
+def _cache_desc(cache, table, lengths) -> CacheDesc:
+    k, v, k_scale, v_scale = cache
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4:
+        raise ValueError("the cache's k must be a CUDA tensor [pages, Hk, T, d]")
+    if k.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"the cache's k must be float8_e4m3fn or uint8, got {k.dtype}")
+    _check_tensor("k", k, k.shape, k.dtype, k.device)
+    _check_tensor("v", v, k.shape, k.dtype, k.device)
+    _check_tensor("k_scale", k_scale, k.shape[:2], torch.float32, k.device)
+    _check_tensor("v_scale", v_scale, k.shape[:2], torch.float32, k.device)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be an int32 tensor [B, M]")
+    _check_tensor("table", table, table.shape, torch.int32, k.device)
+    _check_tensor("lengths", lengths, table.shape[:1], torch.int32, k.device)
+    desc = CacheDesc()
+    desc.pages, desc.H_kv, desc.T, desc.d = k.shape
+    desc.B, desc.M = table.shape
+    if desc.T not in (16, 32, 64, 128) or desc.d not in (64, 128):
+        raise ValueError(f"pages hold 16, 32, 64 or 128 tokens of d = 64 or 128, not {desc.T} of {desc.d}")
+    return desc
+
+
+def cache8_append(cache, table, lengths, k, v, counts=None) -> None:
+    """Write new tokens k, v [B, Hk, N, d] (bf16, any strides with d contiguous) into the cache behind the lengths (int32
+    [B]) tokens that each sequence holds: counts[b] of them (int32 [B], clamped to N; None: N).  A page's scale is the
+    smallest power of two 2^e, e >= -100, that brings every finite value within 448, and never shrinks while the page is
+    being filled: tokens that it holds are rounded again where it grows.  NaN and infinities are stored as NaN.  Tokens
+    behind the table, or of a page outside the cache, are not written.  lengths stay as they are (lengths + counts is for
+    the caller to keep); two sequences must not append to one page in one call."""
+    held = _cache(cache)
+    key, known = _lookup("cache8_append", _tensors(*held, table, lengths, k, v, counts))
+    if known is None:
+        desc = _cache_desc(held, table, lengths)
+        desc.x, desc.y = _heads("k", k, (torch.bfloat16,), held[0].device), _heads("v", v, (torch.bfloat16,), held[0].device, k.shape)
+        if tuple(k.shape[:2]) + (k.shape[3],) != (desc.B, desc.H_kv, desc.d):
+            raise ValueError(f"k and v must be [B, Hk, N, d] = ({desc.B}, {desc.H_kv}, N, {desc.d}), got {tuple(k.shape)}")
+        if counts is not None:
+            _check_tensor("counts", counts, (desc.B,), torch.int32, held[0].device)
+        desc.N = k.shape[2]
+        known = _remember(key, (desc, held[0].device))
+    desc, device = known
+    _raise(_on(device, load().streamkl_cache8_append, desc, *[t.data_ptr() for t in held], table.data_ptr(),
+               lengths.data_ptr(), k.data_ptr(), v.data_ptr(), _address(counts)), "streamkl_cache8_append")
+
+
+def cache8_read(cache, table, lengths, tokens=None, out=None):
+    """(K, V): the first ``tokens`` tokens (None: as many as the table's pages hold) of each sequence as bf16 [B, Hk, tokens,
+    d], for attn_fwd over what a cache holds: zeros behind lengths[b], NaN for pages outside the cache.  Exact for scales
+    that are powers of two.  out: two bf16 tensors of that shape, any strides; new contiguous ones otherwise."""
+    held = _cache(cache)
+    tokens = None if tokens is None else int(tokens)
+    key, known = _lookup("cache8_read", _tensors(*held, table, lengths, *(out or ())), tokens)
+    if known is None:
+        desc = _cache_desc(held, table, lengths)
+        desc.N = desc.M * desc.T if tokens is None else tokens
+        if desc.N < 0:
+            raise ValueError(f"tokens must not be negative, got {tokens}")
+        shape, device = (desc.B, desc.H_kv, desc.N, desc.d), held[0].device
+        if out is None:
+            desc.x = desc.y = _contiguous(shape)
+        else:
+            desc.x = _heads("out[0]", out[0], (torch.bfloat16,), device, shape)
+            desc.y = _heads("out[1]", out[1], (torch.bfloat16,), device, shape)
+        known = _remember(key, (desc, shape, device))
+    desc, shape, device = known
+    if out is None:
+        out = tuple([torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)])
+    _raise(_on(device, load().streamkl_cache8_read, desc, *[t.data_ptr() for t in held], table.data_ptr(),
+               lengths.data_ptr(), out[0].data_ptr(), out[1].data_ptr()), "streamkl_cache8_read")
+    return out
+
+
+def _attn_cache8_desc(Q, held, table, lengths) -> CacheDesc:
+    desc = _cache_desc(held, table, lengths)
+    desc.x = _heads("Q", Q, (torch.bfloat16,), held[0].device)
+    B, desc.H, desc.N, d = Q.shape
+    if (B, d) != (desc.B, desc.d):
+        raise ValueError(f"Q must be [B, H, Nq, d] with B = {desc.B} and d = {desc.d}, got {tuple(Q.shape)}")
+    if desc.H_kv < 1 or desc.H % desc.H_kv != 0:
+        raise ValueError("the cache's head count must divide the query head count")
+    return desc
+
+
+def attn_cache8_plan(Q, cache, table, lengths, num_splits=0) -> Plan:
+    plan, desc = Plan(), _attn_cache8_desc(Q, _cache(cache), table, lengths)
+    desc.y = _contiguous(Q.shape)
+    with torch.cuda.device(Q.device):
+        _raise(load().streamkl_attn_cache8_plan(ctypes.byref(desc), ctypes.byref(_opts(num_splits)), ctypes.byref(plan)),
+               "streamkl_attn_cache8_plan")
+    return plan
+
+
+def attn_cache8(Q, cache, table, lengths, scale=None, out=None, num_splits=0, workspace=None):
+    """(O, LSE): softmax attention of the last Nq tokens (1 to 16) of each sequence, Q [B, H, Nq, d] (bf16, any strides with
+    d contiguous), over the lengths[b] tokens that it holds in the cache, its own among them: row i sees the keys before
+    lengths[b] - Nq + 1 + i.  Hk divides H.  A row that sees no key has O = 0 and LSE = -inf; a row that sees a page
+    outside the cache, and a sequence longer than its table, is NaN.  Longer chunks: attn_fwd over cache8_read."""
+    held = _cache(cache)
+    num_splits = int(num_splits)
+    key, known = _lookup("attn_cache8", _tensors(Q, *held, table, lengths, *(() if out is None else (out,))), num_splits)
+    if known is None:
+        desc = _attn_cache8_desc(Q, held, table, lengths)
+        desc.y = _contiguous(Q.shape) if out is None else _heads("out", out, (torch.bfloat16,), Q.device, Q.shape)
+        opts, plan = _opts(num_splits), Plan()
+        with torch.cuda.device(Q.device):
+            _raise(load().streamkl_attn_cache8_plan(ctypes.byref(desc), ctypes.byref(opts), ctypes.byref(plan)),
+                   "streamkl_attn_cache8_plan")
+        known = _remember(key, (desc, opts, plan.workspace_bytes, tuple(Q.shape), Q.device))
+    desc, opts, nbytes, shape, device = known
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    LSE = torch.empty(shape[:3], dtype=torch.float32, device=device)
+    workspace = _scratch(workspace, nbytes, device)
+    _raise(_on(device, load().streamkl_attn_cache8, desc, Q.data_ptr(), *[t.data_ptr() for t in held], table.data_ptr(),
+               lengths.data_ptr(), 0.0 if scale is None else float(scale), out.data_ptr(), LSE.data_ptr(),
+               workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_cache8")
+    return out, LSE

@@ -453,6 +453,62 @@ STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const 
                                                size_t workspace_bytes, const streamkl_options* opt,
                                                streamkl_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged cache of keys and values in 8 bits, and attention over it.
+ *
+ * k, v [pages, H_kv, T, d] are e4m3 bytes, contiguous, 16-byte aligned; T is 16,
+ * 32, 64 or 128 and d is 64 or 128.  k_scale, v_scale [pages, H_kv] are float32,
+ * positive and normal: a stored value stands for itself times its page's and
+ * head's scale.  Token j of sequence b stands in row j % T of page
+ * table[b][j / T]; table is int32 [B, M], lengths int32 [B] (tokens held before
+ * the call of append, in all for the others; below 0 counts as 0).  A page may be
+ * listed by several sequences as long as none of them appends to it.
+ *
+ * append writes counts[b] (int32 [B], clamped to 0 .. N; NULL: N) new tokens of
+ * new_k, new_v [B, H_kv, N, d] (bf16) behind each sequence's lengths[b].  A page's
+ * scale becomes the smallest 2^e, e >= -100, with every finite value of its new
+ * tokens within 448 2^e, and no less than it was when the page held tokens
+ * of the sequence before; those are then rounded to the new scale.  NaN and
+ * infinities are stored as NaN.  Rows of the page behind the new tokens stay as
+ * they are.  Tokens behind the table, or of a page outside [0, pages), are not
+ * written.  Two sequences must not append to one page in one call.
+ *
+ * read gathers the first N tokens of each sequence as bf16 [B, H_kv, N, d]: zeros
+ * behind lengths[b], NaN for pages that are not there.
+ *
+ * attn_cache8: softmax attention of the last N tokens (1 to 16) of each sequence,
+ * Q [B, H, N, d] bf16, row i seeing keys j < lengths[b] - N + 1 + i; query head h
+ * uses key head h / (H / H_kv).  O is bf16 [B, H, N, d], LSE float32 [B, H, N]; a
+ * row that sees no key has O = 0 and LSE = -inf; a row that sees a page that is
+ * not there, or a sequence longer than its table, is NaN.  Equal inputs give equal
+ * bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t pages, H_kv, T, d;
+    int32_t B, M;
+    int32_t H;          /* attn_cache8: query heads */
+    int32_t N;          /* tokens of x and y */
+    streamkl_strides x; /* new_k, out_k, or Q: element strides, multiples of 8 */
+    streamkl_strides y; /* new_v, out_v, or O */
+} streamkl_cache8;
+
+STREAMKL_API streamkl_status streamkl_cache8_append(const streamkl_cache8* desc, void* k, void* v, float* k_scale,
+                                                    float* v_scale, const int32_t* table, const int32_t* lengths,
+                                                    const void* new_k, const void* new_v, const int32_t* counts,
+                                                    streamkl_stream_t stream);
+STREAMKL_API streamkl_status streamkl_cache8_read(const streamkl_cache8* desc, const void* k, const void* v,
+                                                  const float* k_scale, const float* v_scale, const int32_t* table,
+                                                  const int32_t* lengths, void* out_k, void* out_v,
+                                                  streamkl_stream_t stream);
+STREAMKL_API streamkl_status streamkl_attn_cache8_plan(const streamkl_cache8* desc, const streamkl_options* opt,
+                                                       streamkl_plan* plan);
+STREAMKL_API streamkl_status streamkl_attn_cache8(const streamkl_cache8* desc, const void* Q, const void* k, const void* v,
+                                                  const float* k_scale, const float* v_scale, const int32_t* table,
+                                                  const int32_t* lengths, float scale, void* O, float* LSE,
+                                                  void* workspace, size_t workspace_bytes, const streamkl_options* opt,
+                                                  streamkl_stream_t stream);
+
 /* Synchronises `stream`, reads the workspace's device error word into
  * *device_error (if not NULL), clears it, and returns STREAMKL_ERR_TIMEOUT if
  * it was set, STREAMKL_OK otherwise (or CUDA on a failed copy). */
