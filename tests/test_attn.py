@@ -122,6 +122,7 @@ SHAPES = [
     (1, 1, 1, 1, 1, 64), (1, 4, 2, 1, 300, 128), (2, 8, 2, 5, 777, 64), (1, 6, 2, 33, 129, 128), (2, 3, 1, 128, 128, 64),
     (1, 4, 4, 129, 129, 128), (1, 2, 1, 257, 1000, 128), (2, 6, 2, 300, 300, 64), (1, 16, 2, 16, 4097, 128),
     (1, 5, 1, 200, 513, 64), (1, 2, 2, 1024, 1024, 128), (3, 3, 3, 64, 640, 64),
+    (3, 3, 1, 1001, 1001, 64), (1, 4, 1, 1500, 1500, 128), (1, 1, 1, 700, 2600, 64),
 ]
 
 
@@ -155,3 +156,62 @@ def test_gradients(shape, kind):
     Ref(Q, K, V, ranges).check_grads(dO, *grads)
     again = sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges)
     assert torch.equal(again[1], grads[1]) and torch.equal(again[2], grads[2])
+
+
+def dirty(t, hidden, value):
+    """t with `value` in the rows of [B, h, N, d] that `hidden` [B, N] marks."""
+    t = t.clone()
+    t.masked_fill_(hidden[:, None, :, None], value)
+    return t
+
+
+@gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("shape", [(2, 4, 2, 700, 700, 128), (2, 3, 3, 1100, 1100, 64), (2, 8, 2, 3, 900, 128)], ids=str)
+def test_what_no_row_sees_has_no_effect(shape, value):
+    """Keys and values behind a sequence, and queries and output gradients of rows that see nothing."""
+    B, H, Hk, Nq, Nk, d = shape
+    Q, K, V = inputs(*shape)
+    dO = torch.randn((B, H, Nq, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).to(BF16)
+    n = torch.tensor([Nk - 133, Nk // 2 + 1], dtype=torch.int32, device=DEV)
+    ranges = sk.key_ranges(B, Nq, Nk, DEV, q_lengths=n.clamp(max=Nq), k_lengths=n)
+    want = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True)
+    grads = sk.attn_bwd(dO, Q, K, V, *want[:2], rest=want[2], ranges=ranges)
+    keys = torch.arange(Nk, device=DEV) >= n[:, None]
+    rows = torch.arange(Nq, device=DEV) >= n[:, None]
+    Q2, K2, V2, dO2 = dirty(Q, rows, value), dirty(K, keys, value), dirty(V, keys, value), dirty(dO, rows, value)
+    got = sk.attn_fwd(Q2, K2, V2, ranges=ranges, rest=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dirty_grads = sk.attn_bwd(dO2, Q2, K2, V2, *got[:2], rest=got[2], ranges=ranges)
+    assert all(torch.equal(a, b) for a, b in zip(dirty_grads[1:], grads[1:]))
+    Ref(Q, K, V, ranges).check_grads(dO, *dirty_grads)
+
+
+@gpu
+@pytest.mark.parametrize("which", ["K", "V", "Q", "dO"])
+@pytest.mark.parametrize("shape", [(1, 4, 2, 600, 600, 128), (1, 3, 1, 900, 900, 64)], ids=str)
+def test_a_broken_token_reaches_those_who_see_it_alone(shape, which):
+    """Causal rows: a NaN at token 333 is in the outputs of that row or of the rows from it on, and in no other."""
+    B, H, Hk, Nq, Nk, d = shape
+    Q, K, V = inputs(*shape)
+    dO = torch.randn((B, H, Nq, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).to(BF16)
+    want = sk.attn_fwd(Q, K, V, causal=True, rest=True)
+    clean = sk.attn_bwd(dO, Q, K, V, *want[:2], rest=want[2], causal=True)
+    at = 333
+    t = dict(Q=Q.clone(), K=K.clone(), V=V.clone(), dO=dO.clone())
+    t[which][:, :, at, 5] = math.nan
+    O, LSE, rest = sk.attn_fwd(t["Q"], t["K"], t["V"], causal=True, rest=True)
+    dQ, dK, dV = sk.attn_bwd(t["dO"], t["Q"], t["K"], t["V"], O, LSE, rest=rest, causal=True)
+    row = torch.arange(Nq, device=DEV)
+    hit = dict(K=row >= at, V=row >= at, Q=row == at, dO=row < 0)[which]
+    assert torch.equal(O.isnan().any(-1), hit.expand(B, H, Nq))
+    assert torch.equal(O[:, :, ~hit], want[0][:, :, ~hit]) and torch.equal(LSE[:, :, ~hit], want[1][:, :, ~hit])
+    back = hit if which != "dO" else row == at
+    assert torch.equal(dQ.isnan().any(-1), back.expand(B, H, Nq))
+    bound = Ref(Q, K, V, causal=True)  # rows that do not see it have their gradient, up to the order of sums
+    diff = (dQ[:, :, ~back].double() - clean[0][:, :, ~back].double()).abs()
+    assert bool((diff <= 2.0 ** -7 * clean[0][:, :, ~back].double().abs() + 1e-6).all()) and bound.live.all()
+    # keys that a hit row sees have a term of it; keys behind every hit row (Q, dO) have none
+    seen = row <= at if which in ("Q", "dO") else row >= 0
+    assert bool(dK[:, :, seen].isnan().any(-1).all())
+    assert torch.equal(dK[:, :, ~seen], clean[1][:, :, ~seen]) and torch.equal(dV[:, :, ~seen], clean[2][:, :, ~seen])
