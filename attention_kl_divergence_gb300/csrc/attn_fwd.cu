@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         for (int s = 0; s < NST; ++s) {
             mbar_init(base + L::bar_full + 8 * s, 1);
-            mbar_init(base + L::bar_empty + 8 * s, 3);  // the MMAs, and for value tiles the two checking warps
+            mbar_init(base + L::bar_empty + 8 * s, 3);  // the MMAs and the two checking warps
             mbar_init(base + L::bar_clean + 8 * s, 2);
         }
         mbar_init(base + L::bar_done, 1);
@@ -282,10 +282,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 if (t >= t0 && !have_v && !(ok = mbar_wait(base + L::bar_full + 8 * (nv % NST), (nv / NST) & 1, wc, kErrWaitK))) break;
                 if (t + 1 < t1 && !have_k && !(ok = mbar_wait(base + L::bar_full + 8 * (nk % NST), (nk / NST) & 1, wc, kErrWaitK))) break;
                 if (t >= t0) tc_commit(base + L::bar_empty + 8 * (nv % NST));
-                if (t + 1 < t1) {
-                    mbar_arrive_n(base + L::bar_empty + 8 * (nk % NST), 2);
-                    tc_commit(base + L::bar_empty + 8 * (nk % NST));
-                }
+                if (t + 1 < t1) tc_commit(base + L::bar_empty + 8 * (nk % NST));
             }
             if (*abort_flag && issued > 0) {  // let the issued MMAs retire before TMEM is freed
                 tc_commit(base + L::bar_done);
@@ -296,14 +293,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         // ------------------------------------------------------------ value check
         // A probability of 0 does not hide a NaN or an infinity in the value that it meets in the MMA.  In tiles
         // that some row does not see all of, keys with such values get zeros, and rows that see them become NaN.
-        // The warps see every value tile, and its stage is not released without them.  The k-th check uses slot
-        // k % NST: the ring holds fewer value tiles than there are slots.
+        // The warps wait for every copy of the ring in turn and release every stage with the MMAs: a wait that skipped
+        // a stage's use would take the use before it for its own.  The k-th check uses slot k % NST: the ring holds
+        // fewer value tiles than there are slots.
         const int w = warp - 10;
         int k_check = 0;
-        for (int t = t0; t < t1; ++t) {
-            const int n = 2 * (t - t0) + 1, st = n % NST;
+        for (int n = 0; n < 2 * (t1 - t0); ++n) {
+            const int st = n % NST, t = t0 + (n >> 1);
             if (!wait_all(base + L::bar_full + 8 * st, (n / NST) & 1, wc, kErrWaitK)) break;
-            if (!checked(t)) {
+            if (!(n & 1) || !checked(t)) {
                 if (lane == 0) mbar_arrive(base + L::bar_empty + 8 * st);
                 continue;
             }
