@@ -128,6 +128,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 }  // namespace
 
+namespace {
+// A driver call on a host thread that may not have used the device yet (an autograd worker): the runtime binds the
+// device's context to a thread on its first use, driver calls do not.
+template <typename Call>
+bool bound(const Call& call) {
+    CUresult r = call();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+        r = call();
+    }
+    return r == CUDA_SUCCESS;
+}
+}  // namespace
+
 // 4-D map over [B, heads, N, d] bf16 with a (64 x rows x heads) box, 128-byte
 // swizzle; rows outside [0, N) read as zero.  A box of several heads lands
 // in shared memory as heads * rows consecutive 128-byte rows, head-major.
@@ -139,20 +154,26 @@ bool make_map_strided(CUtensorMap* m, const void* ptr, int d, int64_t N, int hea
     cuuint64_t strides[3] = {cuuint64_t(st.n * 2), cuuint64_t(st.h * 2), cuuint64_t(st.b * 2)};
     cuuint32_t box[4] = {cuuint32_t(kSwizzleCols), cuuint32_t(box_rows), cuuint32_t(box_heads), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    auto encode = [&] {
+    return bound([&] {
         return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    CUresult r = encode();
-    if (r == CUDA_ERROR_INVALID_CONTEXT) {
-        // a host thread that has not used the device yet (an autograd worker): the runtime
-        // binds the device's context to a thread on its first use, driver calls do not
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
-        r = encode();
-    }
-    return r == CUDA_SUCCESS;
+    });
+}
+
+// 2-D map over `rows` rows of d bytes with boxes of 16 rows, swizzled by d-byte rows.
+bool make_map_bytes(CUtensorMap* m, const void* ptr, int d, int64_t rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cuuint64_t(d), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(d)};
+    cuuint32_t box[2] = {cuuint32_t(d), 16};
+    cuuint32_t estr[2] = {1, 1};
+    return bound([&] {
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads) {

@@ -1,5 +1,6 @@
 // api_cache8.cu -- C ABI of the 8-bit cache and the attention over it: argument
 // validation, planning and launches on the caller's stream.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,8 +34,9 @@ streamkl_status check_cache(const streamkl_cache8* s) {
     if (s->pages < 1 || s->H_kv < 1 || s->B < 1 || s->M < 1) return STREAMKL_ERR_INVALID_ARG;
     if (s->d != 64 && s->d != 128) return STREAMKL_ERR_UNSUPPORTED;
     if (s->T != 16 && s->T != 32 && s->T != 64 && s->T != 128) return STREAMKL_ERR_UNSUPPORTED;
-    // token positions are counted in 32 bits, heads in a grid's y
-    if (int64_t(s->M) * s->T > (int64_t(1) << 30) || s->H_kv > 65535) return STREAMKL_ERR_UNSUPPORTED;
+    // token positions and the pool's rows are counted in 32 bits, heads in a grid's y
+    if (int64_t(s->M) * s->T > (int64_t(1) << 30) || s->H_kv > 65535 || int64_t(s->pages) * s->H_kv > INT32_MAX / s->T)
+        return STREAMKL_ERR_UNSUPPORTED;
     return STREAMKL_OK;
 }
 
@@ -62,7 +64,7 @@ bool make_view(const streamkl_cache8* s, void* k, void* v, float* k_scale, float
 }
 
 struct CacheAttnPlan {
-    int row_tiles, splits, ctas;
+    int tile_rows, row_groups, teams, spread, ctas;
     size_t ws_bytes;
 };
 
@@ -73,20 +75,26 @@ streamkl_status plan_cache_attn(const streamkl_cache8* s, const streamkl_options
     if (s->N > kDecodeMaxQ || int64_t(s->B) * s->H > (int64_t(1) << 24)) return STREAMKL_ERR_UNSUPPORTED;
     if (!strides_ok(s->x, s->B, s->H, s->N, s->d, false) || !strides_ok(s->y, s->B, s->H, s->N, s->d, true))
         return STREAMKL_ERR_INVALID_ARG;
-    if (opt && (opt->num_splits < 0 || opt->bwd_mode != 0 || opt->grad_bf16 != 0 || opt->debug_flags != 0))
+    if (opt && (opt->num_splits < 0 || opt->bwd_mode != 0 || opt->grad_bf16 != 0 ||
+                (opt->debug_flags & ~STREAMKL_DEBUG_INJECT_STALL)))
         return STREAMKL_ERR_INVALID_ARG;
     int sms = 0;
     if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
-    pl->row_tiles = (s->H / s->H_kv * s->N + 15) / 16;
-    const int64_t units = int64_t(s->B) * s->H_kv * pl->row_tiles;
-    const int steps = (s->M * s->T + 127) / 128;  // 128 keys: a chunk of each warp
-    int splits = opt && opt->num_splits > 0 ? opt->num_splits : static_cast<int>(std::max<int64_t>(1, 2 * sms / units));
-    splits = std::min({splits, steps, kMaxSplits});
-    if (units > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
-    pl->splits = splits;
-    pl->ctas = static_cast<int>(std::min<int64_t>(units * splits, INT32_MAX));
+    const int64_t rows = int64_t(s->H / s->H_kv) * s->N;
+    pl->tile_rows = rows <= 8 ? 8 : 16;
+    const int64_t row_tiles = (rows + pl->tile_rows - 1) / pl->tile_rows;
+    pl->teams = 1;
+    while (pl->teams < row_tiles && pl->teams < kCacheTeams) pl->teams *= 2;
+    const int64_t row_groups = (row_tiles + pl->teams - 1) / pl->teams, segments = int64_t(s->B) * s->H_kv * row_groups;
+    if (segments > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    pl->row_groups = static_cast<int>(row_groups);
+    // One CTA per segment where even the longest that the table allows is short, or where there are many of them.
+    const int64_t capacity = int64_t(s->M) * s->T, steps = (capacity + 255) / 256;  // 256 keys: a chunk of each warp
+    const int64_t wanted = opt && opt->num_splits > 0 ? opt->num_splits : capacity > 1024 && segments < 8 * int64_t(sms) ? sms : 0;
+    pl->spread = wanted > 0;
+    pl->ctas = static_cast<int>(wanted > 0 ? std::min<int64_t>({wanted, segments * steps, int64_t(1) << 20}) : segments);
     pl->ws_bytes = kStatusBytes;
-    if (splits > 1) pl->ws_bytes += size_t(splits) * s->B * s->H * s->N * (size_t(s->d) + 4) * sizeof(float);
+    if (pl->spread) pl->ws_bytes += size_t(pl->ctas) * 2 * pl->tile_rows * pl->teams * (size_t(s->d) + 4) * sizeof(float);
     return STREAMKL_OK;
 }
 
@@ -147,9 +155,9 @@ streamkl_status streamkl_attn_cache8_plan(const streamkl_cache8* desc, const str
     streamkl_status st = plan_cache_attn(desc, opt, &pl);
     if (st != STREAMKL_OK) return st;
     plan->path = 1;
-    plan->num_splits = pl.splits;
+    plan->num_splits = pl.spread ? pl.ctas : 1;
     plan->num_ctas = pl.ctas;
-    plan->launches = pl.splits > 1 ? 2 : 1;
+    plan->launches = pl.spread ? 2 : 1;
     plan->workspace_bytes = pl.ws_bytes;
     return STREAMKL_OK;
 }
@@ -173,19 +181,27 @@ streamkl_status streamkl_attn_cache8(const streamkl_cache8* desc, const void* Q,
     p.H = s.H;
     p.Nq = s.N;
     p.group = s.H / s.H_kv;
-    p.row_tiles = pl.row_tiles;
-    p.num_splits = pl.splits;
+    p.tile_rows = pl.tile_rows;
+    p.row_groups = pl.row_groups;
+    p.teams = pl.teams;
+    p.spread = pl.spread;
     p.Q = Q;
     p.q_b = s.x.b, p.q_h = s.x.h, p.q_n = s.x.n;
     p.O = O;
     p.o_b = s.y.b, p.o_h = s.y.h, p.o_n = s.y.n;
     p.LSE = LSE;
     p.scale_log2e = resolve_scale(scale, s.d) * kLog2e;
-    if (pl.splits > 1) {
+    if (pl.spread) {
         p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-        p.part_state = reinterpret_cast<float4*>(p.part + size_t(pl.splits) * s.B * s.H * s.N * s.d);
+        p.part_state = reinterpret_cast<float4*>(p.part + size_t(pl.ctas) * 2 * pl.tile_rows * pl.teams * s.d);
     }
-    return launch_cache8_attn(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+    p.status = static_cast<unsigned int*>(workspace);
+    p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));
+    p.inject_stall = (opt && (opt->debug_flags & STREAMKL_DEBUG_INJECT_STALL)) ? 1 : 0;
+    CUtensorMap maps[2];
+    const int64_t rows = int64_t(s.pages) * s.H_kv * s.T;
+    if (!make_map_bytes(&maps[0], k, s.d, rows) || !make_map_bytes(&maps[1], v, s.d, rows)) return STREAMKL_ERR_CUDA;
+    return launch_cache8_attn(maps, p, pl.ctas, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -39,16 +39,23 @@ struct CacheReadParams {
 struct CacheAttnParams {
     CacheView c;
     int H, Nq, group;
-    int row_tiles;         // 16-row tiles of a key head's group x Nq rows
-    int num_splits;
+    int tile_rows;         // 8 (one tile holds a key head's group x Nq rows) or 16
+    int row_groups;        // of up to kCacheTeams tiles, of those rows
+    int teams;             // tiles that a CTA works on at a time: 1, 2, 4 or 8
+    int spread;            // CTAs take equal shares of all chunks, and parts are combined; else one CTA per segment
     const void* Q;         // [B, H, Nq, d] bf16
     int64_t q_b, q_h, q_n;
     void* O;               // [B, H, Nq, d] bf16
     int64_t o_b, o_h, o_n;
     float* LSE;            // [B, H, Nq]
     float scale_log2e;
-    float* part;           // several splits: [splits][B*H*Nq][d]
-    float4* part_state;    // [splits][B*H*Nq]
+    float* part;           // spread: [CTAs][2][tile_rows teams][d] sums and
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int inject_stall;
+    float4* part_state;    // [CTAs][2][tile_rows teams] their references
 };
+
+constexpr int kCacheTeams = 8;
 
 }  // namespace streamkl

@@ -3,17 +3,21 @@
 //   x_ij = log2(e) scale s_K q_i k_j,  O_i = sum_j 2^(x_ij - m_i) s_V v_j / l_i
 //
 // with k_j, v_j the stored e4m3 values and s_K, s_V the scales of their page.  Every
-// key and value byte is read once for the 16 rows (query heads of a key head x new
+// key and value byte is read once for the rows (query heads of a key head x new
 // tokens) of a tile, and that is the bound: HBM.  The products are small beside it,
 // so they run on warp-level f16 MMAs, whose operands are the stored bytes turned to
-// f16 (exact) in registers: no pass through shared memory, no wait on another warp.
-// A row of q is f16 after a scaling by a power of two.  Probabilities are f16 with
-// 2^7 more than their value, so that they keep all 11 bits down to 2^-21.
+// f16 (exact) in registers: no wait on another warp.  Keys stand on the MMAs' M side
+// in the scores and features in the output, and 8 rows fill their N side: a tile of
+// 8 rows takes half the MMAs, exponentials and registers of one of 16.  A row of q is
+// f16 after a scaling by a power of two.  Probabilities are f16 with 2^7 more than
+// their value, so that they keep all 11 bits down to 2^-21.
 //
-// Warps take the 16-key chunks of a CTA's share in turn, each with a ring of copies
-// of its own whose bytes are read by the lane that copied them.
-#include <cuda_fp16.h>
-
+// A segment is one sequence's keys of one key head.  Its chunks are dealt out to the
+// warps of a CTA, each of which has a ring of its own that TMA fills, 16 tokens of a
+// page at a time.  With more than one row tile, teams of warps share the copies.
+// The lengths are known on the device alone: where there are too few segments to
+// fill the GPU evenly, every CTA takes the same number of chunks of all of them, one
+// after the other, and a second kernel adds up the parts of segments that were cut.
 #include "bwd_common.cuh"
 #include "cache8.cuh"
 #include "common.cuh"
@@ -25,18 +29,33 @@ namespace streamkl {
 
 namespace {
 
-constexpr int kCwWarps = 8;
-constexpr int kCwStages = 4;      // chunks in flight per warp
+// Row tiles of 8 NQ rows; chunks of KH halves of 16 keys, each half of one page.  Both
+// shapes take 256 keys in a step of the CTA.  16 warps hide the latencies of their
+// dependent steps where 8 rows leave the registers for them.
+template <int NQ>
+struct CacheShape {
+    static constexpr int kHalves = NQ == 1 ? 1 : 2;
+    static constexpr int kWarps = 16 / kHalves;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kRows = 8 * NQ;
+    static constexpr int kKeys = 16 * kHalves;
+};
+constexpr int kCwStages = 3;      // a warp's chunks in its ring: one in use, the others on their way
 constexpr float kCwTau = 8.f;     // references may stay this far (log2) below the largest value
 constexpr float kCwShift = 7.f;   // probabilities are at most 2^(8 + 7) < 65504
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
-    const uint32_t n = there ? BYTES : 0;  // the rest is zeros
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// 16 rows of d bytes, swizzled so that 8 rows' pieces lie in different banks.
+__device__ __forceinline__ void copy_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
+        : "memory");
+}
+
+// Byte offset of 16-byte piece `piece` of row `row` under the swizzle of d-byte rows (128: 8 pieces, 64: 4).
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t u) {
@@ -51,10 +70,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
 // A page's value scale as 2^e x f with 1 <= f < 2, so that no factor made of it leaves float32's range.  0 (and
@@ -65,6 +84,13 @@ __device__ __forceinline__ float2 split_scale(float s) {
     return make_float2(-INFINITY, s > 0.f && s < INFINITY ? 0.f : 0.f * s);
 }
 
+// What a half needs of its page.
+struct PageEntry {
+    int page;  // -1: not there
+    float ks, vs;
+    int pad;
+};
+
 // States of one row merge by their references: m of the probabilities, w of the output.
 struct CacheState {
     float m, l, w;
@@ -72,50 +98,138 @@ struct CacheState {
 
 __device__ __forceinline__ float ratio(float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); }
 
+// Chunks of `keys` keys of sequence b.
+__device__ __forceinline__ int chunks_of(const CacheView& c, int b, int keys) {
+    const int64_t n = min(static_cast<int64_t>(max(c.lengths[b], 0)), static_cast<int64_t>(c.M) * c.T);
+    return static_cast<int>((n + keys - 1) / keys);
+}
+
+// A warp sums the chunks of all sequences, and of those before b.
+__device__ __forceinline__ int64_t sum_chunks(const CacheView& c, int b, int keys, int64_t* before) {
+    int64_t all = 0, less = 0;
+    for (int k = threadIdx.x & 31; k < c.B; k += 32) {
+        const int n = chunks_of(c, k, keys);
+        all += n;
+        less += k < b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        less += __shfl_xor_sync(0xffffffffu, less, o);
+    }
+    *before = less;
+    return all;
+}
+
+// A CTA's share of `total` chunks: a multiple of what its warps take at a time.
+__device__ __forceinline__ int64_t share_of(int64_t total, int ctas, int warps) {
+    const int64_t n = (total + ctas - 1) / ctas;
+    return max((n + warps - 1) / warps * warps, int64_t(warps));
+}
+
+// The 8 x 8 transpose of f16 pairs: lane 4g + t gives (row g, columns 2t, 2t + 1) and gets (row 2t, 2t + 1; column g).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // The row's output from sums relative to m and w.
 __device__ __forceinline__ float output_factor(const CacheState& s) { return s.w == -INFINITY ? 0.f / s.l : ex2(s.w - kCwShift - s.m) / s.l; }
 
-}  // namespace
-
-template <int D>
-__global__ void __launch_bounds__(32 * kCwWarps, 1) cache8_attn_kernel(const __grid_constant__ CacheAttnParams p) {
+// One segment's chunks [c0, c1) for a group of row tiles; the sums go to the outputs, or (part >= 0) to that part.
+// `uses`: how many steps filled the rings before, to tell the phases of their barriers.  False: a wait gave up, and
+// the rows are NaN; nothing is copied in a segment that begins with `alive` false.
+template <int D, int NQ, bool SHARED>
+__device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorMap* tK, const CUtensorMap* tV, uint8_t* smem, int& uses,
+                                       const WaitCtx& wc, bool alive, int b, int hk, int rg, int c0, int c1, int64_t part) {
+    using S = CacheShape<NQ>;
+    constexpr int W = S::kWarps, KH = S::kHalves, ROWS = S::kRows;
     constexpr int KS = D / 16;                // k-steps of a score
-    constexpr int NT = D / 8;                 // 8-column tiles of the output
-    constexpr int kStage = 2 * 16 * D;        // bytes of a chunk: 16 keys and values
+    constexpr int MT = D / 16;                // 16-feature tiles of the output
+    constexpr int kHalf = 2 * 16 * D;         // bytes of a half: 16 keys, then 16 values
+    constexpr int kStage = KH * kHalf;
     constexpr int VB = D / 8;                 // bytes that a lane reads of a value row
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kBlock = S::kThreads;       // halves whose pages are looked up at a time, one per thread
     const CacheView& c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rt = blockIdx.x % p.row_tiles, bh = blockIdx.x / p.row_tiles, split = blockIdx.y;
-    const int b = bh / c.H_kv, hk = bh - b * c.H_kv;
+    const int teams = SHARED ? p.teams : 1, team = SHARED ? warp % teams : 0;
+    const int rt = rg * teams + team;
     const int R = p.group * p.Nq;
     const int64_t capacity = static_cast<int64_t>(c.M) * c.T;
     const int given = max(c.lengths[b], 0);
     const int len = static_cast<int>(min(static_cast<int64_t>(given), capacity));
-    // rows g and g + 8 of the tile: keys below lim are seen
-    int lim[2];
-    const uint16_t* qrow[2];
+
+    // the pages of the segment's halves, a block ahead of the copies
+    const int count = alive ? c1 - c0 : 0, steps = (count + W - 1) / W;
+    const float nan = __int_as_float(0x7fc00000);
+    PageEntry* entries = reinterpret_cast<PageEntry*>(smem + W * kCwStages * kStage);  // [2][kBlock]
+    auto look_up = [&](int block) {
+        PageEntry e{-1, nan, 0.f, 0};
+        const int64_t j0 = (static_cast<int64_t>(KH * c0) + block * kBlock + threadIdx.x) * 16;
+        if (j0 < len) {
+            const int page = c.table[static_cast<int64_t>(b) * c.M + (j0 >> c.log_T)];
+            if (page >= 0 && page < c.pages) {  // else: a page that is not there, its scores are NaN
+                const int64_t ph = static_cast<int64_t>(page) * c.H_kv + hk;
+                e.page = page;
+                e.ks = c.scales[0][ph];
+                e.vs = c.scales[1][ph];
+            }
+        }
+        return e;
+    };
+    auto entry_of = [&](int half) { return entries[half % (2 * kBlock)]; };
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t bars = ring + W * kCwStages * kStage + 2 * kBlock * static_cast<uint32_t>(sizeof(PageEntry));  // [stages][W]
+    int fetched = 0;
+    // step s: the warp's chunk W s + warp.  Every slot is used in every step, by a copy or by an arrival alone.
+    auto fetch = [&](int s) {
+        const int chunk = W * s + warp, slot = (uses + s) % kCwStages;
+        if (s >= steps) return;
+        ++fetched;
+        if (lane != 0 || (p.inject_stall && blockIdx.x == 0 && warp == 0 && s == 0)) return;  // the latter a test aid
+        uint32_t dst = ring + (slot * W + warp) * kStage;
+        const uint32_t bar = bars + 8 * (slot * W + warp);
+        int page[KH];
+        uint32_t bytes = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = rt * 16 + g + 8 * k, h = r / p.Nq, i = r - h * p.Nq;
-        lim[k] = r < R ? len - p.Nq + 1 + i : 0;
-        qrow[k] = r < R ? static_cast<const uint16_t*>(p.Q) + b * p.q_b + (hk * p.group + h) * p.q_h + i * p.q_n : nullptr;
-    }
-    // Query fragments.  Any order of d serves a score, if q and k have the same: lane t holds the 16-byte pieces
-    // t (and t + 4, d = 128) of a row, four values of one piece to a k-step.
-    uint32_t q[KS][4];
-    float qf[2];
+        for (int half = 0; half < KH; ++half) {
+            page[half] = chunk < count ? entry_of(KH * chunk + half).page : -1;
+            bytes += page[half] >= 0 ? kHalf : 0;
+        }
+        mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t raw[KS][2];
+        for (int half = 0; half < KH; ++half, dst += kHalf) {
+            if (page[half] < 0) continue;
+            const int j0 = (c0 + chunk) * S::kKeys + 16 * half, row = (page[half] * c.H_kv + hk) * c.T + (j0 & (c.T - 1));
+            copy_rows(dst, tK, bar, row);
+            copy_rows(dst + 16 * D, tV, bar, row);
+        }
+    };
+    bool ok = alive;
+    entries[threadIdx.x] = look_up(0);
+    PageEntry ahead = look_up(1);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kCwStages; ++s) fetch(s);
+
+    // Query fragments: lane (g, t) has row g of each 8-row tile.  Any order of d serves a score, if q and k have the
+    // same: the lane holds the 16-byte pieces t (and t + 4, d = 128) of a row, four values of one piece to a k-step.
+    uint32_t q[NQ][KS][2];
+    float qf[NQ][2];   // of rows 2t and 2t + 1 of a tile, the lane's columns of a score: its factor
+    int lim[NQ][2];    // and the keys below lim are seen
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = rt * ROWS + 8 * n + g, h = r / p.Nq, i = r - h * p.Nq;
+        const uint16_t* row = r < R ? static_cast<const uint16_t*>(p.Q) + b * p.q_b + (hk * p.group + h) * p.q_h + i * p.q_n : nullptr;
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const uint2 u = qrow[k] ? *reinterpret_cast<const uint2*>(qrow[k] + 64 * (s >> 2) + 16 * t + 4 * (s & 3)) : make_uint2(0u, 0u);
-            raw[s][0] = u.x, raw[s][1] = u.y;
+            const uint2 u = row ? *reinterpret_cast<const uint2*>(row + 64 * (s >> 2) + 16 * t + 4 * (s & 3)) : make_uint2(0u, 0u);
+            q[n][s][0] = u.x, q[n][s][1] = u.y;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t a = raw[s][e] & 0x7fff7fffu;
+                const uint32_t a = q[n][s][e] & 0x7fff7fffu;
                 top = __vmaxu2(top, a & ~__vcmpgeu2(a, 0x7f807f80u));
             }
         }
@@ -124,242 +238,331 @@ __global__ void __launch_bounds__(32 * kCwWarps, 1) cache8_attn_kernel(const __g
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
         const int e = max((most >> 7) - 127, -100);  // the row's largest magnitude is below 2^(e + 1)
         const float up = __int_as_float((10 - e + 127) << 23);  // brings it to [2^10, 2^11): f16 takes every bit of the row's larger values
-        qf[k] = p.scale_log2e * __int_as_float((e - 10 + 127) << 23);
+        const float down = p.scale_log2e * __int_as_float((e - 10 + 127) << 23);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                q[s][k + 2 * x] = pack_f16(__uint_as_float(raw[s][x] << 16) * up, __uint_as_float(raw[s][x] & 0xffff0000u) * up);
+                q[n][s][x] = pack_f16(__uint_as_float(q[n][s][x] << 16) * up, __uint_as_float(q[n][s][x] & 0xffff0000u) * up);
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+            const int x = 2 * t + e2, rx = rt * ROWS + 8 * n + x;
+            qf[n][e2] = __shfl_sync(0xffffffffu, down, 4 * x);
+            lim[n][e2] = rx < R ? len - p.Nq + 1 + rx % p.Nq : 0;
+        }
     }
 
-    // this split's share of the chunks, of which the warp takes every kCwWarps-th
-    const int chunks = (len + 15) / 16, per = (chunks + p.num_splits - 1) / p.num_splits;
-    const int first = split * per + warp, last = min(chunks, split * per + per);
-    const int mine = first < last ? (last - first + kCwWarps - 1) / kCwWarps : 0;
-    const float nan = __int_as_float(0x7fc00000);
-    // lane l knows the page and the scales of the warp's chunks 32 i + l: of this group and the next
-    int page[2] = {-1, -1};
-    float ks[2] = {nan, nan}, vs[2] = {0.f, 0.f};
-    auto look_up = [&](int group, int& pg, float& sk, float& sv) {
-        const int k = 32 * group + lane;
-        pg = -1, sk = nan, sv = 0.f;
-        if (k < mine) {
-            const int m = (first + k * kCwWarps) * 16 >> c.log_T;
-            pg = c.table[static_cast<int64_t>(b) * c.M + m];
-            if (pg >= 0 && pg < c.pages) {
-                const int64_t ph = static_cast<int64_t>(pg) * c.H_kv + hk;
-                sk = c.scales[0][ph];
-                sv = c.scales[1][ph];
-            } else {
-                pg = -1;  // a page that is not there: its scores are NaN
-            }
-        }
-    };
-    const uint32_t ring = smem_u32(smem) + warp * (kCwStages * kStage);
-    auto fetch = [&](int k) {  // chunk k of the warp, whose page stands in group k / 32
-        const int pg = __shfl_sync(0xffffffffu, (k >> 5) & 1 ? page[1] : page[0], k & 31);
-        if (k < mine) {
-            const int j0 = (first + k * kCwWarps) * 16, row0 = j0 & (c.T - 1);
-            const int64_t at = ((static_cast<int64_t>(max(pg, 0)) * c.H_kv + hk) * c.T + row0) * D;
-            const uint8_t* kp = c.values[0] + at;
-            const uint8_t* vp = c.values[1] + at;
-            uint32_t dst = ring + (k % kCwStages) * kStage + lane * 16;
+    float o[NQ][MT][4];
+    float m[NQ][2], w[NQ][2], l[NQ][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+    for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h, dst += 512)
-                    copy_async<16>(dst, kp + (8 * j + g) * D + 64 * h + 16 * t, pg >= 0 && j0 + 8 * j + g < len);
-            dst = ring + (k % kCwStages) * kStage + 16 * D + lane * VB;
-#pragma unroll
-            for (int x = 0; x < 4; ++x, dst += 32 * VB) {
-                const int j = 2 * t + (x & 1) + 8 * (x >> 1);
-                copy_async<VB>(dst, vp + j * D + VB * g, pg >= 0 && j0 + j < len);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    look_up(0, page[0], ks[0], vs[0]);
-    look_up(1, page[1], ks[1], vs[1]);
-#pragma unroll
-    for (int k = 0; k < kCwStages - 1; ++k) fetch(k);
-
-    float o[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, w[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int x = 0; x < MT; ++x) o[n][x][0] = o[n][x][1] = o[n][x][2] = o[n][x][3] = 0.f;
+        m[n][0] = m[n][1] = w[n][0] = w[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+    }
     const int all = len - p.Nq + 1;  // keys that every row sees
-    for (int k = 0; k < mine; ++k) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kCwStages - 2) : "memory");
-        const uint32_t at = ring + (k % kCwStages) * kStage;
-        const float sk = __shfl_sync(0xffffffffu, (k >> 5) & 1 ? ks[1] : ks[0], k & 31);
-        const float sv = __shfl_sync(0xffffffffu, (k >> 5) & 1 ? vs[1] : vs[0], k & 31);
-        const int j0 = (first + k * kCwWarps) * 16;
-        float s[2][4];
+    // the segment's chunk, in the ring at `at`
+    auto take = [&](int chunk, uint32_t at) {
+        float ks[KH], lv[KH];
+        float2 scale[KH];
+        float s[KH][NQ][4];  // (key g, rows 2t, 2t + 1), (key g + 8, the same)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        for (int half = 0; half < KH; ++half) {
+            const PageEntry en = entry_of(KH * chunk + half);
+            ks[half] = en.ks;
+            scale[half] = split_scale(en.vs);
+            lv[half] = scale[half].x + 1.f;  // log2 of a bound of the scale
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[half][n][0] = s[half][n][1] = s[half][n][2] = s[half][n][3] = 0.f;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
-                uint32_t u[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at + (j * (D / 64) + h) * 512 + lane * 16) : "memory");
+                uint32_t u[2][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma_f16(s[j], q[4 * h + e], f16x2_of_e4m3x2(u[e] & 0xffffu), f16x2_of_e4m3x2(u[e] >> 16));
+                for (int j = 0; j < 2; ++j)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[j][0]), "=r"(u[j][1]), "=r"(u[j][2]), "=r"(u[j][3]) : "r"(at + half * kHalf + piece_at<D>(8 * j + g, 4 * h + t)) : "memory");
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t a[4] = {f16x2_of_e4m3x2(u[0][e] & 0xffffu), f16x2_of_e4m3x2(u[1][e] & 0xffffu),
+                                           f16x2_of_e4m3x2(u[0][e] >> 16), f16x2_of_e4m3x2(u[1][e] >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) mma_f16(s[half][n], a, q[n][4 * h + e]);
+                }
             }
         }
-        const float f[2] = {qf[0] * sk, qf[1] * sk};
-        const bool masked = j0 + 16 > all;
+        const int j0 = (c0 + chunk) * S::kKeys;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int half = 0; half < KH; ++half)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[j][e] *= f[e >> 1];
-                if (masked && j0 + 8 * j + 2 * t + (e & 1) >= lim[e >> 1]) s[j][e] = -INFINITY;
-            }
-        const float2 scale = split_scale(sv);
-        const float lv = scale.x + 1.f;  // log2 of a bound of the scale
-        float top[2];
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[half][n][e] *= qf[n][e & 1] * ks[half];
+        if (j0 + S::kKeys > all) {
+#pragma unroll
+            for (int half = 0; half < KH; ++half)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j0 + 16 * half + 8 * (e >> 1) + g >= lim[n][e & 1]) s[half][n][e] = -INFINITY;
+        }
         bool raise = false;
+        float top[KH][NQ][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            raise |= top[r] > m[r] + kCwTau || top[r] + lv > w[r] + kCwTau;
-        }
+        for (int half = 0; half < KH; ++half)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[half][n][e] = fmaxf(s[half][n][e], s[half][n][2 + e]);
+                    raise |= top[half][n][e] > m[n][e] + kCwTau || top[half][n][e] + lv[half] > w[n][e] + kCwTau;
+                }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                if (top[r] > m[r] + kCwTau) {
-                    const float next = ceilf(top[r]);
-                    l[r] *= ratio(m[r], next);
-                    m[r] = next;
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float tm = top[0][n][e], tw = top[0][n][e] + lv[0];
+                    if (KH == 2) tm = fmaxf(tm, top[KH - 1][n][e]), tw = fmaxf(tw, top[KH - 1][n][e] + lv[KH - 1]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
+                        tw = fmaxf(tw, __shfl_xor_sync(0xffffffffu, tw, x));
+                    }
+                    if (tm > m[n][e] + kCwTau) {
+                        const float next = ceilf(tm);
+                        l[n][e] *= ratio(m[n][e], next);
+                        m[n][e] = next;
+                    }
+                    if (tw > w[n][e] + kCwTau) {
+                        const float next = ceilf(tw), f = ratio(w[n][e], next);
+#pragma unroll
+                        for (int x = 0; x < MT; ++x) o[n][x][e] *= f, o[n][x][2 + e] *= f;
+                        w[n][e] = next;
+                    }
                 }
-                if (top[r] + lv > w[r] + kCwTau) {
-                    const float next = ceilf(top[r]) + lv, x = ratio(w[r], next);
+        }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) o[n][2 * r] *= x, o[n][2 * r + 1] *= x;
-                    w[r] = next;
+        for (int half = 0; half < KH; ++half) {
+            uint32_t pr[NQ][2];  // (keys 2t, 2t + 1 and 2t + 8, 2t + 9; row g)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
+                    // a probability's factor in the output's units
+                    const float x = w[n][e] == -INFINITY ? 0.f * scale[half].y
+                                                         : scale[half].y * ex2(ref - w[n][e] + kCwShift + fmaxf(scale[half].x, -256.f));
+                    const float p0 = ex2(s[half][n][e] - ref), p1 = ex2(s[half][n][2 + e] - ref);
+                    l[n][e] += p0 + p1;
+                    v[e] = p0 * x;
+                    v[2 + e] = p1 * x;
                 }
+                pr[n][0] = transpose8(pack_f16(v[0], v[1]));
+                pr[n][1] = transpose8(pack_f16(v[2], v[3]));
             }
-        }
-        uint32_t a[4];
+            // values: lane (g, t) has bytes VB g .. of keys 2t, 2t + 1, 2t + 8, 2t + 9; output tile x has bytes 2x, 2x + 1
+            uint32_t v[4][VB / 4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float ref = m[r] == -INFINITY ? 0.f : m[r];
-            // a probability's factor in the output's units
-            const float x = w[r] == -INFINITY ? 0.f * scale.y : scale.y * ex2(ref - w[r] + kCwShift + fmaxf(scale.x, -256.f));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float p0 = ex2(s[j][2 * r] - ref), p1 = ex2(s[j][2 * r + 1] - ref);
-                l[r] += p0 + p1;
-                a[2 * j + r] = pack_f16(p0 * x, p1 * x);
+            for (int x = 0; x < 4; ++x) {
+                const int key = 2 * t + (x & 1) + 8 * (x >> 1);
+                const uint32_t src = at + half * kHalf + 16 * D + (VB == 16 ? piece_at<D>(key, g) : piece_at<D>(key, g >> 1) + 8 * (g & 1));
+                if (VB == 16)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[x][0]), "=r"(v[x][1]), "=r"(v[x][VB / 4 - 2]), "=r"(v[x][VB / 4 - 1]) : "r"(src) : "memory");
+                else
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[x][0]), "=r"(v[x][1]) : "r"(src) : "memory");
             }
-        }
-        // values: lane (g, t) has bytes VB g .. of keys 2t, 2t + 1, 2t + 8, 2t + 9; output tile n is byte n of each
-        uint32_t v[4][VB / 4];
+            if (j0 + 16 * half + 16 > len) {  // what stands behind the tokens may be NaN, which a probability of 0 does not hide
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t src = at + 16 * D + x * 32 * VB + lane * VB;
-            if (VB == 16)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[x][0]), "=r"(v[x][1]), "=r"(v[x][VB / 4 - 2]), "=r"(v[x][VB / 4 - 1]) : "r"(src) : "memory");
-            else
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[x][0]), "=r"(v[x][1]) : "r"(src) : "memory");
-        }
-        // into the slot of the chunk before this one
-        const int next = k + kCwStages - 1;
-        if ((next & 31) == 8 && next > 32) {  // the group behind next's: its pages replace those of the group before
-            if ((next >> 5) & 1)
-                look_up((next >> 5) + 1, page[0], ks[0], vs[0]);
-            else
-                look_up((next >> 5) + 1, page[1], ks[1], vs[1]);
-        }
-        fetch(next);
+                for (int x = 0; x < 4; ++x)
+                    if (j0 + 16 * half + 2 * t + (x & 1) + 8 * (x >> 1) >= len) {
 #pragma unroll
-        for (int e = 0; e < VB / 4; ++e)
-#pragma unroll
-            for (int pair = 0; pair < 2; ++pair) {
-                const uint32_t sel = pair ? 0x7362u : 0x5140u;  // bytes (2 pair, 2 pair + 1) of both keys
-                const uint32_t x = __byte_perm(v[0][e], v[1][e], sel), y = __byte_perm(v[2][e], v[3][e], sel);
-                mma_f16(o[4 * e + 2 * pair], a, f16x2_of_e4m3x2(x & 0xffffu), f16x2_of_e4m3x2(y & 0xffffu));
-                mma_f16(o[4 * e + 2 * pair + 1], a, f16x2_of_e4m3x2(x >> 16), f16x2_of_e4m3x2(y >> 16));
+                        for (int e = 0; e < VB / 4; ++e) v[x][e] = 0u;
+                    }
             }
+#pragma unroll
+            for (int e = 0; e < VB / 4; ++e)
+#pragma unroll
+                for (int pair = 0; pair < 2; ++pair) {
+                    const uint32_t sel = pair ? 0x7362u : 0x5140u;  // bytes (2 pair, 2 pair + 1) of both keys
+                    const uint32_t x = __byte_perm(v[0][e], v[1][e], sel), y = __byte_perm(v[2][e], v[3][e], sel);
+                    const uint32_t a[4] = {f16x2_of_e4m3x2(x & 0xffffu), f16x2_of_e4m3x2(x >> 16), f16x2_of_e4m3x2(y & 0xffffu),
+                                           f16x2_of_e4m3x2(y >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) mma_f16(o[n][2 * e + pair], a, pr[n]);
+                }
+        }
+    };
+    constexpr int kBlockSteps = kBlock / (KH * W);
+    for (int s = 0; s < steps; ++s) {
+        if (s % kBlockSteps == 0) {  // the next block's pages replace those of the block before this one
+            const int block = s / kBlockSteps;
+            __syncthreads();
+            entries[(block + 1) % 2 * kBlock + threadIdx.x] = ahead;
+            __syncthreads();
+            ahead = look_up(block + 2);
+        }
+        // the step before is done with: its slot takes the copy of the last step of the ring
+        if (SHARED)
+            __syncthreads();
+        else
+            __syncwarp();
+        if (ok && s > 0) fetch(s + kCwStages - 1);
+        const int slot = (uses + s) % kCwStages, phase = (uses + s) / kCwStages & 1;
+        const uint32_t slots = ring + slot * W * kStage, full = bars + 8 * slot * W;
+        if (SHARED) {
+#pragma unroll 1
+            for (int j = warp / teams; j < W; j += W / teams) {
+                const int chunk = W * s + j;
+                ok = ok && wait_all(full + 8 * j, phase, wc, kErrWaitK);
+                if (ok && chunk < count) take(chunk, slots + j * kStage);
+            }
+        } else {
+            ok = ok && wait_all(full + 8 * warp, phase, wc, kErrWaitK);
+            if (ok && W * s + warp < count) take(W * s + warp, slots + warp * kStage);
+        }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
+    uses += steps;
+    ok = __syncthreads_and(ok);
+    if (!ok) {
+        for (int s = max(0, fetched - kCwStages); s < fetched; ++s)  // the warp's copies land before the CTA ends
+            drain_wait_b(bars + 8 * ((uses - steps + s) % kCwStages * W + warp), (uses - steps + s) / kCwStages & 1, kDrainNs);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) l[n][0] = l[n][1] = nan;
+        __syncthreads();
+    }
 
-    // the warps' states and sums meet in shared memory (the rings are done with)
-    float* sums = reinterpret_cast<float*>(smem);                      // [warps][16][D]
-    float* states = sums + kCwWarps * 16 * D;                          // [warps][3][16]
+    // the states and sums of a team's warps meet in shared memory (the ring is done with)
+    float* sums = reinterpret_cast<float*>(smem);                      // [warps][ROWS][D]
+    float* states = sums + W * ROWS * D;                               // [warps][3][ROWS]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const int row = g + 8 * r;
-        if (t == 0) {
-            states[(warp * 3) * 16 + row] = m[r];
-            states[(warp * 3 + 1) * 16 + row] = l[r];
-            states[(warp * 3 + 2) * 16 + row] = w[r];
-        }
-        float* dst = sums + (warp * 16 + row) * D + 2 * NT * t;  // columns 2t and 2t + 1 of tile n: d = 2 NT t + n, + NT
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; n += 4) {
-            *reinterpret_cast<float4*>(dst + n) = make_float4(o[n][2 * r], o[n + 1][2 * r], o[n + 2][2 * r], o[n + 3][2 * r]);
-            *reinterpret_cast<float4*>(dst + NT + n) =
-                make_float4(o[n][2 * r + 1], o[n + 1][2 * r + 1], o[n + 2][2 * r + 1], o[n + 3][2 * r + 1]);
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+            const int row = 8 * n + 2 * t + e;
+            if (g == 0) {
+                states[(warp * 3) * ROWS + row] = m[n][e];
+                states[(warp * 3 + 1) * ROWS + row] = l[n][e];
+                states[(warp * 3 + 2) * ROWS + row] = w[n][e];
+            }
+            float* dst = sums + (warp * ROWS + row) * D + VB * g;  // tile x: d = VB g + 2x, + 1
+#pragma unroll
+            for (int x = 0; x < MT; x += 2)
+                *reinterpret_cast<float4*>(dst + 2 * x) = make_float4(o[n][x][e], o[n][x][2 + e], o[n][x + 1][e], o[n][x + 1][2 + e]);
         }
-    }
     __syncthreads();
-    constexpr int kPer = 16 * D / (32 * kCwWarps);  // values of a row per thread: 16 threads to a row
-    const int row = threadIdx.x / 16, d0 = (threadIdx.x % 16) * kPer, r = rt * 16 + row;
-    if (r >= R) return;
-    CacheState st{-INFINITY, 0.f, -INFINITY};
-#pragma unroll
-    for (int x = 0; x < kCwWarps; ++x) {
-        st.m = fmaxf(st.m, states[(x * 3) * 16 + row]);
-        st.w = fmaxf(st.w, states[(x * 3 + 2) * 16 + row]);
+    for (int x = threadIdx.x; x < teams * ROWS * (D / 4); x += S::kThreads) {
+        const int line = x / (D / 4), d0 = (x % (D / 4)) * 4, row = line % ROWS, tm = line / ROWS, r = (rg * teams + tm) * ROWS + row;
+        if (r >= R) continue;
+        CacheState st{-INFINITY, 0.f, -INFINITY};
+        for (int y = tm; y < W; y += teams) {
+            st.m = fmaxf(st.m, states[(y * 3) * ROWS + row]);
+            st.w = fmaxf(st.w, states[(y * 3 + 2) * ROWS + row]);
+        }
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = tm; y < W; y += teams) {
+            const float mx = states[(y * 3) * ROWS + row], lx = states[(y * 3 + 1) * ROWS + row], wx = states[(y * 3 + 2) * ROWS + row];
+            st.l += mx == -INFINITY ? lx : lx * ex2(mx - st.m);  // without a reference: 0, or NaN scores alone
+            const float f = wx == -INFINITY ? 1.f : ex2(wx - st.w);
+            const float4 u = *reinterpret_cast<const float4*>(sums + (y * ROWS + row) * D + d0);
+            v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+        }
+        if (given > capacity) st.l = nan;  // tokens that the table has no page for
+        if (part >= 0) {
+            const int64_t at = part * (ROWS * teams) + line;
+            *reinterpret_cast<float4*>(p.part + at * D + d0) = v;
+            if (d0 == 0) p.part_state[at] = make_float4(st.m, st.l, st.w, 0.f);
+            continue;
+        }
+        const int h = hk * p.group + r / p.Nq, i = r % p.Nq;
+        const bool empty = len - p.Nq + 1 + i <= 0;
+        const float f = empty ? 0.f : output_factor(st);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + d0) =
+            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+        if (d0 == 0) p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
     }
-    float v[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] = 0.f;
-#pragma unroll
-    for (int x = 0; x < kCwWarps; ++x) {
-        const float mx = states[(x * 3) * 16 + row], lx = states[(x * 3 + 1) * 16 + row], wx = states[(x * 3 + 2) * 16 + row];
-        st.l += mx == -INFINITY ? lx : lx * ex2(mx - st.m);  // without a reference: 0, or NaN scores alone
-        const float f = wx == -INFINITY ? 1.f : ex2(wx - st.w);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] = fmaf(sums[(x * 16 + row) * D + d0 + e], f, v[e]);
-    }
-    if (given > capacity) st.l = nan;  // tokens that the table has no page for
-    const int h = hk * p.group + r / p.Nq, i = r % p.Nq;
-    const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
-    if (p.num_splits > 1) {
-        const size_t at = static_cast<size_t>(split) * c.B * p.H * p.Nq + flat;
-        float4* dst = reinterpret_cast<float4*>(p.part + at * D + d0);
-#pragma unroll
-        for (int e = 0; e < kPer; e += 4) dst[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        if (d0 == 0) p.part_state[at] = make_float4(st.m, st.l, st.w, 0.f);
-        return;
-    }
-    const bool empty = len - p.Nq + 1 + i <= 0 && given <= capacity;
-    const float f = empty ? 0.f : output_factor(st);
-    uint16_t* out = static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + d0;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 4)
-        *reinterpret_cast<uint2*>(out + e) = empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v[e] * f, v[e + 1] * f), pack_bf16(v[e + 2] * f, v[e + 3] * f));
-    if (d0 == 0) p.LSE[flat] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
+    fence_proxy_async_smem();  // the ring may be filled again
+    __syncthreads();
+    return ok;
 }
 
-// One warp per row: the splits' sums, brought to the largest references.
-template <int D>
-__global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_constant__ CacheAttnParams p) {
-    constexpr int V = D / 32;
-    const size_t R = static_cast<size_t>(p.c.B) * p.H * p.Nq, row = blockIdx.x * size_t(8) + (threadIdx.x >> 5);
-    if (row >= R) return;
+}  // namespace
+
+template <int D, int NQ, bool SHARED>
+__global__ void __launch_bounds__(CacheShape<NQ>::kThreads, 1)
+    cache8_attn_kernel(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
+                       const __grid_constant__ CacheAttnParams p) {
+    using S = CacheShape<NQ>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ int abort_word;
+    const CacheView& c = p.c;
+    const uint32_t bars = smem_u32(smem) + S::kWarps * kCwStages * 2 * S::kKeys * D + 2 * S::kThreads * static_cast<uint32_t>(sizeof(PageEntry));
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tK);
+        prefetch_tensormap(&tV);
+        for (int k = 0; k < kCwStages * S::kWarps; ++k) mbar_init(bars + 8 * k, 1);
+        abort_word = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    const WaitCtx wc{&abort_word, p.status, p.wait_ns};
+    int uses = 0;
+    bool alive = true;
+    const int per_b = c.H_kv * p.row_groups;  // segments of a sequence
+    if (!p.spread) {
+        const int b = blockIdx.x / per_b, s = blockIdx.x - b * per_b;
+        attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups, 0, chunks_of(c, b, S::kKeys), -1);
+        return;
+    }
+    // this CTA's chunks [lo, hi) of all, counted through the segments of one sequence after the other
+    int64_t before = 0;
+    const int64_t total = sum_chunks(c, 0, S::kKeys, &before) * per_b, share = share_of(total, gridDim.x, S::kWarps);
+    const int64_t lo = blockIdx.x * share, hi = min(total, lo + share);
+    int64_t at = 0;  // first chunk of sequence b
+    for (int b = 0; b < c.B && at < hi; ++b) {
+        const int n = chunks_of(c, b, S::kKeys);
+        const int64_t end = at + static_cast<int64_t>(n) * per_b;
+        if (end > lo && n > 0) {
+            for (int s = lo > at ? static_cast<int>((lo - at) / n) : 0; s < per_b; ++s) {
+                const int64_t a = at + static_cast<int64_t>(s) * n;  // first chunk of the segment
+                if (a >= hi) break;
+                const bool whole = a >= lo && a + n <= hi;
+                alive = attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups,
+                                      static_cast<int>(max(lo - a, int64_t(0))), static_cast<int>(min(hi - a, static_cast<int64_t>(n))),
+                                      whole ? int64_t(-1) : 2 * static_cast<int64_t>(blockIdx.x) + (a < lo ? 0 : 1));
+            }
+        }
+        at = end;
+    }
+}
+
+// One warp per row: the parts of a segment that was cut, brought to the largest
+// references; rows of sequences without tokens.
+template <int D, int NQ>
+__global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_constant__ CacheAttnParams p, int ctas) {
+    constexpr int V = D / 32, ROWS = CacheShape<NQ>::kRows, keys = CacheShape<NQ>::kKeys;
+    const CacheView& c = p.c;
+    const size_t rows = static_cast<size_t>(c.B) * p.H * p.Nq, row = blockIdx.x * size_t(8) + (threadIdx.x >> 5);
+    if (row >= rows) return;
     const int lane = threadIdx.x & 31;
     const int i = static_cast<int>(row % p.Nq), h = static_cast<int>(row / p.Nq % p.H), b = static_cast<int>(row / p.Nq / p.H);
+    const int hk = h / p.group, r = (h - hk * p.group) * p.Nq + i, line = r % (ROWS * p.teams), rg = r / (ROWS * p.teams);
+    const int per_b = c.H_kv * p.row_groups, n = chunks_of(c, b, keys);
+    int64_t before = 0;
+    const int64_t total = sum_chunks(c, b, keys, &before) * per_b;
+    const int64_t share = share_of(total, ctas, CacheShape<NQ>::kWarps);
+    const int64_t a = before * per_b + static_cast<int64_t>(hk * p.row_groups + rg) * n;
+    const int first = static_cast<int>(a / share), last = n > 0 ? static_cast<int>((a + n - 1) / share) : first;
+    if (n > 0 && first == last) return;  // the segment's CTA has written the row
     CacheState st{-INFINITY, 0.f, -INFINITY};
-    for (int s = lane; s < p.num_splits; s += 32) {
-        const float4 x = p.part_state[s * R + row];
+    auto index = [&](int k) { return (2 * static_cast<int64_t>(k) + (a < k * share ? 0 : 1)) * (ROWS * p.teams) + line; };
+    for (int k = first + lane; n > 0 && k <= last; k += 32) {
+        const float4 x = p.part_state[index(k)];
         st.m = fmaxf(st.m, x.x);
         st.w = fmaxf(st.w, x.z);
     }
@@ -371,15 +574,15 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_consta
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
-    for (int s = 0; s < p.num_splits; ++s) {
-        const float4 x = p.part_state[s * R + row];
+    for (int k = first; n > 0 && k <= last; ++k) {
+        const float4 x = p.part_state[index(k)];
         st.l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - st.m);
         const float f = x.z == -INFINITY ? 1.f : ex2(x.z - st.w);
-        const float* part = p.part + (s * R + row) * D + lane * V;
+        const float* part = p.part + index(k) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
     }
-    const bool empty = p.c.lengths[b] - p.Nq + 1 + i <= 0;
+    const bool empty = c.lengths[b] - p.Nq + 1 + i <= 0;
     const float f = empty ? 0.f : output_factor(st);
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + lane * V);
 #pragma unroll
@@ -388,23 +591,33 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_consta
 }
 
 namespace {
-template <int D>
-cudaError_t launch_cache8_attn_d(const CacheAttnParams& p, cudaStream_t stream) {
-    constexpr int ring = kCwWarps * kCwStages * 2 * 16 * D, merge = (kCwWarps * 16 * D + kCwWarps * 48) * 4;
-    constexpr int bytes = ring > merge ? ring : merge;
-    auto k = cache8_attn_kernel<D>;
+template <int D, int NQ, bool SHARED>
+cudaError_t launch_cache8_attn_d(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream) {
+    using S = CacheShape<NQ>;
+    constexpr int ring = S::kWarps * kCwStages * 2 * S::kKeys * D, merge = S::kWarps * S::kRows * (D + 3) * 4;
+    static_assert(merge <= ring, "the states meet in the ring's space");
+    constexpr int bytes = ring + 2 * S::kThreads * static_cast<int>(sizeof(PageEntry)) + 8 * kCwStages * S::kWarps + 1024;
+    static_assert(bytes <= 232448, "shared memory");
+    auto k = cache8_attn_kernel<D, NQ, SHARED>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3(static_cast<unsigned>(p.c.B) * p.c.H_kv * p.row_tiles, p.num_splits), 32 * kCwWarps, bytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || p.num_splits == 1) return e;
+    k<<<ctas, S::kThreads, bytes, stream>>>(maps[0], maps[1], p);
+    if ((e = cudaGetLastError()) != cudaSuccess || !p.spread) return e;
     const int64_t rows = int64_t(p.c.B) * p.H * p.Nq;
-    cache8_combine_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
+    cache8_combine_kernel<D, NQ><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p, ctas);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_cache8_attn_r(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream) {
+    return p.tile_rows == 8 ? launch_cache8_attn_d<D, 1, false>(maps, p, ctas, stream)
+           : p.teams == 1   ? launch_cache8_attn_d<D, 2, false>(maps, p, ctas, stream)
+                            : launch_cache8_attn_d<D, 2, true>(maps, p, ctas, stream);
 }
 }  // namespace
 
-cudaError_t launch_cache8_attn(const CacheAttnParams& p, cudaStream_t stream) {
-    return p.c.d == 128 ? launch_cache8_attn_d<128>(p, stream) : launch_cache8_attn_d<64>(p, stream);
+cudaError_t launch_cache8_attn(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream) {
+    return p.c.d == 128 ? launch_cache8_attn_r<128>(maps, p, ctas, stream) : launch_cache8_attn_r<64>(maps, p, ctas, stream);
 }
 
 }  // namespace streamkl

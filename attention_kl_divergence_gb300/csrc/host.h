@@ -23,6 +23,7 @@ int bwd_splits(int64_t units, int64_t iterations, int sms);
 bool make_map(CUtensorMap* m, const void* ptr, const streamkl_shape* s, bool is_q, int box_rows, int box_heads = 1);
 bool make_map_strided(CUtensorMap* m, const void* ptr, int d, int64_t N, int heads, int B, const streamkl_strides& st,
                       int box_rows, int box_heads = 1);
+bool make_map_bytes(CUtensorMap* m, const void* ptr, int d, int64_t rows);
 float resolve_scale(float scale, int d);
 int64_t wait_limit(const streamkl_options* opt);
 

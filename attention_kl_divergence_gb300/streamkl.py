@@ -1206,18 +1206,20 @@ def attn_cache8_plan(Q, cache, table, lengths, num_splits=0) -> Plan:
     return plan
 
 
-def attn_cache8(Q, cache, table, lengths, scale=None, out=None, num_splits=0, workspace=None):
+def attn_cache8(Q, cache, table, lengths, scale=None, out=None, num_splits=0, workspace=None, wait_limit_ns=0,
+                debug_flags=0):
     """(O, LSE): softmax attention of the last Nq tokens (1 to 16) of each sequence, Q [B, H, Nq, d] (bf16, any strides with
     d contiguous), over the lengths[b] tokens that it holds in the cache, its own among them: row i sees the keys before
     lengths[b] - Nq + 1 + i.  Hk divides H.  A row that sees no key has O = 0 and LSE = -inf; a row that sees a page
     outside the cache, and a sequence longer than its table, is NaN.  Longer chunks: attn_fwd over cache8_read."""
     held = _cache(cache)
-    num_splits = int(num_splits)
-    key, known = _lookup("attn_cache8", _tensors(Q, *held, table, lengths, *(() if out is None else (out,))), num_splits)
+    num_splits, wait_limit_ns, debug_flags = int(num_splits), int(wait_limit_ns), int(debug_flags)
+    key, known = _lookup("attn_cache8", _tensors(Q, *held, table, lengths, *(() if out is None else (out,))), num_splits,
+                         wait_limit_ns, debug_flags)
     if known is None:
         desc = _attn_cache8_desc(Q, held, table, lengths)
         desc.y = _contiguous(Q.shape) if out is None else _heads("out", out, (torch.bfloat16,), Q.device, Q.shape)
-        opts, plan = _opts(num_splits), Plan()
+        opts, plan = _opts(num_splits, 0, wait_limit_ns, debug_flags), Plan()
         with torch.cuda.device(Q.device):
             _raise(load().streamkl_attn_cache8_plan(ctypes.byref(desc), ctypes.byref(opts), ctypes.byref(plan)),
                    "streamkl_attn_cache8_plan")

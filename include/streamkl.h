@@ -480,8 +480,9 @@ STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const 
  * Q [B, H, N, d] bf16, row i seeing keys j < lengths[b] - N + 1 + i; query head h
  * uses key head h / (H / H_kv).  O is bf16 [B, H, N, d], LSE float32 [B, H, N]; a
  * row that sees no key has O = 0 and LSE = -inf; a row that sees a page that is
- * not there, or a sequence longer than its table, is NaN.  Equal inputs give equal
- * bits.
+ * not there, or a sequence longer than its table, is NaN, and so are rows that a
+ * give-up of a bounded wait left unfinished.  opt->num_splits: CTAs that share out
+ * the keys of all sequences (0 = automatic).  Equal inputs give equal bits.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -231,11 +231,12 @@ ATTENTION = [  # B, H, Hk, Nq, T, d, M, lengths
     (1, 1, 1, 1, 16, 64, 1, [1]), (2, 8, 2, 1, 16, 128, 9, [144, 3]), (3, 6, 2, 5, 64, 64, 5, [300, 4, 0]),
     (1, 16, 2, 16, 128, 128, 3, [384]), (2, 4, 4, 2, 32, 128, 40, [1279, 17]), (4, 8, 1, 1, 64, 128, 70, [4480, 1, 4097, 2000]),
     (2, 24, 8, 7, 16, 64, 20, [319, 6]), (1, 2, 1, 1, 64, 128, 700, [44003]),
+    (2, 8, 2, 9, 16, 128, 60, [900, 33]), (1, 24, 2, 16, 32, 64, 30, [960]), (1, 40, 1, 16, 64, 128, 21, [1300]), (40, 4, 2, 1, 16, 64, 70, list(range(0, 1120, 28))),
 ]
 
 
 @gpu
-@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("splits", [0, 1, 3, 40])
 @pytest.mark.parametrize("shape", ATTENTION, ids=str)
 def test_attention(shape, splits):
     B, H, Hk, Nq, T, d, M, lengths = shape
@@ -349,6 +350,25 @@ def test_outputs_streams_graphs_and_in_place_changes():
 
 
 @gpu
+@pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("Nq", [1, 9])
+def test_a_wait_that_gives_up_leaves_nan_and_a_status(Nq, splits):
+    B, H, Hk, T, d, M = 2, 8, 2, 16, 128, 64
+    table, pages = tables(B, M)
+    cache = pool(pages, Hk, T, d)
+    Q = torch.randn(B, H, Nq, d, device=DEV).to(BF16)
+    n = torch.tensor([1000, 300], dtype=torch.int32, device=DEV)
+    work = sk.new_workspace(sk.attn_cache8_plan(Q, cache, table, n, num_splits=splits).workspace_bytes, DEV)
+    O, LSE = sk.attn_cache8(Q, cache, table, n, num_splits=splits, workspace=work, wait_limit_ns=10 ** 7, debug_flags=sk.DEBUG_INJECT_STALL)
+    assert sk.workspace_status(work) != 0
+    assert bool(O[0, :H // Hk].isnan().all()) and bool(LSE[0, :H // Hk].isnan().all())  # the first segment's rows
+    want = sk.attn_cache8(Q, cache, table, n, num_splits=splits, workspace=work)
+    assert sk.workspace_status(work) == 0 and not bool(want[0].isnan().any())
+    good = ~O.isnan()
+    assert torch.equal(O[good], want[0][good])
+
+
+@gpu
 def test_refusals():
     table, pages = tables(2, 3)
     cache = pool(pages, 2, 16, 64)
@@ -389,9 +409,8 @@ def test_refusals():
     bad(sk.attn_cache8, Q[:, :, :0], cache, table, n)
     bad(sk.attn_cache8, Q, cache, table, n, out=Q.float())
     bad(sk.attn_cache8, Q, cache, table, n, num_splits=-1)
-    long = table.repeat(1, 7)  # 336 tokens: a split takes 128 at least
-    assert sk.attn_cache8_plan(Q, cache, long, n, num_splits=2).workspace_bytes > 256
-    bad(sk.attn_cache8, Q, cache, long, n, num_splits=2, workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
+    assert sk.attn_cache8_plan(Q, cache, table, n, num_splits=2).workspace_bytes > 256
+    bad(sk.attn_cache8, Q, cache, table, n, num_splits=2, workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
     sk.cache8_append(cache, table, n, k[:, :, :0], k[:, :, :0])  # no tokens is allowed
     assert sk.cache8_read(cache, table, n, tokens=0)[0].shape == (2, 2, 0, 64)
 
