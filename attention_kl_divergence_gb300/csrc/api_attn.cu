@@ -87,19 +87,27 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
     const int64_t heads = int64_t(s->B) * s->H_kv * p.units_h, units = heads * p.units_q;
     if (units > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     const int k_tiles = (s->Nk - 1) / kBlockK + 1;
+    p.dual = p.blocks == 1 && p.q_tiles == 1 && k_tiles >= 8;
     int splits = 1;
     if (opt && opt->num_splits > 0) {
         splits = std::min({opt->num_splits, k_tiles, kMaxSplits});
+    } else if (p.dual) {
+        // Bound by HBM: one wave of CTAs, which saturates it from about two thirds of the SMs on; more waves start and
+        // end more often than unequal lengths cost (4 caches of up to 65536 keys, 8 key heads: 3 splits 185 us, 4 158,
+        // 5 164, 9 163, 19 178; one cache: 8 splits 78, 14 62, 19 63, 28 86).
+        splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, k_tiles / 4)));
     } else {
         const int n = choose_splits(units, k_tiles, sms);
         if ((k_tiles + n - 1) / n + 3 < k_tiles) splits = n;
     }
+    splits = std::min(splits, kMaxSplits);
     if (units * splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     p.num_splits = splits;
+    p.parts = p.dual ? 2 * splits : splits;
     pl->ctas = static_cast<int>(units * splits);
     p.order_group = order_group(heads, p.units_q, sms);
     pl->ws_bytes = kStatusBytes;
-    if (splits > 1) pl->ws_bytes += size_t(splits) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
+    if (p.parts > 1) pl->ws_bytes += size_t(p.parts) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
     return STREAMKL_OK;
 }
 
@@ -155,7 +163,7 @@ streamkl_status streamkl_attn_fwd_plan(const streamkl_attn* desc, const streamkl
     plan->path = 0;
     plan->num_splits = pl.p.num_splits;
     plan->num_ctas = pl.ctas;
-    plan->launches = pl.p.num_splits > 1 ? 2 : 1;
+    plan->launches = pl.p.parts > 1 ? 2 : 1;
     plan->workspace_bytes = pl.ws_bytes;
     return STREAMKL_OK;
 }
@@ -171,10 +179,10 @@ streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, cons
         if (!q || !aligned16(q)) return STREAMKL_ERR_INVALID_ARG;
     if (!aligned16(rest) || !LSE || !aligned4(LSE) || !aligned4(begin) || !aligned4(end) || !aligned4(offset))
         return STREAMKL_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
     AttnFwdPlan pl{};
     if ((st = plan_attn_fwd(desc, opt, &pl)) != STREAMKL_OK) return st;
-    if (workspace_bytes < pl.ws_bytes) return STREAMKL_ERR_WORKSPACE;
+    // without parts only the error word stands in the workspace
+    if (workspace ? !aligned16(workspace) || workspace_bytes < pl.ws_bytes : pl.p.parts > 1) return STREAMKL_ERR_WORKSPACE;
 
     AttnFwdParams& p = pl.p;
     CUtensorMap maps[3];
@@ -190,9 +198,9 @@ streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, cons
     p.o_n = s.o.n;
     p.rest = rest;
     p.LSE = LSE;
-    if (p.num_splits > 1) {
+    if (p.parts > 1) {
         p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-        p.part_ml = reinterpret_cast<float2*>(p.part + size_t(p.num_splits) * s.B * s.H * s.Nq * s.d);
+        p.part_ml = reinterpret_cast<float2*>(p.part + size_t(p.parts) * s.B * s.H * s.Nq * s.d);
     }
     p.status = static_cast<unsigned int*>(workspace);
     p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));

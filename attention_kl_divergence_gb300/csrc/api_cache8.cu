@@ -174,10 +174,10 @@ streamkl_status streamkl_attn_cache8(const streamkl_cache8* desc, const void* Q,
                    table, lengths, &p.c) ||
         !Q || !O || !LSE || !aligned16(Q) || !aligned16(O) || !aligned4(LSE))
         return STREAMKL_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
     CacheAttnPlan pl{};
     if ((st = plan_cache_attn(desc, opt, &pl)) != STREAMKL_OK) return st;
-    if (workspace_bytes < pl.ws_bytes) return STREAMKL_ERR_WORKSPACE;
+    // where no parts are combined only the error word stands in the workspace
+    if (workspace ? !aligned16(workspace) || workspace_bytes < pl.ws_bytes : pl.spread != 0) return STREAMKL_ERR_WORKSPACE;
     p.H = s.H;
     p.Nq = s.N;
     p.group = s.H / s.H_kv;

@@ -20,15 +20,17 @@ struct AttnFwdParams {
     int blocks, q_tiles;     // tiles of a key head: head blocks x query tiles
     int pair_heads;          // a pair is two head blocks (else two query tiles)
     int units_h, units_q;    // pairs of a key head
+    int dual;                // a tile without another to pair with stands twice, each with every second key tile
     int num_splits;
+    int parts;               // of a row: num_splits, twice that if dual; 1: outputs
     int order_group;         // see grouped_order
     float c;                 // softmax scale * log2(e)
     void* O;                 // bf16, strided
     int64_t o_b, o_h, o_n;
     void* rest;              // bf16 [B, H, Nq, d] or null: O before its rounding, less O
     float* LSE;              // [B, H, Nq]
-    float* part;             // several splits: [splits][B*H*Nq][d] sums of 2^(x - m) v
-    float2* part_ml;         // [splits][B*H*Nq]: m (log2) and the sum of 2^(x - m)
+    float* part;             // several parts: [parts][B*H*Nq][d] sums of 2^(x - m) v
+    float2* part_ml;         // [parts][B*H*Nq]: m (log2) and the sum of 2^(x - m)
     unsigned int* status;
     unsigned long long wait_ns;
     int inject_stall;

@@ -19,6 +19,7 @@
 #include "attn.cuh"
 #include "bwd_common.cuh"
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "score.cuh"
@@ -599,7 +600,8 @@ cudaError_t launch_attn_bwd_d(const CUtensorMap* m, const AttnBwdParams& p, cons
     constexpr int bytes = AttnKvSmem<D>::alloc;
     static_assert(bytes <= 232448, "shared memory");
     auto k = attn_bwd_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k, bytes, &done);
     if (e != cudaSuccess) return e;
     attn_prepare_kernel<D><<<static_cast<unsigned>(p.B * p.H) * p.num_q_tiles, 256, 0, st>>>(p, sp);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

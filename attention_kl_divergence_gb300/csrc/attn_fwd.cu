@@ -8,6 +8,7 @@
 #include "attn.cuh"
 #include "bwd_common.cuh"
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "score.cuh"
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const int bkv = at.x / p.units_h, hb = at.x - bkv * p.units_h, qu = p.units_q - 1 - at.y;
     const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
     auto block_of = [&](int s) { return p.pair_heads ? 2 * hb + s : hb; };
-    auto qtile_of = [&](int s) { return p.pair_heads ? qu : 2 * qu + s; };
+    auto qtile_of = [&](int s) { return p.pair_heads || p.dual ? qu : 2 * qu + s; };
     auto exists = [&](int s) { return block_of(s) < p.blocks && qtile_of(s) < p.q_tiles; };
 
     // a softmax thread's row: its keys, and whether there is such a row
@@ -188,7 +189,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         t0 = lo + split * per;
         t1 = max(t0, min(hi, t0 + per));
     }
-    auto active = [&](int s, int t) { return s == 0 ? t >= ta.x && t < ta.y : t >= tb.x && t < tb.y; };
+    auto active = [&](int s, int t) {
+        return (s == 0 ? t >= ta.x && t < ta.y : t >= tb.x && t < tb.y) && !(p.dual && ((t - t0) & 1) != s);
+    };
     // a value tile is checked when some row of an active tile does not see all of its keys
     auto checked = [&](int t) {
         const int j0 = t * kBlockK;
@@ -251,27 +254,54 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 tc_commit(base + L::bar_s + 8 * s);
                 ++issued;
             };
-            for (int t = t0 - 1; ok && t < t1; ++t) {
+            auto values = [&](int s, int st) {
+                const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + st * L::kTile, kBlockK * 128);
+#pragma unroll
+                for (int kk = 0; kk < kBlockK / 16; ++kk)
+                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi, id_o,
+                                     (n_p[s] | kk) != 0);
+                ++n_p[s];
+            };
+            auto landed = [&](int n) { return mbar_wait(base + L::bar_full + 8 * (n % NST), (n / NST) & 1, wc, kErrWaitK); };
+            if (p.dual) {  // the tile's rows twice: every second key tile each
+                for (int s = 0; ok && s < 2 && t0 + s < t1; ++s) {
+                    if (!(ok = mbar_wait(base + L::bar_q + 8 * s, 0, wc, kErrWaitQ) && landed(2 * s))) break;
+                    tc_fence_after();
+                    scores(s, t0 + s);
+                    tc_commit(base + L::bar_empty + 8 * (2 * s % NST));
+                }
+                for (int t = t0; ok && t < t1; ++t) {
+                    const int s = (t - t0) & 1, nv = 2 * (t - t0) + 1, nk = nv + 3;
+                    if (!(ok = landed(nv) && mbar_wait(base + L::bar_p + 8 * s, n_p[s] & 1, wc, kErrWaitS))) break;
+                    tc_fence_after();
+                    values(s, nv % NST);
+                    tc_commit(base + L::bar_empty + 8 * (nv % NST));
+                    if (t + 2 >= t1) {
+                        tc_commit(base + L::bar_o + 8 * s);
+                        continue;
+                    }
+                    if (!(ok = landed(nk))) break;
+                    tc_fence_after();
+                    scores(s, t + 2);
+                    tc_commit(base + L::bar_empty + 8 * (nk % NST));
+                }
+            }
+            for (int t = t0 - 1; ok && !p.dual && t < t1; ++t) {
                 const int nv = 2 * (t - t0) + 1, nk = nv + 1;  // ring positions of V(t) and K(t + 1)
                 bool have_v = false, have_k = false;
                 for (int s = 0; ok && s < 2; ++s) {
                     if (t >= t0 && active(s, t)) {
-                        if (!have_v && !(ok = mbar_wait(base + L::bar_full + 8 * (nv % NST), (nv / NST) & 1, wc, kErrWaitK))) break;
+                        if (!have_v && !(ok = landed(nv))) break;
                         have_v = true;
                         if (!(ok = mbar_wait(base + L::bar_p + 8 * s, n_p[s] & 1, wc, kErrWaitS))) break;
                         tc_fence_after();
-                        const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + (nv % NST) * L::kTile, kBlockK * 128);
-#pragma unroll
-                        for (int kk = 0; kk < kBlockK / 16; ++kk)
-                            tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi, id_o,
-                                             (n_p[s] | kk) != 0);
-                        ++n_p[s];
+                        values(s, nv % NST);
                         if (t + 1 == t1 || !active(s, t + 1)) tc_commit(base + L::bar_o + 8 * s);
                     }
                     if (t + 1 < t1 && active(s, t + 1)) {
                         if (t + 1 == t0 || !active(s, t))
                             if (!(ok = mbar_wait(base + L::bar_q + 8 * s, 0, wc, kErrWaitQ))) break;
-                        if (!have_k && !(ok = mbar_wait(base + L::bar_full + 8 * (nk % NST), (nk / NST) & 1, wc, kErrWaitK))) break;
+                        if (!have_k && !(ok = landed(nk))) break;
                         have_k = true;
                         tc_fence_after();
                         scores(s, t + 1);
@@ -279,8 +309,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 if (!ok) break;
                 // tiles between two separate ranges are read by no MMA: their copies have to land first
-                if (t >= t0 && !have_v && !(ok = mbar_wait(base + L::bar_full + 8 * (nv % NST), (nv / NST) & 1, wc, kErrWaitK))) break;
-                if (t + 1 < t1 && !have_k && !(ok = mbar_wait(base + L::bar_full + 8 * (nk % NST), (nk / NST) & 1, wc, kErrWaitK))) break;
+                if (t >= t0 && !have_v && !(ok = landed(nv))) break;
+                if (t + 1 < t1 && !have_k && !(ok = landed(nk))) break;
                 if (t >= t0) tc_commit(base + L::bar_empty + 8 * (nv % NST));
                 if (t + 1 < t1) tc_commit(base + L::bar_empty + 8 * (nk % NST));
             }
@@ -417,7 +447,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         float l = (la.x + la.y) + (lb.x + lb.y);
         if (fail || broken) l = nan;
         const bool empty = range.x >= range.y;
-        if (p.num_splits == 1) {
+        if (p.parts == 1) {
             const float inv = empty ? 0.f : 1.f / l;
             uint8_t* out = static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
 #pragma unroll 1
@@ -443,7 +473,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             }
             if (valid) p.LSE[flat] = empty ? -INFINITY : fmaf(ref, kLn2, logf(l));
         } else {
-            const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq, at_row = split * R + flat;
+            const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq, at_row = (p.dual ? 2 * split + sub : split) * R + flat;
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
                 float v[32];
@@ -481,13 +511,13 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
     const int i = static_cast<int>(row % p.Nq), h = static_cast<int>(row / p.Nq % p.H), b = static_cast<int>(row / p.Nq / p.H);
     const int2 range = row_range(sp, p.Nq, p.Nk, b, i);
     float m = -INFINITY;
-    for (int s = lane; s < p.num_splits; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
+    for (int s = lane; s < p.parts; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f, v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
-    for (int s = 0; s < p.num_splits; ++s) {
+    for (int s = 0; s < p.parts; ++s) {
         const float2 ml = p.part_ml[s * R + row];
         if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this split's keys are hidden from the row
         const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
@@ -516,11 +546,12 @@ cudaError_t launch_attn_d(const CUtensorMap* m, const AttnFwdParams& p, const Sc
     constexpr int bytes = AttnSmem<D>::alloc;
     static_assert(bytes <= 232448, "shared memory");
     auto k = attn_fwd_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k, bytes, &done);
     if (e != cudaSuccess) return e;
     k<<<ctas, kAfThreads, bytes, st>>>(m[0], m[1], m[2], p, sp);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.num_splits == 1) return e;
+    if (e != cudaSuccess || p.parts == 1) return e;
     const int64_t rows = int64_t(p.B) * p.H * p.Nq;
     attn_combine_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(p, sp);
     return cudaGetLastError();

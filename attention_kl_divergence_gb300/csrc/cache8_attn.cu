@@ -21,6 +21,7 @@
 #include "bwd_common.cuh"
 #include "cache8.cuh"
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "score.cuh"
@@ -599,7 +600,8 @@ cudaError_t launch_cache8_attn_d(const CUtensorMap* maps, const CacheAttnParams&
     constexpr int bytes = ring + 2 * S::kThreads * static_cast<int>(sizeof(PageEntry)) + 8 * kCwStages * S::kWarps + 1024;
     static_assert(bytes <= 232448, "shared memory");
     auto k = cache8_attn_kernel<D, NQ, SHARED>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k, bytes, &done);
     if (e != cudaSuccess) return e;
     k<<<ctas, S::kThreads, bytes, stream>>>(maps[0], maps[1], p);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.spread) return e;

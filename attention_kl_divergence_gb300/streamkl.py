@@ -526,6 +526,15 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _own_scratch(workspace, nbytes, device):
+    """(address, bytes, tensor to keep until the call returns) for calls that need none where nothing but the error word
+    would stand there."""
+    if workspace is None and nbytes <= 256:
+        return None, 0, None
+    workspace = _scratch(workspace, nbytes, device)
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
 def _scratch(workspace, nbytes, device):
     """A caller's workspace, checked, or a new one.  A new one is not cleared: its error word is never read (the score
     kernels mark with NaN what a give-up leaves undone; the norm's wait for nothing)."""
@@ -1003,11 +1012,11 @@ def attn_fwd(Q, K, V, ranges=None, causal=False, scale=None, rest=False, out=Non
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)
     left = torch.empty(shape, dtype=torch.bfloat16, device=device) if rest else None
     LSE = torch.empty(shape[:3], dtype=torch.float32, device=device)
-    workspace = _scratch(workspace, nbytes, device)
+    at, size, _keep = _own_scratch(workspace, nbytes, device)
     begin, end, offset = given if len(given) == 3 else (None, None, None)
     _raise(_on(device, load().streamkl_attn_fwd, desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _address(begin),
                _address(end), _address(offset), 0.0 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
-               _address(left), LSE.data_ptr(), workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_fwd")
+               _address(left), LSE.data_ptr(), at, size, opts), "streamkl_attn_fwd")
     return (out, LSE, left) if rest else (out, LSE)
 
 
@@ -1228,8 +1237,8 @@ def attn_cache8(Q, cache, table, lengths, scale=None, out=None, num_splits=0, wo
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)
     LSE = torch.empty(shape[:3], dtype=torch.float32, device=device)
-    workspace = _scratch(workspace, nbytes, device)
+    at, size, _keep = _own_scratch(workspace, nbytes, device)
     _raise(_on(device, load().streamkl_attn_cache8, desc, Q.data_ptr(), *[t.data_ptr() for t in held], table.data_ptr(),
-               lengths.data_ptr(), 0.0 if scale is None else float(scale), out.data_ptr(), LSE.data_ptr(),
-               workspace.data_ptr(), workspace.numel(), opts), "streamkl_attn_cache8")
+               lengths.data_ptr(), 0.0 if scale is None else float(scale), out.data_ptr(), LSE.data_ptr(), at, size, opts),
+           "streamkl_attn_cache8")
     return out, LSE

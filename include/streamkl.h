@@ -422,6 +422,8 @@ STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t
  *    outputs are float32 until their one rounding.
  *  - Equal inputs give equal bits.  A give-up of a bounded wait leaves NaN in
  *    the rows that it left unfinished.
+ *  - workspace may be NULL for a forward whose plan has 256 bytes (one split):
+ *    nothing but the error word would stand there.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------- */
 typedef struct {
@@ -482,7 +484,8 @@ STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const 
  * row that sees no key has O = 0 and LSE = -inf; a row that sees a page that is
  * not there, or a sequence longer than its table, is NaN, and so are rows that a
  * give-up of a bounded wait left unfinished.  opt->num_splits: CTAs that share out
- * the keys of all sequences (0 = automatic).  Equal inputs give equal bits.
+ * the keys of all sequences (0 = automatic).  workspace may be NULL where the plan
+ * has 256 bytes.  Equal inputs give equal bits.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------- */
 typedef struct {

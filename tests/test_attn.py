@@ -158,6 +158,19 @@ def test_gradients(shape, kind):
     assert torch.equal(again[1], grads[1]) and torch.equal(again[2], grads[2])
 
 
+@gpu
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 64])
+@pytest.mark.parametrize("shape", [(2, 8, 2, 1, 5000, 128), (1, 3, 3, 40, 1500, 64), (2, 4, 2, 130, 1100, 128), (1, 6, 2, 7, 1025, 64)], ids=str)
+def test_forward_with_split_keys(shape, splits):
+    Q, K, V = inputs(*shape)
+    for kind in ("causal", "padded", "two ends"):
+        ranges = masks(kind, shape[0], *shape[3:5])
+        ref = Ref(Q, K, V, ranges)
+        O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True, num_splits=splits)
+        ref.check(O, LSE)
+        assert bool(((O.double() + rest.double() - ref.O).abs() <= ref.o_tol - (2.0 ** -8 - 2.0 ** -16) * ref.O.abs()).all())
+
+
 def dirty(t, hidden, value):
     """t with `value` in the rows of [B, h, N, d] that `hidden` [B, N] marks."""
     t = t.clone()

@@ -454,4 +454,3 @@ def test_abi_rejects_bad_descriptions_and_pointers_without_a_device():
             assert call(desc(), tuple((258 if k in small else 264) if k == e else 256 for e in range(count))) == sk.ERR_INVALID_ARG
     for k in range(9):
         assert attn(desc(), tuple(0 if k == e else 256 for e in range(9))) == sk.ERR_INVALID_ARG
-    assert attn(desc(), ws=0) == sk.ERR_WORKSPACE and attn(desc(), ws=8) == sk.ERR_WORKSPACE
