@@ -8,12 +8,12 @@
 // tensor memory, dQ is added to float32 in L2 by bulk reductions.  Row constants
 // and key ranges are prepared by a first kernel.
 //
-// P enters dV, and dS enters dK, rounded to bf16; dS enters dQ as two bf16 terms.
-// A row's dS sum to zero, and so what its keys have in common cancels in dQ; one
-// term's roundings (2^-8 of each dS) do not.  The MMA that takes both terms as one
-// operand of twice the columns takes as long as with one.  D is a product with O
-// and what its rounding left (`rest`), for the same reason: an error of D is a
-// multiple of the row's mean key in dQ.
+// P enters dV rounded to bf16; dS enters dQ and dK as two bf16 terms.  A row's dS sum
+// to zero, and so what its keys have in common cancels in dQ; one term's roundings
+// (2^-8 of each dS) do not.  For dQ the MMA that takes both terms as one operand of
+// twice the columns takes as long as with one.  D is a product with O and what its
+// rounding left (`rest`), for the same reason: an error of D is a multiple of the
+// row's mean key in dQ.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -371,8 +371,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     for (int kk = 0; kk < kBwdTile / 16; ++kk)
                         tc_mma_bf16_w(t_dv, p_lo + ((kk * 32) >> 4), dhi, g_lo + ((kk * 16 * 128) >> 4), dhi, id_dk, (kk | m) != 0);
 #pragma unroll
-                    for (int kk = 0; kk < kBwdTile / 16; ++kk)
-                        tc_mma_bf16_w(t_dk, ds_lo + ((kk * 32) >> 4), dhi, q_lo + ((kk * 16 * 128) >> 4), dhi, id_dk, (kk | m) != 0);
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < kBwdTile / 16; ++kk)
+                            tc_mma_bf16_w(t_dk, ds_lo + ((part * L::kDsBytes + kk * 32) >> 4), dhi, q_lo + ((kk * 16 * 128) >> 4), dhi, id_dk,
+                                          (kk | part | m) != 0);
                     ++issued;
                     if (!mbar_wait(base + L::bar_dqempty, (m & 1) ^ 1, wc, kErrWaitOther)) break;
                     tc_fence_after();

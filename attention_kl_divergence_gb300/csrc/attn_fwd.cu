@@ -2,7 +2,10 @@
 //
 //   O_i = sum_j 2^(x_ij - m_i) v_j / l_i,  l_i = sum_j 2^(x_ij - m_i),  x = log2(e) scale q k
 //
-// over the keys of row i's range, one pass over the keys.  m_i is a whole number
+// over the keys of row i's range, one pass over the keys.  The probabilities enter
+// the product with V as one bf16 term, or, where the backward is to follow (`rest` is
+// asked for), as two: the backward's row sums of dO O take O as that of exact
+// probabilities, and an error of theirs is a multiple of the row's mean key in dQ.  m_i is a whole number
 // near the running maximum (at most 2^8 below it): every rescale is by a power of
 // two, exact in the sums, in O and in probabilities already rounded to bf16.
 #include "attn.cuh"
@@ -48,9 +51,14 @@ __device__ __forceinline__ int2 tiles_of(int4 span) {
     return span.x < span.y ? make_int2(span.x / kBlockK, (span.y + kBlockK - 1) / kBlockK) : make_int2(0, 0);
 }
 
-// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs; their float32 sum is added to la, lb.
-__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, uint32_t (&w)[16]) {
-    const float2 cc = splat(c), nr = splat(-ref);
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+
+// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their float32
+// sum is added to la, lb; with one term the sum of the rounded ones to ra, rb.
+template <int TERMS>
+__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, float2& ra, float2& rb,
+                                          uint32_t (&w)[16], uint32_t (&less)[16]) {
+    const float2 cc = splat(c), nr = splat(-ref), minus = splat(-1.f);
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
         const float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), cc, nr), b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), cc, nr);
@@ -59,6 +67,15 @@ __device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float r
         lb = __fadd2_rn(lb, pb);
         w[e / 2] = pack_bf16(pa.x, pa.y);
         w[e / 2 + 1] = pack_bf16(pb.x, pb.y);
+        const float2 qa = unpack_bf16(w[e / 2]), qb = unpack_bf16(w[e / 2 + 1]);
+        if (TERMS == 2) {
+            const float2 da = __ffma2_rn(qa, minus, pa), db = __ffma2_rn(qb, minus, pb);
+            less[e / 2] = pack_bf16(da.x, da.y);
+            less[e / 2 + 1] = pack_bf16(db.x, db.y);
+        } else {
+            ra = __fadd2_rn(ra, qa);
+            rb = __fadd2_rn(rb, qb);
+        }
     }
 }
 
@@ -72,9 +89,10 @@ __device__ __forceinline__ float max_chunk(const float (&z)[32]) {
     return fmaxf(a, b);
 }
 
-// O (d columns at t_o) and the tile's probabilities in front of chunk `ch` times f.
+// O (d columns at t_o) and the tile's stored probabilities, `chunks` of 16 columns, times f.
 template <int D>
-__device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int ch, float f) {
+__device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int chunks, float f) {
+    tc_wait_st();  // the chunks are there
     if (has_o) {
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
@@ -87,7 +105,7 @@ __device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int
         }
     }
 #pragma unroll 1
-    for (int k = 0; k < ch; ++k) {
+    for (int k = 0; k < chunks; ++k) {
         float v[16];
         tmem_ld16(t_p + 16 * k, v);
         tc_wait_ld();
@@ -104,7 +122,7 @@ __device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int
 
 }  // namespace
 
-template <int D>
+template <int D, int TERMS>
 __global__ void __launch_bounds__(kAfThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
                     const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnFwdParams p,
@@ -257,8 +275,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto values = [&](int s, int st) {
                 const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + st * L::kTile, kBlockK * 128);
 #pragma unroll
-                for (int kk = 0; kk < kBlockK / 16; ++kk)
-                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi, id_o,
+                for (int kk = 0; kk < TERMS * kBlockK / 16; ++kk)
+                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + (((kk & 7) * 16 * 128) >> 4), dhi, id_o,
                                      (n_p[s] | kk) != 0);
                 ++n_p[s];
             };
@@ -371,7 +389,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const uint32_t t_s = tl + sub * 128, t_o = tl + 256 + sub * 128;
         const float c = p.c;
         float ref = -INFINITY;  // m
-        float2 la = splat(0.f), lb = splat(0.f);
+        float2 la = splat(0.f), lb = splat(0.f), ra = splat(0.f), rb = splat(0.f);
         bool broken = false;
         bool ok = true;
         int n = 0, k_check = 0;
@@ -403,13 +421,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 __syncwarp();
             }
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
+            // Chunk ch of the scores becomes chunk ch of the probabilities, 16 columns, in the scores' place.  The second
+            // terms, chunks 4 to 7, take the place of scores that are read later: those of chunks 0 and 1 wait.
+            uint32_t held[2][16];
+            auto chunk = [&](int ch, uint32_t (&less)[16]) {
                 uint32_t w[16];
                 const int c0 = j0 + 32 * ch;
                 if (c0 >= mine.y || c0 + 32 <= mine.x) {  // no row of the warp sees any of these keys
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = 0u;
+                    for (int e = 0; e < 16; ++e) w[e] = less[e] = 0u;
                 } else {
                     float z[32];
                     tmem_ld32(t_s + 32 * ch, z);
@@ -426,12 +446,41 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         const float next = raise ? ceilf(top) : ref, f = raise ? ex2(ref - next) : 1.f;
                         la = __fmul2_rn(la, splat(f));
                         lb = __fmul2_rn(lb, splat(f));
+                        ra = __fmul2_rn(ra, splat(f));
+                        rb = __fmul2_rn(rb, splat(f));
                         ref = next;
                         if (n > 0 || ch > 0) rescale<D>(t_o, n > 0, t_s, ch, f);
+                        if (TERMS == 2 && ch > 0) {  // a power of two: exact
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 x = unpack_bf16(held[0][e]), y = unpack_bf16(held[1][e]);
+                                held[0][e] = pack_bf16(x.x * f, x.y * f);
+                                held[1][e] = pack_bf16(y.x * f, y.y * f);
+                            }
+                            if (ch == 3) rescale<D>(t_o, false, t_s + 64, 2, f);
+                        }
                     }
-                    exp_chunk(z, c, ref == -INFINITY ? 0.f : ref, la, lb, w);
+                    exp_chunk<TERMS>(z, c, ref == -INFINITY ? 0.f : ref, la, lb, ra, rb, w, less);
                 }
                 tmem_st16(t_s + 16 * ch, w);
+            };
+            if (TERMS == 1) {
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) chunk(ch, held[0]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) held[1][e] = 0u;
+                chunk(0, held[0]);
+                chunk(1, held[1]);
+                uint32_t less[16];
+                chunk(2, less);
+                tmem_st16(t_s + 64, held[0]);
+                tmem_st16(t_s + 80, held[1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) held[0][e] = less[e];
+                chunk(3, less);
+                tmem_st16(t_s + 96, held[0]);
+                tmem_st16(t_s + 112, less);
             }
             tc_wait_st();
             tc_fence_before();
@@ -444,11 +493,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const bool fail = __any_sync(0xffffffffu, !ok || *abort_flag);
         const int h = hk * p.group + block_of(sub) * p.heads + in_block;
         const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
-        float l = (la.x + la.y) + (lb.x + lb.y);
-        if (fail || broken) l = nan;
+        // With one term O is divided by the sum of the rounded probabilities: what their roundings have in common, such
+        // as the only key's, cancels.
+        float l = (la.x + la.y) + (lb.x + lb.y), lo = TERMS == 1 ? (ra.x + ra.y) + (rb.x + rb.y) : l;
+        if (fail || broken) l = lo = nan;
         const bool empty = range.x >= range.y;
         if (p.parts == 1) {
-            const float inv = empty ? 0.f : 1.f / l;
+            const float inv = empty ? 0.f : 1.f / lo;
             uint8_t* out = static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
@@ -487,7 +538,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 if (valid) store_grad32(p.part + at_row * D, k, v, 1.f, false);
                 __syncwarp();
             }
-            if (valid) p.part_ml[at_row] = make_float2(ref, l);
+            if (valid) p.part_ml[at_row] = make_float4(ref, l, lo, 0.f);
         }
     }
 
@@ -514,20 +565,21 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
     for (int s = lane; s < p.parts; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, v[V];
+    float l = 0.f, lo = 0.f, v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
     for (int s = 0; s < p.parts; ++s) {
-        const float2 ml = p.part_ml[s * R + row];
+        const float4 ml = p.part_ml[s * R + row];
         if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this split's keys are hidden from the row
         const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         l = fmaf(ml.y, f, l);
+        lo = fmaf(ml.z, f, lo);
         const float* part = p.part + (s * R + row) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
     }
     const bool empty = range.x >= range.y;
-    const float inv = empty ? 0.f : 1.f / l;
+    const float inv = empty ? 0.f : 1.f / lo;
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + i * p.o_n) + lane * V);
     uint32_t* rest = p.rest ? reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.rest) + row * D + lane * V) : nullptr;
 #pragma unroll
@@ -541,11 +593,11 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
 }
 
 namespace {
-template <int D>
+template <int D, int TERMS>
 cudaError_t launch_attn_d(const CUtensorMap* m, const AttnFwdParams& p, const ScoreParams& sp, int ctas, cudaStream_t st) {
     constexpr int bytes = AttnSmem<D>::alloc;
     static_assert(bytes <= 232448, "shared memory");
-    auto k = attn_fwd_kernel<D>;
+    auto k = attn_fwd_kernel<D, TERMS>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(k, bytes, &done);
     if (e != cudaSuccess) return e;
@@ -560,7 +612,9 @@ cudaError_t launch_attn_d(const CUtensorMap* m, const AttnFwdParams& p, const Sc
 
 cudaError_t launch_attn_fwd(int d, const CUtensorMap* maps, const AttnFwdParams& p, const ScoreParams& sp, int ctas,
                             cudaStream_t stream) {
-    return d == 128 ? launch_attn_d<128>(maps, p, sp, ctas, stream) : launch_attn_d<64>(maps, p, sp, ctas, stream);
+    if (p.rest)  // for training: see the second term's use above
+        return d == 128 ? launch_attn_d<128, 2>(maps, p, sp, ctas, stream) : launch_attn_d<64, 2>(maps, p, sp, ctas, stream);
+    return d == 128 ? launch_attn_d<128, 1>(maps, p, sp, ctas, stream) : launch_attn_d<64, 1>(maps, p, sp, ctas, stream);
 }
 
 }  // namespace streamkl

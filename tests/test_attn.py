@@ -7,14 +7,16 @@ the visible pairs a score is off by  del = (d + 32) 2^-24 A + 2^-20 (M + 1).
 LSE is off by at most del + N 2^-24 (the sum of up to N terms) + its rounding.
 A probability enters the product with V rounded to bf16 (2^-8 of it) from a
 value off by a factor 1 +- 2 del, the product accumulates in float32, and O is
-rounded once:  (2^-8 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|.
+rounded once:  (2^-7 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|, where the sum
+of rounded probabilities that O is divided by counts 2^-8 too.  With `rest` they are
+two bf16 terms, off by 2^-16, and O + rest is off by
+(2^-16 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-16 |O|.
 
 Gradients.  P is off by a factor 1 +- 2 del and enters dV rounded (2^-8 of it).
 dP is a float32 sum, off by (d + 32) 2^-24 of |dO| |V|^T; D is a float32 sum of
-products with O + rest, which is off from O by o_tol - 2^-8 |O| + 2^-16 |O|
-(o_tol's first part).  dS = P (dP - D) takes its share of all of these; it
-enters dK rounded to bf16 (2^-8) and dQ as two terms (2^-16), sums are float32
-((N + 128) 2^-24 of the magnitudes), outputs are rounded once (2^-8).
+products with O + rest.  dS = P (dP - D) takes its share of all of these; it
+enters dQ and dK as two terms (2^-16), sums are float32 ((N + 128) 2^-24 of the
+magnitudes), outputs are rounded once (2^-8).
 """
 import math
 
@@ -62,7 +64,9 @@ class Ref:
         A = big(self.q.abs() @ self.k.abs().transpose(2, 3)) * self.scale
         self.delta = (d + 32) * 2.0 ** -24 * A + 2.0 ** -20 * (big(s) + 1)
         self.acc = (Nk + 128) * 2.0 ** -24
-        self.o_tol = (2.0 ** -8 + 4 * self.delta + self.acc) * (self.p @ v.abs()) + 2.0 ** -8 * self.O.abs() + 1e-30
+        mag = self.p @ v.abs()
+        self.o_tol = (2.0 ** -7 + 4 * self.delta + self.acc) * mag + 2.0 ** -8 * self.O.abs() + 1e-30
+        self.two_terms = (2.0 ** -16 + 4 * self.delta + self.acc) * mag + 2.0 ** -16 * self.O.abs() + 1e-30
 
     def check_grads(self, dO, dQ, dK, dV):
         B, H, Nq, d = self.q.shape
@@ -72,13 +76,13 @@ class Ref:
         mag = g.abs() @ self.v.abs().transpose(2, 3)
         dP = g @ self.v.transpose(2, 3)
         D = (g * self.O).sum(-1, keepdim=True)
-        d_err = ((self.o_tol - 2.0 ** -8 * self.O.abs() + (2.0 ** -16 + (d + 32) * 2.0 ** -24) * self.O.abs()) * g.abs()).sum(-1, keepdim=True)
+        d_err = ((self.two_terms + (d + 32) * 2.0 ** -24 * self.O.abs()) * g.abs()).sum(-1, keepdim=True)
         dS = self.p * (dP - D) * self.scale
         err = self.p * self.scale * (2 * self.delta * (dP - D).abs() + (d + 32) * 2.0 ** -24 * mag + d_err)
         acc = 2.0 ** -24 * (max(Nk, Nq * self.G) + 128)
         want = dS @ self.k, back(dS.transpose(2, 3) @ self.q), back(self.p.transpose(2, 3) @ g)
         tol = ((err + (2.0 ** -16 + acc) * dS.abs()) @ self.k.abs(),
-               back((err + (2.0 ** -8 + acc) * dS.abs()).transpose(2, 3) @ self.q.abs()),
+               back((err + (2.0 ** -16 + acc) * dS.abs()).transpose(2, 3) @ self.q.abs()),
                back((self.p * (2.0 ** -8 + 2 * self.delta + acc)).transpose(2, 3) @ g.abs()))
         for name, got, w, t in zip(("dQ", "dK", "dV"), (dQ, dK, dV), want, tol):
             bound = t * 1.01 + 2.0 ** -8 * w.abs() + 1e-30  # 1.01: products of the terms above
@@ -136,11 +140,17 @@ def test_forward(shape, kind):
     O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True)
     ref = Ref(Q, K, V, ranges)
     ref.check(O, LSE)
-    # the rest is what the rounding left: O + rest has 16 bits
     err = (O.double() + rest.double() - ref.O).abs()
-    assert bool((err <= ref.o_tol - 2.0 ** -8 * ref.O.abs() + 2.0 ** -16 * ref.O.abs()).all())
-    again = sk.attn_fwd(Q, K, V, ranges=ranges)
-    assert torch.equal(again[0], O) and torch.equal(again[1], LSE)
+    assert bool((err <= ref.two_terms).all()), float((err / ref.two_terms).max())
+    plain = sk.attn_fwd(Q, K, V, ranges=ranges)
+    ref.check(*plain)
+    for got in (sk.attn_fwd(Q, K, V, ranges=ranges, rest=True), sk.attn_fwd(Q, K, V, ranges=ranges) + (None,)):
+        want = (O, LSE, rest) if got[2] is not None else plain
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # a row with one key alone has its value, bit for bit
+    one = (ref.vis.sum(-1) == 1).expand_as(LSE)
+    rows = torch.where(one[..., None], ref.O, 0.0)
+    assert torch.equal(torch.where(one[..., None], plain[0].double(), 0.0), rows)
 
 
 @gpu
@@ -168,7 +178,8 @@ def test_forward_with_split_keys(shape, splits):
         ref = Ref(Q, K, V, ranges)
         O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True, num_splits=splits)
         ref.check(O, LSE)
-        assert bool(((O.double() + rest.double() - ref.O).abs() <= ref.o_tol - (2.0 ** -8 - 2.0 ** -16) * ref.O.abs()).all())
+        assert bool(((O.double() + rest.double() - ref.O).abs() <= ref.two_terms).all())
+        ref.check(*sk.attn_fwd(Q, K, V, ranges=ranges, num_splits=splits))
 
 
 def dirty(t, hidden, value):
@@ -228,3 +239,39 @@ def test_a_broken_token_reaches_those_who_see_it_alone(shape, which):
     seen = row <= at if which in ("Q", "dO") else row >= 0
     assert bool(dK[:, :, seen].isnan().any(-1).all())
     assert torch.equal(dK[:, :, ~seen], clean[1][:, :, ~seen]) and torch.equal(dV[:, :, ~seen], clean[2][:, :, ~seen])
+
+
+@gpu
+@pytest.mark.parametrize("splits", [1, 2, 5])
+@pytest.mark.parametrize("shape", [(1, 8, 2, 300, 300, 128), (2, 3, 1, 129, 1000, 64), (1, 2, 2, 700, 260, 128)], ids=str)
+def test_gradients_with_shared_key_tiles(shape, splits):
+    B, H, Hk, Nq, Nk, d = shape
+    Q, K, V = inputs(*shape)
+    dO = torch.randn((B, H, Nq, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).to(BF16)
+    for kind in ("full", "two ends") + (("causal",) if Nq <= Nk else ()):
+        ranges = masks(kind, B, Nq, Nk)
+        O, LSE, rest = sk.attn_fwd(Q, K, V, ranges=ranges, rest=True)
+        Ref(Q, K, V, ranges).check_grads(dO, *sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges, num_splits=splits))
+
+
+@gpu
+@pytest.mark.parametrize("peak", [0.3, 2.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_keys_and_values_with_a_common_offset(d, peak):
+    """What a row's keys have in common cancels in dQ, and what its values have in common in D: neither the roundings of
+    probabilities nor those of dS may show there.  The bound is the outputs' own rounding (2^-8 / sqrt 3 of the norm at
+    most) and a third of it for everything else."""
+    Q, K, V = inputs(1, 4, 2, 500, 500, d, peak=peak)
+    K[..., : d // 8] += 16.0
+    V += 4.0
+    dO = torch.randn((1, 4, 500, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).to(BF16)
+    O, LSE, rest = sk.attn_fwd(Q, K, V, causal=True, rest=True)
+    got = sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, causal=True)
+    leaves = [t.double().requires_grad_() for t in (Q, K, V)]
+    s = leaves[0] @ leaves[1].repeat_interleave(2, 1).transpose(2, 3) * d ** -0.5
+    s = s.masked_fill(torch.ones(500, 500, device=DEV).triu(1).bool(), -math.inf)
+    out = torch.softmax(s, -1) @ leaves[2].repeat_interleave(2, 1)
+    want = torch.autograd.grad((out * dO.double()).sum(), leaves)
+    for name, a, b in list(zip(("dQ", "dK"), got, want)):
+        err = float((a.double() - b).norm() / b.norm())
+        assert err <= 2.0 ** -8 / 3 ** 0.5 * 4 / 3, (name, err)
