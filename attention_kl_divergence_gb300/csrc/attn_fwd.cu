@@ -53,25 +53,26 @@ __device__ __forceinline__ int2 tiles_of(int4 span) {
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their float32
-// sum is added to la, lb; with one term the sum of the rounded ones to ra, rb.
-template <int TERMS>
-__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, float2& ra, float2& rb,
-                                          uint32_t (&w)[16], uint32_t (&less)[16]) {
+// 2^(z c - ref) of 32 of the scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their
+// float32 sums are added to la, lb; with one term those of the rounded ones to ra, rb.
+template <int TERMS, int FROM>
+__device__ __forceinline__ void exp_quarter(const float (&z)[64], float c, float ref, float2& la, float2& lb, float2& ra, float2& rb,
+                                            uint32_t (&w)[16], uint32_t (&less)[16]) {
     const float2 cc = splat(c), nr = splat(-ref), minus = splat(-1.f);
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
+    for (int k = 0; k < 32; k += 4) {
+        const int e = FROM + k;
         const float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), cc, nr), b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), cc, nr);
         const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
         la = __fadd2_rn(la, pa);
         lb = __fadd2_rn(lb, pb);
-        w[e / 2] = pack_bf16(pa.x, pa.y);
-        w[e / 2 + 1] = pack_bf16(pb.x, pb.y);
-        const float2 qa = unpack_bf16(w[e / 2]), qb = unpack_bf16(w[e / 2 + 1]);
+        w[k / 2] = pack_bf16(pa.x, pa.y);
+        w[k / 2 + 1] = pack_bf16(pb.x, pb.y);
+        const float2 qa = unpack_bf16(w[k / 2]), qb = unpack_bf16(w[k / 2 + 1]);
         if (TERMS == 2) {
             const float2 da = __ffma2_rn(qa, minus, pa), db = __ffma2_rn(qb, minus, pb);
-            less[e / 2] = pack_bf16(da.x, da.y);
-            less[e / 2 + 1] = pack_bf16(db.x, db.y);
+            less[k / 2] = pack_bf16(da.x, da.y);
+            less[k / 2 + 1] = pack_bf16(db.x, db.y);
         } else {
             ra = __fadd2_rn(ra, qa);
             rb = __fadd2_rn(rb, qb);
@@ -79,14 +80,14 @@ __device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float r
     }
 }
 
-__device__ __forceinline__ float max_chunk(const float (&z)[32]) {
-    float a = -INFINITY, b = -INFINITY;
+__device__ __forceinline__ float max_half(const float (&z)[64]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        a = max3f(a, z[e], z[e + 1]);
-        b = max3f(b, z[e + 2], z[e + 3]);
+    for (int e = 0; e < 64; e += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = max3f(m[k], z[e + 2 * k], z[e + 2 * k + 1]);
     }
-    return fmaxf(a, b);
+    return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
 }
 
 // O (d columns at t_o) and the tile's stored probabilities, `chunks` of 16 columns, times f.
@@ -275,9 +276,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto values = [&](int s, int st) {
                 const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + st * L::kTile, kBlockK * 128);
 #pragma unroll
-                for (int kk = 0; kk < TERMS * kBlockK / 16; ++kk)
-                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, v_lo + (((kk & 7) * 16 * 128) >> 4), dhi, id_o,
-                                     (n_p[s] | kk) != 0);
+                for (int kk = 0; kk < TERMS * kBlockK / 16; ++kk)  // columns: see the softmax
+                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + (kk >> 3) * 32 + (kk >> 2 & 1) * 64 + (kk & 3) * 8,
+                                     v_lo + (((kk & 7) * 16 * 128) >> 4), dhi, id_o, (n_p[s] | kk) != 0);
                 ++n_p[s];
             };
             auto landed = [&](int n) { return mbar_wait(base + L::bar_full + 8 * (n % NST), (n / NST) & 1, wc, kErrWaitK); };
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const uint32_t t_s = tl + sub * 128, t_o = tl + 256 + sub * 128;
         const float c = p.c;
         float ref = -INFINITY;  // m
-        float2 la = splat(0.f), lb = splat(0.f), ra = splat(0.f), rb = splat(0.f);
+        float l = 0.f, lo = 0.f;  // sums of the probabilities, and of the rounded ones
         bool broken = false;
         bool ok = true;
         int n = 0, k_check = 0;
@@ -421,66 +422,56 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 __syncwarp();
             }
-            // Chunk ch of the scores becomes chunk ch of the probabilities, 16 columns, in the scores' place.  The second
-            // terms, chunks 4 to 7, take the place of scores that are read later: those of chunks 0 and 1 wait.
-            uint32_t held[2][16];
-            auto chunk = [&](int ch, uint32_t (&less)[16]) {
-                uint32_t w[16];
-                const int c0 = j0 + 32 * ch;
-                if (c0 >= mine.y || c0 + 32 <= mine.x) {  // no row of the warp sees any of these keys
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = less[e] = 0u;
-                } else {
-                    float z[32];
-                    tmem_ld32(t_s + 32 * ch, z);
-                    tc_wait_ld();
-                    if (!whole) {
-                        const int lo = first - 32 * ch, hi = last - 32 * ch;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e < lo || e > hi) z[e] = -INFINITY;
-                    }
-                    const float top = c * max_chunk(z);
-                    const bool raise = valid && top > ref + kAttnTau;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float next = raise ? ceilf(top) : ref, f = raise ? ex2(ref - next) : 1.f;
-                        la = __fmul2_rn(la, splat(f));
-                        lb = __fmul2_rn(lb, splat(f));
-                        ra = __fmul2_rn(ra, splat(f));
-                        rb = __fmul2_rn(rb, splat(f));
-                        ref = next;
-                        if (n > 0 || ch > 0) rescale<D>(t_o, n > 0, t_s, ch, f);
-                        if (TERMS == 2 && ch > 0) {  // a power of two: exact
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 x = unpack_bf16(held[0][e]), y = unpack_bf16(held[1][e]);
-                                held[0][e] = pack_bf16(x.x * f, x.y * f);
-                                held[1][e] = pack_bf16(y.x * f, y.y * f);
-                            }
-                            if (ch == 3) rescale<D>(t_o, false, t_s + 64, 2, f);
-                        }
-                    }
-                    exp_chunk<TERMS>(z, c, ref == -INFINITY ? 0.f : ref, la, lb, ra, rb, w, less);
-                }
-                tmem_st16(t_s + 16 * ch, w);
-            };
-            if (TERMS == 1) {
+            // Half hf of the scores, columns 64 hf .. 64 hf + 63, makes room for its probabilities: the (first) terms
+            // in the first 32 of these columns, the second terms in the others.
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) chunk(ch, held[0]);
-            } else {
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t t_h = t_s + 64 * hf;
+                const int c0 = j0 + 64 * hf;
+                if (c0 >= mine.y || c0 + 64 <= mine.x) {  // no row of the warp sees any of these keys
+                    uint32_t zeros[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) held[1][e] = 0u;
-                chunk(0, held[0]);
-                chunk(1, held[1]);
-                uint32_t less[16];
-                chunk(2, less);
-                tmem_st16(t_s + 64, held[0]);
-                tmem_st16(t_s + 80, held[1]);
+                    for (int e = 0; e < 16; ++e) zeros[e] = 0u;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) held[0][e] = less[e];
-                chunk(3, less);
-                tmem_st16(t_s + 96, held[0]);
-                tmem_st16(t_s + 112, less);
+                    for (int k = 0; k < 2 * TERMS; ++k) tmem_st16(t_h + 16 * k, zeros);
+                    continue;
+                }
+                float z[64];
+                tmem_ld32(t_h, *reinterpret_cast<float(*)[32]>(z));
+                tmem_ld32(t_h + 32, *reinterpret_cast<float(*)[32]>(z + 32));
+                tc_wait_ld();
+                if (!whole) {
+                    const int from = first - 64 * hf, to = last - 64 * hf;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (e < from || e > to) z[e] = -INFINITY;
+                }
+                // The exponentials do not wait for the maximum: where it turns out that m has to rise, which it seldom
+                // does after the first tiles, they are taken again.
+                float2 la, lb, ra, rb;
+                for (;;) {
+                    la = lb = ra = rb = splat(0.f);
+                    const float r = ref == -INFINITY ? 0.f : ref;
+                    {
+                        uint32_t w[16], less[16];
+                        exp_quarter<TERMS, 0>(z, c, r, la, lb, ra, rb, w, less);
+                        tmem_st16(t_h, w);
+                        if (TERMS == 2) tmem_st16(t_h + 32, less);
+                        exp_quarter<TERMS, 32>(z, c, r, la, lb, ra, rb, w, less);
+                        tmem_st16(t_h + 16, w);
+                        if (TERMS == 2) tmem_st16(t_h + 48, less);
+                    }
+                    const float top = c * max_half(z);
+                    const bool raise = valid && top > ref + kAttnTau;
+                    if (!__any_sync(0xffffffffu, raise)) break;
+                    const float next = raise ? ceilf(top) : ref, f = raise ? ex2(ref - next) : 1.f;
+                    l *= f;
+                    lo *= f;
+                    ref = next;
+                    if (n > 0 || hf > 0) rescale<D>(t_o, n > 0, t_s, 2 * TERMS * hf, f);
+                }
+                l += (la.x + la.y) + (lb.x + lb.y);
+                lo += (ra.x + ra.y) + (rb.x + rb.y);
             }
             tc_wait_st();
             tc_fence_before();
@@ -495,7 +486,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
         // With one term O is divided by the sum of the rounded probabilities: what their roundings have in common, such
         // as the only key's, cancels.
-        float l = (la.x + la.y) + (lb.x + lb.y), lo = TERMS == 1 ? (ra.x + ra.y) + (rb.x + rb.y) : l;
+        if (TERMS == 2) lo = l;
         if (fail || broken) l = lo = nan;
         const bool empty = range.x >= range.y;
         if (p.parts == 1) {
