@@ -107,7 +107,7 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
     pl->ctas = static_cast<int>(units * splits);
     p.order_group = order_group(heads, p.units_q, sms);
     pl->ws_bytes = kStatusBytes;
-    if (p.parts > 1) pl->ws_bytes += size_t(p.parts) * s->B * s->H * s->Nq * (size_t(s->d) + 4) * sizeof(float);
+    if (p.parts > 1) pl->ws_bytes += size_t(p.parts) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
     return STREAMKL_OK;
 }
 
@@ -200,7 +200,7 @@ streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const void* Q, cons
     p.LSE = LSE;
     if (p.parts > 1) {
         p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-        p.part_ml = reinterpret_cast<float4*>(p.part + size_t(p.parts) * s.B * s.H * s.Nq * s.d);
+        p.part_ml = reinterpret_cast<float2*>(p.part + size_t(p.parts) * s.B * s.H * s.Nq * s.d);
     }
     p.status = static_cast<unsigned int*>(workspace);
     p.wait_ns = static_cast<unsigned long long>(wait_limit(opt));

@@ -30,7 +30,7 @@ struct AttnFwdParams {
     void* rest;              // bf16 [B, H, Nq, d] or null: O before its rounding, less O
     float* LSE;              // [B, H, Nq]
     float* part;             // several parts: [parts][B*H*Nq][d] sums of 2^(x - m) v
-    float4* part_ml;         // [parts][B*H*Nq]: m (log2), the sum of 2^(x - m), that of the rounded ones
+    float2* part_ml;         // [parts][B*H*Nq]: m (log2) and the sum of 2^(x - m)
     unsigned int* status;
     unsigned long long wait_ns;
     int inject_stall;

@@ -5,9 +5,8 @@
 // over the keys of row i's range, one pass over the keys.  The probabilities enter
 // the product with V as one bf16 term, or, where the backward is to follow (`rest` is
 // asked for), as two: the backward's row sums of dO O take O as that of exact
-// probabilities, and an error of theirs is a multiple of the row's mean key in dQ.  m_i is a whole number
-// near the running maximum (at most 2^8 below it): every rescale is by a power of
-// two, exact in the sums, in O and in probabilities already rounded to bf16.
+// probabilities, and an error of theirs is a multiple of the row's mean key in dQ.  m_i is a
+// running maximum that may stay up to 2^8 behind.
 #include "attn.cuh"
 #include "bwd_common.cuh"
 #include "common.cuh"
@@ -21,9 +20,11 @@ namespace streamkl {
 namespace {
 
 constexpr float kAttnTau = 8.f;  // m may stay this far (log2) below the largest score
-// warps 0-7 softmax (a warpgroup per tile of the pair, a row per thread), 8 copies,
-// 9 MMAs, 10 and 11 look for NaN and infinities in values that some row must not see
-constexpr int kAfThreads = 384;
+// warps 0-15 softmax (two warpgroups per tile of the pair: a thread has half of a row's
+// scores), 16 copies, 17 MMAs, 18 and 19 look for NaN and infinities in values that some
+// row must not see.  One warpgroup per tile, a row per thread, left its latencies
+// bare: 32768 causal rows, 8 heads, 1912 us.
+constexpr int kAfThreads = 640;
 
 template <int D>
 struct AttnSmem {
@@ -42,8 +43,9 @@ struct AttnSmem {
     static constexpr int misc = bar_done + 8;               // tmem base, abort flag
     static constexpr int spans = (misc + 8 + 15) / 16 * 16; // [2] int4: union and common range of a tile's rows
     static constexpr int bad = spans + 32;                  // [kNst][4] keys whose values are not finite
-    static constexpr int total = bad + 16 * kNst;
-    static constexpr int alloc = total + 1024;              // slack for 1024-byte alignment
+    static constexpr int tops = bad + 16 * kNst;            // [2][2][128] maxima of the halves of the rows
+    static constexpr int alloc = tops + 2048;               // no slack: the kernel checks the base is 1024-byte aligned
+    static constexpr int sums = q;                          // [2][2][2][128] at the end, when the query tiles are done with
 };
 
 // The key tiles [lo, hi) of a range of keys.
@@ -53,70 +55,73 @@ __device__ __forceinline__ int2 tiles_of(int4 span) {
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// 2^(z c - ref) of 32 of the scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their
-// float32 sums are added to la, lb; with one term those of the rounded ones to ra, rb.
-template <int TERMS, int FROM>
-__device__ __forceinline__ void exp_quarter(const float (&z)[64], float c, float ref, float2& la, float2& lb, float2& ra, float2& rb,
-                                            uint32_t (&w)[16], uint32_t (&less)[16]) {
+// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their float32
+// sums are added to la, lb.
+template <int TERMS>
+__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, uint32_t (&w)[16],
+                                          uint32_t (&less)[16]) {
     const float2 cc = splat(c), nr = splat(-ref), minus = splat(-1.f);
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-        const int e = FROM + k;
+    for (int e = 0; e < 32; e += 4) {
         const float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), cc, nr), b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), cc, nr);
         const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
         la = __fadd2_rn(la, pa);
         lb = __fadd2_rn(lb, pb);
-        w[k / 2] = pack_bf16(pa.x, pa.y);
-        w[k / 2 + 1] = pack_bf16(pb.x, pb.y);
-        const float2 qa = unpack_bf16(w[k / 2]), qb = unpack_bf16(w[k / 2 + 1]);
+        w[e / 2] = pack_bf16(pa.x, pa.y);
+        w[e / 2 + 1] = pack_bf16(pb.x, pb.y);
         if (TERMS == 2) {
-            const float2 da = __ffma2_rn(qa, minus, pa), db = __ffma2_rn(qb, minus, pb);
-            less[k / 2] = pack_bf16(da.x, da.y);
-            less[k / 2 + 1] = pack_bf16(db.x, db.y);
-        } else {
-            ra = __fadd2_rn(ra, qa);
-            rb = __fadd2_rn(rb, qb);
+            const float2 da = __ffma2_rn(unpack_bf16(w[e / 2]), minus, pa), db = __ffma2_rn(unpack_bf16(w[e / 2 + 1]), minus, pb);
+            less[e / 2] = pack_bf16(da.x, da.y);
+            less[e / 2 + 1] = pack_bf16(db.x, db.y);
         }
     }
 }
 
-__device__ __forceinline__ float max_half(const float (&z)[64]) {
+__device__ __forceinline__ float max_chunk(const float (&z)[32]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 64; e += 8) {
+    for (int e = 0; e < 32; e += 8) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = max3f(m[k], z[e + 2 * k], z[e + 2 * k + 1]);
     }
     return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
 }
 
-// O (d columns at t_o) and the tile's stored probabilities, `chunks` of 16 columns, times f.
+// Hidden scores become -inf.
+__device__ __forceinline__ void hide_chunk(float (&z)[32], int first, int last) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e < first || e > last) z[e] = -INFINITY;
+}
+
 template <int D>
-__device__ __noinline__ void rescale(uint32_t t_o, bool has_o, uint32_t t_p, int chunks, float f) {
-    tc_wait_st();  // the chunks are there
-    if (has_o) {
-#pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
-            float v[32];
-            tmem_ld32(t_o + k, v);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= f;
-            tmem_st32(t_o + k, v);
-        }
+__device__ __noinline__ void mark_row(const AttnFwdParams& p, int split, int sub, int b, int h, int i) {
+    const float nan = __int_as_float(0x7fc00000);
+    const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq, flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
+    if (p.parts > 1) {
+        const size_t at = (p.dual ? 2 * split + sub : split) * R + flat;
+        p.part_ml[at] = make_float2(0.f, nan);
+        for (int k = 0; k < D; ++k) p.part[at * D + k] = nan;
+        return;
     }
+    uint16_t* out = static_cast<uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
+    for (int k = 0; k < D; ++k) {
+        out[k] = 0x7fc0;
+        if (p.rest) static_cast<uint16_t*>(p.rest)[flat * D + k] = 0x7fc0;
+    }
+    p.LSE[flat] = nan;
+}
+
+// n columns of O at t_o times f.
+__device__ __noinline__ void rescale(uint32_t t_o, int n, float f) {
 #pragma unroll 1
-    for (int k = 0; k < chunks; ++k) {
-        float v[16];
-        tmem_ld16(t_p + 16 * k, v);
+    for (int k = 0; k < n; k += 32) {
+        float v[32];
+        tmem_ld32(t_o + k, v);
         tc_wait_ld();
-        uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t u = __float_as_uint(v[e]);
-            w[e] = pack_bf16(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-        }
-        tmem_st16(t_p + 16 * k, w);
+        for (int e = 0; e < 32; ++e) v[e] *= f;
+        tmem_st32(t_o + k, v);
     }
     tc_wait_st();
 }
@@ -130,9 +135,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     const __grid_constant__ ScoreParams sp) {
     using L = AttnSmem<D>;
     constexpr int NST = L::kNst;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    uint8_t* gbase = smem_raw;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
     int4* spans = reinterpret_cast<int4*>(gbase + L::spans);
@@ -148,11 +153,16 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     auto qtile_of = [&](int s) { return p.pair_heads || p.dual ? qu : 2 * qu + s; };
     auto exists = [&](int s) { return block_of(s) < p.blocks && qtile_of(s) < p.q_tiles; };
 
-    // a softmax thread's row: its keys, and whether there is such a row
-    const int sub = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
+    // a softmax thread's row: its keys, and whether there is such a row; the thread has 64 of a tile's columns
+    const int sub = (warp >> 3) & 1, side = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
     const int in_block = row / p.rows, i = qtile_of(sub) * kBlockQ + row - in_block * p.rows;
-    const bool valid = warp < 8 && exists(sub) && in_block < p.heads && i < p.Nq;
+    const bool valid = warp < 16 && exists(sub) && in_block < p.heads && i < p.Nq;
     const int2 range = valid ? row_range(sp, p.Nq, p.Nk, b, i) : make_int2(0, 0);
+    if (base & 1023u) {  // reported, not expected: every row becomes NaN
+        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kErrSmemAlign);
+        if (valid && side == 0) mark_row<D>(p, split, sub, b, hk * p.group + block_of(sub) * p.heads + in_block, i);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tQ);
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(base + L::bar_q + 8 * s, 1);
             mbar_init(base + L::bar_s + 8 * s, 1);
-            mbar_init(base + L::bar_p + 8 * s, 128);
+            mbar_init(base + L::bar_p + 8 * s, 256);
             mbar_init(base + L::bar_o + 8 * s, 1);
             spans[s] = make_int4(INT32_MAX, 0, 0, INT32_MAX);
         }
@@ -175,11 +185,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         fence_barrier_init();
         fence_proxy_async_smem();
     }
-    if (warp == 9) tmem_alloc(base + L::misc, 512);
+    if (warp == 17) tmem_alloc(base + L::misc, 512);
     __syncthreads();
     // keys that some row of the warp sees, and those that all of its rows see
     int4 mine = make_int4(0, 0, 0, 0);
-    if (warp < 8) {
+    if (warp < 16) {
         const bool live = range.x < range.y;
         mine.x = __reduce_min_sync(0xffffffffu, live ? range.x : INT32_MAX);
         mine.y = __reduce_max_sync(0xffffffffu, live ? range.y : 0);
@@ -212,13 +222,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         return (s == 0 ? t >= ta.x && t < ta.y : t >= tb.x && t < tb.y) && !(p.dual && ((t - t0) & 1) != s);
     };
     // a value tile is checked when some row of an active tile does not see all of its keys
-    auto checked = [&](int t) {
-        const int j0 = t * kBlockK;
-        return (active(0, t) && !(j0 >= spans[0].z && j0 + kBlockK <= spans[0].w)) ||
-               (active(1, t) && !(j0 >= spans[1].z && j0 + kBlockK <= spans[1].w));
-    };
+    const int2 wa = make_int2((spans[0].z - 1) / kBlockK + (spans[0].z > 0), spans[0].w / kBlockK);  // tiles that all rows see all of
+    const int2 wb = make_int2((spans[1].z - 1) / kBlockK + (spans[1].z > 0), spans[1].w / kBlockK);
+    auto checked = [&](int t) { return (active(0, t) && !(t >= wa.x && t < wa.y)) || (active(1, t) && !(t >= wb.x && t < wb.y)); };
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && t1 > t0) {
             const uint64_t keep = policy_evict_last();  // key and value tiles are read again by other query tiles
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 if (!*abort_flag) drain_wait_b(base + L::bar_empty + 8 * (j % NST), (j / NST) & 1, kDrainNs);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------------------ MMAs
         // S_s(t) = Q_s K(t)^T, then O_s += P_s(t) V(t) with P_s over S_s in tensor memory.  While one tile's
         // softmax runs, the tensor core works for the other.  The MMAs of a thread run in order: S_s(t + 1)
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 const uint32_t v_lo = smem_desc_lo_mn128(base + L::kv + st * L::kTile, kBlockK * 128);
 #pragma unroll
                 for (int kk = 0; kk < TERMS * kBlockK / 16; ++kk)  // columns: see the softmax
-                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + (kk >> 3) * 32 + (kk >> 2 & 1) * 64 + (kk & 3) * 8,
+                    tc_mma_bf16_ta_w(tmem + 256 + s * 128, tmem + s * 128 + (kk >> 1 & 3) * 32 + (kk >> 3) * 16 + (kk & 1) * 8,
                                      v_lo + (((kk & 7) * 16 * 128) >> 4), dhi, id_o, (n_p[s] | kk) != 0);
                 ++n_p[s];
             };
@@ -338,14 +346,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 drain_wait_b(base + L::bar_done, 0, kDrainNs);
             }
         }
-    } else if (warp >= 10) {
+    } else if (warp >= 18) {
         // ------------------------------------------------------------ value check
         // A probability of 0 does not hide a NaN or an infinity in the value that it meets in the MMA.  In tiles
         // that some row does not see all of, keys with such values get zeros, and rows that see them become NaN.
         // The warps wait for every copy of the ring in turn and release every stage with the MMAs: a wait that skipped
         // a stage's use would take the use before it for its own.  The k-th check uses slot k % NST: the ring holds
         // fewer value tiles than there are slots.
-        const int w = warp - 10;
+        const int w = warp - 18;
         int k_check = 0;
         for (int n = 0; n < 2 * (t1 - t0); ++n) {
             const int st = n % NST, t = t0 + (n >> 1);
@@ -387,10 +395,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     } else {
         // ------------------------------------------------------------ softmax
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        const uint32_t t_s = tl + sub * 128, t_o = tl + 256 + sub * 128;
+        const uint32_t t_s = tl + sub * 128 + 64 * side, t_o = tl + 256 + sub * 128;
         const float c = p.c;
-        float ref = -INFINITY;  // m
-        float l = 0.f, lo = 0.f;  // sums of the probabilities, and of the rounded ones
+        float ref = -INFINITY;     // m, the same on both sides of a row
+        float l = 0.f;             // sum of the probabilities of this side
+        float* tops = reinterpret_cast<float*>(gbase + L::tops) + sub * 256 + row;
         bool broken = false;
         bool ok = true;
         int n = 0, k_check = 0;
@@ -399,80 +408,72 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             const int slot = k_check % NST, phase = (k_check / NST) & 1;
             k_check += check;
             if (!active(sub, t)) continue;
-            if (!wait_all(base + L::bar_s + 8 * sub, n & 1, wc, kErrWaitS)) {
-                ok = false;
-                break;
-            }
+            ok = wait_all(base + L::bar_s + 8 * sub, n & 1, wc, kErrWaitS) &&
+                 (!check || wait_all(base + L::bar_clean + 8 * slot, phase, wc, kErrWaitOther));
             tc_fence_after();
-            const int j0 = t * kBlockK;
+            const int j0 = t * kBlockK + 64 * side;
             const int first = range.x - j0, last = range.y - 1 - j0;  // columns that the row sees
-            const bool whole = j0 >= mine.z && j0 + kBlockK <= mine.w;
-            if (check) {
-                if (!wait_all(base + L::bar_clean + 8 * slot, phase, wc, kErrWaitOther)) {
-                    ok = false;
-                    break;
-                }
+            const bool whole = j0 >= mine.z && j0 + 64 <= mine.w;
+            const bool any0 = j0 < mine.y && j0 + 32 > mine.x, any1 = j0 + 32 < mine.y && j0 + 64 > mine.x;
+            if (check && ok) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t u = bad[4 * slot + k];
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t u = bad[4 * slot + 2 * side + k];
                     if (u) {
-                        const int lo = max(first - 32 * k, 0), hi = min(last - 32 * k, 31);
-                        if (lo <= hi) broken |= ((u >> lo) << lo & (0xffffffffu >> (31 - hi))) != 0u;
+                        const int from = max(first - 32 * k, 0), to = min(last - 32 * k, 31);
+                        if (from <= to) broken |= ((u >> from) << from & (0xffffffffu >> (31 - to))) != 0u;
                     }
                 }
                 __syncwarp();
             }
-            // Half hf of the scores, columns 64 hf .. 64 hf + 63, makes room for its probabilities: the (first) terms
-            // in the first 32 of these columns, the second terms in the others.
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t t_h = t_s + 64 * hf;
-                const int c0 = j0 + 64 * hf;
-                if (c0 >= mine.y || c0 + 64 <= mine.x) {  // no row of the warp sees any of these keys
-                    uint32_t zeros[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) zeros[e] = 0u;
-#pragma unroll
-                    for (int k = 0; k < 2 * TERMS; ++k) tmem_st16(t_h + 16 * k, zeros);
-                    continue;
-                }
-                float z[64];
-                tmem_ld32(t_h, *reinterpret_cast<float(*)[32]>(z));
-                tmem_ld32(t_h + 32, *reinterpret_cast<float(*)[32]>(z + 32));
+            // the largest score; the second 32 columns stay, the first are read once more
+            float z[32];
+            float top = -INFINITY;
+            if (any0) {
+                tmem_ld32(t_s, z);
                 tc_wait_ld();
-                if (!whole) {
-                    const int from = first - 64 * hf, to = last - 64 * hf;
-#pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (e < from || e > to) z[e] = -INFINITY;
-                }
-                // The exponentials do not wait for the maximum: where it turns out that m has to rise, which it seldom
-                // does after the first tiles, they are taken again.
-                float2 la, lb, ra, rb;
-                for (;;) {
-                    la = lb = ra = rb = splat(0.f);
-                    const float r = ref == -INFINITY ? 0.f : ref;
-                    {
-                        uint32_t w[16], less[16];
-                        exp_quarter<TERMS, 0>(z, c, r, la, lb, ra, rb, w, less);
-                        tmem_st16(t_h, w);
-                        if (TERMS == 2) tmem_st16(t_h + 32, less);
-                        exp_quarter<TERMS, 32>(z, c, r, la, lb, ra, rb, w, less);
-                        tmem_st16(t_h + 16, w);
-                        if (TERMS == 2) tmem_st16(t_h + 48, less);
-                    }
-                    const float top = c * max_half(z);
-                    const bool raise = valid && top > ref + kAttnTau;
-                    if (!__any_sync(0xffffffffu, raise)) break;
-                    const float next = raise ? ceilf(top) : ref, f = raise ? ex2(ref - next) : 1.f;
-                    l *= f;
-                    lo *= f;
-                    ref = next;
-                    if (n > 0 || hf > 0) rescale<D>(t_o, n > 0, t_s, 2 * TERMS * hf, f);
-                }
-                l += (la.x + la.y) + (lb.x + lb.y);
-                lo += (ra.x + ra.y) + (rb.x + rb.y);
+                if (!whole) hide_chunk(z, first, last);
+                top = max_chunk(z);
             }
+            if (any1) {
+                tmem_ld32(t_s + 32, z);
+                tc_wait_ld();
+                if (!whole) hide_chunk(z, first - 32, last - 32);
+                top = fmaxf(top, max_chunk(z));
+            }
+            top *= c;
+            if (bar_sync_or(1 + sub, 256, (valid && top > ref + kAttnTau) || !ok)) {
+                // some row's m rises (or a wait gave up): both sides of the rows take the larger of their maxima
+                tops[128 * side] = top;
+                if (!(ok = bar_sync_and(1 + sub, 256, ok))) break;
+                top = fmaxf(top, tops[128 * (side ^ 1)]);
+                const bool raise = valid && top > ref + kAttnTau;
+                const float f = raise ? ex2(ref - top) : 1.f;
+                l *= f;
+                if (raise) ref = top;
+                if (n > 0 && __any_sync(0xffffffffu, raise)) rescale(t_o + side * (D / 2), D / 2, f);
+            }
+            // 32 scores make room for their probabilities: 16 columns of (first) terms, 16 of second terms
+            const float r = ref == -INFINITY ? 0.f : ref;
+            float2 la = splat(0.f), lb = la;
+            uint32_t w[16], less[16];
+#pragma unroll
+            for (int q = 1; q >= 0; --q) {
+                if (q ? any1 : any0) {
+                    if (q == 0) {
+                        tmem_ld32(t_s, z);
+                        tc_wait_ld();
+                        if (!whole) hide_chunk(z, first, last);
+                    }
+                    exp_chunk<TERMS>(z, c, r, la, lb, w, less);
+                } else {  // no row of the warp sees any of these keys
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = less[e] = 0u;
+                }
+                tmem_st16(t_s + 32 * q, w);
+                if (TERMS == 2) tmem_st16(t_s + 32 * q + 16, less);
+            }
+            l += (la.x + la.y) + (lb.x + lb.y);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(base + L::bar_p + 8 * sub);
@@ -480,20 +481,31 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         if (ok && n > 0) ok = wait_all(base + L::bar_o + 8 * sub, 0, wc, kErrWaitOther);
         tc_fence_after();
+        // both sides' sums; the query tile is done with where there was anything to do
+        {
+            float* sums = reinterpret_cast<float*>(gbase + L::sums + sub * L::kTile) + row;
+            ok = bar_sync_and(1 + sub, 256, ok);
+            if (n > 0 && ok) {
+                sums[side * 256] = l;
+                sums[side * 256 + 128] = broken ? 1.f : 0.f;
+            }
+            ok = bar_sync_and(1 + sub, 256, ok);
+            if (n > 0 && ok) {
+                l += sums[(side ^ 1) * 256];
+                broken |= sums[(side ^ 1) * 256 + 128] != 0.f;
+            }
+        }
         const float nan = __int_as_float(0x7fc00000);
         const bool fail = __any_sync(0xffffffffu, !ok || *abort_flag);
         const int h = hk * p.group + block_of(sub) * p.heads + in_block;
         const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
-        // With one term O is divided by the sum of the rounded probabilities: what their roundings have in common, such
-        // as the only key's, cancels.
-        if (TERMS == 2) lo = l;
-        if (fail || broken) l = lo = nan;
+        if (fail || broken) l = nan;
         const bool empty = range.x >= range.y;
         if (p.parts == 1) {
-            const float inv = empty ? 0.f : 1.f / lo;
+            const float inv = empty ? 0.f : 1.f / l;
             uint8_t* out = static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
 #pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
+            for (int k = side * (D / 2); k < (side + 1) * (D / 2); k += 32) {
                 float v[32];
                 if (n > 0 && !fail) {
                     tmem_ld32(t_o + k, v);
@@ -513,11 +525,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 __syncwarp();
             }
-            if (valid) p.LSE[flat] = empty ? -INFINITY : fmaf(ref, kLn2, logf(l));
+            if (valid && side == 0) p.LSE[flat] = empty ? -INFINITY : fmaf(ref, kLn2, logf(l));
         } else {
             const size_t R = static_cast<size_t>(p.B) * p.H * p.Nq, at_row = (p.dual ? 2 * split + sub : split) * R + flat;
 #pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
+            for (int k = side * (D / 2); k < (side + 1) * (D / 2); k += 32) {
                 float v[32];
                 if (n > 0 && !fail) {
                     tmem_ld32(t_o + k, v);
@@ -529,13 +541,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 if (valid) store_grad32(p.part + at_row * D, k, v, 1.f, false);
                 __syncwarp();
             }
-            if (valid) p.part_ml[at_row] = make_float4(ref, l, lo, 0.f);
+            if (valid && side == 0) p.part_ml[at_row] = make_float2(ref, l);
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -556,21 +568,20 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
     for (int s = lane; s < p.parts; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, lo = 0.f, v[V];
+    float l = 0.f, v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
     for (int s = 0; s < p.parts; ++s) {
-        const float4 ml = p.part_ml[s * R + row];
+        const float2 ml = p.part_ml[s * R + row];
         if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this split's keys are hidden from the row
         const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         l = fmaf(ml.y, f, l);
-        lo = fmaf(ml.z, f, lo);
         const float* part = p.part + (s * R + row) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
     }
     const bool empty = range.x >= range.y;
-    const float inv = empty ? 0.f : 1.f / lo;
+    const float inv = empty ? 0.f : 1.f / l;
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + i * p.o_n) + lane * V);
     uint32_t* rest = p.rest ? reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.rest) + row * D + lane * V) : nullptr;
 #pragma unroll

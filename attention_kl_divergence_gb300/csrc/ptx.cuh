@@ -391,6 +391,20 @@ __device__ __forceinline__ bool bar_sync_and(uint32_t id, uint32_t n, bool v) {
     return r != 0;
 }
 
+// The same with an OR.
+__device__ __forceinline__ bool bar_sync_or(uint32_t id, uint32_t n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
 // Bulk add of `bytes` of float32 from shared to global memory (L2 reduction),
 // tracked by this thread's bulk async-group.
 __device__ __forceinline__ void bulk_reduce_add_f32(float* gdst, uint32_t ssrc, uint32_t bytes) {

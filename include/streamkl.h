@@ -418,9 +418,8 @@ STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t
  *    least where that value counts and at most in the whole row.
  *  - rest (NULL or bf16 [B, H, Nq, d], contiguous): what the rounding of O to
  *    bf16 left, for the backward's row sums of dO * O.
- *  - Probabilities enter the product with V rounded to bf16 (and O is divided by
- *    the sum of the rounded ones), with rest as two bf16 terms; sums, maxima and
- *    outputs are float32 until their one rounding.
+ *  - Probabilities enter the product with V rounded to bf16, with rest as two
+ *    bf16 terms; sums, maxima and outputs are float32 until their one rounding.
  *  - Equal inputs give equal bits.  A give-up of a bounded wait leaves NaN in
  *    the rows that it left unfinished.
  *  - workspace may be NULL for a forward whose plan has 256 bytes (one split):

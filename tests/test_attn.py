@@ -7,9 +7,8 @@ the visible pairs a score is off by  del = (d + 32) 2^-24 A + 2^-20 (M + 1).
 LSE is off by at most del + N 2^-24 (the sum of up to N terms) + its rounding.
 A probability enters the product with V rounded to bf16 (2^-8 of it) from a
 value off by a factor 1 +- 2 del, the product accumulates in float32, and O is
-rounded once:  (2^-7 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|, where the sum
-of rounded probabilities that O is divided by counts 2^-8 too.  With `rest` they are
-two bf16 terms, off by 2^-16, and O + rest is off by
+rounded once:  (2^-8 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-8 |O|.  With `rest`
+they are two bf16 terms, off by 2^-16, and O + rest is off by
 (2^-16 + 4 del + (N + 128) 2^-24) sum P |V| + 2^-16 |O|.
 
 Gradients.  P is off by a factor 1 +- 2 del and enters dV rounded (2^-8 of it).
@@ -65,7 +64,7 @@ class Ref:
         self.delta = (d + 32) * 2.0 ** -24 * A + 2.0 ** -20 * (big(s) + 1)
         self.acc = (Nk + 128) * 2.0 ** -24
         mag = self.p @ v.abs()
-        self.o_tol = (2.0 ** -7 + 4 * self.delta + self.acc) * mag + 2.0 ** -8 * self.O.abs() + 1e-30
+        self.o_tol = (2.0 ** -8 + 4 * self.delta + self.acc) * mag + 2.0 ** -8 * self.O.abs() + 1e-30
         self.two_terms = (2.0 ** -16 + 4 * self.delta + self.acc) * mag + 2.0 ** -16 * self.O.abs() + 1e-30
 
     def check_grads(self, dO, dQ, dK, dV):
