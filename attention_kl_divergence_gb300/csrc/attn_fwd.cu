@@ -55,24 +55,25 @@ __device__ __forceinline__ int2 tiles_of(int4 span) {
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 
-// 2^(z c - ref) of 32 scores as 16 words of bf16 pairs, and with two terms what they lack as 16 more.  Their float32
-// sums are added to la, lb.
-template <int TERMS>
-__device__ __forceinline__ void exp_chunk(const float (&z)[32], float c, float ref, float2& la, float2& lb, uint32_t (&w)[16],
-                                          uint32_t (&less)[16]) {
+// 2^(z c - ref) of 16 scores, from FROM on, as 8 words of bf16 pairs, and with two terms what they lack as 8 more.
+// Their float32 sums are added to la, lb.
+template <int TERMS, int FROM>
+__device__ __forceinline__ void exp_part(const float (&z)[32], float c, float ref, float2& la, float2& lb, uint32_t (&w)[8],
+                                         uint32_t (&less)[8]) {
     const float2 cc = splat(c), nr = splat(-ref), minus = splat(-1.f);
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
+    for (int k = 0; k < 16; k += 4) {
+        const int e = FROM + k;
         const float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), cc, nr), b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), cc, nr);
         const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
         la = __fadd2_rn(la, pa);
         lb = __fadd2_rn(lb, pb);
-        w[e / 2] = pack_bf16(pa.x, pa.y);
-        w[e / 2 + 1] = pack_bf16(pb.x, pb.y);
+        w[k / 2] = pack_bf16(pa.x, pa.y);
+        w[k / 2 + 1] = pack_bf16(pb.x, pb.y);
         if (TERMS == 2) {
-            const float2 da = __ffma2_rn(unpack_bf16(w[e / 2]), minus, pa), db = __ffma2_rn(unpack_bf16(w[e / 2 + 1]), minus, pb);
-            less[e / 2] = pack_bf16(da.x, da.y);
-            less[e / 2 + 1] = pack_bf16(db.x, db.y);
+            const float2 da = __ffma2_rn(unpack_bf16(w[k / 2]), minus, pa), db = __ffma2_rn(unpack_bf16(w[k / 2 + 1]), minus, pb);
+            less[k / 2] = pack_bf16(da.x, da.y);
+            less[k / 2 + 1] = pack_bf16(db.x, db.y);
         }
     }
 }
@@ -470,22 +471,28 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             // 32 scores make room for their probabilities: 16 columns of (first) terms, 16 of second terms
             const float r = ref == -INFINITY ? 0.f : ref;
             float2 la = splat(0.f), lb = la;
-            uint32_t w[16], less[16];
+            uint32_t w[8], less[8];
 #pragma unroll
             for (int q = 1; q >= 0; --q) {
+                const uint32_t t_q = t_s + 32 * q;
                 if (q ? any1 : any0) {
                     if (q == 0) {
                         tmem_ld32(t_s, z);
                         tc_wait_ld();
                         if (!whole) hide_chunk(z, first, last);
                     }
-                    exp_chunk<TERMS>(z, c, r, la, lb, w, less);
+                    exp_part<TERMS, 0>(z, c, r, la, lb, w, less);
+                    tmem_st8(t_q, w);
+                    if (TERMS == 2) tmem_st8(t_q + 16, less);
+                    exp_part<TERMS, 16>(z, c, r, la, lb, w, less);
+                    tmem_st8(t_q + 8, w);
+                    if (TERMS == 2) tmem_st8(t_q + 24, less);
                 } else {  // no row of the warp sees any of these keys
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = less[e] = 0u;
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
+#pragma unroll
+                    for (int k = 0; k < 2 * TERMS; ++k) tmem_st8(t_q + 8 * k, w);
                 }
-                tmem_st16(t_s + 32 * q, w);
-                if (TERMS == 2) tmem_st16(t_s + 32 * q + 16, less);
             }
             l += (la.x + la.y) + (lb.x + lb.y);
             if (check) ok = wait_all(base + L::bar_clean + 8 * slot, phase, wc, kErrWaitOther);
