@@ -975,6 +975,8 @@ def _ranges(ranges, Q):
 
 
 def _given_ranges(ranges):
+    if ranges is None:
+        return None, None, None
     return tuple(ranges) if isinstance(ranges, (tuple, list)) else (ranges,)
 
 
@@ -1013,7 +1015,7 @@ def attn_fwd(Q, K, V, ranges=None, causal=False, scale=None, rest=False, out=Non
     left = torch.empty(shape, dtype=torch.bfloat16, device=device) if rest else None
     LSE = torch.empty(shape[:3], dtype=torch.float32, device=device)
     at, size, _keep = _own_scratch(workspace, nbytes, device)
-    begin, end, offset = given if len(given) == 3 else (None, None, None)
+    begin, end, offset = given
     _raise(_on(device, load().streamkl_attn_fwd, desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _address(begin),
                _address(end), _address(offset), 0.0 if scale is None else float(scale), 1 if causal else 0, out.data_ptr(),
                _address(left), LSE.data_ptr(), at, size, opts), "streamkl_attn_fwd")
@@ -1060,7 +1062,7 @@ def attn_bwd(dO, Q, K, V, O, LSE, rest=None, ranges=None, causal=False, scale=No
             _check_tensor(name, t, s, torch.bfloat16, device)
     dQ, dK, dV = out
     workspace = _scratch(workspace, nbytes, device)
-    begin, end, offset = given if len(given) == 3 else (None, None, None)
+    begin, end, offset = given
     _raise(_on(device, load().streamkl_attn_bwd, desc, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
                _address(rest), LSE.data_ptr(), _address(begin), _address(end), _address(offset),
                0.0 if scale is None else float(scale), 1 if causal else 0, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),

@@ -67,7 +67,8 @@ class Ref:
         self.o_tol = (2.0 ** -8 + 4 * self.delta + self.acc) * mag + 2.0 ** -8 * self.O.abs() + 1e-30
         self.two_terms = (2.0 ** -16 + 4 * self.delta + self.acc) * mag + 2.0 ** -16 * self.O.abs() + 1e-30
 
-    def check_grads(self, dO, dQ, dK, dV):
+    def grads(self, dO):
+        """(dQ, dK, dV) and the bounds of their errors but for the outputs' rounding."""
         B, H, Nq, d = self.q.shape
         Nk = self.k.shape[2]
         g = dO.double().masked_fill(~self.live[..., None], 0.0)
@@ -83,7 +84,10 @@ class Ref:
         tol = ((err + (2.0 ** -16 + acc) * dS.abs()) @ self.k.abs(),
                back((err + (2.0 ** -16 + acc) * dS.abs()).transpose(2, 3) @ self.q.abs()),
                back((self.p * (2.0 ** -8 + 2 * self.delta + acc)).transpose(2, 3) @ g.abs()))
-        for name, got, w, t in zip(("dQ", "dK", "dV"), (dQ, dK, dV), want, tol):
+        return want, tol
+
+    def check_grads(self, dO, dQ, dK, dV):
+        for name, got, w, t in zip(("dQ", "dK", "dV"), (dQ, dK, dV), *self.grads(dO)):
             bound = t * 1.01 + 2.0 ** -8 * w.abs() + 1e-30  # 1.01: products of the terms above
             e = (got.double() - w).abs()
             assert bool((e <= bound).all()), (name, float((e / bound).max()))

@@ -350,6 +350,31 @@ def test_outputs_streams_graphs_and_in_place_changes():
 
 
 @gpu
+def test_pages_beyond_32_bits_of_bytes():
+    """The last pages of a cache of 4.4 GB each for keys and values, and the same pages of a small one."""
+    B, H, Hk, T, d, M = 2, 8, 2, 128, 128, 5
+    far = 2 ** 32 // (Hk * T * d) + 700
+    big = sk.Cache8(*(torch.empty(far, Hk, T, d, dtype=torch.uint8, device=DEV) for _ in range(2)),
+                    *(torch.empty(far, Hk, device=DEV) for _ in range(2)))
+    small = sk.Cache8.empty(B * M, Hk, T, d, DEV)
+    for a, s in zip(big.tensors(), small.tensors()):
+        a[-B * M:] = s.view(torch.uint8) if s.dtype == E4M3 else s
+    table = torch.arange(B * M, dtype=torch.int32, device=DEV).flip(0).reshape(B, M).contiguous()
+    held = torch.zeros(B, dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(B, Hk, 500, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(s)).to(BF16) for s in (1, 2))
+    Q = torch.randn(B, H, 3, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3)).to(BF16)
+    got = []
+    for cache, at in ((big, table + (far - B * M)), (small, table)):
+        n = held.clone()
+        for part in ((0, 499), (499, 500)):
+            sk.cache8_append(cache, at, n, k[:, :, slice(*part)], v[:, :, slice(*part)])
+            n += part[1] - part[0]
+        got.append((*sk.attn_cache8(Q, cache, at, n), *sk.cache8_read(cache, at, n)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    Ref(Q, small, table, n).check(*got[0][:2])
+
+
+@gpu
 @pytest.mark.parametrize("splits", [0, 3])
 @pytest.mark.parametrize("Nq", [1, 9])
 def test_a_wait_that_gives_up_leaves_nan_and_a_status(Nq, splits):
