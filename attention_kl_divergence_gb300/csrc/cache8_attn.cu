@@ -345,6 +345,8 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
         }
 #pragma unroll
         for (int half = 0; half < KH; ++half) {
+            const int h0 = j0 + 16 * half;
+            const bool tail = h0 + 16 > all;  // some row does not see all of these keys
             uint32_t pr[NQ][2];  // (keys 2t, 2t + 1 and 2t + 8, 2t + 9; row g)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
@@ -359,6 +361,10 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                     l[n][e] += p0 + p1;
                     v[e] = p0 * x;
                     v[2 + e] = p1 * x;
+                    if (tail) {  // a scale that is no number must not reach rows that do not see its page
+                        if (h0 + g >= lim[n][e]) v[e] = 0.f;
+                        if (h0 + 8 + g >= lim[n][e]) v[2 + e] = 0.f;
+                    }
                 }
                 pr[n][0] = transpose8(pack_f16(v[0], v[1]));
                 pr[n][1] = transpose8(pack_f16(v[2], v[3]));
@@ -374,13 +380,32 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                 else
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[x][0]), "=r"(v[x][1]) : "r"(src) : "memory");
             }
-            if (j0 + 16 * half + 16 > len) {  // what stands behind the tokens may be NaN, which a probability of 0 does not hide
+            if (tail) {
+                // A probability of 0 does not hide a NaN (e4m3 has no infinity): keys that not every row sees and that have
+                // one become zeros, as what stands behind the tokens does, and the rows that see them NaN.
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (j0 + 16 * half + 2 * t + (x & 1) + 8 * (x >> 1) >= len) {
+                for (int x = 0; x < 4; ++x) {
+                    const int mine = h0 + 2 * t + (x & 1) + 8 * (x >> 1);
+                    uint32_t found = 0u;
+#pragma unroll
+                    for (int e = 0; e < VB / 4; ++e) found |= __vcmpeq4(v[x][e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, found != 0u && mine >= all && mine < len);
+                    if (mine >= len || (lanes >> t & 0x11111111u)) {
 #pragma unroll
                         for (int e = 0; e < VB / 4; ++e) v[x][e] = 0u;
                     }
+                    if (lanes == 0u) continue;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if ((lanes >> k & 0x11111111u) && h0 + 2 * k + (x & 1) + 8 * (x >> 1) < lim[n][e]) {
+#pragma unroll
+                                    for (int y = 0; y < MT; ++y) o[n][y][e] = o[n][y][2 + e] = nan;
+                                }
+                }
             }
 #pragma unroll
             for (int e = 0; e < VB / 4; ++e)

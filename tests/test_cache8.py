@@ -295,6 +295,42 @@ def test_what_a_row_does_not_see_has_no_effect():
     got = sk.attn_cache8(Q, cache, table, n)
     assert torch.equal(got[0][0], want[0][0]) and bool(got[0][1, :, 2].isnan().all())
     assert torch.equal(got[1], want[1])
+    assert torch.equal(got[0][1, :, :2], want[0][1, :, :2])
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,Nq,T", [(1, 3, 16), (4, 16, 64), (5, 7, 16)])  # rows in one 8-row tile, in teams of 16-row tiles
+def test_a_broken_new_token_reaches_the_rows_that_see_it_alone(group, Nq, T, d):
+    """The token at distance `back` from the last: NaN in its key, in a byte of its value, or a page of its own that has a
+    scale which is no number."""
+    B, Hk, M = 2, 2, 8
+    table, pages = tables(B, M)
+    Q = torch.randn(B, group * Hk, Nq, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(BF16)
+    rows = torch.arange(Nq, device=DEV)
+    for length in (2 * T + 1, 3 * T, 5 * T - 2):
+        n = torch.tensor([length, length - 1], dtype=torch.int32, device=DEV)
+        for back in sorted({0, 1, Nq - 2, Nq - 1}):
+            for which in ("key", "value", "scale"):
+                cache = pool(pages, Hk, T, d)
+                want = sk.attn_cache8(Q, cache, table, n)
+                at = length - 1 - back
+                page = int(table[0, at // T])
+                if which == "scale":  # the whole page: every token of it
+                    cache.v_scale[page] = math.inf
+                    at = at // T * T
+                else:
+                    (cache.k if which == "key" else cache.v).view(torch.uint8)[page, 1, at % T, d - 3] = 0x7f
+                O, LSE = sk.attn_cache8(Q, cache, table, n)
+                hit = (length - Nq + rows >= at) & torch.ones(B, Hk, group, Nq, dtype=torch.bool, device=DEV)
+                hit[1] = False
+                if which != "scale":
+                    hit[:, 0] = False
+                hit = hit.view(B, Hk * group, Nq)
+                assert torch.equal(O.isnan().any(-1), hit), (length, back, which)
+                assert torch.equal(O[~hit], want[0][~hit])
+                clean = ~hit if which == "key" else torch.ones_like(hit)
+                assert torch.equal(LSE[clean], want[1][clean])
 
 
 @gpu
