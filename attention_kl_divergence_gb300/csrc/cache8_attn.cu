@@ -207,6 +207,18 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             copy_rows(dst + 16 * D, tV, bar, row);
         }
     };
+    // the query rows (see below) are on their way while the pages are looked up
+    uint32_t q[NQ][KS][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = rt * ROWS + 8 * n + g, h = r / p.Nq, i = r - h * p.Nq;
+        const uint16_t* row = r < R ? static_cast<const uint16_t*>(p.Q) + b * p.q_b + (hk * p.group + h) * p.q_h + i * p.q_n : nullptr;
+#pragma unroll
+        for (int s = 0; s < KS; s += 2) {
+            const uint4 u = row ? *reinterpret_cast<const uint4*>(row + 64 * (s >> 2) + 16 * t + 4 * (s & 3)) : make_uint4(0u, 0u, 0u, 0u);
+            q[n][s][0] = u.x, q[n][s][1] = u.y, q[n][s + 1][0] = u.z, q[n][s + 1][1] = u.w;
+        }
+    }
     bool ok = alive;
     entries[threadIdx.x] = look_up(0);
     PageEntry ahead = look_up(1);
@@ -216,18 +228,13 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
 
     // Query fragments: lane (g, t) has row g of each 8-row tile.  Any order of d serves a score, if q and k have the
     // same: the lane holds the 16-byte pieces t (and t + 4, d = 128) of a row, four values of one piece to a k-step.
-    uint32_t q[NQ][KS][2];
     float qf[NQ][2];   // of rows 2t and 2t + 1 of a tile, the lane's columns of a score: its factor
     int lim[NQ][2];    // and the keys below lim are seen
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        const int r = rt * ROWS + 8 * n + g, h = r / p.Nq, i = r - h * p.Nq;
-        const uint16_t* row = r < R ? static_cast<const uint16_t*>(p.Q) + b * p.q_b + (hk * p.group + h) * p.q_h + i * p.q_n : nullptr;
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const uint2 u = row ? *reinterpret_cast<const uint2*>(row + 64 * (s >> 2) + 16 * t + 4 * (s & 3)) : make_uint2(0u, 0u);
-            q[n][s][0] = u.x, q[n][s][1] = u.y;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t a = q[n][s][e] & 0x7fff7fffu;
@@ -480,19 +487,31 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                 *reinterpret_cast<float4*>(dst + 2 * x) = make_float4(o[n][x][e], o[n][x][2 + e], o[n][x + 1][e], o[n][x + 1][2 + e]);
         }
     __syncthreads();
-    for (int x = threadIdx.x; x < teams * ROWS * (D / 4); x += S::kThreads) {
-        const int line = x / (D / 4), d0 = (x % (D / 4)) * 4, row = line % ROWS, tm = line / ROWS, r = (rg * teams + tm) * ROWS + row;
-        if (r >= R) continue;
+    // the rows' references, and what each warp's sums are worth against them
+    float* merged = states + 3 * W * ROWS;                             // [3][teams x ROWS]
+    for (int x = threadIdx.x; x < teams * ROWS; x += S::kThreads) {
+        const int row = x % ROWS, tm = x / ROWS;
         CacheState st{-INFINITY, 0.f, -INFINITY};
         for (int y = tm; y < W; y += teams) {
             st.m = fmaxf(st.m, states[(y * 3) * ROWS + row]);
             st.w = fmaxf(st.w, states[(y * 3 + 2) * ROWS + row]);
         }
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int y = tm; y < W; y += teams) {
             const float mx = states[(y * 3) * ROWS + row], lx = states[(y * 3 + 1) * ROWS + row], wx = states[(y * 3 + 2) * ROWS + row];
             st.l += mx == -INFINITY ? lx : lx * ex2(mx - st.m);  // without a reference: 0, or NaN scores alone
-            const float f = wx == -INFINITY ? 1.f : ex2(wx - st.w);
+            states[(y * 3 + 2) * ROWS + row] = wx == -INFINITY ? 1.f : ex2(wx - st.w);
+        }
+        merged[x] = st.m, merged[teams * ROWS + x] = st.l, merged[2 * teams * ROWS + x] = st.w;
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < teams * ROWS * (D / 4); x += S::kThreads) {
+        const int line = x / (D / 4), d0 = (x % (D / 4)) * 4, row = line % ROWS, tm = line / ROWS, r = (rg * teams + tm) * ROWS + row;
+        if (r >= R) continue;
+        CacheState st{merged[line], merged[teams * ROWS + line], merged[2 * teams * ROWS + line]};
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int y = tm; y < W; y += teams) {
+            const float f = states[(y * 3 + 2) * ROWS + row];
             const float4 u = *reinterpret_cast<const float4*>(sums + (y * ROWS + row) * D + d0);
             v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
         }
@@ -620,7 +639,7 @@ namespace {
 template <int D, int NQ, bool SHARED>
 cudaError_t launch_cache8_attn_d(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream) {
     using S = CacheShape<NQ>;
-    constexpr int ring = S::kWarps * kCwStages * 2 * S::kKeys * D, merge = S::kWarps * S::kRows * (D + 3) * 4;
+    constexpr int ring = S::kWarps * kCwStages * 2 * S::kKeys * D, merge = S::kWarps * S::kRows * (D + 6) * 4;
     static_assert(merge <= ring, "the states meet in the ring's space");
     constexpr int bytes = ring + 2 * S::kThreads * static_cast<int>(sizeof(PageEntry)) + 8 * kCwStages * S::kWarps + 1024;
     static_assert(bytes <= 232448, "shared memory");
