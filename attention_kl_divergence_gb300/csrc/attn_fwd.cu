@@ -43,9 +43,9 @@ struct AttnSmem {
     static constexpr int misc = bar_done + 8;               // tmem base, abort flag
     static constexpr int spans = (misc + 8 + 15) / 16 * 16; // [2] int4: union and common range of a tile's rows
     static constexpr int bad = spans + 32;                  // [kNst][4] keys whose values are not finite
-    static constexpr int tops = bad + 16 * kNst;            // [2][2][128] maxima of the halves of the rows
+    static constexpr int tops = bad + 16 * kNst;            // [2][2][128] maxima of the halves of the rows, their sums at the end
     static constexpr int alloc = tops + 2048;               // no slack: the kernel checks the base is 1024-byte aligned
-    static constexpr int sums = q;                          // [2][2][2][128] at the end, when the query tiles are done with
+    static constexpr int stage = q;                         // outputs at the end, when the query tiles are done with
 };
 
 // The key tiles [lo, hi) of a range of keys.
@@ -134,6 +134,26 @@ __device__ __noinline__ void rescale(uint32_t t_o, int n, float f) {
     tc_wait_st();
 }
 
+// A lane's row of 16 CH words -> memory at `out` (null: not written), through shared memory: what a lane holds are 64 CH
+// bytes of a row of its own, and the lanes of a store cover whole rows.
+template <int CH>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[CH][16], uint8_t* out, int lane) {
+    constexpr int kLanes = 4 * CH;  // of a row
+    auto at = [&](int row, int piece) { return stage + row * (64 * CH) + ((piece ^ (CH == 2 ? row & 7 : row >> 1 & 3)) << 4); };
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k)
+        *reinterpret_cast<uint4*>(at(lane, k)) = make_uint4(w[k / 4][k % 4 * 4], w[k / 4][k % 4 * 4 + 1], w[k / 4][k % 4 * 4 + 2], w[k / 4][k % 4 * 4 + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) {
+        const int row = k * (32 / kLanes) + lane / kLanes, piece = lane % kLanes;
+        uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), row));
+        const uint4 u = *reinterpret_cast<const uint4*>(at(row, piece));
+        if (to) *reinterpret_cast<uint4*>(to + 16 * piece) = u;
+    }
+    __syncwarp();
+}
+
 }  // namespace
 
 template <int D, int TERMS>
@@ -172,7 +192,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         return;
     }
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 512) {
         prefetch_tensormap(&tQ);
         prefetch_tensormap(&tK);
         prefetch_tensormap(&tV);
@@ -514,49 +534,49 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         if (ok && n > 0) ok = wait_all(base + L::bar_o + 8 * sub, 0, wc, kErrWaitOther);
         tc_fence_after();
-        // both sides' sums; the query tile is done with where there was anything to do
-        {
-            float* sums = reinterpret_cast<float*>(gbase + L::sums + sub * L::kTile) + row;
-            ok = bar_sync_and(1 + sub, 256, ok);
-            if (n > 0 && ok) {
-                sums[side * 256] = l;
-                sums[side * 256 + 128] = broken ? 1.f : 0.f;
-            }
-            ok = bar_sync_and(1 + sub, 256, ok);
-            if (n > 0 && ok) {
-                l += sums[(side ^ 1) * 256];
-                broken |= sums[(side ^ 1) * 256 + 128] != 0.f;
-            }
-        }
+        // both sides' sums
+        if (broken) l = __int_as_float(0x7fc00000);
+        ok = bar_sync_and(1 + sub, 256, ok);
+        tops[128 * side] = l;
+        ok = bar_sync_and(1 + sub, 256, ok);
+        l += tops[128 * (side ^ 1)];
+        if (ok && exists(sub)) ok = wait_all(base + L::bar_q + 8 * sub, 0, wc, kErrWaitQ);  // the stage's bytes
         const float nan = __int_as_float(0x7fc00000);
         const bool fail = __any_sync(0xffffffffu, !ok || *abort_flag);
         const int h = hk * p.group + block_of(sub) * p.heads + in_block;
         const size_t flat = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
-        if (fail || broken) l = nan;
+        if (fail) l = nan;
         const bool empty = range.x >= range.y;
         if (p.parts == 1) {
             const float inv = empty ? 0.f : 1.f / l;
-            uint8_t* out = static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n);
-#pragma unroll 1
-            for (int k = side * (D / 2); k < (side + 1) * (D / 2); k += 32) {
+            uint32_t w[D / 64][16], less[D / 64][16];
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
                 float v[32];
                 if (n > 0 && !fail) {
-                    tmem_ld32(t_o + k, v);
+                    tmem_ld32(t_o + side * (D / 2) + 32 * k, v);
                     tc_wait_ld();
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : n > 0 && !fail ? v[e] * inv : nan;
-                if (valid) store_grad32(out, k, v, 1.f, true);
-                if (valid && p.rest) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint32_t u = pack_bf16(v[e], v[e + 1]);
-                        v[e] -= __uint_as_float(u << 16);
-                        v[e + 1] -= __uint_as_float(u & 0xffff0000u);
-                    }
-                    store_grad32(static_cast<uint8_t*>(p.rest) + flat * (2 * D), k, v, 1.f, true);
+                for (int e = 0; e < 32; e += 2) {
+                    const float x = empty ? 0.f : n > 0 && !fail ? v[e] * inv : nan, y = empty ? 0.f : n > 0 && !fail ? v[e + 1] * inv : nan;
+                    const uint32_t u = pack_bf16(x, y);
+                    w[k][e / 2] = u;
+                    if (TERMS == 2) less[k][e / 2] = pack_bf16(x - __uint_as_float(u << 16), y - __uint_as_float(u & 0xffff0000u));
                 }
-                __syncwarp();
+            }
+            uint8_t* out = valid ? static_cast<uint8_t*>(p.O) + 2 * (b * p.o_b + h * p.o_h + static_cast<int64_t>(i) * p.o_n) + side * D : nullptr;
+            uint8_t* rest = valid ? static_cast<uint8_t*>(p.rest) + flat * (2 * D) + side * D : nullptr;
+            uint8_t* stage = gbase + L::stage + sub * L::kTile + (4 * side + wq) * (32 * D);
+            if (!fail) {
+                store_rows<D / 64>(stage, w, out, lane);
+                if (TERMS == 2) store_rows<D / 64>(stage, less, rest, lane);
+            } else if (valid) {  // the query tile may still be on its way
+#pragma unroll 1
+                for (int k = 0; k < D; k += 16) {
+                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+                    if (TERMS == 2) *reinterpret_cast<uint4*>(rest + k) = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+                }
             }
             if (valid && side == 0) p.LSE[flat] = empty ? -INFINITY : fmaf(ref, kLn2, logf(l));
         } else {
