@@ -93,8 +93,8 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
         splits = std::min({opt->num_splits, k_tiles, kMaxSplits});
     } else if (p.dual) {
         // Bound by HBM: one wave of CTAs, which saturates it from about two thirds of the SMs on; more waves start and
-        // end more often than unequal lengths cost (4 caches of up to 65536 keys, 8 key heads: 3 splits 185 us, 4 158,
-        // 5 164, 9 163, 19 178; one cache: 8 splits 78, 14 62, 19 63, 28 86).
+        // end more often than unequal lengths cost (4 caches of up to 65536 keys, 8 key heads: 3 splits 186 us, 4 160,
+        // 5 167, 9 168, 19 185; one cache: 8 splits 77, 14 62, 19 62, 28 83).
         splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, k_tiles / 4)));
     } else {
         const int n = choose_splits(units, k_tiles, sms);

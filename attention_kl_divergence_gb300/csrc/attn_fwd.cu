@@ -621,18 +621,25 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
     for (int s = lane; s < p.parts; s += 32) m = fmaxf(m, p.part_ml[s * R + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // a lane weighs a part each, then all lanes add up the parts; the loads of several are under way at a time
     float l = 0.f, v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
-    for (int s = 0; s < p.parts; ++s) {
-        const float2 ml = p.part_ml[s * R + row];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this split's keys are hidden from the row
-        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-        l = fmaf(ml.y, f, l);
-        const float* part = p.part + (s * R + row) * D + lane * V;
+    for (int s0 = 0; s0 < p.parts; s0 += 32) {
+        const float2 ml = s0 + lane < p.parts ? p.part_ml[(s0 + lane) * R + row] : make_float2(-INFINITY, 0.f);
+        const float mine = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);  // 1: zeros, all of whose keys are hidden, or NaN
+        l = fmaf(ml.y, mine, l);
+        const float* part = p.part + (s0 * R + row) * D + lane * V;
+        const int n = min(32, p.parts - s0);
+#pragma unroll 8
+        for (int s = 0; s < n; ++s, part += R * D) {
+            const float f = __shfl_sync(0xffffffffu, mine, s);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
+            for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
+        }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const bool empty = range.x >= range.y;
     const float inv = empty ? 0.f : 1.f / l;
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + i * p.o_n) + lane * V);
