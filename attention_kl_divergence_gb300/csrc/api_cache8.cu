@@ -144,9 +144,7 @@ streamkl_status streamkl_cache8_read(const streamkl_cache8* desc, const void* k,
     p.y_b[0] = s.x.b, p.y_h[0] = s.x.h, p.y_n[0] = s.x.n;
     p.y_b[1] = s.y.b, p.y_h[1] = s.y.h, p.y_n[1] = s.y.n;
     p.N = s.N;
-    int sms = 0;
-    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
-    return launch_cache8_read(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+    return launch_cache8_read(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
 }
 
 streamkl_status streamkl_attn_cache8_plan(const streamkl_cache8* desc, const streamkl_options* opt, streamkl_plan* plan) {

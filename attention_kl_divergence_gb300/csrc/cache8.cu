@@ -46,18 +46,29 @@ __device__ __forceinline__ int scale_exponent(float a) {
     return max((u & 0x7fffff) <= 0x600000 ? k - 8 : k - 7, kCacheLeastExponent);
 }
 
-// 8 bf16 times r as e4m3; what is not finite becomes NaN.
+// 8 bf16 times r as e4m3; what is not finite becomes NaN (CHECK: there may be such values).
+template <bool CHECK>
 __device__ __forceinline__ uint2 quantize8(uint4 x, float r) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t q[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
-        lo = fabsf(lo) < INFINITY ? lo * r : __int_as_float(0x7fc00000);
-        hi = fabsf(hi) < INFINITY ? hi * r : __int_as_float(0x7fc00000);
+        lo = !CHECK || fabsf(lo) < INFINITY ? lo * r : __int_as_float(0x7fc00000);
+        hi = !CHECK || fabsf(hi) < INFINITY ? hi * r : __int_as_float(0x7fc00000);
         q[k] = cvt_e4m3x2(lo, hi);
     }
     return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// The block's largest half of `top`.
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
+    uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kCaThreads / 32; ++k) most = max(most, red[k]);
+    return most;
 }
 
 __device__ __forceinline__ uint32_t requantize4(uint32_t u, float r) {
@@ -104,22 +115,30 @@ __global__ void __launch_bounds__(kCaThreads) cache8_append_kernel(const __grid_
     for (int k = 0; k < STEPS; ++k) {
         const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t a = w[e] & 0x7fff7fffu;
-            top = __vmaxu2(top, a & ~__vcmpgeu2(a, 0x7f807f80u));
-        }
+        for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
     }
-    uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
-    __syncthreads();
+    uint32_t most = block_max(top, red);
+    const bool odd = most >= 0x7f80u;  // there are values that are not finite: they do not count
+    if (odd) {
+        top = 0;
 #pragma unroll
-    for (int k = 0; k < kCaThreads / 32; ++k) most = max(most, red[k]);
+        for (int k = 0; k < STEPS; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[e] & 0x7fff7fffu;
+                top = __vmaxu2(top, a & ~__vcmpgeu2(a, 0x7f807f80u));
+            }
+        }
+        __syncthreads();
+        most = block_max(top, red);
+    }
     const float want = power_of_two(scale_exponent(__uint_as_float(most << 16)));
     const float now = lo > 0 ? fmaxf(old, want) : want, r = 1.f / now;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
         const int v = threadIdx.x + k * kCaThreads, row = v / W;
-        if (row >= lo && row < hi) *reinterpret_cast<uint2*>(dst + 8 * v) = quantize8(x[k], r);
+        if (row >= lo && row < hi) *reinterpret_cast<uint2*>(dst + 8 * v) = odd ? quantize8<true>(x[k], r) : quantize8<false>(x[k], r);
     }
     if (lo > 0 && now != old) {  // the tokens that the page held move to the new scale
         for (int v = threadIdx.x; v < lo * W; v += kCaThreads) {
@@ -131,40 +150,60 @@ __global__ void __launch_bounds__(kCaThreads) cache8_append_kernel(const __grid_
     if (threadIdx.x == 0 && now != old) *scale = now;
 }
 
-// 16 values per thread and step.  Rows behind a sequence's length are zeros, rows of
-// a page that is not there are NaN.
+// 16 values of a row per thread, of kReadRows rows whose look-ups and loads are under way together.  Rows behind a
+// sequence's length are zeros, rows of a page that is not there are NaN.
+constexpr int kReadRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) cache8_read_kernel(const __grid_constant__ CacheReadParams p) {
-    constexpr int W = D / 16;
+    constexpr int W = D / 16, kRows = 256 / W;
     const CacheView& c = p.c;
-    const int64_t total = static_cast<int64_t>(c.B) * c.H_kv * p.N * W;
-    const int kv = blockIdx.y;
-    for (int64_t k = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; k < total; k += int64_t(gridDim.x) * blockDim.x) {
-        const int w = static_cast<int>(k % W);
-        const int64_t row = k / W;
-        const int n = static_cast<int>(row % p.N), hk = static_cast<int>(row / p.N % c.H_kv), b = static_cast<int>(row / p.N / c.H_kv);
-        uint32_t out[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        if (n < c.lengths[b]) {
-            const int m = n / c.T, page = m < c.M ? c.table[static_cast<int64_t>(b) * c.M + m] : -1;
-            if (page >= 0 && page < c.pages) {
-                const int64_t ph = static_cast<int64_t>(page) * c.H_kv + hk;
-                const float s = c.scales[kv][ph];
-                const uint4 u = *reinterpret_cast<const uint4*>(c.values[kv] + (ph * c.T + n % c.T) * D + 16 * w);
-                const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    const int kv = blockIdx.z, w = threadIdx.x % W;
+    const uint32_t n0 = blockIdx.x * (kReadRows * kRows) + threadIdx.x / W;
+    for (int64_t bh = blockIdx.y; bh < static_cast<int64_t>(c.B) * c.H_kv; bh += gridDim.y) {
+        const int b = static_cast<int>(bh / c.H_kv), hk = static_cast<int>(bh - static_cast<int64_t>(b) * c.H_kv), len = c.lengths[b];
+        const int32_t* table = c.table + static_cast<int64_t>(b) * c.M;
+        int page[kReadRows];  // -1: not there
+        float s[kReadRows];
+        uint4 u[kReadRows];
+#pragma unroll
+        for (int k = 0; k < kReadRows; ++k) {
+            const uint32_t n = n0 + k * kRows, m = n >> c.log_T;
+            page[k] = static_cast<int64_t>(n) < len && n < static_cast<uint32_t>(p.N) && m < static_cast<uint32_t>(c.M) ? table[m] : -1;
+            if (page[k] >= c.pages) page[k] = -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kReadRows; ++k) {
+            if (page[k] < 0) continue;
+            const int64_t ph = static_cast<int64_t>(page[k]) * c.H_kv + hk;
+            s[k] = c.scales[kv][ph];
+            u[k] = *reinterpret_cast<const uint4*>(c.values[kv] + (ph * c.T + ((n0 + k * kRows) & (c.T - 1))) * D + 16 * w);
+        }
+#pragma unroll
+        for (int k = 0; k < kReadRows; ++k) {
+            const uint32_t n = n0 + k * kRows;
+            if (n >= static_cast<uint32_t>(p.N)) break;
+            uint32_t out[8];
+            if (page[k] >= 0) {
+                const uint32_t q[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 a = cvt_from_e4m3x2(q[e] & 0xffffu), d = cvt_from_e4m3x2(q[e] >> 16);
-                    out[2 * e] = pack_bf16(a.x * s, a.y * s);
-                    out[2 * e + 1] = pack_bf16(d.x * s, d.y * s);
+                    out[2 * e] = pack_bf16(a.x * s[k], a.y * s[k]);
+                    out[2 * e + 1] = pack_bf16(d.x * s[k], d.y * s[k]);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) out[e] = 0x7fc07fc0u;
+                for (int e = 0; e < 8; ++e) out[e] = static_cast<int64_t>(n) < len ? 0x7fc07fc0u : 0u;
+            }
+            uint16_t* y = static_cast<uint16_t*>(p.y[kv]) + b * p.y_b[kv] + hk * p.y_h[kv] + n * p.y_n[kv] + 16 * w;
+            if ((reinterpret_cast<uintptr_t>(y) & 31u) == 0) {
+                st_global_v8(y, out[0], out[1], out[2], out[3], out[4], out[5], out[6], out[7]);
+            } else {
+                reinterpret_cast<uint4*>(y)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+                reinterpret_cast<uint4*>(y)[1] = make_uint4(out[4], out[5], out[6], out[7]);
             }
         }
-        uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y[kv]) + b * p.y_b[kv] + hk * p.y_h[kv] + n * p.y_n[kv] + 16 * w);
-        y[0] = make_uint4(out[0], out[1], out[2], out[3]);
-        y[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
@@ -179,9 +218,9 @@ cudaError_t launch_cache8_append(const CacheAppendParams& p, cudaStream_t stream
     return cudaGetLastError();
 }
 
-cudaError_t launch_cache8_read(const CacheReadParams& p, int sms, cudaStream_t stream) {
-    const int64_t items = static_cast<int64_t>(p.c.B) * p.c.H_kv * p.N * (p.c.d / 16);
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, int64_t(sms) * 8)), 2);
+cudaError_t launch_cache8_read(const CacheReadParams& p, cudaStream_t stream) {
+    const unsigned rows = kReadRows * 256 / (p.c.d / 16);
+    const dim3 grid((static_cast<unsigned>(p.N) + rows - 1) / rows, std::min<int64_t>(int64_t(p.c.B) * p.c.H_kv, 65535), 2);
     if (p.c.d == 128)
         cache8_read_kernel<128><<<grid, 256, 0, stream>>>(p);
     else

@@ -56,7 +56,7 @@ cudaError_t launch_attn_bwd(int d, const CUtensorMap* maps, const AttnBwdParams&
 
 // 8-bit cache: new tokens in, tokens out, and attention of a few new tokens over it.
 cudaError_t launch_cache8_append(const CacheAppendParams& p, cudaStream_t stream);
-cudaError_t launch_cache8_read(const CacheReadParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_cache8_read(const CacheReadParams& p, cudaStream_t stream);
 // maps = {keys, values}: the pool's rows of d bytes, boxes of 16 rows.
 cudaError_t launch_cache8_attn(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream);
 
