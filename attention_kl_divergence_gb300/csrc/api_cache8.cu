@@ -64,7 +64,7 @@ bool make_view(const streamkl_cache8* s, void* k, void* v, float* k_scale, float
 }
 
 struct CacheAttnPlan {
-    int tile_rows, row_groups, teams, spread, ctas;
+    int tile_rows, row_groups, teams, spread, cluster, ctas;
     size_t ws_bytes;
 };
 
@@ -92,7 +92,10 @@ streamkl_status plan_cache_attn(const streamkl_cache8* s, const streamkl_options
     const int64_t capacity = int64_t(s->M) * s->T, steps = (capacity + 255) / 256;  // 256 keys: a chunk of each warp
     const int64_t wanted = opt && opt->num_splits > 0 ? opt->num_splits : capacity > 1024 && segments < 8 * int64_t(sms) ? sms : 0;
     pl->spread = wanted > 0;
-    pl->ctas = static_cast<int>(wanted > 0 ? std::min<int64_t>({wanted, segments * steps, int64_t(1) << 20}) : segments);
+    // A few CTAs share a short segment where they find room: a step takes about as long as adding up their sums.
+    pl->cluster = 1;
+    while (!pl->spread && pl->cluster < 8 && 2 * pl->cluster <= steps && segments * 2 * pl->cluster <= sms) pl->cluster *= 2;
+    pl->ctas = static_cast<int>(wanted > 0 ? std::min<int64_t>({wanted, segments * steps, int64_t(1) << 20}) : segments * pl->cluster);
     pl->ws_bytes = kStatusBytes;
     if (pl->spread) pl->ws_bytes += size_t(pl->ctas) * 2 * pl->tile_rows * pl->teams * (size_t(s->d) + 4) * sizeof(float);
     return STREAMKL_OK;
@@ -153,7 +156,7 @@ streamkl_status streamkl_attn_cache8_plan(const streamkl_cache8* desc, const str
     streamkl_status st = plan_cache_attn(desc, opt, &pl);
     if (st != STREAMKL_OK) return st;
     plan->path = 1;
-    plan->num_splits = pl.spread ? pl.ctas : 1;
+    plan->num_splits = pl.spread ? pl.ctas : pl.cluster;
     plan->num_ctas = pl.ctas;
     plan->launches = pl.spread ? 2 : 1;
     plan->workspace_bytes = pl.ws_bytes;
@@ -183,6 +186,7 @@ streamkl_status streamkl_attn_cache8(const streamkl_cache8* desc, const void* Q,
     p.row_groups = pl.row_groups;
     p.teams = pl.teams;
     p.spread = pl.spread;
+    p.cluster = pl.cluster;
     p.Q = Q;
     p.q_b = s.x.b, p.q_h = s.x.h, p.q_n = s.x.n;
     p.O = O;

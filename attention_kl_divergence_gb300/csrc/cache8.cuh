@@ -42,7 +42,8 @@ struct CacheAttnParams {
     int tile_rows;         // 8 (one tile holds a key head's group x Nq rows) or 16
     int row_groups;        // of up to kCacheTeams tiles, of those rows
     int teams;             // tiles that a CTA works on at a time: 1, 2, 4 or 8
-    int spread;            // CTAs take equal shares of all chunks, and parts are combined; else one CTA per segment
+    int spread;            // CTAs take equal shares of all chunks, and parts are combined; else a cluster per segment
+    int cluster;           // its CTAs, each with a share of the segment's chunks
     const void* Q;         // [B, H, Nq, d] bf16
     int64_t q_b, q_h, q_n;
     void* O;               // [B, H, Nq, d] bf16

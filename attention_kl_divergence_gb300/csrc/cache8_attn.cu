@@ -135,10 +135,29 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // The row's output from sums relative to m and w.
 __device__ __forceinline__ float output_factor(const CacheState& s) { return s.w == -INFINITY ? 0.f / s.l : ex2(s.w - kCwShift - s.m) / s.l; }
 
-// One segment's chunks [c0, c1) for a group of row tiles; the sums go to the outputs, or (part >= 0) to that part.
+constexpr int64_t kToOutputs = -1, kToCluster = -2;
+
+// One segment's chunks [c0, c1) for a group of row tiles; the sums go to the outputs, together with those of the
+// cluster's other CTAs, or (part >= 0) to that part.
 // `uses`: how many steps filled the rings before, to tell the phases of their barriers.  False: a wait gave up, and
 // the rows are NaN; nothing is copied in a segment that begins with `alive` false.
 template <int D, int NQ, bool SHARED>
@@ -489,6 +508,15 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
     __syncthreads();
     // the rows' references, and what each warp's sums are worth against them
     float* merged = states + 3 * W * ROWS;                             // [3][teams x ROWS]
+    float* outbox = merged + 3 * W * ROWS;                             // [teams x ROWS][D], [teams x ROWS][4]
+    auto store = [&](int r, int d0, const CacheState& st, const float4& v) {
+        const int h = hk * p.group + r / p.Nq, i = r % p.Nq;
+        const bool empty = len - p.Nq + 1 + i <= 0;
+        const float f = empty ? 0.f : output_factor(st);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + d0) =
+            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+        if (d0 == 0) p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
+    };
     for (int x = threadIdx.x; x < teams * ROWS; x += S::kThreads) {
         const int row = x % ROWS, tm = x / ROWS;
         CacheState st{-INFINITY, 0.f, -INFINITY};
@@ -516,18 +544,43 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
         }
         if (given > capacity) st.l = nan;  // tokens that the table has no page for
+        if (part == kToCluster) {
+            *reinterpret_cast<float4*>(outbox + line * D + d0) = v;
+            if (d0 == 0) *reinterpret_cast<float4*>(outbox + teams * ROWS * D + 4 * line) = make_float4(st.m, st.l, st.w, 0.f);
+            continue;
+        }
         if (part >= 0) {
             const int64_t at = part * (ROWS * teams) + line;
             *reinterpret_cast<float4*>(p.part + at * D + d0) = v;
             if (d0 == 0) p.part_state[at] = make_float4(st.m, st.l, st.w, 0.f);
             continue;
         }
-        const int h = hk * p.group + r / p.Nq, i = r % p.Nq;
-        const bool empty = len - p.Nq + 1 + i <= 0;
-        const float f = empty ? 0.f : output_factor(st);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + d0) =
-            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
-        if (d0 == 0) p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
+        store(r, d0, st, v);
+    }
+    if (part == kToCluster) {  // the sums of the cluster's CTAs, each of which writes some of the rows
+        cluster_sync();
+        const uint32_t box = smem_u32(outbox);
+        const int rank = blockIdx.x % p.cluster;
+        for (int x = rank * S::kThreads + threadIdx.x; x < teams * ROWS * (D / 4); x += p.cluster * S::kThreads) {
+            const int line = x / (D / 4), d0 = (x % (D / 4)) * 4, r = rg * teams * ROWS + line;
+            if (r >= R) continue;
+            CacheState st{-INFINITY, 0.f, -INFINITY};
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < p.cluster; ++k) {
+                const float4 s = ld_cluster(of_rank(box + 4 * (teams * ROWS * D + 4 * line), k));
+                st.m = fmaxf(st.m, s.x);
+                st.w = fmaxf(st.w, s.z);
+            }
+            for (int k = 0; k < p.cluster; ++k) {
+                const float4 s = ld_cluster(of_rank(box + 4 * (teams * ROWS * D + 4 * line), k));
+                const float4 u = ld_cluster(of_rank(box + 4 * (line * D + d0), k));
+                const float f = s.z == -INFINITY ? 1.f : ex2(s.z - st.w);
+                st.l += s.x == -INFINITY ? s.y : s.y * ex2(s.x - st.m);
+                v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+            }
+            store(r, d0, st, v);
+        }
+        cluster_sync();  // the others read this CTA's shared memory
     }
     fence_proxy_async_smem();  // the ring may be filled again
     __syncthreads();
@@ -560,8 +613,12 @@ __global__ void __launch_bounds__(CacheShape<NQ>::kThreads, 1)
     bool alive = true;
     const int per_b = c.H_kv * p.row_groups;  // segments of a sequence
     if (!p.spread) {
-        const int b = blockIdx.x / per_b, s = blockIdx.x - b * per_b;
-        attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups, 0, chunks_of(c, b, S::kKeys), -1);
+        const int segment = blockIdx.x / p.cluster, rank = blockIdx.x - segment * p.cluster, b = segment / per_b, s = segment - b * per_b;
+        const int n = chunks_of(c, b, S::kKeys);
+        const int64_t share = static_cast<int64_t>((n + S::kWarps - 1) / S::kWarps + p.cluster - 1) / p.cluster * S::kWarps;  // whole steps
+        attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups,
+                              static_cast<int>(min(rank * share, int64_t(n))), static_cast<int>(min((rank + 1) * share, int64_t(n))),
+                              p.cluster > 1 ? kToCluster : kToOutputs);
         return;
     }
     // this CTA's chunks [lo, hi) of all, counted through the segments of one sequence after the other
@@ -579,7 +636,7 @@ __global__ void __launch_bounds__(CacheShape<NQ>::kThreads, 1)
                 const bool whole = a >= lo && a + n <= hi;
                 alive = attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups,
                                       static_cast<int>(max(lo - a, int64_t(0))), static_cast<int>(min(hi - a, static_cast<int64_t>(n))),
-                                      whole ? int64_t(-1) : 2 * static_cast<int64_t>(blockIdx.x) + (a < lo ? 0 : 1));
+                                      whole ? kToOutputs : 2 * static_cast<int64_t>(blockIdx.x) + (a < lo ? 0 : 1));
             }
         }
         at = end;
@@ -640,13 +697,27 @@ template <int D, int NQ, bool SHARED>
 cudaError_t launch_cache8_attn_d(const CUtensorMap* maps, const CacheAttnParams& p, int ctas, cudaStream_t stream) {
     using S = CacheShape<NQ>;
     constexpr int ring = S::kWarps * kCwStages * 2 * S::kKeys * D, merge = S::kWarps * S::kRows * (D + 6) * 4;
-    static_assert(merge <= ring, "the states meet in the ring's space");
+    static_assert(merge + S::kRows * kCacheTeams * (D + 4) * 4 <= ring, "the states meet in the ring's space");
     constexpr int bytes = ring + 2 * S::kThreads * static_cast<int>(sizeof(PageEntry)) + 8 * kCwStages * S::kWarps + 1024;
     static_assert(bytes <= 232448, "shared memory");
     auto k = cache8_attn_kernel<D, NQ, SHARED>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(k, bytes, &done);
     if (e != cudaSuccess) return e;
+    if (p.cluster > 1) {
+        cudaLaunchAttribute shape{};
+        shape.id = cudaLaunchAttributeClusterDimension;
+        shape.val.clusterDim.x = p.cluster;
+        shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+        cudaLaunchConfig_t how{};
+        how.gridDim = dim3(ctas);
+        how.blockDim = dim3(S::kThreads);
+        how.dynamicSmemBytes = bytes;
+        how.stream = stream;
+        how.attrs = &shape;
+        how.numAttrs = 1;
+        return cudaLaunchKernelEx(&how, k, maps[0], maps[1], p);
+    }
     k<<<ctas, S::kThreads, bytes, stream>>>(maps[0], maps[1], p);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.spread) return e;
     const int64_t rows = int64_t(p.c.B) * p.H * p.Nq;
