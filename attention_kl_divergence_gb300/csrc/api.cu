@@ -313,7 +313,7 @@ streamkl_status plan_bwd(const streamkl_shape* s, int setting, int causal, const
 
 extern "C" {
 
-int streamkl_version(void) { return 300; }  // 0.3.0: score-modified divergence, norm with rotation
+int streamkl_version(void) { return 400; }  // 0.4.0: attention with gradients, 8-bit cache, rotation on several axes
 
 const char* streamkl_status_string(streamkl_status s) {
     switch (s) {

@@ -88,13 +88,19 @@ streamkl_status plan_cache_attn(const streamkl_cache8* s, const streamkl_options
     const int64_t row_groups = (row_tiles + pl->teams - 1) / pl->teams, segments = int64_t(s->B) * s->H_kv * row_groups;
     if (segments > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     pl->row_groups = static_cast<int>(row_groups);
-    // One CTA per segment where even the longest that the table allows is short, or where there are many of them.
-    const int64_t capacity = int64_t(s->M) * s->T, steps = (capacity + 255) / 256;  // 256 keys: a chunk of each warp
-    const int64_t wanted = opt && opt->num_splits > 0 ? opt->num_splits : capacity > 1024 && segments < 8 * int64_t(sms) ? sms : 0;
+    // A segment's CTAs form a cluster, as many as find room at a time (with this much shared memory no more than about a
+    // dozen clusters of 8).  Where that leaves a CTA more than a few steps of 256 keys, for the longest sequence that the
+    // table allows, equal shares of all sequences serve better than equal CTAs for unequal ones.  One token, 32 heads on
+    // 8, unequal lengths up to 4096 / 8192 / 16384 of 4 sequences: 12.9 / 16.9 / 26.3 us with clusters of 4, 21.4 / 24.1 /
+    // 30.3 with equal shares; of 8 sequences: 16.8 / 25.3 / 45.3 with clusters of 2, 24.1 / 29.0 / 45.1.  Eight tokens of
+    // 8: 38.0 / 64.7 / 117.6 against 42.5 / 58.8 / 94.7.
+    const int64_t capacity = int64_t(s->M) * s->T, steps = (capacity + 255) / 256;
+    int cluster = 1;
+    while (cluster < 8 && 2 * cluster <= steps && segments * 2 * cluster <= (cluster == 4 ? sms / 2 : sms)) cluster *= 2;
+    const bool few = (steps + cluster - 1) / cluster <= (pl->tile_rows == 8 ? 16 : 8);
+    const int64_t wanted = opt && opt->num_splits > 0 ? opt->num_splits : !few && segments < 8 * int64_t(sms) ? sms : 0;
     pl->spread = wanted > 0;
-    // A few CTAs share a short segment where they find room: a step takes about as long as adding up their sums.
-    pl->cluster = 1;
-    while (!pl->spread && pl->cluster < 8 && 2 * pl->cluster <= steps && segments * 2 * pl->cluster <= sms) pl->cluster *= 2;
+    pl->cluster = pl->spread ? 1 : cluster;
     pl->ctas = static_cast<int>(wanted > 0 ? std::min<int64_t>({wanted, segments * steps, int64_t(1) << 20}) : segments * pl->cluster);
     pl->ws_bytes = kStatusBytes;
     if (pl->spread) pl->ws_bytes += size_t(pl->ctas) * 2 * pl->tile_rows * pl->teams * (size_t(s->d) + 4) * sizeof(float);

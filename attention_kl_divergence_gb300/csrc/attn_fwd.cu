@@ -7,6 +7,15 @@
 // asked for), as two: the backward's row sums of dO O take O as that of exact
 // probabilities, and an error of theirs is a multiple of the row's mean key in dQ.  m_i is a
 // running maximum that may stay up to 2^8 behind.
+//
+// A CTA takes a pair of 128-row tiles that read the same keys (two heads of a key head, or
+// neighbouring rows): each key and value tile that TMA brings serves both, and while the
+// softmax of one runs the tensor core has the other's products.  A key tile takes a pair
+// about 3450 cycles, of which its MMAs need 2515 at the measured peak.  32768 causal rows,
+// 8 heads, d = 128: 1600 us, 1375 TFLOP/s.  8192 causal rows, 32 heads on 8, with rest:
+// 613 us, 897 TFLOP/s, and half as much again for the second term.  8192 rows in documents:
+// 191 us, 720 TFLOP/s; a CTA spends about 13000 cycles on its start and end there and 33000
+// on its key tiles.  One token over 4 caches of up to 65536 keys: 160 us, 5.9 TB/s.
 #include "attn.cuh"
 #include "bwd_common.cuh"
 #include "common.cuh"
@@ -23,7 +32,7 @@ constexpr float kAttnTau = 8.f;  // m may stay this far (log2) below the largest
 // warps 0-15 softmax (two warpgroups per tile of the pair: a thread has half of a row's
 // scores), 16 copies, 17 MMAs, 18 and 19 look for NaN and infinities in values that some
 // row must not see.  One warpgroup per tile, a row per thread, left its latencies
-// bare: 32768 causal rows, 8 heads, 1912 us.
+// bare: 1912 us where two took 1757, 32768 causal rows, 8 heads.
 constexpr int kAfThreads = 640;
 
 template <int D>
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         // S_s(t) = Q_s K(t)^T, then O_s += P_s(t) V(t) with P_s over S_s in tensor memory.  While one tile's
         // softmax runs, the tensor core works for the other.  The MMAs of a thread run in order: S_s(t + 1)
         // does not overwrite P_s(t) before O_s has taken it, and S_s(t + 1) complete means that O_s is too.
-        // (A thread for each tile: 2223 us instead of 1745 for 32768 causal rows, 8 heads: the MMAs of two
+        // (A thread for each tile: 2223 us where one takes 1745, 32768 causal rows, 8 heads: the MMAs of two
         // threads get in each other's way.)
         if (lane == 0 && t1 > t0) {
             constexpr uint32_t id_s = idesc_bf16_f32(kBlockQ, kBlockK), id_o = idesc_bf16_f32(kBlockQ, D, 0, 1);

@@ -15,9 +15,16 @@
 // A segment is one sequence's keys of one key head.  Its chunks are dealt out to the
 // warps of a CTA, each of which has a ring of its own that TMA fills, 16 tokens of a
 // page at a time.  With more than one row tile, teams of warps share the copies.
-// The lengths are known on the device alone: where there are too few segments to
-// fill the GPU evenly, every CTA takes the same number of chunks of all of them, one
-// after the other, and a second kernel adds up the parts of segments that were cut.
+// Short segments have a cluster of CTAs each, which add up their sums through shared
+// memory.  The lengths are known on the device alone: where the table allows long
+// ones, every CTA takes the same number of chunks of all segments, one after the
+// other, and a second kernel adds up the parts of segments that were cut.
+//
+// One token, 32 heads on 8, d = 128, 4 sequences of up to 131072 tokens: 160 us, 5.8 TB/s
+// (a copy: 6.8): about 20 us are start, ends and the second kernel, the rest runs near
+// the copy rate.  Five tokens of 3 sequences of up to 1000: 12.7 us (one CTA a segment:
+// 21.5), a chain of latencies.  With two teams (17 to 32 rows) the MMAs and conversions,
+// which each team does for itself, are the bound: 6600 cycles for 256 keys, 2.9 TB/s.
 #include "bwd_common.cuh"
 #include "cache8.cuh"
 #include "common.cuh"

@@ -23,7 +23,23 @@ key heads with their rotation:
     qk_norm_rope(q, k, wq, wk, table, positions=None) -> (q', k')
     qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, table, positions=None) -> (dq, dk, dwq, dwk)
 
-and ``QKNormRope``, its autograd Function.  There is no fallback: without the compiled library
+and ``QKNormRope``, its autograd Function; with positions on several axes (time, height, width) and
+``axes=rope_axes(sections)`` each pair turns by the position on an axis of its own.  The attention itself, over
+whole prompts and with gradients:
+
+    attn_fwd(Q, K, V, ranges=key_ranges(...)) -> (O, LSE)
+    attn_fwd(Q, K, V, ranges, rest=True) -> (O, LSE, rest)
+    attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges) -> (dQ, dK, dV)
+
+and ``Attention``, its autograd Function.  For serving, a paged cache of keys and values in 8 bits and the attention of a
+few new tokens over it:
+
+    cache = Cache8.empty(pages, heads, tokens, d, device)
+    cache8_append(cache, table, lengths, k, v, counts=None)
+    attn_cache8(Q, cache, table, lengths) -> (O, LSE)
+    cache8_read(cache, table, lengths) -> (K, V)
+
+There is no fallback: without the compiled library
 every call raises.
 """
 from __future__ import annotations
