@@ -40,6 +40,8 @@ streamkl_status check_desc(const streamkl_attn* s, bool backward) {
         !strides_ok(s->v, s->B, s->H_kv, s->Nk, s->d) || !strides_ok(s->o, s->B, s->H, s->Nq, s->d) ||
         (backward && !strides_ok(s->d_o, s->B, s->H, s->Nq, s->d)))
         return STREAMKL_ERR_INVALID_ARG;
+    // rows and keys are counted in 32 bits, up to the end of their tiles
+    if (s->Nq > INT32_MAX - 2 * kBlockQ || s->Nk > INT32_MAX - 2 * kBlockK) return STREAMKL_ERR_UNSUPPORTED;
     if (int64_t(s->B) * s->H > (int64_t(1) << 24) || int64_t(s->B) * s->H * s->Nq > (int64_t(1) << 38))
         return STREAMKL_ERR_UNSUPPORTED;
     return STREAMKL_OK;
@@ -105,7 +107,15 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
     p.num_splits = splits;
     p.parts = p.dual ? 2 * splits : splits;
     pl->ctas = static_cast<int>(units * splits);
-    p.order_group = order_group(heads, p.units_q, sms);
+    const int group = order_group(heads, p.units_q, sms), last = static_cast<int>(heads % group);
+    if (int64_t(group) * p.units_q > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
+    p.order_group = FastDiv::by(group);
+    p.order_last = FastDiv::by(last ? last : group);
+    p.order_units = FastDiv::by(int64_t(group) * p.units_q);
+    p.by_splits = FastDiv::by(splits);
+    p.by_units_h = FastDiv::by(p.units_h);
+    p.by_H_kv = FastDiv::by(p.H_kv);
+    p.by_rows = FastDiv::by(p.rows);
     pl->ws_bytes = kStatusBytes;
     if (p.parts > 1) pl->ws_bytes += size_t(p.parts) * s->B * s->H * s->Nq * (size_t(s->d) + 2) * sizeof(float);
     return STREAMKL_OK;

@@ -9,6 +9,26 @@
 
 namespace streamkl {
 
+// Division of 0 <= n < 2^31 by a number that the host knows: with 2^s >= d the smallest such power and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n m / 2^32 + n) / 2^s, all rounded down.  A CTA's first steps are a chain of
+// six of them (the smallest call, in a graph: 8.2 us with the compiler's, 7.8 with these).
+struct FastDiv {
+    uint32_t d, m;
+    int s;
+    static FastDiv by(int64_t d) {
+        FastDiv f{static_cast<uint32_t>(d), 0, 0};
+        while ((int64_t(1) << f.s) < d) ++f.s;
+        f.m = static_cast<uint32_t>((uint64_t(1) << 32) * static_cast<uint64_t>((int64_t(1) << f.s) - d) / static_cast<uint64_t>(d) + 1);
+        return f;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const {
+        const uint32_t t = __umulhi(static_cast<uint32_t>(n), m);
+        return static_cast<int>(s == 0 ? n : (t + ((n - t) >> 1)) >> (s - 1));
+    }
+#endif
+};
+
 // Forward.  A 128-row tile holds `heads` query heads of one key head with `rows`
 // rows each (few rows: several heads share a tile; else one head and 128 rows).  A
 // work item is a pair of tiles that read the same keys: two head blocks, or two
@@ -23,7 +43,10 @@ struct AttnFwdParams {
     int dual;                // a tile without another to pair with stands twice, each with every second key tile
     int num_splits;
     int parts;               // of a row: num_splits, twice that if dual; 1: outputs
-    int order_group;         // see grouped_order
+    // units in groups of heads, tiles slow and heads fast in a group (see grouped_order): heads of a group, of the last
+    // one, and units of a group
+    FastDiv order_group, order_last, order_units;
+    FastDiv by_splits, by_units_h, by_H_kv, by_rows;
     float c;                 // softmax scale * log2(e)
     void* O;                 // bf16, strided
     int64_t o_b, o_h, o_n;

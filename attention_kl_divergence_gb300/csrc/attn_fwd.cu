@@ -182,17 +182,20 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the pair's tiles; in a group of heads the last query tiles of every head come first
-    const int unit = blockIdx.x / p.num_splits, split = blockIdx.x - unit * p.num_splits;
-    const int2 at = grouped_order(unit, p.units_q, p.B * p.H_kv * p.units_h, p.order_group);
-    const int bkv = at.x / p.units_h, hb = at.x - bkv * p.units_h, qu = p.units_q - 1 - at.y;
-    const int b = bkv / p.H_kv, hk = bkv - b * p.H_kv;
+    const int unit = p.by_splits.of(blockIdx.x), split = blockIdx.x - unit * p.num_splits;
+    const int og = p.order_units.of(unit), first_head = og * p.order_group.d, rest_units = unit - first_head * p.units_q;
+    const bool last_group = first_head + static_cast<int>(p.order_group.d) >= p.B * p.H_kv * p.units_h;
+    const int from_end = last_group ? p.order_last.of(rest_units) : p.order_group.of(rest_units);
+    const int head = first_head + rest_units - from_end * static_cast<int>(last_group ? p.order_last.d : p.order_group.d);
+    const int bkv = p.by_units_h.of(head), hb = head - bkv * p.units_h, qu = p.units_q - 1 - from_end;
+    const int b = p.by_H_kv.of(bkv), hk = bkv - b * p.H_kv;
     auto block_of = [&](int s) { return p.pair_heads ? 2 * hb + s : hb; };
     auto qtile_of = [&](int s) { return p.pair_heads || p.dual ? qu : 2 * qu + s; };
     auto exists = [&](int s) { return block_of(s) < p.blocks && qtile_of(s) < p.q_tiles; };
 
     // a softmax thread's row: its keys, and whether there is such a row; the thread has 64 of a tile's columns
     const int sub = (warp >> 3) & 1, side = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
-    const int in_block = row / p.rows, i = qtile_of(sub) * kBlockQ + row - in_block * p.rows;
+    const int in_block = p.by_rows.of(row), i = qtile_of(sub) * kBlockQ + row - in_block * p.rows;
     const bool valid = warp < 16 && exists(sub) && in_block < p.heads && i < p.Nq;
     const int2 range = valid ? row_range(sp, p.Nq, p.Nk, b, i) : make_int2(0, 0);
     if (base & 1023u) {  // reported, not expected: every row becomes NaN

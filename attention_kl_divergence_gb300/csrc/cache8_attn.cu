@@ -108,8 +108,7 @@ __device__ __forceinline__ float ratio(float from, float to) { return from == -I
 
 // Chunks of `keys` keys of sequence b.
 __device__ __forceinline__ int chunks_of(const CacheView& c, int b, int keys) {
-    const int64_t n = min(static_cast<int64_t>(max(c.lengths[b], 0)), static_cast<int64_t>(c.M) * c.T);
-    return static_cast<int>((n + keys - 1) / keys);
+    return (min(max(c.lengths[b], 0), c.M * c.T) + keys - 1) / keys;  // a table has up to 2^30 tokens
 }
 
 // A warp sums the chunks of all sequences, and of those before b.
@@ -567,7 +566,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
     if (part == kToCluster) {  // the sums of the cluster's CTAs, each of which writes some of the rows
         cluster_sync();
         const uint32_t box = smem_u32(outbox);
-        const int rank = blockIdx.x % p.cluster;
+        const int rank = blockIdx.x & (p.cluster - 1);  // a power of two
         for (int x = rank * S::kThreads + threadIdx.x; x < teams * ROWS * (D / 4); x += p.cluster * S::kThreads) {
             const int line = x / (D / 4), d0 = (x % (D / 4)) * 4, r = rg * teams * ROWS + line;
             if (r >= R) continue;
@@ -620,12 +619,12 @@ __global__ void __launch_bounds__(CacheShape<NQ>::kThreads, 1)
     bool alive = true;
     const int per_b = c.H_kv * p.row_groups;  // segments of a sequence
     if (!p.spread) {
-        const int segment = blockIdx.x / p.cluster, rank = blockIdx.x - segment * p.cluster, b = segment / per_b, s = segment - b * per_b;
-        const int n = chunks_of(c, b, S::kKeys);
-        const int64_t share = static_cast<int64_t>((n + S::kWarps - 1) / S::kWarps + p.cluster - 1) / p.cluster * S::kWarps;  // whole steps
-        attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, s / p.row_groups, s % p.row_groups,
-                              static_cast<int>(min(rank * share, int64_t(n))), static_cast<int>(min((rank + 1) * share, int64_t(n))),
-                              p.cluster > 1 ? kToCluster : kToOutputs);
+        const int cluster = p.cluster, segment = static_cast<unsigned>(blockIdx.x) >> (__ffs(cluster) - 1), rank = blockIdx.x & (cluster - 1);
+        const int b = segment / per_b, s = segment - b * per_b, hk = p.row_groups == 1 ? s : s / p.row_groups;
+        const int n = chunks_of(c, b, S::kKeys);  // below 2^26
+        const int share = (((n + S::kWarps - 1) / S::kWarps + cluster - 1) >> (__ffs(cluster) - 1)) * S::kWarps;  // whole steps
+        attend<D, NQ, SHARED>(p, &tK, &tV, smem, uses, wc, alive, b, hk, s - hk * p.row_groups, min(rank * share, n),
+                              min((rank + 1) * share, n), cluster > 1 ? kToCluster : kToOutputs);
         return;
     }
     // this CTA's chunks [lo, hi) of all, counted through the segments of one sequence after the other
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
     }
-    const bool empty = c.lengths[b] - p.Nq + 1 + i <= 0;
+    const bool empty = max(c.lengths[b], 0) - p.Nq + 1 + i <= 0;
     const float f = empty ? 0.f : output_factor(st);
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + lane * V);
 #pragma unroll

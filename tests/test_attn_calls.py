@@ -442,7 +442,8 @@ def test_abi_rejects_bad_descriptions_and_pointers_without_a_device():
                                      *[P(p) for p in ptrs[10:]], P(ws), nbytes, opts, P(0))
 
     wrong = [(None, sk.ERR_INVALID_ARG), (desc(d=96), sk.ERR_UNSUPPORTED), (desc(H=3), sk.ERR_INVALID_ARG),
-             (desc(H=1 << 24, H_kv=1 << 24), sk.ERR_UNSUPPORTED)]
+             (desc(H=1 << 24, H_kv=1 << 24), sk.ERR_UNSUPPORTED), (desc(Nq=2 ** 31 - 1), sk.ERR_UNSUPPORTED),
+             (desc(Nk=2 ** 31 - 1), sk.ERR_UNSUPPORTED)]
     wrong += [(desc(**{n: v}), sk.ERR_INVALID_ARG) for n in ("B", "H", "H_kv", "Nq", "Nk") for v in (0, -1)]
     for name in ("q", "k", "v", "o"):
         for st in ((56, 512, 64), (2048, 512, 0), (2048, 516, 64), (-2048, 512, 64), (2048, 512, 1 << 39), (0, 512, 64), (2048, 0, 64)):

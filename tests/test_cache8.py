@@ -386,6 +386,19 @@ def test_outputs_streams_graphs_and_in_place_changes():
 
 
 @gpu
+@pytest.mark.parametrize("splits", [0, 3])
+def test_lengths_below_zero_are_zero(splits):
+    B, H, Hk, Nq, T, d, M = 4, 4, 2, 5, 16, 64, 100
+    table, pages = tables(B, M)
+    cache = pool(pages, Hk, T, d)
+    Q = torch.randn(B, H, Nq, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(BF16)
+    n = torch.tensor([-2 ** 31, -1, 1000, 0], dtype=torch.int32, device=DEV)
+    O, LSE = sk.attn_cache8(Q, cache, table, n, num_splits=splits)
+    Ref(Q, cache, table, n.clamp(min=0)).check(O, LSE)
+    assert all(bool((t[[0, 1, 3]] == 0).all()) for t in sk.cache8_read(cache, table, n))
+
+
+@gpu
 def test_pages_beyond_32_bits_of_bytes():
     """The last pages of a cache of 4.4 GB each for keys and values, and the same pages of a small one."""
     B, H, Hk, T, d, M = 2, 8, 2, 128, 128, 5
