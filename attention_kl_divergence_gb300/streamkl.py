@@ -1169,7 +1169,7 @@ def cache8_append(cache, table, lengths, k, v, counts=None) -> None:
     smallest power of two 2^e, e >= -100, that brings every finite value within 448, and never shrinks while the page is
     being filled: tokens that it holds are rounded again where it grows.  NaN and infinities are stored as NaN.  Tokens
     behind the table, or of a page outside the cache, are not written.  lengths stay as they are (lengths + counts is for
-    the caller to keep); two sequences must not append to one page in one call."""
+    the caller to keep).  A page that a call appends to must be listed once, by one sequence."""
     held = _cache(cache)
     key, known = _lookup("cache8_append", _tensors(*held, table, lengths, k, v, counts))
     if known is None:

@@ -473,7 +473,7 @@ STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const 
  * of the sequence before; those are then rounded to the new scale.  NaN and
  * infinities are stored as NaN.  Rows of the page behind the new tokens stay as
  * they are.  Tokens behind the table, or of a page outside [0, pages), are not
- * written.  Two sequences must not append to one page in one call.
+ * written.  A page that a call appends to is listed once, by one sequence.
  *
  * read gathers the first N tokens of each sequence as bf16 [B, H_kv, N, d]: zeros
  * behind lengths[b], NaN for pages that are not there.
