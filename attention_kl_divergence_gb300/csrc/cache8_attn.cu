@@ -20,7 +20,7 @@
 // ones, every CTA takes the same number of chunks of all segments, one after the
 // other, and a second kernel adds up the parts of segments that were cut.
 //
-// One token, 32 heads on 8, d = 128, 4 sequences of up to 131072 tokens: 160 us, 5.8 TB/s
+// One token, 32 heads on 8, d = 128, 4 sequences of up to 131072 tokens: 162 us, 5.7 TB/s
 // (a copy: 6.8): about 20 us are start, ends and the second kernel, the rest runs near
 // the copy rate.  Five tokens of 3 sequences of up to 1000: 12.7 us (one CTA a segment:
 // 21.5), a chain of latencies.  With two teams (17 to 32 rows) the MMAs and conversions,
