@@ -12,8 +12,8 @@
 // neighbouring rows): each key and value tile that TMA brings serves both, and while the
 // softmax of one runs the tensor core has the other's products.  A key tile takes a pair
 // about 3450 cycles, of which its MMAs need 2515 at the measured peak.  32768 causal rows,
-// 8 heads, d = 128: 1600 us, 1375 TFLOP/s.  8192 causal rows, 32 heads on 8, with rest:
-// 613 us, 897 TFLOP/s, and half as much again for the second term.  8192 rows in documents:
+// 8 heads, d = 128: 1594 us, 1379 TFLOP/s.  8192 causal rows, 32 heads on 8, with rest:
+// 592 us, 929 TFLOP/s, and half as much again for the second term.  8192 rows in documents:
 // 191 us, 720 TFLOP/s; a CTA spends about 13000 cycles on its start and end there and 33000
 // on its key tiles.  One token over 4 caches of up to 65536 keys: 160 us, 5.9 TB/s.
 #include "attn.cuh"
@@ -30,10 +30,10 @@ namespace {
 
 constexpr float kAttnTau = 8.f;  // m may stay this far (log2) below the largest score
 // warps 0-15 softmax (two warpgroups per tile of the pair: a thread has half of a row's
-// scores), 16 copies, 17 MMAs, 18 and 19 look for NaN and infinities in values that some
-// row must not see.  One warpgroup per tile, a row per thread, left its latencies
+// scores), 16 copies, 17 MMAs, 18 looks for NaN and infinities in values that some row must
+// not see (two such warps: 8192 causal rows, 32 heads on 8, with rest 613 us, one 592).  One warpgroup per tile, a row per thread, left its latencies
 // bare: 1912 us where two took 1757, 32768 causal rows, 8 heads.
-constexpr int kAfThreads = 640;
+constexpr int kAfThreads = 608;
 
 template <int D>
 struct AttnSmem {
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         for (int s = 0; s < NST; ++s) {
             mbar_init(base + L::bar_full + 8 * s, 1);
-            mbar_init(base + L::bar_empty + 8 * s, 3);  // the MMAs and the two checking warps
-            mbar_init(base + L::bar_clean + 8 * s, 2);
+            mbar_init(base + L::bar_empty + 8 * s, 2);  // the MMAs and the checking warp
+            mbar_init(base + L::bar_clean + 8 * s, 1);
         }
         mbar_init(base + L::bar_done, 1);
         *abort_flag = 0;
@@ -405,11 +405,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 drain_wait_b(base + L::bar_done, 0, kDrainNs);
             }
         }
-    } else if (warp >= 18) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------ value check
         // A probability of 0 does not hide a NaN or an infinity in the value that it meets in the MMA.  In tiles
         // that some row does not see all of, keys with such values get zeros, and rows that see them become NaN.
-        // The warps wait for every copy of the ring in turn and release every stage with the MMAs: a wait that skipped
+        // The warp waits for every copy of the ring in turn and releases every stage with the MMAs: a wait that skipped
         // a stage's use would take the use before it for its own.  The k-th check uses slot k % NST: the ring holds
         // fewer value tiles than there are slots.
         int k_check = 0;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             const int slot = k_check++ % NST;
             const uint8_t* tile = gbase + L::kv + st * L::kTile;
 #pragma unroll 1
-            for (int r0 = 32 * (warp - 18); r0 < kBlockK; r0 += 64) {
+            for (int r0 = 0; r0 < kBlockK; r0 += 32) {
                 const int r = r0 + lane;
                 uint32_t sum = 0u;  // 0 x: NaN where x is not finite
 #pragma unroll 2
