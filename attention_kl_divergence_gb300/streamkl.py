@@ -134,6 +134,8 @@ def library_path() -> str:
 def load(build_if_stale: bool = True):
     """Load libstreamkl.so (building it first when sources are newer)."""
     global _lib
+    if _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -512,9 +514,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(device, function, *args):
     """function(*args, current stream of device) with the device current."""
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         return function(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
         return function(*args, torch.cuda.current_stream(device).cuda_stream)
