@@ -127,10 +127,9 @@ __device__ __noinline__ void mark_attn_gradients(const AttnBwdParams& p, int d, 
 }
 
 // ---------------------------------------------------------------------------
-// CTA = 128 keys; 64-row query tiles.  Warps: 0 copies, 1 TMEM + the MMAs of S and
-// dP, 2-9 P and dS (two warpgroups, one key per thread, each taking 32 of the
-// tile's 64 query rows), 10-13 dQ^T accumulator -> bulk reduce-add into global dQ,
-// 14 gradient MMAs.  TMEM: S^T | dP^T (cols 0-127), dK (128-255), dV (256-383), dQ^T
+// CTA = 128 keys; 64-row query tiles.  Warps: 0 copies, 1 TMEM + the MMAs, 2-9 P and
+// dS (two warpgroups, one key per thread, each taking 32 of the tile's 64 query
+// rows), 10-13 dQ^T accumulator -> bulk reduce-add into global dQ.  TMEM: S^T | dP^T (cols 0-127), dK (128-255), dV (256-383), dQ^T
 // of the hi | lo halves of dS (384-511).
 // ---------------------------------------------------------------------------
 template <int D>
@@ -165,12 +164,12 @@ struct AttnKvSmem {
     static constexpr int bar_dqfull = bar_dsempty + 8;
     static constexpr int bar_dqempty = bar_dqfull + 8;
     static constexpr int bar_done = bar_dqempty + 8;
-    static constexpr int bar_drain = bar_done + 8;     // the score issuer's own drain on abort
+    static constexpr int bar_drain = bar_done + 8;     // the issuer's own drain on abort
     static constexpr int misc = bar_drain + 8;         // tmem base, abort flag, first and last query tile
     static constexpr int alloc = misc + 16;            // no slack: the kernel checks the base is 1024-byte aligned
 };
 
-constexpr int kAbThreads = 480;
+constexpr int kAbThreads = 448;
 
 template <int D>
 __global__ void __launch_bounds__(kAbThreads, 1)
@@ -185,7 +184,6 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::misc);
     int* tile_span = reinterpret_cast<int*>(gbase + L::misc + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kGradWarp = kAbThreads / 32 - 1;
 
     // groups of key heads, a few waves of CTAs each, so that resident CTAs share query tiles through L2; in a
     // group the first key tiles of every head, which the most rows see under a causal mask, come first
@@ -316,90 +314,80 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         if (lane == 0) drain_wait_b(base + L::bar_k, 0, kDrainNs);
     } else if (warp == 1) {
-        // ------------------------------------------------ S^T = K Q^T, dP^T = V dO^T
-        // Two threads issue the MMAs: this one the scores of tile m, the gradient warp's first thread the dV, dK
-        // and dQ^T MMAs of earlier tiles; neither waits on the other's barriers.
-        if (lane == 0) {
+        // ------------------------------------------------ MMAs
+        // Scores of tile m: S^T = K Q^T, dP^T = V dO^T.  Gradients of tile m: dV += P^T dO, dK += dS^T Q and
+        // [dQ^T_hi | dQ^T_lo] = K^T [dS^T_hi | dS^T_lo].  One thread issues them in the order in which they are wanted:
+        // the scores of tile m + 2 behind the gradients of tile m, for whose end the update warps wait with P and dS of
+        // tile m + 1.  (Issued by a thread of their own they got between the gradients: 8192 causal rows, 32 heads on
+        // 8, 1623 us.)
+        if (lane == 0 && n_tiles > 0) {
             constexpr uint32_t id_s = idesc_bf16_f32(kBlockK, kBwdTile);
-            const uint32_t dhi = smem_desc_hi();
-            const uint32_t k_lo = smem_desc_lo_k128(base + L::k), v_lo = smem_desc_lo_k128(base + L::v);
-            int issued = 0;
-            // test aid: a wait on a barrier that nothing arrives on before the end
-            const bool stalled = p.inject_stall && blockIdx.x == 0 && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther);
-            if (!stalled && n_tiles > 0 && mbar_wait(base + L::bar_k, 0, wc, kErrWaitK)) {
-                for (int m = 0; m < n_tiles; ++m) {
-                    const int st = m % L::kNst;
-                    if (!mbar_wait(base + L::bar_full + 8 * st, (m / L::kNst) & 1, wc, kErrWaitQ)) break;
-                    if (!mbar_wait(base + L::bar_sempty, (m & 1) ^ 1, wc, kErrWaitS)) break;
-                    tc_fence_after();
-                    const uint32_t q_lo = smem_desc_lo_k128(base + L::q + st * L::kQBytes), g_lo = smem_desc_lo_k128(base + L::g + st * L::kQBytes);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t ko = ((kk >> 2) * kBlockK * 128 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * kBwdTile * 128 + (kk & 3) * 32) >> 4;
-                        tc_mma_bf16_w(tmem, k_lo + ko, dhi, q_lo + qo, dhi, id_s, kk > 0);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t ko = ((kk >> 2) * kBlockK * 128 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * kBwdTile * 128 + (kk & 3) * 32) >> 4;
-                        tc_mma_bf16_w(tmem + 64, v_lo + ko, dhi, g_lo + qo, dhi, id_s, kk > 0);
-                    }
-                    tc_commit(base + L::bar_sfull);
-                    ++issued;
-                }
-            }
-            if (*abort_flag && issued > 0) {  // let the issued MMAs retire before TMEM is freed
-                tc_commit(base + L::bar_drain);
-                drain_wait_b(base + L::bar_drain, 0, kDrainNs);
-            }
-        }
-    } else if (warp == kGradWarp) {
-        // ------------------------------------------------ gradient MMAs
-        // tile m's P and dS (from the update warps) -> dV += P^T dO, dK += dS^T Q and
-        // [dQ^T_hi | dQ^T_lo] = K^T [dS^T_hi | dS^T_lo]; then the buffers and the query stage are released.
-        // (Tile m's scores finished before its dS existed, so these commits also cover the MMAs that read the stage.)
-        if (lane == 0) {
             constexpr uint32_t id_dk = idesc_bf16_f32(kBlockK, D, 0, 1);
             constexpr uint32_t id_dq = idesc_bf16_f32(128, 2 * kBwdTile, 1, 1);  // M = 128 features (d = 64: padded)
             // A = K^T as 64-feature atoms: the tile's second block, or the zero atom when d = 64
             const uint32_t a_atom = D == 128 ? kBlockK * 128 : L::zero - L::k;
             const uint32_t t_dk = tmem + 128, t_dv = tmem + 256, t_dq = tmem + 384;
             const uint32_t dhi = smem_desc_hi();
+            const uint32_t k_lo = smem_desc_lo_k128(base + L::k), v_lo = smem_desc_lo_k128(base + L::v);
             const uint32_t ds_lo = smem_desc_lo_k128(base + L::ds), p_lo = smem_desc_lo_k128(base + L::pt);
             const uint32_t dsmn_lo = smem_desc_lo_mn128(base + L::ds, L::kDsBytes);
             const uint32_t kt_lo = smem_desc_lo_mn128(base + L::k, a_atom);
             int issued = 0;
-            if (n_tiles > 0 && mbar_wait(base + L::bar_k, 0, wc, kErrWaitK)) {
-                for (int m = 0; m < n_tiles; ++m) {
-                    const int st = m % L::kNst;
-                    if (!mbar_wait(base + L::bar_dsfull, m & 1, wc, kErrWaitOther)) break;
-                    tc_fence_after();
-                    const uint32_t q_lo = smem_desc_lo_mn128(base + L::q + st * L::kQBytes, kBwdTile * 128);
-                    const uint32_t g_lo = smem_desc_lo_mn128(base + L::g + st * L::kQBytes, kBwdTile * 128);
+            auto scores = [&](int m) {
+                const int st = m % L::kNst;
+                if (!mbar_wait(base + L::bar_full + 8 * st, (m / L::kNst) & 1, wc, kErrWaitQ)) return false;
+                if (!mbar_wait(base + L::bar_sempty, (m & 1) ^ 1, wc, kErrWaitS)) return false;
+                tc_fence_after();
+                const uint32_t q_lo = smem_desc_lo_k128(base + L::q + st * L::kQBytes), g_lo = smem_desc_lo_k128(base + L::g + st * L::kQBytes);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ko = ((kk >> 2) * kBlockK * 128 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * kBwdTile * 128 + (kk & 3) * 32) >> 4;
+                    tc_mma_bf16_w(tmem, k_lo + ko, dhi, q_lo + qo, dhi, id_s, kk > 0);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ko = ((kk >> 2) * kBlockK * 128 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * kBwdTile * 128 + (kk & 3) * 32) >> 4;
+                    tc_mma_bf16_w(tmem + 64, v_lo + ko, dhi, g_lo + qo, dhi, id_s, kk > 0);
+                }
+                tc_commit(base + L::bar_sfull);
+                ++issued;
+                return true;
+            };
+            auto gradients = [&](int m) {
+                const int st = m % L::kNst;
+                if (!mbar_wait(base + L::bar_dsfull, m & 1, wc, kErrWaitOther)) return false;
+                tc_fence_after();
+                const uint32_t q_lo = smem_desc_lo_mn128(base + L::q + st * L::kQBytes, kBwdTile * 128);
+                const uint32_t g_lo = smem_desc_lo_mn128(base + L::g + st * L::kQBytes, kBwdTile * 128);
+#pragma unroll
+                for (int kk = 0; kk < kBwdTile / 16; ++kk)
+                    tc_mma_bf16_w(t_dv, p_lo + ((kk * 32) >> 4), dhi, g_lo + ((kk * 16 * 128) >> 4), dhi, id_dk, (kk | m) != 0);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kBwdTile / 16; ++kk)
-                        tc_mma_bf16_w(t_dv, p_lo + ((kk * 32) >> 4), dhi, g_lo + ((kk * 16 * 128) >> 4), dhi, id_dk, (kk | m) != 0);
+                        tc_mma_bf16_w(t_dk, ds_lo + ((part * L::kDsBytes + kk * 32) >> 4), dhi, q_lo + ((kk * 16 * 128) >> 4), dhi, id_dk,
+                                      (kk | part | m) != 0);
+                ++issued;
+                if (!mbar_wait(base + L::bar_dqempty, (m & 1) ^ 1, wc, kErrWaitOther)) return false;
+                tc_fence_after();
+                // B = the hi and lo tiles as two 64-query atoms of one N = 128 operand, K = 128 keys
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int kk = 0; kk < kBwdTile / 16; ++kk)
-                            tc_mma_bf16_w(t_dk, ds_lo + ((part * L::kDsBytes + kk * 32) >> 4), dhi, q_lo + ((kk * 16 * 128) >> 4), dhi, id_dk,
-                                          (kk | part | m) != 0);
-                    ++issued;
-                    if (!mbar_wait(base + L::bar_dqempty, (m & 1) ^ 1, wc, kErrWaitOther)) break;
-                    tc_fence_after();
-                    // B = the hi and lo tiles as two 64-query atoms of one N = 128 operand, K = 128 keys
-#pragma unroll
-                    for (int kk = 0; kk < kBlockK / 16; ++kk)
-                        tc_mma_bf16_w(t_dq, kt_lo + ((kk * 16 * 128) >> 4), dhi, dsmn_lo + ((kk * 16 * 128) >> 4), dhi, id_dq, kk > 0);
-                    tc_commit(base + L::bar_dqfull);
-                    tc_commit(base + L::bar_dsempty);
-                    tc_commit(base + L::bar_empty + 8 * st);
-                    if (m + 1 == n_tiles) tc_commit(base + L::bar_done);
-                }
-            }
+                for (int kk = 0; kk < kBlockK / 16; ++kk)
+                    tc_mma_bf16_w(t_dq, kt_lo + ((kk * 16 * 128) >> 4), dhi, dsmn_lo + ((kk * 16 * 128) >> 4), dhi, id_dq, kk > 0);
+                tc_commit(base + L::bar_dsempty);
+                tc_commit(base + L::bar_dqfull);
+                tc_commit(base + L::bar_empty + 8 * st);
+                if (m + 1 == n_tiles) tc_commit(base + L::bar_done);
+                return true;
+            };
+            // test aid: a wait on a barrier that nothing arrives on before the end
+            bool ok = !(p.inject_stall && blockIdx.x == 0 && !mbar_wait(base + L::bar_done, 0, wc, kErrWaitOther));
+            ok = ok && mbar_wait(base + L::bar_k, 0, wc, kErrWaitK) && scores(0) && (n_tiles == 1 || scores(1));
+            for (int m = 0; ok && m < n_tiles; ++m) ok = gradients(m) && (m + 2 >= n_tiles || scores(m + 2));
             if (*abort_flag && issued > 0) {  // let the issued MMAs retire before TMEM is freed
-                tc_commit(base + L::bar_done);
-                drain_wait_b(base + L::bar_done, 0, kDrainNs);
+                tc_commit(base + L::bar_drain);
+                drain_wait_b(base + L::bar_drain, 0, kDrainNs);
             }
         }
     } else if (warp < 10) {
