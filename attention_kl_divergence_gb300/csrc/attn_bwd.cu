@@ -17,9 +17,11 @@
 //
 // Bound by shared memory: of its 128 bytes a cycle the MMAs of a tile take about 2000 cycles
 // (an operand of 64 rows is read for no more than 64 columns) and the stores of P, dS and dQ
-// with the copies about 1150, of 3500 that a tile takes.  8192 causal rows, 32 heads on 8,
-// d = 128: 1623 us, 847 TFLOP/s of the five products, and 57 + 27 us for the first and the
-// last kernel, which are bound by HBM.  128-row query tiles, with P and dS as operands in
+// with the copies about 1150, of 3200 that a tile takes.  8192 causal rows, 32 heads on 8,
+// d = 128: 1568 us, 877 TFLOP/s of the five products, and 55 + 27 us for the first and the
+// last kernel, which are bound by HBM.  Reductions into dQ out of registers, without the
+// stage in shared memory, took 1660 us for the three where these take 1653 (d = 64: 1524,
+// 1420).  128-row query tiles, with P and dS as operands in
 // tensor memory and dQ in dP's place there, took 3357 us: no space is left for a second tile,
 // and the steps of one stand in a chain.
 #include <algorithm>
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         // [dQ^T_hi | dQ^T_lo] = K^T [dS^T_hi | dS^T_lo].  One thread issues them in the order in which they are wanted:
         // the scores of tile m + 2 behind the gradients of tile m, for whose end the update warps wait with P and dS of
         // tile m + 1.  (Issued by a thread of their own they got between the gradients: 8192 causal rows, 32 heads on
-        // 8, 1623 us.)
+        // 8, 1713 us for the three kernels where one thread takes 1652; 16 heads, full, 1729 and 1557.)
         if (lane == 0 && n_tiles > 0) {
             constexpr uint32_t id_s = idesc_bf16_f32(kBlockK, kBwdTile);
             constexpr uint32_t id_dk = idesc_bf16_f32(kBlockK, D, 0, 1);
