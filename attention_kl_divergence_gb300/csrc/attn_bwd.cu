@@ -15,9 +15,10 @@
 // rounding left (`rest`), for the same reason: an error of D is a multiple of the
 // row's mean key in dQ.
 //
-// Bound by shared memory: of its 128 bytes a cycle the MMAs of a tile take about 2000 cycles
-// (an operand of 64 rows is read for no more than 64 columns) and the stores of P, dS and dQ
-// with the copies about 1150, of 3200 that a tile takes.  8192 causal rows, 32 heads on 8,
+// Bound by the tensor core: the issuing thread never waits for more than a barrier's own
+// latency, and is held back by 36 MMAs a tile of 65 to 82 cycles each, 2600 of about 3200.
+// The scores' have N = 64 and take 73, no less than those with N = 128 (d = 64: 28 MMAs,
+// 2100 of 2830 cycles, with half the operations).  8192 causal rows, 32 heads on 8,
 // d = 128: 1568 us, 877 TFLOP/s of the five products, and 55 + 27 us for the first and the
 // last kernel, which are bound by HBM.  Reductions into dQ out of registers, without the
 // stage in shared memory, took 1660 us for the three where these take 1653 (d = 64: 1524,
