@@ -51,6 +51,7 @@ struct CacheShape {
 constexpr int kCwStages = 3;      // a warp's chunks in its ring: one in use, the others on their way
 constexpr float kCwTau = 8.f;     // references may stay this far (log2) below the largest value
 constexpr float kCwShift = 7.f;   // probabilities are at most 2^(8 + 7) < 65504
+constexpr float kCwNone = -1e30f; // the output's reference where there is none yet
 
 // 16 rows of d bytes, swizzled so that 8 rows' pieces lie in different banks.
 __device__ __forceinline__ void copy_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row) {
@@ -99,12 +100,19 @@ struct PageEntry {
     int pad;
 };
 
-// States of one row merge by their references: m of the probabilities, w of the output.
+// States of one row merge by their references: m of the probabilities, and how far above it (log2) that of the output's
+// sums lies.  (A distance: both are whole numbers, and float32 adds 7 or a scale's exponent to a distance exactly, to a
+// score beyond 2^24 not.)
 struct CacheState {
-    float m, l, w;
+    float m, l, up;
 };
 
 __device__ __forceinline__ float ratio(float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); }
+
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+
+// The distance from another m, not below the state's own; -inf without a reference: 0 sums, or NaN scores alone.
+__device__ __forceinline__ float up_from(float m, float up, float top) { return m == -INFINITY ? -INFINITY : up + (m - top); }
 
 // Chunks of `keys` keys of sequence b.
 __device__ __forceinline__ int chunks_of(const CacheView& c, int b, int keys) {
@@ -157,8 +165,12 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     return v;
 }
 
-// The row's output from sums relative to m and w.
-__device__ __forceinline__ float output_factor(const CacheState& s) { return s.w == -INFINITY ? 0.f / s.l : ex2(s.w - kCwShift - s.m) / s.l; }
+// The row's output from its sums: two factors, one after the other.  `up` is at most 137 (scales up to 2^127) and may be any
+// number below, so that its power of two alone may leave float32's range where the output does not.
+__device__ __forceinline__ float2 output_factors(const CacheState& s) {
+    const float e = s.up - kCwShift, near = fminf(fmaxf(e, -100.f), 100.f);
+    return s.up == -INFINITY ? make_float2(0.f / s.l, 1.f) : make_float2(ex2(near) / s.l, ex2(e - near));
+}
 
 constexpr int64_t kToOutputs = -1, kToCluster = -2;
 
@@ -179,6 +191,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
     constexpr int kBlock = S::kThreads;       // halves whose pages are looked up at a time, one per thread
     const CacheView& c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int TW = SHARED ? W / 2 : W;    // warps of a team at most
     const int teams = SHARED ? p.teams : 1, team = SHARED ? warp % teams : 0;
     const int rt = rg * teams + team;
     const int R = p.group * p.Nq;
@@ -286,12 +299,12 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
     }
 
     float o[NQ][MT][4];
-    float m[NQ][2], w[NQ][2], l[NQ][2];
+    float m[NQ][2], up[NQ][2], l[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
         for (int x = 0; x < MT; ++x) o[n][x][0] = o[n][x][1] = o[n][x][2] = o[n][x][3] = 0.f;
-        m[n][0] = m[n][1] = w[n][0] = w[n][1] = -INFINITY;
+        m[n][0] = m[n][1] = -INFINITY, up[n][0] = up[n][1] = kCwNone;
         l[n][0] = l[n][1] = 0.f;
     }
     const int all = len - p.Nq + 1;  // keys that every row sees
@@ -305,7 +318,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             const PageEntry en = entry_of(KH * chunk + half);
             ks[half] = en.ks;
             scale[half] = split_scale(en.vs);
-            lv[half] = scale[half].x + 1.f;  // log2 of a bound of the scale
+            lv[half] = fmaxf(scale[half].x, -1e29f) + 1.f;  // log2 of a bound of the scale
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[half][n][0] = s[half][n][1] = s[half][n][2] = s[half][n][3] = 0.f;
 #pragma unroll
@@ -339,39 +352,46 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                     for (int e = 0; e < 4; ++e)
                         if (j0 + 16 * half + 8 * (e >> 1) + g >= lim[n][e & 1]) s[half][n][e] = -INFINITY;
         }
+        // scores against m from here on (without one yet, as they are: up is kCwNone then, and any score raises)
         bool raise = false;
-        float top[KH][NQ][2];
 #pragma unroll
         for (int half = 0; half < KH; ++half)
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    top[half][n][e] = fmaxf(s[half][n][e], s[half][n][2 + e]);
-                    raise |= top[half][n][e] > m[n][e] + kCwTau || top[half][n][e] + lv[half] > w[n][e] + kCwTau;
+                    const float ref = reference(m[n][e]);
+                    s[half][n][e] -= ref;
+                    s[half][n][2 + e] -= ref;
+                    const float top = fmaxf(s[half][n][e], s[half][n][2 + e]);
+                    raise |= top > kCwTau || top + lv[half] > up[n][e] + kCwTau;
                 }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float tm = top[0][n][e], tw = top[0][n][e] + lv[0];
-                    if (KH == 2) tm = fmaxf(tm, top[KH - 1][n][e]), tw = fmaxf(tw, top[KH - 1][n][e] + lv[KH - 1]);
+                    float tm = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                    if (KH == 2) tm = fmaxf(tm, fmaxf(s[KH - 1][n][e], s[KH - 1][n][2 + e]));
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
-                        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
-                        tw = fmaxf(tw, __shfl_xor_sync(0xffffffffu, tw, x));
-                    }
-                    if (tm > m[n][e] + kCwTau) {
-                        const float next = ceilf(tm);
+                    for (int x = 4; x < 32; x <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
+                    if (tm > (m[n][e] == -INFINITY ? -INFINITY : kCwTau)) {
+                        const float ref = reference(m[n][e]), next = ref + ceilf(tm), by = next - ref;
                         l[n][e] *= ratio(m[n][e], next);
+                        up[n][e] -= by;
+#pragma unroll
+                        for (int half = 0; half < KH; ++half) s[half][n][e] -= by, s[half][n][2 + e] -= by;
                         m[n][e] = next;
                     }
-                    if (tw > w[n][e] + kCwTau) {
-                        const float next = ceilf(tw), f = ratio(w[n][e], next);
+                    float tw = fmaxf(s[0][n][e], s[0][n][2 + e]) + lv[0];
+                    if (KH == 2) tw = fmaxf(tw, fmaxf(s[KH - 1][n][e], s[KH - 1][n][2 + e]) + lv[KH - 1]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) tw = fmaxf(tw, __shfl_xor_sync(0xffffffffu, tw, x));
+                    if (tw > up[n][e] + kCwTau) {
+                        const float next = ceilf(tw), f = ex2(up[n][e] - next);
 #pragma unroll
                         for (int x = 0; x < MT; ++x) o[n][x][e] *= f, o[n][x][2 + e] *= f;
-                        w[n][e] = next;
+                        up[n][e] = next;
                     }
                 }
         }
@@ -385,18 +405,17 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
-                    // a probability's factor in the output's units
-                    const float x = w[n][e] == -INFINITY ? 0.f * scale[half].y
-                                                         : scale[half].y * ex2(ref - w[n][e] + kCwShift + fmaxf(scale[half].x, -256.f));
-                    const float p0 = ex2(s[half][n][e] - ref), p1 = ex2(s[half][n][2 + e] - ref);
-                    l[n][e] += p0 + p1;
-                    v[e] = p0 * x;
-                    v[2 + e] = p1 * x;
-                    if (tail) {  // a scale that is no number must not reach rows that do not see its page
-                        if (h0 + g >= lim[n][e]) v[e] = 0.f;
-                        if (h0 + 8 + g >= lim[n][e]) v[2 + e] = 0.f;
-                    }
+                    l[n][e] += ex2(s[half][n][e]) + ex2(s[half][n][2 + e]);
+                    // In the output's units a probability has an exponent of its own.  (As a factor of the one against m it may
+                    // be infinite: the largest score may stand in pages of so small a scale that others, far behind, weigh more.)
+                    const float by = kCwShift + scale[half].x - up[n][e];
+                    v[e] = scale[half].y * ex2(s[half][n][e] + by);
+                    v[2 + e] = scale[half].y * ex2(s[half][n][2 + e] + by);
+                }
+                if (tail) {  // a scale that is no number must not reach rows that do not see its page
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (h0 + 8 * (e >> 1) + g >= lim[n][e & 1]) v[e] = 0.f;
                 }
                 pr[n][0] = transpose8(pack_f16(v[0], v[1]));
                 pr[n][1] = transpose8(pack_f16(v[2], v[3]));
@@ -504,7 +523,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             if (g == 0) {
                 states[(warp * 3) * ROWS + row] = m[n][e];
                 states[(warp * 3 + 1) * ROWS + row] = l[n][e];
-                states[(warp * 3 + 2) * ROWS + row] = w[n][e];
+                states[(warp * 3 + 2) * ROWS + row] = up[n][e];
             }
             float* dst = sums + (warp * ROWS + row) * D + VB * g;  // tile x: d = VB g + 2x, + 1
 #pragma unroll
@@ -518,24 +537,30 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
     auto store = [&](int r, int d0, const CacheState& st, const float4& v) {
         const int h = hk * p.group + r / p.Nq, i = r % p.Nq;
         const bool empty = len - p.Nq + 1 + i <= 0;
-        const float f = empty ? 0.f : output_factor(st);
+        const float2 f = output_factors(st);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + d0) =
-            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v.x * f.x * f.y, v.y * f.x * f.y), pack_bf16(v.z * f.x * f.y, v.w * f.x * f.y));
         if (d0 == 0) p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
     };
     for (int x = threadIdx.x; x < teams * ROWS; x += S::kThreads) {
         const int row = x % ROWS, tm = x / ROWS;
-        CacheState st{-INFINITY, 0.f, -INFINITY};
-        for (int y = tm; y < W; y += teams) {
-            st.m = fmaxf(st.m, states[(y * 3) * ROWS + row]);
-            st.w = fmaxf(st.w, states[(y * 3 + 2) * ROWS + row]);
+        CacheState st{-INFINITY, 0.f, -INFINITY}, in[TW];
+#pragma unroll
+        for (int k = 0; k < TW; ++k) {
+            const float* at = states + (tm + k * teams) * 3 * ROWS + row;
+            in[k] = tm + k * teams < W ? CacheState{at[0], at[ROWS], at[2 * ROWS]} : CacheState{-INFINITY, 0.f, -INFINITY};
+            st.m = fmaxf(st.m, in[k].m);
         }
-        for (int y = tm; y < W; y += teams) {
-            const float mx = states[(y * 3) * ROWS + row], lx = states[(y * 3 + 1) * ROWS + row], wx = states[(y * 3 + 2) * ROWS + row];
-            st.l += mx == -INFINITY ? lx : lx * ex2(mx - st.m);  // without a reference: 0, or NaN scores alone
-            states[(y * 3 + 2) * ROWS + row] = wx == -INFINITY ? 1.f : ex2(wx - st.w);
+#pragma unroll
+        for (int k = 0; k < TW; ++k) {
+            in[k].up = up_from(in[k].m, in[k].up, st.m);
+            st.up = fmaxf(st.up, in[k].up);
+            st.l += in[k].m == -INFINITY ? in[k].l : in[k].l * ex2(in[k].m - st.m);
         }
-        merged[x] = st.m, merged[teams * ROWS + x] = st.l, merged[2 * teams * ROWS + x] = st.w;
+#pragma unroll
+        for (int k = 0; k < TW; ++k)
+            if (tm + k * teams < W) states[((tm + k * teams) * 3 + 2) * ROWS + row] = in[k].up == -INFINITY ? 1.f : ex2(in[k].up - st.up);
+        merged[x] = st.m, merged[teams * ROWS + x] = st.l, merged[2 * teams * ROWS + x] = st.up;
     }
     __syncthreads();
     for (int x = threadIdx.x; x < teams * ROWS * (D / 4); x += S::kThreads) {
@@ -552,13 +577,13 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
         if (given > capacity) st.l = nan;  // tokens that the table has no page for
         if (part == kToCluster) {
             *reinterpret_cast<float4*>(outbox + line * D + d0) = v;
-            if (d0 == 0) *reinterpret_cast<float4*>(outbox + teams * ROWS * D + 4 * line) = make_float4(st.m, st.l, st.w, 0.f);
+            if (d0 == 0) *reinterpret_cast<float4*>(outbox + teams * ROWS * D + 4 * line) = make_float4(st.m, st.l, st.up, 0.f);
             continue;
         }
         if (part >= 0) {
             const int64_t at = part * (ROWS * teams) + line;
             *reinterpret_cast<float4*>(p.part + at * D + d0) = v;
-            if (d0 == 0) p.part_state[at] = make_float4(st.m, st.l, st.w, 0.f);
+            if (d0 == 0) p.part_state[at] = make_float4(st.m, st.l, st.up, 0.f);
             continue;
         }
         store(r, d0, st, v);
@@ -572,17 +597,30 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             if (r >= R) continue;
             CacheState st{-INFINITY, 0.f, -INFINITY};
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < p.cluster; ++k) {
-                const float4 s = ld_cluster(of_rank(box + 4 * (teams * ROWS * D + 4 * line), k));
-                st.m = fmaxf(st.m, s.x);
-                st.w = fmaxf(st.w, s.z);
+            CacheState in[8];
+            float4 u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                in[k] = CacheState{-INFINITY, 0.f, -INFINITY};
+                u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < p.cluster) {
+                    const float4 s = ld_cluster(of_rank(box + 4 * (teams * ROWS * D + 4 * line), k));
+                    in[k] = CacheState{s.x, s.y, s.z};
+                    u[k] = ld_cluster(of_rank(box + 4 * (line * D + d0), k));
+                }
             }
-            for (int k = 0; k < p.cluster; ++k) {
-                const float4 s = ld_cluster(of_rank(box + 4 * (teams * ROWS * D + 4 * line), k));
-                const float4 u = ld_cluster(of_rank(box + 4 * (line * D + d0), k));
-                const float f = s.z == -INFINITY ? 1.f : ex2(s.z - st.w);
-                st.l += s.x == -INFINITY ? s.y : s.y * ex2(s.x - st.m);
-                v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) st.m = fmaxf(st.m, in[k].m);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                in[k].up = up_from(in[k].m, in[k].up, st.m);
+                st.up = fmaxf(st.up, in[k].up);
+                st.l += in[k].m == -INFINITY ? in[k].l : in[k].l * ex2(in[k].m - st.m);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = in[k].up == -INFINITY ? 1.f : ex2(in[k].up - st.up);
+                v.x = fmaf(u[k].x, f, v.x), v.y = fmaf(u[k].y, f, v.y), v.z = fmaf(u[k].z, f, v.z), v.w = fmaf(u[k].w, f, v.w);
             }
             store(r, d0, st, v);
         }
@@ -669,32 +707,31 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_consta
     if (n > 0 && first == last) return;  // the segment's CTA has written the row
     CacheState st{-INFINITY, 0.f, -INFINITY};
     auto index = [&](int k) { return (2 * static_cast<int64_t>(k) + (a < k * share ? 0 : 1)) * (ROWS * p.teams) + line; };
+    for (int k = first + lane; n > 0 && k <= last; k += 32) st.m = fmaxf(st.m, p.part_state[index(k)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
     for (int k = first + lane; n > 0 && k <= last; k += 32) {
         const float4 x = p.part_state[index(k)];
-        st.m = fmaxf(st.m, x.x);
-        st.w = fmaxf(st.w, x.z);
+        st.up = fmaxf(st.up, up_from(x.x, x.z, st.m));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
-        st.w = fmaxf(st.w, __shfl_xor_sync(0xffffffffu, st.w, o));
-    }
+    for (int o = 16; o > 0; o >>= 1) st.up = fmaxf(st.up, __shfl_xor_sync(0xffffffffu, st.up, o));
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
     for (int k = first; n > 0 && k <= last; ++k) {
         const float4 x = p.part_state[index(k)];
         st.l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - st.m);
-        const float f = x.z == -INFINITY ? 1.f : ex2(x.z - st.w);
+        const float f = x.z == -INFINITY ? 1.f : ex2(up_from(x.x, x.z, st.m) - st.up);
         const float* part = p.part + index(k) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);
     }
     const bool empty = max(c.lengths[b], 0) - p.Nq + 1 + i <= 0;
-    const float f = empty ? 0.f : output_factor(st);
+    const float2 f = output_factors(st);
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + i * p.o_n + lane * V);
 #pragma unroll
-    for (int e = 0; e < V; e += 2) out[e / 2] = empty ? 0u : pack_bf16(v[e] * f, v[e + 1] * f);
+    for (int e = 0; e < V; e += 2) out[e / 2] = empty ? 0u : pack_bf16(v[e] * f.x * f.y, v[e + 1] * f.x * f.y);
     if (lane == 0) p.LSE[row] = empty ? -INFINITY : fmaf(st.m, kLn2, logf(st.l));
 }
 
