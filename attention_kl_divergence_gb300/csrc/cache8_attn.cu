@@ -342,7 +342,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[half][n][e] *= qf[n][e & 1] * ks[half];
+                for (int e = 0; e < 4; ++e) s[half][n][e] = s[half][n][e] * qf[n][e & 1] * ks[half];  // qf ks may be infinite where the score is 0
         if (j0 + S::kKeys > all) {
 #pragma unroll
             for (int half = 0; half < KH; ++half)

@@ -86,6 +86,23 @@ def test_outputs_at_both_ends_of_the_range(d, group, Nq, places, splits):
 
 
 @pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("group,Nq", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_queries_over_keys_of_zeros_with_a_large_scale(d, group, Nq, splits):
+    """A page that held large keys and holds zeros now: its scores are 0, whatever 2^70 (the queries) times 2^80 (the scale)
+    is.  The other pages' keys are small ones."""
+    cache, table, n, Q, scale = filled({3: (2.0, 1.0), 16: (-3.0, 5.0)}, 34, 2, d, group, Nq)
+    cache.k_scale *= 2.0 ** -70
+    Q *= 2.0 ** 70
+    for m in (0, 5, 19):
+        page = int(table[0, m])
+        assert not bool(cache.k.view(torch.uint8)[page].any())
+        cache.k_scale[page] = 2.0 ** 80
+    O, LSE = sk.attn_cache8(Q, cache, table, n, scale=scale, num_splits=splits)
+    Ref(Q, cache, table, n, scale).check(O, LSE)
+
+
+@pytest.mark.parametrize("splits", [0, 3])
 @pytest.mark.parametrize("places", PLACES, ids=str)
 @pytest.mark.parametrize("group,Nq", ROWS)
 @pytest.mark.parametrize("d", [64, 128])
