@@ -546,12 +546,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         if (ok && n > 0) ok = wait_all(base + L::bar_o + 8 * sub, 0, wc, kErrWaitOther);
         tc_fence_after();
-        // both sides' sums
-        if (broken) l = __int_as_float(0x7fc00000);
+        // both sides' sums, which are not below 0: the sign says that a value which the row sees is broken.  Its outputs are
+        // NaN then; LSE has no values in it.
         ok = bar_sync_and(1 + sub, 256, ok);
-        tops[128 * side] = l;
+        tops[128 * side] = broken ? -l : l;
         ok = bar_sync_and(1 + sub, 256, ok);
-        l += tops[128 * (side ^ 1)];
+        const float theirs = tops[128 * (side ^ 1)];
+        l += fabsf(theirs);
+        broken |= signbit(theirs);
         if (ok && exists(sub)) ok = wait_all(base + L::bar_q + 8 * sub, 0, wc, kErrWaitQ);  // the stage's bytes
         const float nan = __int_as_float(0x7fc00000);
         const bool fail = __any_sync(0xffffffffu, !ok || *abort_flag);
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         if (fail) l = nan;
         const bool empty = range.x >= range.y;
         if (p.parts == 1) {
-            const float inv = empty ? 0.f : 1.f / l;
+            const float inv = empty ? 0.f : broken ? nan : 1.f / l;
             uint32_t w[D / 64][16], less[D / 64][16];
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
-                if (valid) store_grad32(p.part + at_row * D, k, v, 1.f, false);
+                if (valid) store_grad32(p.part + at_row * D, k, v, broken ? nan : 1.f, false);
                 __syncwarp();
             }
             if (valid && side == 0) p.part_ml[at_row] = make_float2(ref, l);

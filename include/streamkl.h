@@ -414,8 +414,9 @@ STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t
  *    h / (H / H_kv).  Base pointers are 16-byte aligned.
  *  - A row that sees no key has O = 0 and LSE = -inf, and no effect on any
  *    gradient.  What a row does not see (NaN and infinities included) has no
- *    effect on it; a row that sees a NaN or an infinite value of V gets NaN, at
- *    least where that value counts and at most in the whole row.
+ *    effect on it; a row that sees a NaN or an infinite value of V gets NaN or an
+ *    infinity in O, at least where that value counts and at most in the whole row.
+ *    LSE has no values in it.
  *  - rest (NULL or bf16 [B, H, Nq, d], contiguous): what the rounding of O to
  *    bf16 left, for the backward's row sums of dO * O.
  *  - Probabilities enter the product with V rounded to bf16, with rest as two
