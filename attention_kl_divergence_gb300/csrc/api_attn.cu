@@ -272,6 +272,8 @@ streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const void* dO, con
     p.order_group = pl.group;
     p.scale = resolve_scale(scale, s.d);
     p.c = p.scale * kLog2e;
+    p.K = K;
+    p.k_b = s.k.b, p.k_h = s.k.h, p.k_n = s.k.n;
     p.dO = dO;
     p.g_b = s.d_o.b, p.g_h = s.d_o.h, p.g_n = s.d_o.n;
     p.O = O;

@@ -67,6 +67,8 @@ struct AttnBwdParams {
     int num_splits;          // CTAs that share a key tile's query tiles
     int order_group;
     float scale, c;          // softmax scale; times log2(e)
+    const void* K;           // bf16, strided; for keys that are not finite
+    int64_t k_b, k_h, k_n;
     const void* dO;          // bf16, strided
     int64_t g_b, g_h, g_n;
     const void* O;           // bf16, strided

@@ -15,6 +15,11 @@
 // rounding left (`rest`), for the same reason: an error of D is a multiple of the
 // row's mean key in dQ.
 //
+// A zero P or dS does not hide a NaN or an infinity in the operand that it meets in an MMA.
+// Rows that see none of such a token must not get it: keys that hold one become zero rows
+// before the first gradient MMA, query rows in tiles where somebody does not see them.
+// Where they are seen, P and dS are NaN, or dQ gets its NaN apart.
+//
 // Bound by the tensor core: the issuing thread never waits for more than a barrier's own
 // latency, and is held back by 36 MMAs a tile of 65 to 82 cycles each, 2600 of about 3200.
 // The scores' have N = 64 and take 73, no less than those with N = 128 (d = 64: 28 MMAs,
@@ -44,7 +49,9 @@ constexpr int kAbRowBytes = 2 * kBwdTile * 4;  // a tile's row constants
 // One block per (64-row query tile, batch and head), a warp per row at a time: the
 // row's constants, the ranges of the tile (the first head's block) and zeros in its
 // rows of dQ.  A row that sees no key gets zero constants; an infinite LSE (from an
-// infinite score) counts as NaN, as in its own softmax.
+// infinite score) counts as NaN, as in its own softmax, and so does the LSE of a row
+// whose dO has a NaN or an infinity: the key-tile kernel may clear that row of dO, and
+// its P has to carry it into dV.
 template <int D>
 __global__ void __launch_bounds__(256) attn_prepare_kernel(const __grid_constant__ AttnBwdParams p,
                                                            const __grid_constant__ ScoreParams sp) {
@@ -59,10 +66,12 @@ __global__ void __launch_bounds__(256) attn_prepare_kernel(const __grid_constant
     float* out = p.rows + block * (2 * kBwdTile);
     const int half = lane >> 4, at = (lane & 15) * (D / 16);
     float sums[4];
+    bool broken[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int r = 8 * warp + 2 * k + half, i = tile * kBwdTile + r;
         float s = 0.f;
+        bool found = false;
         if (i < p.Nq) {
             const uint32_t* g = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.dO) + (b * p.g_b + h * p.g_h + i * p.g_n) + at);
             const uint32_t* o = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.O) + (b * p.o_b + h * p.o_h + i * p.o_n) + at);
@@ -70,11 +79,13 @@ __global__ void __launch_bounds__(256) attn_prepare_kernel(const __grid_constant
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const uint32_t ug = g[w], uo = o[w], ue = e ? e[w] : 0u;
+                found |= has_nonfinite_bf16(ug);
                 s = fmaf(__uint_as_float(ug << 16), __uint_as_float(uo << 16) + __uint_as_float(ue << 16), s);
                 s = fmaf(__uint_as_float(ug & 0xffff0000u), __uint_as_float(uo & 0xffff0000u) + __uint_as_float(ue & 0xffff0000u), s);
             }
         }
         sums[k] = s;
+        broken[k] = (__ballot_sync(0xffffffffu, found) >> (lane & 16) & 0xffffu) != 0u;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -86,7 +97,7 @@ __global__ void __launch_bounds__(256) attn_prepare_kernel(const __grid_constant
             float nl = 0.f, nd = 0.f;
             if (keys.x < keys.y) {
                 const float l = p.LSE[static_cast<size_t>(bh) * p.Nq + i];
-                nl = fabsf(l) < INFINITY ? -l * kLog2e : __int_as_float(0x7fc00000);
+                nl = fabsf(l) < INFINITY && !broken[k] ? -l * kLog2e : __int_as_float(0x7fc00000);
                 nd = -p.scale * sums[k];
             }
             out[r] = nl;
@@ -173,6 +184,37 @@ struct AttnKvSmem {
 };
 
 constexpr int kAbThreads = 448;
+
+// Whether key `row` of the 128-key tile at `kt` holds a NaN or an infinity.
+template <int D>
+__device__ __forceinline__ bool key_row_broken(const uint8_t* kt, int row) {
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < D / kSwizzleCols; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint4 u = *reinterpret_cast<const uint4*>(kt + c * kBlockK * 128 + row * 128 + ((k ^ (row & 7)) << 4));
+            found |= has_nonfinite_bf16(u.x) | has_nonfinite_bf16(u.y) | has_nonfinite_bf16(u.z) | has_nonfinite_bf16(u.w);
+        }
+    return found;
+}
+
+// NaN in the features that are not finite in the broken key j, of the dQ rows of the wg-th halves of iterations
+// [m0, m0 + n) (see mark_attn_gradients) that see it: what a dS of 0 times it is, without what the tile's other rows
+// would get of it from the MMA.
+__device__ __noinline__ void poison_rows(const AttnBwdParams& p, int d, int b, int hk, int j, int wg, int t0, int per_head, int m0, int n) {
+    const uint16_t* key = static_cast<const uint16_t*>(p.K) + (b * p.k_b + hk * p.k_h + static_cast<int64_t>(j) * p.k_n);
+    const KeyBlock* blocks = static_cast<const KeyBlock*>(p.keys) + static_cast<size_t>(b) * p.num_q_tiles;
+    for (int m = m0; m < m0 + n; ++m) {
+        const int h = hk * p.group + m / per_head, t = t0 + m % per_head;
+        for (int r = 32 * wg; r < 32 * wg + 32; ++r) {
+            if (j < blocks[t].begin[r] || j >= blocks[t].end[r]) continue;
+            float* dq = p.dQacc + ((static_cast<size_t>(b) * p.H + h) * p.Nq + t * kBwdTile + r) * d;
+            for (int f = 0; f < d; ++f)
+                if (has_nonfinite_bf16(key[f])) red_add_f32(dq + f, __int_as_float(0x7fc00000));
+        }
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kAbThreads, 1)
@@ -400,8 +442,13 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const int j = n0 + row;  // key index
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float2 cc = splat(p.c), sc = splat(p.scale);
-        bool ok = true;
-        for (int m = 0; m < n_tiles; ++m) {
+        // Keys with a NaN or an infinity become zero rows before the first gradient MMA: a dS of 0 would not hide them from
+        // rows that do not see them.  The first tiles' scores may be under way and see part of the zeros: for such a key
+        // scores do not count (see below).  The barrier: both threads of a key have read it.
+        bool ok = n_tiles == 0 || wait_all(base + L::bar_k, 0, wc, kErrWaitK);
+        const bool broken = ok && n_tiles > 0 && key_row_broken<D>(gbase + L::k, row);
+        if (bar_sync_or(1, 256, broken)) clear_key_row<D>(base + L::k, row);
+        for (int m = 0; ok && m < n_tiles; ++m) {
             const int sv = m % L::kNv;
             if (!wait_all(base + L::bar_sfull, m & 1, wc, kErrWaitS) ||
                 !wait_all(base + L::bar_vfull + 8 * sv, (m / L::kNv) & 1, wc, kErrWaitQ)) {
@@ -418,6 +465,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const KeyBlock& kb = reinterpret_cast<const KeyBlock*>(gbase + L::keys)[sv];
             const int4 bounds = kb.bounds[wg];
             const bool whole = bounds.z <= n0 && bounds.w >= n0 + kBlockK;  // every row sees every key
+            if (__any_sync(0xffffffffu, broken)) {  // a finite LSE means that the row's score with a broken key is -inf; a NaN in LSE stays
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (broken) z[e] = -INFINITY;
+            }
             uint32_t vis = 0xffffffffu;  // bit e: query row e of the half sees this thread's key
             bool bad = false;
             if (!whole) {
@@ -432,12 +484,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         const int e = 4 * e4 + k;
                         const bool finite = fabsf(z[e]) < INFINITY && fabsf(dp[e]) < INFINITY;
-                        if (j >= los[k] && j < his[k]) {
+                        if (j >= los[k] && j < his[k])
                             vis |= 1u << e;
-                            if (!finite) z[e] = __int_as_float(0x7fc00000);  // the operands' rows are cleared below
-                        } else {
+                        else
                             bad |= !finite;
-                        }
                     }
                 }
             }
@@ -463,12 +513,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 for (int e = 0; e < 32; ++e)
                     if (!((vis >> e) & 1u)) z[e] = dp[e] = 0.f;
                 // A zero P or dS does not hide a NaN or an infinity in the operand it meets in the gradient MMAs:
-                // rows with one become zero rows.  (Where such a row is visible, P and dS are NaN.)
+                // query rows with one become zero rows.  (Where such a row is visible, P and dS are NaN.)
                 if (__any_sync(0xffffffffu, bad)) {
                     const int st = m % L::kNst;
                     clear_query_rows<D>(base + L::q + st * L::kQBytes, wg * 32, lane);
                     clear_query_rows<D>(base + L::g + st * L::kQBytes, wg * 32, lane);
-                    clear_key_row<D>(base + L::k, row);
                 }
             }
             if (!wait_all(base + L::bar_dsempty, (m & 1) ^ 1, wc, kErrWaitOther)) {
@@ -486,6 +535,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(base + L::bar_dsfull);
         }
+        if (broken) poison_rows(p, D, b, hk, j, wg, m_start, per_head, m0, n_tiles);
+        __syncwarp();
         // epilogue: the first warpgroup writes dK, the second dV
         if (ok && (n_tiles == 0 || wait_all(base + L::bar_done, 0, wc, kErrWaitOther))) {
             tc_fence_after();

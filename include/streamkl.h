@@ -446,7 +446,9 @@ STREAMKL_API streamkl_status streamkl_attn_fwd(const streamkl_attn* desc, const 
  * of a key head.  O, rest and LSE are the forward's for the same inputs; without
  * rest (NULL) the row sums of dO * O carry O's rounding, which shows in dQ where
  * keys have much in common.  dQ is added up in no fixed order; dK and dV are the
- * same on every run. */
+ * same on every run.  Tokens that are not finite reach the gradients as in the
+ * formulas (a visible key that scores -inf has P = dS = 0, and dQ = 0 * -inf where
+ * it is infinite), but for those of dO: they make all features of dV NaN. */
 STREAMKL_API streamkl_status streamkl_attn_bwd_plan(const streamkl_attn* desc, const streamkl_options* opt,
                                                     streamkl_plan* plan);
 STREAMKL_API streamkl_status streamkl_attn_bwd(const streamkl_attn* desc, const void* dO, const void* Q, const void* K,
