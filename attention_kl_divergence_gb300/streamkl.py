@@ -1093,12 +1093,15 @@ def attn_bwd(dO, Q, K, V, O, LSE, rest=None, ranges=None, causal=False, scale=No
 
 class Attention(torch.autograd.Function):
     """O of attn_fwd with gradients to Q, K and V, in bf16 like the inputs.  Saves its inputs, O, what O's rounding left
-    and LSE, and recomputes the probabilities in the backward."""
+    and LSE, and recomputes the probabilities in the backward.  Where no input requires a gradient it is attn_fwd without
+    rest, and saves nothing."""
 
     @staticmethod
     def forward(ctx, Q, K, V, ranges=None, causal=False, scale=None):
         _guard_capture(Q, K, V)
         causal, scale = bool(causal), None if scale is None else float(scale)  # the backward's are the forward's
+        if not any(ctx.needs_input_grad[:3]):
+            return attn_fwd(Q, K, V, ranges, causal, scale)[0]
         O, LSE, rest = attn_fwd(Q, K, V, ranges, causal, scale, rest=True)
         ctx.save_for_backward(Q, K, V, O, LSE, rest, *(ranges if ranges is not None else ()))
         ctx.how = dict(causal=causal, scale=scale)
