@@ -13,6 +13,7 @@ import torch
 
 from attention_kl_divergence_gb300 import streamkl as sk
 from test_attn import BF16, DEV, Ref, inputs, masks
+from test_attn_calls import spread
 from test_attn_broken_value import AT, F, SHAPES, plain_ranges
 
 pytestmark = pytest.mark.gpu
@@ -59,6 +60,24 @@ def test_a_key_that_scores_minus_infinity(shape, value, kind, splits):
     ref.check_grads(dO, torch.where(nan, want.to(BF16), dQ), without(dK, AT), without(dV, AT))
     again = sk.attn_bwd(dO, Q, K, V, O, LSE, rest=rest, ranges=ranges, num_splits=splits)
     assert torch.equal(again[1], dK) and torch.equal(again[2], dV) and torch.equal(again[0].isnan(), nan)
+
+
+@pytest.mark.parametrize("how", ["rows by token", "padded rows", "heads first", "every second token"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_such_a_key_in_another_layout(shape, how):
+    Q, K, V = inputs(*shape)
+    Q[..., F] = Q[..., F].abs() + 0.25
+    dO = grad_like(Q)
+    K[:, -1, AT, F], K[0, 0, 17, 2 * F] = -math.inf, math.nan
+    want = sk.attn_fwd(Q, K, V, causal=True, rest=True)
+    grads = sk.attn_bwd(dO, Q, K, V, *want[:2], rest=want[2], causal=True)
+    views = [spread(t, how) for t in (Q, K, V)]
+    got = sk.attn_fwd(*views, causal=True, rest=True)
+    again = sk.attn_bwd(spread(dO, how), *views, *got[:2], rest=got[2], causal=True)
+    for a, b in zip((*got, *again), (*want, *grads)):
+        assert torch.equal(a.isnan(), b.isnan())
+    same = [torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip((*got, *again[1:]), (*want, *grads[1:]))]
+    assert all(same) and bool(grads[0].isnan().any()) and not bool(grads[0].isnan().all())
 
 
 @pytest.mark.parametrize("kind", ["full", "causal", "two ends"])
