@@ -89,6 +89,9 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
     const int64_t heads = int64_t(s->B) * s->H_kv * p.units_h, units = heads * p.units_q;
     if (units > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     const int k_tiles = (s->Nk - 1) / kBlockK + 1;
+    // One tile with no other to pair with stands twice from 8 key tiles on.  One token (us, in a graph; with twice, without): 4
+    // caches, 32 heads on 8, of 896 keys 18.5 / 14.4, 1024 16.4 / 16.4, 1536 16.5 / 16.6, 4096 20.5 / 24.6, 8192 36.9 / 36.9;
+    // one cache, 8 heads on 2, 896 keys 16.9 / 14.4, 1024 16.0 / 13.7, 2048 16.4 / 14.4, 4096 18.5 / 18.5.
     p.dual = p.blocks == 1 && p.q_tiles == 1 && k_tiles >= 8;
     int splits = 1;
     if (opt && opt->num_splits > 0) {
@@ -99,6 +102,9 @@ streamkl_status plan_attn_fwd(const streamkl_attn* s, const streamkl_options* op
         // 5 167, 9 168, 19 185; one cache: 8 splits 77, 14 62, 19 62, 28 83).
         splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, k_tiles / 4)));
     } else {
+        // Splits that leave a CTA fewer key tiles by 4 at least: they cost a second kernel.  300 rows, 8 heads (1 split, chosen ones):
+        // 512 keys 18.5 / 18.5 us, 640 18.5 / 18.0, 1024 24.6 / 18.5; 256 rows, 4 heads, d = 64: 640 16.4 / 14.4, 1536 28.7 / 16.4; one
+        // token, 8 heads on 2: 384 12.3 / 12.3, 512 14.4 / 12.3.
         const int n = choose_splits(units, k_tiles, sms);
         if ((k_tiles + n - 1) / n + 3 < k_tiles) splits = n;
     }
@@ -140,6 +146,14 @@ streamkl_status plan_attn_bwd(const streamkl_attn* s, const streamkl_options* op
     // the iterations of a CTA are counted in 32 bits; the prepare kernel has a block per query tile and head
     if (ctas > INT32_MAX || int64_t(s->B) * s->H * pl->num_q_tiles > INT32_MAX || iterations > INT32_MAX)
         return STREAMKL_ERR_UNSUPPORTED;
+    // The rule of the score gradients (see bwd_splits).  Here, us in a graph, 1 split, the chosen number, the best of 1 to 8 where that
+    // is another:
+    //   4096 rows, 8 heads on 2: causal 444, 143 (5), 134 (4); full 444, 299, 237 (2); window of 256 66, 70, 47 (2); documents 182, 83
+    //   1024 rows, 32 on 8: causal 129, 64 (4); full 129, 90, 78 (2); window 45, 49, 37 (2); documents 64, 51, 47 (2)
+    //   2 x 2048 rows, 16 on 4: causal 250, 169 (3), 152 (2); full 248, 274; window 68, 94; documents 119, 102
+    //   3 x 1001 rows, 12 on 4, d = 64: causal 88, 55 (3); full 97, 77; window 33, 39; documents 58, 47, 45 (2)
+    //   4 x 1024 rows, 8 on 8: 1 chosen, and the best under every mask
+    // The parts are twice those of the score gradients (dK and dV), and windows want fewer of them.
     pl->splits = opt && opt->num_splits > 0 ? std::min(opt->num_splits, kMaxSplits) : bwd_splits(ctas, iterations, sms);
     if (ctas * pl->splits > INT32_MAX) return STREAMKL_ERR_UNSUPPORTED;
     pl->ctas = static_cast<int>(ctas * pl->splits);

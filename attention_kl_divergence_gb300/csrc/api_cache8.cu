@@ -93,7 +93,10 @@ streamkl_status plan_cache_attn(const streamkl_cache8* s, const streamkl_options
     // table allows, equal shares of all sequences serve better than equal CTAs for unequal ones.  One token, 32 heads on
     // 8, unequal lengths up to 4096 / 8192 / 16384 of 4 sequences: 12.9 / 16.9 / 26.3 us with clusters of 4, 21.4 / 24.1 /
     // 30.3 with equal shares; of 8 sequences: 16.8 / 25.3 / 45.3 with clusters of 2, 24.1 / 29.0 / 45.1.  Eight tokens of
-    // 8: 38.0 / 64.7 / 117.6 against 42.5 / 58.8 / 94.7.
+    // 8: 38.0 / 64.7 / 117.6 against 42.5 / 58.8 / 94.7.  Nor are equal shares better for so many sequences that their
+    // segments fill the SMs by themselves, from 8 segments an SM on.  One token, 32 heads on 8, sequences of 16384, of up to that, and
+    // one of 16384 among ones of 300 (equal shares / whole segments): 152 sequences 602 / 585, 441 / 350, 111 / 77; 76 sequences
+    // 306 / 296, 253 / 201, 78 / 76; 20 sequences 96 / 147, 92 / 66, 53 / 76.
     const int64_t capacity = int64_t(s->M) * s->T, steps = (capacity + 255) / 256;
     int cluster = 1;
     while (cluster < 8 && 2 * cluster <= steps && segments * 2 * cluster <= (cluster == 4 ? sms / 2 : sms)) cluster *= 2;

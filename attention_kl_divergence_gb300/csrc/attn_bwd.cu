@@ -24,8 +24,9 @@
 // latency, and is held back by 36 MMAs a tile of 65 to 82 cycles each, 2600 of about 3200.
 // The scores' have N = 64 and take 73, no less than those with N = 128 (d = 64: 28 MMAs,
 // 2100 of 2830 cycles, with half the operations).  8192 causal rows, 32 heads on 8,
-// d = 128: 1568 us, 877 TFLOP/s of the five products, and 55 + 27 us for the first and the
-// last kernel, which are bound by HBM.  Reductions into dQ out of registers, without the
+// d = 128: 1575 us, 873 TFLOP/s of the five products, and 56 + 27 us for the first and the
+// last kernel, which are bound by HBM (without the search for tokens that are not finite, whose
+// registers spill 24 bytes: 1568 and 55).  Reductions into dQ out of registers, without the
 // stage in shared memory, took 1660 us for the three where these take 1653 (d = 64: 1524,
 // 1420).  128-row query tiles, with P and dS as operands in
 // tensor memory and dQ in dP's place there, took 3357 us: no space is left for a second tile,

@@ -15,7 +15,8 @@
 // 8 heads, d = 128: 1594 us, 1379 TFLOP/s.  8192 causal rows, 32 heads on 8, with rest:
 // 592 us, 929 TFLOP/s, and half as much again for the second term.  8192 rows in documents:
 // 191 us, 720 TFLOP/s; a CTA spends about 13000 cycles on its start and end there and 33000
-// on its key tiles.  One token over 4 caches of up to 65536 keys: 160 us, 5.9 TB/s.
+// on its key tiles.  At the 96 registers that 19 warps leave a thread the kernels spill 48 to 60
+// bytes.  One token over 4 caches of up to 65536 keys: 160 us, 5.9 TB/s.
 #include "attn.cuh"
 #include "bwd_common.cuh"
 #include "common.cuh"

@@ -12,6 +12,11 @@
 // f16 after a scaling by a power of two.  Probabilities are f16 with 2^7 more than
 // their value, so that they keep all 11 bits down to 2^-21.
 //
+// Sums of the output stand against a reference of their own, as scales of pages may lie any
+// distance apart: a probability has an exponent for l and one for the output.  (Its value for
+// l times a factor is as fast with one row tile, and with 32 rows 111 us where this takes
+// 113, 8 caches of up to 16384; but the factor leaves float32's range.)
+//
 // A segment is one sequence's keys of one key head.  Its chunks are dealt out to the
 // warps of a CTA, each of which has a ring of its own that TMA fills, 16 tokens of a
 // page at a time.  With more than one row tile, teams of warps share the copies.
@@ -20,7 +25,7 @@
 // ones, every CTA takes the same number of chunks of all segments, one after the
 // other, and a second kernel adds up the parts of segments that were cut.
 //
-// One token, 32 heads on 8, d = 128, 4 sequences of up to 131072 tokens: 162 us, 5.7 TB/s
+// One token, 32 heads on 8, d = 128, 4 sequences of up to 131072 tokens: 164 us, 5.7 TB/s
 // (a copy: 6.8): about 20 us are start, ends and the second kernel, the rest runs near
 // the copy rate.  Five tokens of 3 sequences of up to 1000: 12.7 us (one CTA a segment:
 // 21.5), a chain of latencies.  With two teams (17 to 32 rows) the MMAs and conversions,
