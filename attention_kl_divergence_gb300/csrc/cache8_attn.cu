@@ -56,7 +56,7 @@ struct CacheShape {
 constexpr int kCwStages = 3;      // a warp's chunks in its ring: one in use, the others on their way
 constexpr float kCwTau = 8.f;     // references may stay this far (log2) below the largest value
 constexpr float kCwShift = 7.f;   // probabilities are at most 2^(8 + 7) < 65504
-constexpr float kCwNone = -1e30f; // the output's reference where there is none yet
+constexpr float kCwNone = -3.4e38f;  // the output's reference where there is none yet: below any score
 
 // 16 rows of d bytes, swizzled so that 8 rows' pieces lie in different banks.
 __device__ __forceinline__ void copy_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row) {
@@ -116,7 +116,7 @@ __device__ __forceinline__ float ratio(float from, float to) { return from == -I
 
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
-// The distance from another m, not below the state's own; -inf without a reference: 0 sums, or NaN scores alone.
+// The distance from another m, not below the state's own.  A state without m has sums of 0, or NaN: its weight is 1.
 __device__ __forceinline__ float up_from(float m, float up, float top) { return m == -INFINITY ? -INFINITY : up + (m - top); }
 
 // Chunks of `keys` keys of sequence b.
@@ -383,7 +383,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
                     if (tm > (m[n][e] == -INFINITY ? -INFINITY : kCwTau)) {
                         const float ref = reference(m[n][e]), next = ref + ceilf(tm), by = next - ref;
                         l[n][e] *= ratio(m[n][e], next);
-                        up[n][e] -= by;
+                        if (m[n][e] != -INFINITY) up[n][e] -= by;
 #pragma unroll
                         for (int half = 0; half < KH; ++half) s[half][n][e] -= by, s[half][n][2 + e] -= by;
                         m[n][e] = next;
@@ -564,7 +564,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
         }
 #pragma unroll
         for (int k = 0; k < TW; ++k)
-            if (tm + k * teams < W) states[((tm + k * teams) * 3 + 2) * ROWS + row] = in[k].up == -INFINITY ? 1.f : ex2(in[k].up - st.up);
+            if (tm + k * teams < W) states[((tm + k * teams) * 3 + 2) * ROWS + row] = in[k].m == -INFINITY ? 1.f : ex2(in[k].up - st.up);
         merged[x] = st.m, merged[teams * ROWS + x] = st.l, merged[2 * teams * ROWS + x] = st.up;
     }
     __syncthreads();
@@ -624,7 +624,7 @@ __device__ __forceinline__ bool attend(const CacheAttnParams& p, const CUtensorM
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float f = in[k].up == -INFINITY ? 1.f : ex2(in[k].up - st.up);
+                const float f = in[k].m == -INFINITY ? 1.f : ex2(in[k].up - st.up);
                 v.x = fmaf(u[k].x, f, v.x), v.y = fmaf(u[k].y, f, v.y), v.z = fmaf(u[k].z, f, v.z), v.w = fmaf(u[k].w, f, v.w);
             }
             store(r, d0, st, v);
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(const __grid_consta
     for (int k = first; n > 0 && k <= last; ++k) {
         const float4 x = p.part_state[index(k)];
         st.l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - st.m);
-        const float f = x.z == -INFINITY ? 1.f : ex2(up_from(x.x, x.z, st.m) - st.up);
+        const float f = x.x == -INFINITY ? 1.f : ex2(up_from(x.x, x.z, st.m) - st.up);
         const float* part = p.part + index(k) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(part[e], f, v[e]);

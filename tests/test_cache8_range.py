@@ -133,3 +133,22 @@ def test_rows_that_see_nothing_of_a_share(d, group, Nq, splits):
             n.fill_(256 * steps + behind)
             O, LSE = sk.attn_cache8(Q, cache, table, n, num_splits=splits)
             Ref(Q, cache, table, n).check(O, LSE)
+
+
+@pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("places", PLACES, ids=str)
+@pytest.mark.parametrize("group,Nq", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("step", [2.0 ** 60, 2.0 ** 95, 2.0 ** 119])
+def test_scores_far_below_0_and_on_both_sides_of_it(step, d, group, Nq, places, splits):
+    """The largest are 32 steps below 0, or above it with all others as far below it; two pages have it."""
+    for top, rest in ((-32.0, -64.0), (64.0, -64.0)):
+        pages_of = {m: (rest * step, 448.0 * 2.0 ** (m % 7)) for m in range(34)}
+        pages_of[places[0]], pages_of[places[1]] = (top * step, 448 * 2.0 ** 3), (top * step, 448 * 2.0 ** -20)
+        cache, table, n, Q, scale = filled(pages_of, 34, 2, d, group, Nq, step=step)
+        O, LSE = sk.attn_cache8(Q, cache, table, n, scale=scale, num_splits=splits)
+        at = table[0, list(places)].long()
+        v = (cache.v.double() * cache.v_scale.double()[..., None, None])[at].mean((0, 2)).repeat_interleave(group, 0)
+        relative(O, v[None, :, None].expand_as(O), 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -16)
+        want = top * step * math.log(2.0)
+        assert bool(((LSE.double() - want).abs() <= 2.0 ** -21 * abs(want)).all())
