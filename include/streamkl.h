@@ -421,6 +421,8 @@ STREAMKL_API streamkl_status streamkl_rope_table(const double* inv_freq, int64_t
  *    bf16 left, for the backward's row sums of dO * O.
  *  - Probabilities enter the product with V rounded to bf16, with rest as two
  *    bf16 terms; sums, maxima and outputs are float32 until their one rounding.
+ *  - Scores are float32: a probability is off by up to about 2^-22 max |S|, and
+ *    rows with scores beyond 2^28 may be NaN.
  *  - Equal inputs give equal bits.  A give-up of a bounded wait leaves NaN in
  *    the rows that it left unfinished.
  *  - workspace may be NULL for a forward whose plan has 256 bytes (one split):
